@@ -1,0 +1,104 @@
+"""Block tables and slot maps against the 64-bit reference, bit-exact."""
+import numpy as np
+import pytest
+import torch
+
+import step_reference as R
+from linear_attention_decode_04_gb300 import KdaBlockTablesCall, kda_block_tables
+
+pytestmark = pytest.mark.gpu
+
+
+def run(dev, cached, new, bs, *, T=None, M=None, num_blocks=None, free=None, head=0, seed=0, row_pad=0, table=None,
+        with_head=True):
+    rng = np.random.default_rng(seed)
+    cached, new = np.asarray(cached, np.int32), np.asarray(new, np.int32)
+    B = len(cached)
+    need = [max(0, -(-(int(c) + int(n)) // bs)) if c >= 0 and n >= 0 else 0 for c, n in zip(cached, new)]
+    M = max([1] + need) + 1 if M is None else M
+    num_blocks = sum(need) + head + 20 if num_blocks is None else num_blocks
+    ids = rng.permutation(num_blocks).astype(np.int32)
+    if table is None:
+        table = np.full((B, M), -5, np.int32)
+        at = 0
+        for b in range(B):
+            k = min(-(-max(int(cached[b]), 0) // bs), M)
+            table[b, :k] = ids[at:at + k]
+            at += k
+        ids = ids[at:]
+    free = ids if free is None else np.asarray(free, np.int32)
+    T = max(0, int(np.maximum(new, 0).sum())) if T is None else T
+    want = R.block_tables(cached, new, table, free, head, bs, num_blocks, T)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    wide = torch.full((B, M + row_pad), -77, dtype=torch.int32, device=dev)
+    wide[:, :M] = t(table)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    got = kda_block_tables(t(cached), t(new), wide[:, :M], t(free), torch.tensor([head], dtype=torch.int32, device=dev)
+                           if with_head else None, block_size=bs, num_blocks=num_blocks, num_tokens=T, err_flag=err)
+    torch.cuda.synchronize(dev)
+    assert np.array_equal(wide[:, :M].cpu().numpy(), want[0])
+    assert bool((wide[:, M:] == -77).all())
+    for g, w in zip(got, want[1:5]):
+        assert g.cpu().tolist() == list(w)
+    assert got[4].item() == want[5]
+    assert err.item() == want[6]
+    return want[6]
+
+
+@pytest.mark.parametrize("bs", [1, 16, 24, 64, 256])
+def test_random_batches(bs, cuda_device):
+    rng = np.random.default_rng(bs)
+    # around the 512 rows of a CTA and the 2048 requests of a scan tile
+    for B in (1, 7, 511, 513, 2047, 2048, 2049, 5000):
+        new = rng.integers(0, 5, B) * (rng.random(B) < 0.9)
+        new[rng.integers(0, B)] = 300
+        assert run(cuda_device, rng.integers(0, 200, B), new, bs, seed=B, head=3, row_pad=2) == 0
+
+
+def test_edges(cuda_device):
+    assert run(cuda_device, [], [], 16, T=5) == 0                      # no requests: only padding rows
+    assert run(cuda_device, [5, 0, 16], [0, 0, 0], 16, T=0) == 0       # nothing new
+    assert run(cuda_device, [0, 15, 16, 17], [1, 1, 1, 1], 16, T=700) == 0   # a padded step
+    assert run(cuda_device, [0], [4000], 64, with_head=False) == 0     # one long prompt over many CTAs
+    assert run(cuda_device, [0] * 3000, [1] * 3000, 16) == 0
+    assert run(cuda_device, [2 ** 31 - 9], [5], 2 ** 30, M=2) == 0     # positions near 2^31
+
+
+def test_errors_set_bits_and_stay_in_bounds(cuda_device):
+    assert run(cuda_device, [3, -4, 5, 2 ** 31 - 2], [2, 3, -1, 9], 16) == R.SEQLENS
+    assert run(cuda_device, [3, 14, 0], [20, 20, 20], 16, free=[4, 2]) == R.CAPACITY        # the list runs out
+    assert run(cuda_device, [0, 0], [20, 20], 16, free=[4, 2, 1, 3], head=2) == R.CAPACITY  # it began partly used
+    assert run(cuda_device, [0], [20], 16, free=[4, 2], head=7) == R.CAPACITY               # head behind the end
+    assert run(cuda_device, [0], [20], 16, free=[4, 2], head=-1) == R.CAPACITY
+    assert run(cuda_device, [10, 30], [40, 3], 16, M=2, num_blocks=40) == R.CAPACITY        # a row too narrow
+    assert run(cuda_device, [0, 5], [9, 9], 16, T=12) == R.CAPACITY                         # more tokens than rows
+    assert run(cuda_device, [0, 0], [9, 9], 16, free=[40, 1], num_blocks=40) == R.SLOT_RANGE
+    assert run(cuda_device, [3], [2], 16, table=np.array([[99, 1]], np.int32), M=2, num_blocks=40) == R.SLOT_RANGE
+    assert run(cuda_device, [3], [2], 16, table=np.array([[-1, 1]], np.int32), M=2, num_blocks=40) == R.SLOT_RANGE
+
+
+def test_graph_replay_follows_the_lengths(cuda_device):
+    dev, B, bs = cuda_device, 6, 16
+    cached = torch.tensor([0, 15, 16, 40, 63, 7], dtype=torch.int32, device=dev)
+    new = torch.ones(B, dtype=torch.int32, device=dev)
+    table = torch.full((B, 8), -1, dtype=torch.int32, device=dev)
+    table[:, :4] = torch.arange(B * 4, dtype=torch.int32, device=dev).view(B, 4)
+    free = torch.arange(100, 140, dtype=torch.int32, device=dev)
+    head = torch.zeros(1, dtype=torch.int32, device=dev)
+    call = KdaBlockTablesCall(cached, new, table, free, head, block_size=bs, num_blocks=200, num_tokens=B)
+    call()
+    torch.cuda.synchronize(dev)
+    g = torch.cuda.CUDAGraph()
+    table[:, 4:] = -1
+    with torch.cuda.graph(g):
+        call()
+        head.copy_(call.free_head_out)
+        cached.copy_(call.seq_lens)
+    c, t, h = cached.cpu().numpy().copy(), table.cpu().numpy().copy(), 0
+    for _ in range(40):                                # several blocks per request, one token at a time
+        g.replay()
+        torch.cuda.synchronize(dev)
+        t, _, lens, pos, slot, h, err = R.block_tables(c, [1] * B, t, free.tolist(), h, bs, 200, B)
+        assert err == 0 and call.slot_map.tolist() == slot and call.positions.tolist() == pos
+        assert head.item() == h and np.array_equal(table.cpu().numpy(), t)
+        c = np.asarray(lens)
