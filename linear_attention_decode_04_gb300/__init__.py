@@ -1,7 +1,7 @@
 """GB300-native fused KDA (Kimi Delta Attention) single-token decode step and
 chunked varlen prefill, and the operators of a serving step around them
-(block tables, q/k norm with rotation and 8-bit cache write, verification of
-drafted tokens).
+(block tables, q/k norm with rotation and 8-bit cache write, attention over
+that cache, verification of drafted tokens).
 
 The compute lives in one hand-written CUDA library (``csrc/``) behind a C ABI
 (``include/kda_decode.h``); ``kda_decode`` here only marshals torch tensors
@@ -30,9 +30,12 @@ from .binding import (  # noqa: F401
 from .step_ops import (  # noqa: F401
     KDA_ROPE_INTERLEAVED,
     KdaBlockTablesCall,
+    KdaCacheAttentionCall,
     KdaQkRopeCall,
     KdaVerifyDraftCall,
+    cache_attention_workspace,
     kda_block_tables,
+    kda_cache_attention,
     kda_qk_rope,
     kda_verify_draft,
     rope_frequencies,

@@ -1,0 +1,996 @@
+// kda_cache_attention.cu -- causal softmax attention over the 8-bit paged
+// cache (definition in include/kda_cache_attention.h).
+//
+// Single tokens and multi-token steps are bound by HBM (the cache is read
+// once); prompt chunks by the softmax arithmetic and the tensor cores.
+//
+// Products.  Both are formed transposed, so that the cache's codes are the
+// 128-row operand and the few queries the narrow one:
+//   S^T [token][row]   = K [token][d]   Q^T [d][row]      (128 x R, k = 128)
+//   O^T [d][row]       = V^T [d][token] P^T [token][row]  (128 x R, k = 128)
+// with R query rows (tokens x heads of one kv head).  K and V tiles of 128
+// tokens go from the paged cache to shared memory by TMA (128-byte swizzle)
+// and from there to tcgen05 kind::f8f6f4 untouched: K as a K-major operand, V
+// as an M-major one.  The narrow operand is split into two e4m3 parts (leading
+// and remainder), each a product of its own into the same accumulator; the
+// tensor cores have time for that, and no code of the cache is ever converted.
+//
+// Block scales.  k_scale multiplies S.  v_scale is folded into the weights:
+// with z = s + log2(v_scale) a token's weight is w = 2^(z - M), M the largest
+// z of the tile, so a row's weights use e4m3's range whatever the scales are;
+// the softmax sum adds w / v_scale.  Every tile has its own M and its own
+// accumulator, which is added to the row's fp32 sum in registers with the
+// factor 2^(M - running max): an accumulator never has to be rescaled, and
+// a tile of small weights loses no bits beside a large one.
+//
+// Work split.  The tiles of all (sequence, row tile, kv head) units in one
+// row are dealt out evenly to the resident CTAs, whatever the lengths; a unit
+// that several CTAs share leaves partial sums in the workspace, and the CTA
+// that arrives last joins them in order of position (the result does not
+// depend on who is last).
+//
+// Roles.  One producer warp (block table and scales two tiles ahead, TMA
+// into a ring), one warp whose lane 0 issues the products, and one warpgroup
+// per 32 rows: thread = token of S^T, then channel of O^T.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "kda_cache_attention.h"
+#include "kda_chunk_metadata.h"
+#include "kda_internal.h"
+
+namespace {
+
+constexpr int kD = KDA_HEAD_DIM;
+constexpr int kTile = 128;                 // tokens per tile
+constexpr int kTileBytes = kTile * kD;     // of K, and of V
+constexpr int kMaxPages = 8;               // blocks of a tile, at block size 16
+constexpr int kMaxCtas = 304;              // 2 x 152
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Params {
+  int B, T, Hq, Hkv, G, bs, num_blocks, max_blocks;
+  float scale;  // sm_scale * log2(e)
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* out;
+  int64_t out_stride;
+  const int32_t *cu, *lens, *table;
+  int64_t table_stride;
+  const float *k_scale, *v_scale;
+  int32_t* counters;
+  float* partial;
+  int32_t* err;
+};
+
+template <int R>
+struct Cfg {
+  static constexpr int kGroups = R > 32 ? 2 : 1;        // softmax warpgroups
+  static constexpr int kCols = R / kGroups;             // rows of a warpgroup (columns of S^T)
+  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kCtasPerSm = R > 32 ? 1 : 2;
+  // Ring depths in tiles.  A K tile is free after its S product, about a tile's
+  // time before its V tile is; at 32 rows two CTAs fit an SM with K two deep.
+  static constexpr int kK = R > 32 ? 4 : R > 16 ? 2 : 3;
+  static constexpr int kV = R > 32 ? 5 : 3;
+  static constexpr int kNan = kGroups > 1 ? 4 : 1;
+  static constexpr int kTmemCols = 4 * R;               // S and O, two buffers each
+  static constexpr int kPartial = kCols * (kD + 2);     // floats of a partial record
+};
+
+template <int R>
+struct alignas(1024) Smem {
+  using C = Cfg<R>;
+  uint8_t p[2][R * kTile];                // leading part, remainder; [row / 16][token][row % 16]
+  uint8_t q[2][R * kD];                   // likewise; core matrices of 8 rows x 16 bytes
+  uint8_t k[C::kK][kTileBytes], v[C::kV][kTileBytes];
+  uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], sc_full[C::kV + 1];
+  uint64_t s_full[2], o_full[2], p_full, q_full, done;
+  // k_scale, log2(v_scale), 1 / v_scale of a tile's blocks.  One deeper than the
+  // V ring: written before the tile's V place is waited for, when the tile
+  // kV + 1 before it has been weighed.
+  float4 sc[C::kV + 1][kMaxPages];
+  float row_scale[R];
+  int limit[R];
+  float wmax[2][C::kGroups][4][C::kCols];
+  float wsum[C::kGroups][4][C::kCols];
+  int nan_at[C::kNan][kD];                // per unit and channel: first position that holds a NaN value
+  int64_t walk[4];                        // where this CTA's tiles start
+  int64_t scan[C::kThreads / 32];
+  uint32_t tmem;
+  int failed;
+  int last[C::kGroups];
+};
+// Per warp, broadcast to its lanes: the tile's maxima, and the two factors per
+// row of the tile and of the one before.
+template <int R>
+struct Bcast {
+  float mt[Cfg<R>::kCols];
+  float alpha[2][Cfg<R>::kCols], beta[2][Cfg<R>::kCols];
+};
+
+__device__ __forceinline__ uint32_t s32(const void* ptr) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(ptr));
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(s32(b)), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(s32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(s32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase, at most kWaitLimitNs; after any thread of the CTA has
+// given up, no thread waits any more.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, int* failed) {
+  if (bar_try(b, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (bar_try(b, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(failed)) return false;
+    uint64_t now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if (it == 0) t0 = now;
+    else if (now - t0 > kWaitLimitNs) {
+      *reinterpret_cast<volatile int*>(failed) = 1;
+      return false;
+    }
+  }
+}
+// The same without regard to others that gave up: for copies already on their way.
+__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
+  uint64_t t0, now;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+  while (!bar_try(b, parity) && now - t0 < kWaitLimitNs);
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(s32(b)) : "memory");
+}
+// Shared-memory matrix descriptor: start, leading and stride byte offsets in
+// 16-byte units, version 1, swizzle (0 none, 2 = 128 bytes).
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (static_cast<uint64_t>(swizzle) << 61);
+}
+// Instruction descriptor, kind::f8f6f4: f32 accumulator, e4m3 operands, M = 128, N = n.
+__host__ __device__ constexpr uint32_t idesc(uint32_t n, bool a_m_major, bool b_n_major) {
+  return (1u << 4) | (static_cast<uint32_t>(a_m_major) << 15) | (static_cast<uint32_t>(b_n_major) << 16) |
+         ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int tok, int head, int block, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(0), "r"(tok), "r"(head), "r"(block), "r"(s32(b))
+      : "memory");
+}
+// N consecutive columns of this warp's 32 lanes.  The load writes the
+// registers of all 32 threads, so the warp has to be together: a thread still
+// on a branch of its own would find its registers overwritten.
+template <int N>
+__device__ __forceinline__ void tm_ld(uint32_t addr, float (&r)[N]);
+template <>
+__device__ __forceinline__ void tm_ld<16>(uint32_t addr, float (&r)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void tm_ld<32>(uint32_t addr, float (&r)[32]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 0xff in the bytes that are NaN codes (0x7f, 0xff)
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+// Clears the NaN codes of this thread's row of a swizzled tile and notes the
+// position per channel.  Rare; all threads of the warp call it.
+__device__ __forceinline__ void take_out_nan(uint8_t* row, bool mine, int t, int pos, int* nan_at) {
+  if (mine)
+#pragma unroll 1
+    for (int c = 0; c < kD / 4; ++c) {  // four channels at a time, from their swizzled place
+      uint32_t* w = reinterpret_cast<uint32_t*>(row + ((c >> 2) ^ (t & 7)) * 16 + (c & 3) * 4);
+      const uint32_t m = nan_bytes(*w);
+      if (m) {
+        *w &= ~m;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)
+          if ((m >> (8 * j)) & 1) atomicMin(nan_at + 4 * c + j, pos);
+      }
+    }
+  __syncwarp();
+}
+template <int GROUP_THREADS>
+__device__ __forceinline__ void group_sync(int g) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(g + 1), "n"(GROUP_THREADS) : "memory");
+}
+
+// ------------------------------------------------------------------ the walk
+// Units in the order sequence, row tile, kv head; a unit's tiles in order.
+struct Walk {
+  int seq, rt, h;        // current unit
+  int n, len, q0;        // the sequence's queries, length, first query row
+  int rts, nt;           // its row tiles; tiles of the current unit
+};
+template <int R>
+__device__ __forceinline__ int tiles_of(const Params& p, int n, int len, int rt) {
+  const int rows = n * p.G;
+  const int last = min(rows, (rt + 1) * R) - 1;  // last query row of the tile
+  const int limit = len - n + last / p.G + 1;    // tokens it sees
+  return limit <= kTile ? 1 : (limit + kTile - 1) / kTile;
+}
+template <int R>
+__device__ __forceinline__ bool load_seq(const Params& p, Walk& w) {  // false: nothing to do in this sequence
+  if (w.seq < 0 || w.seq >= p.B) {  // cannot be; an empty end of the walk rather than a stray read
+    w.q0 = w.n = w.len = w.rt = w.h = 0;
+    w.rts = 1;
+    return true;
+  }
+  const int a = p.cu[w.seq], b = p.cu[w.seq + 1];
+  w.q0 = a;
+  w.n = b - a;
+  w.len = p.lens[w.seq];
+  if (a < 0 || b < a || b > p.T) w.n = 0;
+  if (w.len > 0x7fffff00) w.len = 0x7fffff00;
+  if (w.len < 0) w.len = 0;
+  w.rt = w.h = 0;
+  w.rts = static_cast<int>((static_cast<int64_t>(w.n) * p.G + R - 1) / R);
+  return w.n > 0;
+}
+template <int R>
+__device__ __forceinline__ void next_unit(const Params& p, Walk& w) {  // only called while units are left
+  if (++w.h < p.Hkv) return;
+  w.h = 0;
+  if (++w.rt >= w.rts) {
+    do ++w.seq;
+    while (!load_seq<R>(p, w));
+  }
+  w.nt = tiles_of<R>(p, w.n, w.len, w.rt);
+}
+template <int R>
+__device__ __forceinline__ int64_t seq_tiles(const Params& p, int i) {
+  Walk w;
+  w.seq = i;
+  if (!load_seq<R>(p, w)) return 0;
+  int64_t s = 0;
+  for (int rt = 0; rt < w.rts; ++rt) s += tiles_of<R>(p, w.n, w.len, rt);
+  return s * p.Hkv;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int R>
+__global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
+    cache_attention_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
+                           const __grid_constant__ CUtensorMap v_map) {
+  using C = Cfg<R>;
+  constexpr int kCols = C::kCols;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<R>& S = *reinterpret_cast<Smem<R>*>(raw);
+  Bcast<R>* bcast = reinterpret_cast<Bcast<R>*>(raw + sizeof(Smem<R>));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::kK; ++i) bar_init(&S.k_full[i], 1), bar_init(&S.k_empty[i], 1);
+    for (int i = 0; i < C::kV; ++i) bar_init(&S.v_full[i], 1), bar_init(&S.v_empty[i], 1);
+    for (int i = 0; i <= C::kV; ++i) bar_init(&S.sc_full[i], 1);
+    for (int i = 0; i < 2; ++i) bar_init(&S.s_full[i], 1), bar_init(&S.o_full[i], 1);
+    bar_init(&S.p_full, 128 * C::kGroups);
+    bar_init(&S.q_full, 128 * C::kGroups);
+    bar_init(&S.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    S.failed = 0;
+  }
+  __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)),
+                 "n"(C::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // ---- where this CTA's tiles lie: total, then the sequence they start in
+  int64_t mine = 0;
+  bool bad = false;
+  for (int i = tid; i < p.B; i += C::kThreads) {
+    mine += seq_tiles<R>(p, i);
+    const int a = p.cu[i], b = p.cu[i + 1];
+    bad |= a < 0 || b < a || b > p.T;
+  }
+  if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, KDA_DEVERR_SEQLENS);
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0) S.scan[warp] = x;
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = S.tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < C::kThreads / 32; ++w) total += S.scan[w];
+  // one tile at least for each CTA that takes part, so that every CTA between
+  // a unit's first and last leaves a part of it
+  const int64_t cta = blockIdx.x, ctas = max(min(static_cast<int64_t>(gridDim.x), total), int64_t{1});
+  const int64_t begin = cta < ctas ? cta * total / ctas : 0, end = cta < ctas ? (cta + 1) * total / ctas : 0;
+  if (begin < end) {
+    int64_t before = 0;
+    for (int base = 0; base < p.B; base += C::kThreads) {
+      __syncthreads();
+      const int i = base + tid;
+      const int64_t t = i < p.B ? seq_tiles<R>(p, i) : 0;
+      int64_t incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) S.scan[warp] = incl;
+      __syncthreads();
+      int64_t prior = before, all = 0;
+#pragma unroll
+      for (int w = 0; w < C::kThreads / 32; ++w) {
+        if (w < warp) prior += S.scan[w];
+        all += S.scan[w];
+      }
+      const int64_t from = prior + incl - t;
+      if (t > 0 && begin >= from && begin < from + t) {
+        Walk w;
+        w.seq = i;
+        load_seq<R>(p, w);
+        int64_t off = begin - from;
+        int nt = tiles_of<R>(p, w.n, w.len, 0);
+        while (off >= static_cast<int64_t>(nt) * p.Hkv) {
+          off -= static_cast<int64_t>(nt) * p.Hkv;
+          nt = tiles_of<R>(p, w.n, w.len, ++w.rt);
+        }
+        S.walk[0] = i;
+        S.walk[1] = w.rt;
+        S.walk[2] = off / nt;
+        S.walk[3] = off % nt;
+      }
+      before += all;
+      if (before > begin) break;
+    }
+    __syncthreads();
+    Walk w;
+    w.seq = static_cast<int>(S.walk[0]);
+    load_seq<R>(p, w);
+    w.rt = static_cast<int>(S.walk[1]);
+    w.h = static_cast<int>(S.walk[2]);
+    w.nt = tiles_of<R>(p, w.n, w.len, w.rt);
+    int t0 = static_cast<int>(S.walk[3]);
+    int64_t left = end - begin;
+
+    if (warp == 4 * C::kGroups) {
+      // ================================================================ producer
+      const int ppt = p.bs >= kTile ? 1 : kTile / p.bs;  // blocks of a tile
+      const int rows = p.bs >= kTile ? kTile : p.bs;     // rows of a copy
+      struct Ref {
+        int block, head, tok;
+      };
+      int t = t0;  // next tile of the walk
+      bool more = true;
+      auto take = [&]() {  // the walk's next tile: this lane's block id in it
+        Ref r;
+        r.block = -1;
+        r.head = w.h;
+        const int64_t pos = static_cast<int64_t>(t) * kTile + lane * rows;
+        r.tok = p.bs > kTile ? static_cast<int>(pos % p.bs) : 0;
+        const int last = min(w.n * p.G, (w.rt + 1) * R) - 1;
+        const int limit = w.len - w.n + last / p.G + 1;
+        if (lane < ppt && pos < limit) {
+          const int64_t e = pos / p.bs;
+          int b = -1;
+          if (e < p.max_blocks) b = p.table[w.seq * p.table_stride + e];
+          if (b < 0 || b >= p.num_blocks) {
+            b = -1;
+            if (p.err) atomicOr(p.err, KDA_DEVERR_SLOT_RANGE);
+          }
+          r.block = b;
+        }
+        if (--left > 0) {
+          if (++t == w.nt) {
+            t = 0;
+            next_unit<R>(p, w);
+          }
+        } else {
+          more = false;
+        }
+        return r;
+      };
+      auto scales = [&](const Ref& r) {
+        if (r.block < 0) return make_float2(0.f, 0.f);
+        const int64_t at = static_cast<int64_t>(r.block) * p.Hkv + r.head;
+        return make_float2(p.k_scale[at], p.v_scale[at]);
+      };
+      const int64_t count = left;
+      Ref a = take(), b = a;
+      if (more) b = take();
+      float2 sa = scales(a);
+      bool ok = true;
+      int64_t k_sent = 0, v_sent = 0;
+      for (int64_t it = 0; it < count; ++it) {
+        const float2 sb = it + 1 < count ? scales(b) : make_float2(0.f, 0.f);
+        Ref c = b;
+        if (more) c = take();
+        const int ks = static_cast<int>(it % C::kK), vs = static_cast<int>(it % C::kV);
+        const int cs = static_cast<int>(it % (C::kV + 1));
+        const uint32_t kr = static_cast<uint32_t>(it / C::kK), vr = static_cast<uint32_t>(it / C::kV);
+        if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
+        if (lane < ppt) {
+          const float sv = fmaxf(sa.y, 0x1p-64f);
+          S.sc[cs][lane] = a.block < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                       : make_float4(sa.x, log2f(sv), 1.f / sv, 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&S.sc_full[cs]), bar_expect(&S.k_full[ks], kTileBytes);
+        __syncwarp();
+        if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
+        ++k_sent;
+        if (vr > 0 && !(ok = bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed))) break;
+        if (lane == 0) bar_expect(&S.v_full[vs], kTileBytes);
+        __syncwarp();
+        if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
+        ++v_sent;
+        a = b, b = c, sa = sb;
+      }
+      if (!ok) {  // nothing may land in shared memory after the CTA is gone
+        for (int64_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
+          bar_drain(&S.k_full[j % C::kK], static_cast<uint32_t>(j / C::kK) & 1);
+        for (int64_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
+          bar_drain(&S.v_full[j % C::kV], static_cast<uint32_t>(j / C::kV) & 1);
+      }
+    } else if (warp == 4 * C::kGroups + 1) {
+      // ======================================================== product issuer
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc(R, false, false), id_o = idesc(R, true, true);
+        int64_t it = 0;
+        uint32_t unit = 0;
+        bool ok = true;
+        auto weigh = [&](int64_t j) {  // O^T of tile j
+          const int st = static_cast<int>(j % C::kV);
+          ok = ok && bar_wait(&S.p_full, static_cast<uint32_t>(j & 1), &S.failed) &&
+               bar_wait(&S.v_full[st], static_cast<uint32_t>(j / C::kV) & 1, &S.failed);
+          if (!ok) return;
+          tc_after();
+          const uint32_t v = s32(S.v[st]), d = tmem + (2 + static_cast<uint32_t>(j & 1)) * R;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma(d, sdesc(v + k * 32 * kD, 0, 1024, 2), sdesc(s32(S.p[part]) + k * 512, 128, 2048, 0), id_o,
+                  part + k > 0);
+          commit(&S.v_empty[st]);
+          commit(&S.o_full[j & 1]);
+        };
+        int t = t0;
+        for (; left > 0 && ok; ++unit) {
+          const int take = static_cast<int>(min(static_cast<int64_t>(w.nt - t), left));
+          for (int k0 = 0; k0 < take && ok; ++k0, ++it) {
+            if (k0 == 0) {
+              // the rows of a new unit are in place only after the old unit's last tile is weighed
+              if (it > 0) weigh(it - 1);
+              ok = ok && bar_wait(&S.q_full, unit & 1, &S.failed);
+            }
+            const int st = static_cast<int>(it % C::kK);
+            ok = ok && bar_wait(&S.k_full[st], static_cast<uint32_t>(it / C::kK) & 1, &S.failed);
+            if (!ok) break;
+            tc_after();
+            const uint32_t kk = s32(S.k[st]), d = tmem + static_cast<uint32_t>(it & 1) * R;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < kD / 32; ++k)
+                mma(d, sdesc(kk + k * 32, 0, 1024, 2), sdesc(s32(S.q[part]) + k * 32 * R, 16 * R, 128, 0), id_s,
+                    part + k > 0);
+            commit(&S.s_full[it & 1]);
+            commit(&S.k_empty[st]);
+            if (k0 > 0) weigh(it - 1);
+          }
+          left -= take;
+          t = 0;
+          if (left > 0) next_unit<R>(p, w);
+        }
+        if (ok && it > 0) weigh(it - 1);
+        commit(&S.done);
+      }
+      __syncwarp();
+    } else {
+      // ================================================================ softmax
+      const int g = warp >> 2, t = tid & 127;  // warpgroup; token of S^T, channel of O^T
+      const int col0 = g * kCols;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
+      Bcast<R>& bc = bcast[warp];
+      float o[kCols], l[kCols];
+      int64_t it = 0;
+      uint32_t unit = 0;
+      int64_t at = begin;  // global index of the unit's first tile here
+      for (; left > 0; ++unit) {
+        const int take = static_cast<int>(min(static_cast<int64_t>(w.nt - t0), left));
+        const int row0 = w.rt * R + col0;                       // first of the group's query rows
+        const int rows = min(max(w.n * p.G - row0, 0), kCols);  // rows that exist
+        const int ctx = w.len - w.n;
+        // ---- the unit's rows: scaled to e4m3's range by a power of two per row, split in two parts
+#pragma unroll 2
+        for (int r0 = 0; r0 < kCols; r0 += 8) {
+          const int c = r0 + (t >> 4), d = (t & 15) * 8, row = row0 + c;
+          float f[8];
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (c < rows)
+            v = *reinterpret_cast<const uint4*>(p.q + (w.q0 + row / p.G) * p.q_stride +
+                                                (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + d);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          float amax = 0.f;
+          bool finite = true;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            finite &= fabsf(f[i]) <= FLT_MAX;
+            amax = fmaxf(amax, fabsf(f[i]));
+          }
+#pragma unroll
+          for (int s = 1; s < 16; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+          const uint32_t who = __ballot_sync(0xffffffffu, finite);
+          finite = ((who >> (lane & 16)) & 0xffffu) == 0xffffu;
+          // 2^e with amax 2^-e in (224, 448]
+          const uint32_t bits = __float_as_uint(amax);
+          int e = static_cast<int>(bits >> 23) - 126 - 9 + ((bits & 0x7fffffu) > 0x600000u);
+          e = min(max(e, -100), 119);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = make_float2(f[2 * i] * inv, f[2 * i + 1] * inv);
+            const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+            const __nv_fp8x2_storage_t l8 =
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+            if (i & 1) hi[i >> 1] |= static_cast<uint32_t>(h8) << 16, lo[i >> 1] |= static_cast<uint32_t>(l8) << 16;
+            else hi[i >> 1] = h8, lo[i >> 1] = l8;
+          }
+          const uint32_t off = (d >> 4) * (16 * R) + (col0 + c) * 16 + (d & 8);
+          *reinterpret_cast<uint2*>(S.q[0] + off) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(S.q[1] + off) = make_uint2(lo[0], lo[1]);
+          if ((t & 15) == 0) {
+            S.row_scale[col0 + c] =
+                finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale : __uint_as_float(0x7fc00000u);
+            S.limit[col0 + c] = c < rows ? ctx + row / p.G + 1 : 0;
+          }
+        }
+        if (g == 0) S.nan_at[unit & (C::kNan - 1)][t] = 0x7fffffff;
+        fence_async();
+        bar_arrive(&S.q_full);
+        group_sync<128>(g);
+        const int first_limit = ctx + row0 / p.G + 1;  // the row that sees least
+        const int tile_rows = min(w.n * p.G, (w.rt + 1) * R);
+        const int least = ctx + (w.rt * R) / p.G + 1, most = ctx + (tile_rows - 1) / p.G + 1;  // of all groups
+        float run = -INFINITY;  // lane c: running maximum of row c
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = 0.f, l[c] = 0.f;
+
+        auto add_tile = [&](int64_t j) {  // the products of tile j join the sums
+          bar_wait(&S.o_full[j & 1], static_cast<uint32_t>(j >> 1) & 1, &S.failed);
+          tc_after();
+          float v[kCols];
+          tm_ld<kCols>(lanes + (2 + static_cast<uint32_t>(j & 1)) * R, v);
+          const float4* al = reinterpret_cast<const float4*>(bc.alpha[j & 1]);
+          const float4* be = reinterpret_cast<const float4*>(bc.beta[j & 1]);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 a4 = al[c / 4], b4 = be[c / 4];
+            o[c] = o[c] * a4.x + v[c] * b4.x;
+            o[c + 1] = o[c + 1] * a4.y + v[c + 1] * b4.y;
+            o[c + 2] = o[c + 2] * a4.z + v[c + 2] * b4.z;
+            o[c + 3] = o[c + 3] * a4.w + v[c + 3] * b4.w;
+          }
+        };
+
+        for (int k = 0; k < take; ++k, ++it) {
+          const int cs = static_cast<int>(it % (C::kV + 1)), vs = static_cast<int>(it % C::kV);
+          const int buf = static_cast<int>(it & 1);
+          const int tile0 = (t0 + k) * kTile, pos = tile0 + t;
+          bar_wait(&S.s_full[buf], static_cast<uint32_t>(it >> 1) & 1, &S.failed);
+          bar_wait(&S.sc_full[cs], static_cast<uint32_t>(it / (C::kV + 1)) & 1, &S.failed);
+          tc_after();
+          float z[kCols];
+          tm_ld<kCols>(lanes + static_cast<uint32_t>(buf) * R, z);
+          const float4 sc = S.sc[cs][p.bs >= kTile ? 0 : t / p.bs];
+          const float4* rs = reinterpret_cast<const float4*>(S.row_scale + col0);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 f = rs[c / 4];
+            z[c] = fmaf(z[c] * sc.x, f.x, sc.y);
+            z[c + 1] = fmaf(z[c + 1] * sc.x, f.y, sc.y);
+            z[c + 2] = fmaf(z[c + 2] * sc.x, f.z, sc.y);
+            z[c + 3] = fmaf(z[c + 3] * sc.x, f.w, sc.y);
+          }
+          const bool edge = tile0 + kTile > first_limit;
+          if (edge) {
+            const int4* li = reinterpret_cast<const int4*>(S.limit + col0);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 4) {
+              const int4 f = li[c / 4];
+              if (pos >= f.x) z[c] = -INFINITY;
+              if (pos >= f.y) z[c + 1] = -INFINITY;
+              if (pos >= f.z) z[c + 2] = -INFINITY;
+              if (pos >= f.w) z[c + 3] = -INFINITY;
+            }
+          }
+          // ---- the tile's maximum of every row: over the warp's tokens, then over the warps
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            const float m = warp_max(z[c]);
+            if (lane == c) top = m;
+          }
+          if (lane < kCols) S.wmax[buf][g][warp & 3][lane] = top;
+          group_sync<128>(g);
+          if (lane < kCols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, S.wmax[buf][g][i][lane]);
+            const float next = fmaxf(run, top);
+            const float ref = next == -INFINITY ? 0.f : next;
+            bc.alpha[buf][lane] = ex2(run - ref);
+            bc.beta[buf][lane] = ex2(top - ref);
+            bc.mt[lane] = (top == -INFINITY ? 0.f : top) - 8.f;  // weights up to 2^8
+            run = next;
+          }
+          __syncwarp();
+          // ---- weights, their sum, their two e4m3 parts
+          const float4* mt = reinterpret_cast<const float4*>(bc.mt);
+          const float4* al = reinterpret_cast<const float4*>(bc.alpha[buf]);
+          const float4* be = reinterpret_cast<const float4*>(bc.beta[buf]);
+          uint32_t hi[kCols / 4], lo[kCols / 4];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 m4 = mt[c / 4], a4 = al[c / 4], b4 = be[c / 4];
+            const float w0 = ex2(z[c] - m4.x), w1 = ex2(z[c + 1] - m4.y), w2 = ex2(z[c + 2] - m4.z),
+                        w3 = ex2(z[c + 3] - m4.w);
+            l[c] = l[c] * a4.x + (b4.x * sc.z) * w0;
+            l[c + 1] = l[c + 1] * a4.y + (b4.y * sc.z) * w1;
+            l[c + 2] = l[c + 2] * a4.z + (b4.z * sc.z) * w2;
+            l[c + 3] = l[c + 3] * a4.w + (b4.w * sc.z) * w3;
+            const __half2 x0 = __floats2half2_rn(w0, w1), x1 = __floats2half2_rn(w2, w3);
+            const __nv_fp8x2_storage_t h0 = __nv_cvt_halfraw2_to_fp8x2(x0, __NV_SATFINITE, __NV_E4M3),
+                                       h1 = __nv_cvt_halfraw2_to_fp8x2(x1, __NV_SATFINITE, __NV_E4M3);
+            const __half2 y0 = __hsub2(x0, __half2(__nv_cvt_fp8x2_to_halfraw2(h0, __NV_E4M3))),
+                          y1 = __hsub2(x1, __half2(__nv_cvt_fp8x2_to_halfraw2(h1, __NV_E4M3)));
+            hi[c / 4] = h0 | (static_cast<uint32_t>(h1) << 16);
+            lo[c / 4] = __nv_cvt_halfraw2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
+                        (static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3)) << 16);
+          }
+          if (it > 0) bar_wait(&S.o_full[(it - 1) & 1], static_cast<uint32_t>((it - 1) >> 1) & 1, &S.failed);
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            const int off = (col0 / 16 + c) * (16 * kTile) + t * 16;
+            *reinterpret_cast<uint4*>(S.p[0] + off) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+            *reinterpret_cast<uint4*>(S.p[1] + off) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+          }
+          // ---- values that some row does not see: a zero weight times NaN is
+          // NaN, so what no row sees is cleared, and a NaN that only some rows
+          // see is taken out here and put back into their results
+          if (g == 0 && tile0 + kTile > least) {
+            bar_wait(&S.v_full[vs], static_cast<uint32_t>(it / C::kV) & 1, &S.failed);
+            __syncwarp();
+            uint4* v = reinterpret_cast<uint4*>(S.v[vs] + t * kD);
+            uint32_t nan = 0;
+            if (pos >= most) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+            } else if (pos >= least) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) nan |= nan_bytes(v[i].x) | nan_bytes(v[i].y) | nan_bytes(v[i].z) | nan_bytes(v[i].w);
+            }
+            if (__any_sync(0xffffffffu, nan != 0)) take_out_nan(S.v[vs] + t * kD, nan != 0, t, pos, S.nan_at[unit & (C::kNan - 1)]);
+          }
+          __syncwarp();
+          fence_async();
+          tc_before();
+          bar_arrive(&S.p_full);
+          if (k > 0) add_tile(it - 1);
+        }
+        add_tile(it - 1);
+
+        // ---- the unit's end: sums over the tokens (threads) of every row
+        float lsum;
+        if constexpr (kCols == 32) {
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+            for (int c = 0; c < s; ++c) {
+              const float send = lane & s ? l[c] : l[c + s], keep = lane & s ? l[c + s] : l[c];
+              l[c] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+            }
+          lsum = l[0];
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
+#pragma unroll
+          for (int s = 8; s > 0; s >>= 1)
+#pragma unroll
+            for (int c = 0; c < s; ++c) {
+              const float send = lane & s ? l[c] : l[c + s], keep = lane & s ? l[c + s] : l[c];
+              l[c] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+            }
+          lsum = l[0];
+        }
+        if (lane < kCols) S.wsum[g][warp & 3][lane] = lsum;
+        group_sync<128>(g);
+        if (lane < kCols) {
+          lsum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lsum += S.wsum[g][i][lane];
+          if (S.row_scale[col0 + lane] != S.row_scale[col0 + lane]) lsum = S.row_scale[col0 + lane];
+        }
+        const int nan_at = S.nan_at[unit & (C::kNan - 1)][t];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (nan_at < S.limit[col0 + c]) o[c] = __uint_as_float(0x7fc00000u);
+        uint16_t* out = p.out + static_cast<int64_t>(w.h) * p.G * kD + t;
+        auto store = [&](int c, float v) {
+          const int row = row0 + c;
+          const __nv_bfloat16 b = __float2bfloat16_rn(v);
+          out[(w.q0 + row / p.G) * p.out_stride + static_cast<int64_t>(row % p.G) * kD] =
+              *reinterpret_cast<const uint16_t*>(&b);
+        };
+        if (take == w.nt) {
+          if (lane < kCols) bc.mt[lane] = lsum == 0.f ? 0.f : 1.f / lsum;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (c < rows) store(c, o[c] * bc.mt[c]);
+          __syncwarp();
+        } else if (rows > 0) {
+          // a part of the unit: a record for the CTA that arrives last
+          const int64_t us = at - t0;
+          const int c0 = static_cast<int>(((us + 1) * ctas - 1) / total);
+          const int c1 = static_cast<int>(((us + w.nt) * ctas - 1) / total);
+          auto record = [&](int c) {  // of CTA c: its tail for the unit's first part, else its head
+            return p.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * C::kGroups + g) * C::kPartial;
+          };
+          float* rec = record(static_cast<int>(cta));
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (c < rows) rec[2 * kCols + c * kD + t] = o[c];
+          if ((warp & 3) == 0 && lane < kCols) rec[lane] = run, rec[kCols + lane] = lsum;
+          __threadfence();
+          group_sync<128>(g);
+          if (t == 0) {
+            int32_t* n = p.counters + c0 * C::kGroups + g;
+            const int arrived = atomicAdd(n, 1);
+            S.last[g] = arrived == c1 - c0;
+            if (arrived == c1 - c0) *n = 0;
+            __threadfence();
+          }
+          group_sync<128>(g);
+          if (S.last[g]) {
+            __threadfence();
+            float m = -INFINITY, sum = 0.f;
+            if (lane < kCols) {
+              for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(record(c) + lane));
+              const float ref = m == -INFINITY ? 0.f : m;
+              for (int c = c0; c <= c1; ++c) sum += ex2(__ldcg(record(c) + lane) - ref) * __ldcg(record(c) + kCols + lane);
+              bc.mt[lane] = ref;
+              bc.alpha[0][lane] = sum == 0.f ? 0.f : 1.f / sum;
+            }
+            __syncwarp();
+            for (int c = 0; c < rows; ++c) {
+              float v = 0.f;
+              for (int i = c0; i <= c1; ++i) {
+                const float* r = record(i);
+                v += ex2(__ldcg(r + c) - bc.mt[c]) * __ldcg(r + 2 * kCols + c * kD + t);
+              }
+              store(c, v * bc.alpha[0][c]);
+            }
+            __syncwarp();
+          }
+        }
+        group_sync<128>(g);  // row_scale and limit are read: the next unit may write them
+        left -= take;
+        at += take;
+        t0 = 0;
+        if (left > 0) next_unit<R>(p, w);
+      }
+    }
+    // every product has ended before the accumulators are given back
+    if (warp == 0) bar_wait(&S.done, 0, &S.failed);
+  }
+  tc_before();
+  __syncthreads();
+  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+  __syncwarp();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::mutex g_mutex;
+int g_sms[64];
+EncodeFn g_encode;
+
+template <int R>
+constexpr size_t smem_bytes() {
+  constexpr size_t n = sizeof(Smem<R>) + 4 * Cfg<R>::kGroups * sizeof(Bcast<R>);
+  // an SM has 228 KB, of which each CTA's system part takes 1 KB
+  static_assert((n + 1024) * Cfg<R>::kCtasPerSm <= 228 * 1024 && n <= 227 * 1024, "shared memory");
+  return n;
+}
+
+cudaError_t setup(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!g_sms[dev]) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeFn>(fn);
+    const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if ((e = cudaFuncSetAttribute(cache_attention_kernel<16>, attr, smem_bytes<16>())) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(cache_attention_kernel<32>, attr, smem_bytes<32>())) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(cache_attention_kernel<64>, attr, smem_bytes<64>())) != cudaSuccess)
+      return e;
+    int n = 0;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    g_sms[dev] = n < kMaxCtas / 2 ? n : kMaxCtas / 2;
+  }
+  *sms = g_sms[dev];
+  return cudaSuccess;
+}
+
+bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
+
+// Rows of a tile: all the queries of a kv head in a single-token or
+// multi-token step, so that the cache is read once; 64 for more.
+int row_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <int R>
+constexpr int64_t partial_bytes() {
+  return 2LL * (kMaxCtas / 2) * Cfg<R>::kCtasPerSm * Cfg<R>::kGroups * Cfg<R>::kPartial * 4;
+}
+
+template <int R>
+cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, int sms, void* stream) {
+  return kda_internal_launch(cache_attention_kernel<R>, dim3(static_cast<unsigned>(sms * Cfg<R>::kCtasPerSm)),
+                             dim3(Cfg<R>::kThreads), smem_bytes<R>(), stream, p, k, v);
+}
+
+}  // namespace
+
+extern "C" int64_t kda_cache_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t max_new) {
+  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads || max_new < 1) return -1;
+  const int r = row_tile(static_cast<int64_t>(max_new) * (num_q_heads / num_kv_heads));
+  return KDA_CACHE_ATTENTION_COUNTER_BYTES +
+         (r == 16 ? partial_bytes<16>() : r == 32 ? partial_bytes<32>() : partial_bytes<64>());
+}
+
+extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream) {
+  kda_internal_clear_error();
+  if (!a) return kda_internal_fail(KDA_ERR_NULLPTR, "args is NULL");
+  if (a->struct_size != sizeof(KdaCacheAttentionArgs))
+    return kda_internal_fail(KDA_ERR_ABI, "struct_size %u, library expects %zu", a->struct_size,
+                             sizeof(KdaCacheAttentionArgs));
+  if (a->head_dim != kD) return kda_internal_fail(KDA_ERR_SHAPE, "head_dim %d (need 128)", a->head_dim);
+  const int Hq = a->num_q_heads, Hkv = a->num_kv_heads, bs = a->block_size;
+  if (a->B < 0 || a->T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65536 || a->num_blocks < 1 || a->max_blocks < 1 ||
+      a->max_new < 1)
+    return kda_internal_fail(KDA_ERR_SHAPE, "B=%d T=%d num_q_heads=%d num_kv_heads=%d num_blocks=%d max_blocks=%d max_new=%d",
+                             a->B, a->T, Hq, Hkv, a->num_blocks, a->max_blocks, a->max_new);
+  if (static_cast<int64_t>(a->T) * (Hq / Hkv) > 0x7fffff00LL)
+    return kda_internal_fail(KDA_ERR_SHAPE, "T=%d is too large", a->T);
+  if (bs != 16 && bs != 32 && bs != 64 && bs != 128 && bs != 256)
+    return kda_internal_fail(KDA_ERR_SHAPE, "block_size %d (need 16, 32, 64, 128 or 256)", bs);
+  if (a->B == 0 || a->T == 0) return KDA_OK;
+  if (!a->q || !a->out || !a->cu_seqlens || !a->seq_lens || !a->block_table || !a->k_cache || !a->v_cache ||
+      !a->k_scale || !a->v_scale || !a->workspace)
+    return kda_internal_fail(KDA_ERR_NULLPTR, "a required pointer is NULL");
+  const int64_t width = static_cast<int64_t>(Hq) * kD;
+  if (a->q_row_stride < width || a->out_row_stride < width || a->block_table_stride < a->max_blocks ||
+      a->token_stride < kD || a->head_stride < kD || a->block_stride < kD)
+    return kda_internal_fail(KDA_ERR_SHAPE, "a stride is smaller than the row");
+  const int64_t need = kda_cache_attention_workspace_bytes(Hq, Hkv, a->max_new);
+  if (a->workspace_bytes < need)
+    return kda_internal_fail(KDA_ERR_SHAPE, "workspace of %lld bytes, %lld needed",
+                             static_cast<long long>(a->workspace_bytes), static_cast<long long>(need));
+  if (misaligned(a->q, 15) || (a->q_row_stride & 7) || misaligned(a->out, 15) || (a->out_row_stride & 7) ||
+      misaligned(a->cu_seqlens, 3) || misaligned(a->seq_lens, 3) || misaligned(a->block_table, 3) ||
+      misaligned(a->k_cache, 15) || misaligned(a->v_cache, 15) || misaligned(a->k_scale, 3) ||
+      misaligned(a->v_scale, 3) || misaligned(a->workspace, 15) || misaligned(a->err_flag, 3) ||
+      ((a->block_stride | a->head_stride | a->token_stride) & 15))
+    return kda_internal_fail(KDA_ERR_ALIGN, "a pointer or stride is not aligned as required");
+  int sms = 0;
+  cudaError_t e = setup(&sms);
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "setup: %s", cudaGetErrorString(e));
+  // one copy: up to 128 rows of one block and head
+  const cuuint64_t dims[4] = {kD, static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(a->num_blocks)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a->token_stride), static_cast<cuuint64_t>(a->head_stride),
+                                 static_cast<cuuint64_t>(a->block_stride)};
+  const cuuint32_t box[4] = {kD, static_cast<cuuint32_t>(bs < kTile ? bs : kTile), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  CUtensorMap maps[2];
+  const uint8_t* base[2] = {a->k_cache, a->v_cache};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = g_encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base[i]), dims, strides,
+                                box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
+  }
+  Params p{};
+  p.B = a->B, p.T = a->T, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.bs = bs;
+  p.num_blocks = a->num_blocks, p.max_blocks = a->max_blocks;
+  p.scale = (a->sm_scale == 0.f ? 0.08838834764831845f : a->sm_scale) * kLog2e;
+  p.q = a->q, p.q_stride = a->q_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
+  p.cu = a->cu_seqlens, p.lens = a->seq_lens, p.table = a->block_table, p.table_stride = a->block_table_stride;
+  p.k_scale = a->k_scale, p.v_scale = a->v_scale, p.err = a->err_flag;
+  p.counters = static_cast<int32_t*>(a->workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + KDA_CACHE_ATTENTION_COUNTER_BYTES);
+  const int r = row_tile(static_cast<int64_t>(a->max_new) * p.G);
+  e = r == 16   ? launch<16>(p, maps[0], maps[1], sms, stream)
+      : r == 32 ? launch<32>(p, maps[0], maps[1], sms, stream)
+                : launch<64>(p, maps[0], maps[1], sms, stream);
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+  return KDA_OK;
+}

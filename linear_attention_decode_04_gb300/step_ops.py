@@ -4,6 +4,8 @@
   maps of a paged cache from the requests' lengths;
 - ``kda_qk_rope`` (``include/kda_qk_rope.h``): per-head norm and rotation of q
   and k, and the write of k and v into the 8-bit cache;
+- ``kda_cache_attention`` (``include/kda_cache_attention.h``): causal softmax
+  attention over that cache, single tokens, multi-token steps and prompt chunks;
 - ``kda_verify_draft`` (``include/kda_verify.h``): verification of the tokens
   that a multi-token decode step ran ahead with.
 
@@ -46,6 +48,17 @@ class KdaQkRopeArgs(ctypes.Structure):
                 ("k_weight", _ptr), ("k_cache", _ptr), ("v_cache", _ptr), ("block_stride", _i64),
                 ("head_stride", _i64), ("token_stride", _i64), ("k_scale", _ptr), ("v_scale", _ptr),
                 ("slot_map", _ptr), ("err_flag", _ptr)]
+
+
+class KdaCacheAttentionArgs(ctypes.Structure):
+    """Mirror of ``KdaCacheAttentionArgs``."""
+    _fields_ = [("struct_size", _u32), ("B", _i32), ("T", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
+                ("head_dim", _i32), ("block_size", _i32), ("num_blocks", _i32), ("max_blocks", _i32),
+                ("max_new", _i32), ("sm_scale", _f32), ("q", _ptr), ("q_row_stride", _i64), ("out", _ptr),
+                ("out_row_stride", _i64), ("cu_seqlens", _ptr), ("seq_lens", _ptr), ("block_table", _ptr),
+                ("block_table_stride", _i64), ("k_cache", _ptr), ("v_cache", _ptr), ("block_stride", _i64),
+                ("head_stride", _i64), ("token_stride", _i64), ("k_scale", _ptr), ("v_scale", _ptr),
+                ("workspace", _ptr), ("workspace_bytes", _i64), ("err_flag", _ptr)]
 
 
 class KdaVerifyArgs(ctypes.Structure):
@@ -284,6 +297,106 @@ def kda_qk_rope(qkv, positions, q_out, *, num_q_heads: int, num_kv_heads: int, r
                   interleaved=interleaved, q_weight=q_weight, k_weight=k_weight, eps=eps, k_out=k_out,
                   k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_map=slot_map,
                   err_flag=err_flag)(stream)
+
+
+# ------------------------------------------------------------------------ attention
+def cache_attention_workspace(num_q_heads: int, num_kv_heads: int, max_new: int, device=None) -> torch.Tensor:
+    """A zeroed workspace for ``kda_cache_attention`` calls with these head
+    counts and at most ``max_new`` queries per sequence.  Calls ordered on one
+    stream (a model's layers, captured or not) may share it; calls that may
+    overlap need one each."""
+    fn = load_library().kda_cache_attention_workspace_bytes
+    fn.argtypes, fn.restype = [ctypes.c_int32] * 3, ctypes.c_int64
+    n = fn(int(num_q_heads), int(num_kv_heads), int(max_new))
+    if n < 0:
+        raise ValueError(f"num_q_heads={num_q_heads} must be a positive multiple of num_kv_heads={num_kv_heads} and "
+                         f"max_new={max_new} positive")
+    return torch.zeros(n // 4, dtype=torch.int32, device="cuda" if device is None else device)
+
+
+class KdaCacheAttentionCall(_Call):
+    """A prepared ``kda_cache_attention`` call.
+
+      q, out       bf16 [T, >= Hq * 128] (rows may be strided)
+      cu_seqlens   int32 [B + 1], seq_lens int32 [B] (cached tokens, the
+                   queries' own included), block_table int32 [B, max_blocks]
+      k_cache, v_cache  float8_e4m3fn [num_blocks, Hkv, block_size, 128] (outer
+                   dimensions in any order by strides), k_scale and v_scale
+                   fp32 [num_blocks, Hkv]
+      num_q_heads  Hq, a multiple of Hkv; by default q's width / 128
+      max_new      the most queries a sequence has in this call (host value,
+                   chooses the row tile; results do not depend on it)
+      workspace    from ``cache_attention_workspace``; by default the call
+                   makes its own, and the constructor then waits for the
+                   current stream once"""
+
+    def __init__(self, q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, out, *,
+                 max_new: int = 1, num_q_heads: int | None = None, sm_scale: float = 0.0, workspace=None,
+                 err_flag=None, _sync: bool = True):
+        dev = q.device
+        _check(q, "q", torch.bfloat16, None)
+        if q.dim() != 2:
+            raise ValueError(f"q must be [T, >= Hq * {HEAD_DIM}] (got {tuple(q.shape)})")
+        T = q.shape[0]
+        if num_q_heads is None:
+            if q.shape[1] % HEAD_DIM:
+                raise ValueError(f"q's width {q.shape[1]} is not a multiple of {HEAD_DIM}")
+            num_q_heads = q.shape[1] // HEAD_DIM
+        Hq = int(num_q_heads)
+        if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+            raise ValueError(f"k_cache must be [num_blocks, Hkv, block_size, {HEAD_DIM}]")
+        Hkv = k_cache.shape[1]
+        if Hkv < 1 or Hq < 1 or Hq % Hkv:
+            raise ValueError(f"num_q_heads={Hq} must be a positive multiple of num_kv_heads={Hkv}")
+        q_stride = _rows(q, "q", T, Hq * HEAD_DIM)
+        _check(out, "out", torch.bfloat16, dev)
+        out_stride = _rows(out, "out", T, Hq * HEAD_DIM)
+        _check(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [B + 1]")
+        _dense(cu_seqlens, "cu_seqlens")
+        B = cu_seqlens.numel() - 1
+        _shaped(seq_lens, "seq_lens", torch.int32, dev, (B,))
+        _check(block_table, "block_table", torch.int32, dev)
+        if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1 or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError(f"block_table must be [{B}, max_blocks] with a unit inner stride (got {tuple(block_table.shape)})")
+        M = block_table.shape[1]
+        table_stride = block_table.stride(0) if B > 1 else max(block_table.stride(0), M)
+        bs, nb, strides = _caches(k_cache, v_cache, k_scale, v_scale, dev, Hkv)
+        _err(err_flag, dev)
+        own = ()
+        if workspace is None:
+            workspace = cache_attention_workspace(Hq, Hkv, max_new, dev)
+            own = (workspace,)
+            # zeroed on the current stream, but the call may run on another
+            if _sync and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(dev).synchronize()
+        else:
+            _check(workspace, "workspace", torch.int32, dev)
+            _dense(workspace, "workspace")
+        self.workspace = workspace
+        args = KdaCacheAttentionArgs(
+            B=B, T=T, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=HEAD_DIM, block_size=bs, num_blocks=nb, max_blocks=M,
+            max_new=int(max_new), sm_scale=float(sm_scale), q=_p(q), q_row_stride=q_stride, out=_p(out),
+            out_row_stride=out_stride, cu_seqlens=_p(cu_seqlens), seq_lens=_p(seq_lens), block_table=_p(block_table),
+            block_table_stride=table_stride, k_cache=_p(k_cache), v_cache=_p(v_cache), block_stride=strides[0],
+            head_stride=strides[1], token_stride=strides[2], k_scale=_p(k_scale), v_scale=_p(v_scale),
+            workspace=_p(workspace), workspace_bytes=workspace.numel() * 4, err_flag=_p(err_flag))
+        self._prepare("kda_cache_attention", args, dev,
+                      (q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, out, workspace,
+                       err_flag), own)
+
+
+def kda_cache_attention(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, out, *,
+                        max_new: int = 1, num_q_heads: int | None = None, sm_scale: float = 0.0, workspace=None,
+                        err_flag=None, stream: torch.cuda.Stream | None = None) -> None:
+    """Causal attention of the batch's queries over the 8-bit paged cache, to
+    ``out`` (see ``KdaCacheAttentionCall``)."""
+    with torch.cuda.stream(stream):
+        KdaCacheAttentionCall(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, out,
+                              max_new=max_new, num_q_heads=num_q_heads, sm_scale=sm_scale, workspace=workspace,
+                              err_flag=err_flag, _sync=False)(stream)
 
 
 # --------------------------------------------------------------------- verification

@@ -37,7 +37,8 @@ def header_fields(header, name):
 
 
 @pytest.mark.parametrize("header, struct", [("kda_block_tables.h", S.KdaBlockTablesArgs),
-                                            ("kda_qk_rope.h", S.KdaQkRopeArgs), ("kda_verify.h", S.KdaVerifyArgs)])
+                                            ("kda_qk_rope.h", S.KdaQkRopeArgs), ("kda_verify.h", S.KdaVerifyArgs),
+                                            ("kda_cache_attention.h", S.KdaCacheAttentionArgs)])
 def test_struct_mirrors(header, struct):
     assert header_fields(header, struct.__name__) == [f for f, _ in struct._fields_]
 
@@ -92,6 +93,30 @@ def test_qk_rope_codes(lib):
     for kw in (dict(qkv=0x10008), dict(q_out=0x10008), dict(qkv_row_stride=1028), dict(token_stride=136),
                dict(slot_map=0x10004), dict(q_weight=0x10004), dict(k_cache=0x10008), dict(positions=0x10002)):
         assert call(**kw) == ALIGN, kw
+
+
+def test_cache_attention_codes(lib):
+    names = ("q", "out", "cu_seqlens", "seq_lens", "block_table", "k_cache", "v_cache", "k_scale", "v_scale", "workspace")
+    size = lib.kda_cache_attention_workspace_bytes
+    size.argtypes, size.restype = [ctypes.c_int32] * 3, ctypes.c_int64
+    call = caller(lib, "kda_cache_attention", S.KdaCacheAttentionArgs,
+                  dict(B=3, T=7, num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=32, num_blocks=9, max_blocks=4,
+                       max_new=3, q_row_stride=1024, out_row_stride=1024, block_table_stride=4, block_stride=8192,
+                       head_stride=4096, token_stride=128, workspace_bytes=size(8, 2, 3),
+                       **{n: 0x10000 * (i + 1) for i, n in enumerate(names)}))
+    for kw in (dict(head_dim=64), dict(B=-1), dict(T=-1), dict(num_q_heads=7), dict(num_kv_heads=0), dict(block_size=8),
+               dict(block_size=48), dict(num_blocks=0), dict(max_blocks=0), dict(max_new=0), dict(q_row_stride=1016),
+               dict(out_row_stride=512), dict(block_table_stride=3), dict(token_stride=64), dict(head_stride=0),
+               dict(workspace_bytes=size(8, 2, 3) - 1), dict(T=2 ** 30)):
+        assert call(**kw) == SHAPE, kw
+    assert call(B=0) == OK and call(T=0) == OK
+    for n in names:
+        assert call(**{n: None}) == NULLPTR, n
+    for kw in (dict(q=0x10008), dict(out=0x10008), dict(q_row_stride=1028), dict(k_cache=0x10008), dict(v_cache=0x10004),
+               dict(token_stride=136), dict(workspace=0x10008), dict(k_scale=0x10002), dict(cu_seqlens=0x10002)):
+        assert call(**kw) == ALIGN, kw
+    assert size(8, 2, 3) > 4096 and size(96, 8, 8) > size(8, 2, 3)
+    assert size(8, 3, 1) == size(0, 1, 1) == size(8, 2, 0) == -1
 
 
 def test_verify_codes(lib):
