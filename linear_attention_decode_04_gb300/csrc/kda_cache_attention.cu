@@ -72,26 +72,29 @@ struct Params {
   int32_t* err;
 };
 
-template <int R>
+// A variant: `GROUPS` softmax warpgroups of `COLS` query rows each.
+template <int COLS, int GROUPS>
 struct Cfg {
-  static constexpr int kGroups = R > 32 ? 2 : 1;        // softmax warpgroups
-  static constexpr int kCols = R / kGroups;             // rows of a warpgroup (columns of S^T)
-  static constexpr int kThreads = 128 * kGroups + 64;
-  static constexpr int kCtasPerSm = R > 32 ? 1 : 2;
+  static constexpr int kCols = COLS, kGroups = GROUPS;
+  static constexpr int kRows = COLS * GROUPS;            // query rows of a tile
+  static constexpr int kN = (kRows + 15) / 16 * 16;      // width of the products
+  static constexpr int kThreads = 128 * GROUPS + 64;
+  static constexpr int kCtasPerSm = GROUPS > 1 ? 1 : 2;
   // Ring depths in tiles.  A K tile is free after its S product, about a tile's
   // time before its V tile is; at 32 rows two CTAs fit an SM with K two deep.
-  static constexpr int kK = R > 32 ? 4 : R > 16 ? 2 : 3;
-  static constexpr int kV = R > 32 ? 5 : 3;
-  static constexpr int kNan = kGroups > 1 ? 4 : 1;
-  static constexpr int kTmemCols = 4 * R;               // S and O, two buffers each
-  static constexpr int kPartial = kCols * (kD + 2);     // floats of a partial record
+  static constexpr int kK = GROUPS > 2 ? 3 : GROUPS > 1 ? 4 : kN > 16 ? 2 : 3;
+  static constexpr int kV = GROUPS > 2 ? 4 : GROUPS > 1 ? 5 : 3;
+  static constexpr int kNan = GROUPS > 1 ? 4 : 1;
+  static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
+  static constexpr int kPartial = COLS * (kD + 2);       // floats of a partial record
+  static constexpr int kBlocks = COLS / 8;               // 8-column blocks of a group's tensor-memory loads
+  static constexpr int kMine = COLS / 4;                 // rows that a thread holds elements of
 };
 
-template <int R>
+template <class C>
 struct alignas(1024) Smem {
-  using C = Cfg<R>;
-  uint8_t p[2][R * kTile];                // leading part, remainder; [row / 16][token][row % 16]
-  uint8_t q[2][R * kD];                   // likewise; core matrices of 8 rows x 16 bytes
+  uint8_t p[2][C::kN * kTile];            // leading part, remainder; [row' / 16][token][row' % 16]
+  uint8_t q[2][C::kN * kD];               // likewise; core matrices of 8 rows x 16 bytes
   uint8_t k[C::kK][kTileBytes], v[C::kV][kTileBytes];
   uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], sc_full[C::kV + 1];
   uint64_t s_full[2], o_full[2], p_full, q_full, done;
@@ -99,8 +102,8 @@ struct alignas(1024) Smem {
   // V ring: written before the tile's V place is waited for, when the tile
   // kV + 1 before it has been weighed.
   float4 sc[C::kV + 1][kMaxPages];
-  float row_scale[R];
-  int limit[R];
+  float row_scale[C::kRows];
+  int limit[C::kRows];
   float wmax[2][C::kGroups][4][C::kCols];
   float wsum[C::kGroups][4][C::kCols];
   int nan_at[C::kNan][kD];                // per unit and channel: first position that holds a NaN value
@@ -112,10 +115,10 @@ struct alignas(1024) Smem {
 };
 // Per warp, broadcast to its lanes: the tile's maxima, and the two factors per
 // row of the tile and of the one before.
-template <int R>
-struct Bcast {
-  float mt[Cfg<R>::kCols];
-  float alpha[2][Cfg<R>::kCols], beta[2][Cfg<R>::kCols];
+template <class C>
+struct alignas(16) Bcast {
+  float mt[C::kCols];
+  float alpha[2][C::kCols], beta[2][C::kCols];
 };
 
 __device__ __forceinline__ uint32_t s32(const void* ptr) {
@@ -193,44 +196,111 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
       ::"r"(dst), "l"(map), "r"(0), "r"(tok), "r"(head), "r"(block), "r"(s32(b))
       : "memory");
 }
-// N consecutive columns of this warp's 32 lanes.  The load writes the
-// registers of all 32 threads, so the warp has to be together: a thread still
-// on a branch of its own would find its registers overwritten.
-template <int N>
-__device__ __forceinline__ void tm_ld(uint32_t addr, float (&r)[N]);
-template <>
-__device__ __forceinline__ void tm_ld<16>(uint32_t addr, float (&r)[16]) {
+// BLOCKS * 8 consecutive columns of this warp's 32 lanes, as fragments: thread
+// i gets of block b, in r[j][2b], r[j][2b + 1], lane i / 4 + 8 j, columns
+// 8 b + 2 (i % 4) and the next.  The load writes the registers of all 32
+// threads, so the warp has to be together: a thread still on a branch of its
+// own would find its registers overwritten.  Load and wait are one statement,
+// so that nothing can come between them.
+template <int BLOCKS>
+__device__ __forceinline__ void tm_ld(uint32_t addr, float (&r)[4][2 * BLOCKS]) {
   __syncwarp();
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-      : "r"(addr)
-      : "memory");
+  const uint32_t up = addr + (16u << 16);  // the upper 16 lanes
+  if constexpr (BLOCKS == 1) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%9];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]),
+          "=f"(r[3][1])
+        : "r"(addr), "r"(up)
+        : "memory");
+  } else if constexpr (BLOCKS == 2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
+          "=f"(r[1][3]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]), "=f"(r[2][3]),
+          "=f"(r[3][2]), "=f"(r[3][3])
+        : "r"(addr), "r"(up)
+        : "memory");
+  } else if constexpr (BLOCKS == 3) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%8,%9,%10,%11}, [%25];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%12,%13,%14,%15,%16,%17,%18,%19}, [%26];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%20,%21,%22,%23}, [%27];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
+          "=f"(r[1][3]), "=f"(r[0][4]), "=f"(r[0][5]), "=f"(r[1][4]), "=f"(r[1][5]), "=f"(r[2][0]), "=f"(r[2][1]),
+          "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]), "=f"(r[2][3]), "=f"(r[3][2]), "=f"(r[3][3]), "=f"(r[2][4]),
+          "=f"(r[2][5]), "=f"(r[3][4]), "=f"(r[3][5])
+        : "r"(addr), "r"(addr + 16), "r"(up), "r"(up + 16)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+        "[%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
+          "=f"(r[1][3]), "=f"(r[0][4]), "=f"(r[0][5]), "=f"(r[1][4]), "=f"(r[1][5]), "=f"(r[0][6]), "=f"(r[0][7]),
+          "=f"(r[1][6]), "=f"(r[1][7]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]),
+          "=f"(r[2][3]), "=f"(r[3][2]), "=f"(r[3][3]), "=f"(r[2][4]), "=f"(r[2][5]), "=f"(r[3][4]), "=f"(r[3][5]),
+          "=f"(r[2][6]), "=f"(r[2][7]), "=f"(r[3][6]), "=f"(r[3][7])
+        : "r"(addr), "r"(up)
+        : "memory");
+  }
 }
-template <>
-__device__ __forceinline__ void tm_ld<32>(uint32_t addr, float (&r)[32]) {
-  __syncwarp();
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(addr)
-      : "memory");
+// A thread's column pairs reduced over the 8 threads that hold the same columns
+// (lane bits 2 to 4), each of them ending with one column: afterwards lane i
+// holds local column own_column(i).
+struct Max {
+  __device__ __forceinline__ static float of(float a, float b) { return fmaxf(a, b); }
+};
+struct Sum {
+  __device__ __forceinline__ static float of(float a, float b) { return a + b; }
+};
+template <class Op, int N>
+__device__ __forceinline__ float reduce_columns(const float (&in)[N], int lane) {
+  constexpr int P = N > 4 ? 8 : N;  // 2, 4 or 8 (6 is padded)
+  float v[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = i < N ? in[i < N ? i : 0] : 0.f;
+#pragma unroll
+  for (int o = 16, h = P / 2; o >= 4; o >>= 1, h >>= 1) {
+    if (h >= 1) {
+#pragma unroll
+      for (int i = 0; i < (h > 0 ? h : 1); ++i) {
+        const float send = lane & o ? v[i] : v[i + h], keep = lane & o ? v[i + h] : v[i];
+        v[i] = Op::of(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      }
+    } else {
+      v[0] = Op::of(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+  return v[0];
+}
+template <int N>
+__device__ __forceinline__ int own_column(int lane) {  // the group's column, >= the width for padding
+  constexpr int P = N > 4 ? 8 : N;
+  const int i = P == 8 ? (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)
+              : P == 4 ? (lane >> 4) * 2 + ((lane >> 3) & 1) : lane >> 4;
+  return 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+}
+// The weights' columns are kept in an order of their own within 16 so that a
+// thread's two pairs are four neighbouring bytes; the accumulator's column
+// 8 b + 2 (lane % 4) then belongs to this row (and the next to the next).
+template <int BLOCKS>
+__device__ __forceinline__ int row_of_column(int b, int lane) {
+  const int a = lane & 3;
+  if (BLOCKS & 1 && b == BLOCKS - 1) return 8 * b + 2 * a;  // an 8-column end keeps its order
+  return (b >> 1) * 16 + 8 * (a & 1) + 4 * (b & 1) + 2 * (a >> 1);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 // 0xff in the bytes that are NaN codes (0x7f, 0xff)
@@ -264,14 +334,14 @@ struct Walk {
   int n, len, q0;        // the sequence's queries, length, first query row
   int rts, nt;           // its row tiles; tiles of the current unit
 };
-template <int R>
+template <class C>
 __device__ __forceinline__ int tiles_of(const Params& p, int n, int len, int rt) {
   const int rows = n * p.G;
-  const int last = min(rows, (rt + 1) * R) - 1;  // last query row of the tile
+  const int last = min(rows, (rt + 1) * C::kRows) - 1;  // last query row of the tile
   const int limit = len - n + last / p.G + 1;    // tokens it sees
   return limit <= kTile ? 1 : (limit + kTile - 1) / kTile;
 }
-template <int R>
+template <class C>
 __device__ __forceinline__ bool load_seq(const Params& p, Walk& w) {  // false: nothing to do in this sequence
   if (w.seq < 0 || w.seq >= p.B) {  // cannot be; an empty end of the walk rather than a stray read
     w.q0 = w.n = w.len = w.rt = w.h = 0;
@@ -286,39 +356,38 @@ __device__ __forceinline__ bool load_seq(const Params& p, Walk& w) {  // false: 
   if (w.len > 0x7fffff00) w.len = 0x7fffff00;
   if (w.len < 0) w.len = 0;
   w.rt = w.h = 0;
-  w.rts = static_cast<int>((static_cast<int64_t>(w.n) * p.G + R - 1) / R);
+  w.rts = static_cast<int>((static_cast<int64_t>(w.n) * p.G + C::kRows - 1) / C::kRows);
   return w.n > 0;
 }
-template <int R>
+template <class C>
 __device__ __forceinline__ void next_unit(const Params& p, Walk& w) {  // only called while units are left
   if (++w.h < p.Hkv) return;
   w.h = 0;
   if (++w.rt >= w.rts) {
     do ++w.seq;
-    while (!load_seq<R>(p, w));
+    while (!load_seq<C>(p, w));
   }
-  w.nt = tiles_of<R>(p, w.n, w.len, w.rt);
+  w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
 }
-template <int R>
+template <class C>
 __device__ __forceinline__ int64_t seq_tiles(const Params& p, int i) {
   Walk w;
   w.seq = i;
-  if (!load_seq<R>(p, w)) return 0;
+  if (!load_seq<C>(p, w)) return 0;
   int64_t s = 0;
-  for (int rt = 0; rt < w.rts; ++rt) s += tiles_of<R>(p, w.n, w.len, rt);
+  for (int rt = 0; rt < w.rts; ++rt) s += tiles_of<C>(p, w.n, w.len, rt);
   return s * p.Hkv;
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int R>
-__global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     cache_attention_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
                            const __grid_constant__ CUtensorMap v_map) {
-  using C = Cfg<R>;
-  constexpr int kCols = C::kCols;
+  constexpr int kCols = C::kCols, kN = C::kN, kBlocks = C::kBlocks, kMine = C::kMine;
   extern __shared__ __align__(1024) uint8_t raw[];
-  Smem<R>& S = *reinterpret_cast<Smem<R>*>(raw);
-  Bcast<R>* bcast = reinterpret_cast<Bcast<R>*>(raw + sizeof(Smem<R>));
+  Smem<C>& S = *reinterpret_cast<Smem<C>*>(raw);
+  Bcast<C>* bcast = reinterpret_cast<Bcast<C>*>(raw + sizeof(Smem<C>));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) bar_init(&S.k_full[i], 1), bar_init(&S.k_empty[i], 1);
@@ -342,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
   int64_t mine = 0;
   bool bad = false;
   for (int i = tid; i < p.B; i += C::kThreads) {
-    mine += seq_tiles<R>(p, i);
+    mine += seq_tiles<C>(p, i);
     const int a = p.cu[i], b = p.cu[i + 1];
     bad |= a < 0 || b < a || b > p.T;
   }
@@ -368,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
     for (int base = 0; base < p.B; base += C::kThreads) {
       __syncthreads();
       const int i = base + tid;
-      const int64_t t = i < p.B ? seq_tiles<R>(p, i) : 0;
+      const int64_t t = i < p.B ? seq_tiles<C>(p, i) : 0;
       int64_t incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -387,12 +456,12 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
       if (t > 0 && begin >= from && begin < from + t) {
         Walk w;
         w.seq = i;
-        load_seq<R>(p, w);
+        load_seq<C>(p, w);
         int64_t off = begin - from;
-        int nt = tiles_of<R>(p, w.n, w.len, 0);
+        int nt = tiles_of<C>(p, w.n, w.len, 0);
         while (off >= static_cast<int64_t>(nt) * p.Hkv) {
           off -= static_cast<int64_t>(nt) * p.Hkv;
-          nt = tiles_of<R>(p, w.n, w.len, ++w.rt);
+          nt = tiles_of<C>(p, w.n, w.len, ++w.rt);
         }
         S.walk[0] = i;
         S.walk[1] = w.rt;
@@ -405,10 +474,10 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
     __syncthreads();
     Walk w;
     w.seq = static_cast<int>(S.walk[0]);
-    load_seq<R>(p, w);
+    load_seq<C>(p, w);
     w.rt = static_cast<int>(S.walk[1]);
     w.h = static_cast<int>(S.walk[2]);
-    w.nt = tiles_of<R>(p, w.n, w.len, w.rt);
+    w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
     int t0 = static_cast<int>(S.walk[3]);
     int64_t left = end - begin;
 
@@ -427,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
         r.head = w.h;
         const int64_t pos = static_cast<int64_t>(t) * kTile + lane * rows;
         r.tok = p.bs > kTile ? static_cast<int>(pos % p.bs) : 0;
-        const int last = min(w.n * p.G, (w.rt + 1) * R) - 1;
+        const int last = min(w.n * p.G, (w.rt + 1) * C::kRows) - 1;
         const int limit = w.len - w.n + last / p.G + 1;
         if (lane < ppt && pos < limit) {
           const int64_t e = pos / p.bs;
@@ -442,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
         if (--left > 0) {
           if (++t == w.nt) {
             t = 0;
-            next_unit<R>(p, w);
+            next_unit<C>(p, w);
           }
         } else {
           more = false;
@@ -494,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
     } else if (warp == 4 * C::kGroups + 1) {
       // ======================================================== product issuer
       if (lane == 0) {
-        constexpr uint32_t id_s = idesc(R, false, false), id_o = idesc(R, true, true);
+        constexpr uint32_t id_s = idesc(kN, false, false), id_o = idesc(kN, true, true);
         int64_t it = 0;
         uint32_t unit = 0;
         bool ok = true;
@@ -504,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
                bar_wait(&S.v_full[st], static_cast<uint32_t>(j / C::kV) & 1, &S.failed);
           if (!ok) return;
           tc_after();
-          const uint32_t v = s32(S.v[st]), d = tmem + (2 + static_cast<uint32_t>(j & 1)) * R;
+          const uint32_t v = s32(S.v[st]), d = tmem + (2 + static_cast<uint32_t>(j & 1)) * kN;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -527,12 +596,12 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
             ok = ok && bar_wait(&S.k_full[st], static_cast<uint32_t>(it / C::kK) & 1, &S.failed);
             if (!ok) break;
             tc_after();
-            const uint32_t kk = s32(S.k[st]), d = tmem + static_cast<uint32_t>(it & 1) * R;
+            const uint32_t kk = s32(S.k[st]), d = tmem + static_cast<uint32_t>(it & 1) * kN;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int k = 0; k < kD / 32; ++k)
-                mma(d, sdesc(kk + k * 32, 0, 1024, 2), sdesc(s32(S.q[part]) + k * 32 * R, 16 * R, 128, 0), id_s,
+                mma(d, sdesc(kk + k * 32, 0, 1024, 2), sdesc(s32(S.q[part]) + k * 32 * kN, 16 * kN, 128, 0), id_s,
                     part + k > 0);
             commit(&S.s_full[it & 1]);
             commit(&S.k_empty[st]);
@@ -540,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
           }
           left -= take;
           t = 0;
-          if (left > 0) next_unit<R>(p, w);
+          if (left > 0) next_unit<C>(p, w);
         }
         if (ok && it > 0) weigh(it - 1);
         commit(&S.done);
@@ -548,184 +617,205 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
       __syncwarp();
     } else {
       // ================================================================ softmax
-      const int g = warp >> 2, t = tid & 127;  // warpgroup; token of S^T, channel of O^T
+      const int g = warp >> 2, wq = warp & 3, t = tid & 127;  // warpgroup, warp in it, thread in it
       const int col0 = g * kCols;
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + col0;
-      Bcast<R>& bc = bcast[warp];
-      float o[kCols], l[kCols];
+      const int r8 = lane >> 2, pair = 2 * (lane & 3);  // of the thread's elements: lanes r8 + 8 j, columns 8 b + pair
+      const int own = own_column<kMine>(lane);
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16) + col0;
+      Bcast<C>& bc = bcast[warp];
+      float o[4][kMine], l[kMine], rs[kMine];
       int64_t it = 0;
       uint32_t unit = 0;
       int64_t at = begin;  // global index of the unit's first tile here
       for (; left > 0; ++unit) {
         const int take = static_cast<int>(min(static_cast<int64_t>(w.nt - t0), left));
-        const int row0 = w.rt * R + col0;                       // first of the group's query rows
+        const int row0 = w.rt * C::kRows + col0;                // first of the group's query rows
         const int rows = min(max(w.n * p.G - row0, 0), kCols);  // rows that exist
         const int ctx = w.len - w.n;
-        // ---- the unit's rows: scaled to e4m3's range by a power of two per row, split in two parts
-#pragma unroll 2
-        for (int r0 = 0; r0 < kCols; r0 += 8) {
-          const int c = r0 + (t >> 4), d = (t & 15) * 8, row = row0 + c;
-          float f[8];
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (c < rows)
-            v = *reinterpret_cast<const uint4*>(p.q + (w.q0 + row / p.G) * p.q_stride +
-                                                (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + d);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          float amax = 0.f;
-          bool finite = true;
+        // ---- the unit's rows: scaled to e4m3's range by a power of two per row, split in two parts.
+        // 16 threads per row, 8 channels each; all loads are under way before the first is used.
+        {
+          uint4 v[kBlocks];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+          for (int i = 0; i < kBlocks; ++i) {
+            const int c = 8 * i + (t >> 4), row = row0 + c;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (c < rows)
+              v[i] = *reinterpret_cast<const uint4*>(p.q + (w.q0 + row / p.G) * p.q_stride +
+                                                     (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + (t & 15) * 8);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            finite &= fabsf(f[i]) <= FLT_MAX;
-            amax = fmaxf(amax, fabsf(f[i]));
-          }
+          for (int i = 0; i < kBlocks; ++i) {
+            const int c = 8 * i + (t >> 4), d = (t & 15) * 8;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float f[8], amax = 0.f;
+            bool finite = true;
 #pragma unroll
-          for (int s = 1; s < 16; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-          const uint32_t who = __ballot_sync(0xffffffffu, finite);
-          finite = ((who >> (lane & 16)) & 0xffffu) == 0xffffu;
-          // 2^e with amax 2^-e in (224, 448]
-          const uint32_t bits = __float_as_uint(amax);
-          int e = static_cast<int>(bits >> 23) - 126 - 9 + ((bits & 0x7fffffu) > 0x600000u);
-          e = min(max(e, -100), 119);
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          uint32_t hi[2], lo[2];
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(u[k] << 16);
+              f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 y = make_float2(f[2 * i] * inv, f[2 * i + 1] * inv);
-            const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            const __nv_fp8x2_storage_t l8 =
-                __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
-            if (i & 1) hi[i >> 1] |= static_cast<uint32_t>(h8) << 16, lo[i >> 1] |= static_cast<uint32_t>(l8) << 16;
-            else hi[i >> 1] = h8, lo[i >> 1] = l8;
-          }
-          const uint32_t off = (d >> 4) * (16 * R) + (col0 + c) * 16 + (d & 8);
-          *reinterpret_cast<uint2*>(S.q[0] + off) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(S.q[1] + off) = make_uint2(lo[0], lo[1]);
-          if ((t & 15) == 0) {
-            S.row_scale[col0 + c] =
-                finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale : __uint_as_float(0x7fc00000u);
-            S.limit[col0 + c] = c < rows ? ctx + row / p.G + 1 : 0;
+            for (int k = 0; k < 8; ++k) {
+              finite &= fabsf(f[k]) <= FLT_MAX;
+              amax = fmaxf(amax, fabsf(f[k]));
+            }
+#pragma unroll
+            for (int s = 1; s < 16; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+            const uint32_t who = __ballot_sync(0xffffffffu, finite);
+            finite = ((who >> (lane & 16)) & 0xffffu) == 0xffffu;
+            // 2^e with amax 2^-e in (224, 448]
+            const uint32_t bits = __float_as_uint(amax);
+            int e = static_cast<int>(bits >> 23) - 126 - 9 + ((bits & 0x7fffffu) > 0x600000u);
+            e = min(max(e, -100), 119);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = make_float2(f[2 * k] * inv, f[2 * k + 1] * inv);
+              const __nv_fp8x2_storage_t h8 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3)));
+              const __nv_fp8x2_storage_t l8 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+              hi[k >> 1] |= static_cast<uint32_t>(h8) << (16 * (k & 1));
+              lo[k >> 1] |= static_cast<uint32_t>(l8) << (16 * (k & 1));
+            }
+            const uint32_t off = (d >> 4) * (16 * kN) + (col0 + c) * 16 + (d & 8);
+            *reinterpret_cast<uint2*>(S.q[0] + off) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(S.q[1] + off) = make_uint2(lo[0], lo[1]);
+            if ((t & 15) == 0) {
+              S.row_scale[col0 + c] = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale
+                                             : __uint_as_float(0x7fc00000u);
+              S.limit[col0 + c] = c < rows ? ctx + (row0 + c) / p.G + 1 : 0;
+            }
           }
         }
         if (g == 0) S.nan_at[unit & (C::kNan - 1)][t] = 0x7fffffff;
         fence_async();
         bar_arrive(&S.q_full);
         group_sync<128>(g);
-        const int first_limit = ctx + row0 / p.G + 1;  // the row that sees least
-        const int tile_rows = min(w.n * p.G, (w.rt + 1) * R);
-        const int least = ctx + (w.rt * R) / p.G + 1, most = ctx + (tile_rows - 1) / p.G + 1;  // of all groups
-        float run = -INFINITY;  // lane c: running maximum of row c
+        const int first_limit = ctx + row0 / p.G + 1;  // of the group's rows, the one that sees least
+        const int tile_rows = min(w.n * p.G, (w.rt + 1) * C::kRows);
+        const int least = ctx + (w.rt * C::kRows) / p.G + 1, most = ctx + (tile_rows - 1) / p.G + 1;  // of all groups
+        float run = -INFINITY;  // running maximum of row `own`
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c] = 0.f, l[c] = 0.f;
+        for (int c = 0; c < kMine; ++c) {
+          rs[c] = S.row_scale[col0 + 8 * (c >> 1) + pair + (c & 1)];
+          l[c] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j][c] = 0.f;
+        }
 
-        auto add_tile = [&](int64_t j) {  // the products of tile j join the sums
-          bar_wait(&S.o_full[j & 1], static_cast<uint32_t>(j >> 1) & 1, &S.failed);
+        auto add_tile = [&](int64_t i) {  // the products of tile i join the sums
+          bar_wait(&S.o_full[i & 1], static_cast<uint32_t>(i >> 1) & 1, &S.failed);
           tc_after();
-          float v[kCols];
-          tm_ld<kCols>(lanes + (2 + static_cast<uint32_t>(j & 1)) * R, v);
-          const float4* al = reinterpret_cast<const float4*>(bc.alpha[j & 1]);
-          const float4* be = reinterpret_cast<const float4*>(bc.beta[j & 1]);
+          float v[4][kMine];
+          tm_ld<kBlocks>(lanes + (2 + static_cast<uint32_t>(i & 1)) * kN, v);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 a4 = al[c / 4], b4 = be[c / 4];
-            o[c] = o[c] * a4.x + v[c] * b4.x;
-            o[c + 1] = o[c + 1] * a4.y + v[c + 1] * b4.y;
-            o[c + 2] = o[c + 2] * a4.z + v[c + 2] * b4.z;
-            o[c + 3] = o[c + 3] * a4.w + v[c + 3] * b4.w;
+          for (int b = 0; b < kBlocks; ++b) {
+            const int row = row_of_column<kBlocks>(b, lane);
+            const float2 al = *reinterpret_cast<const float2*>(bc.alpha[i & 1] + row);
+            const float2 be = *reinterpret_cast<const float2*>(bc.beta[i & 1] + row);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[j][2 * b] = o[j][2 * b] * al.x + v[j][2 * b] * be.x;
+              o[j][2 * b + 1] = o[j][2 * b + 1] * al.y + v[j][2 * b + 1] * be.y;
+            }
           }
         };
 
         for (int k = 0; k < take; ++k, ++it) {
           const int cs = static_cast<int>(it % (C::kV + 1)), vs = static_cast<int>(it % C::kV);
           const int buf = static_cast<int>(it & 1);
-          const int tile0 = (t0 + k) * kTile, pos = tile0 + t;
+          const int tile0 = (t0 + k) * kTile;
           bar_wait(&S.s_full[buf], static_cast<uint32_t>(it >> 1) & 1, &S.failed);
           bar_wait(&S.sc_full[cs], static_cast<uint32_t>(it / (C::kV + 1)) & 1, &S.failed);
           tc_after();
-          float z[kCols];
-          tm_ld<kCols>(lanes + static_cast<uint32_t>(buf) * R, z);
-          const float4 sc = S.sc[cs][p.bs >= kTile ? 0 : t / p.bs];
-          const float4* rs = reinterpret_cast<const float4*>(S.row_scale + col0);
+          float z[4][kMine];
+          tm_ld<kBlocks>(lanes + static_cast<uint32_t>(buf) * kN, z);
+          // a block is at least 16 tokens: lanes 0 .. 15 lie in one, 16 .. 31 in one
+          const float4 sc0 = S.sc[cs][p.bs >= kTile ? 0 : 32 * wq / p.bs];
+          const float4 sc1 = S.sc[cs][p.bs >= kTile ? 0 : (32 * wq + 16) / p.bs];
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 f = rs[c / 4];
-            z[c] = fmaf(z[c] * sc.x, f.x, sc.y);
-            z[c + 1] = fmaf(z[c + 1] * sc.x, f.y, sc.y);
-            z[c + 2] = fmaf(z[c + 2] * sc.x, f.z, sc.y);
-            z[c + 3] = fmaf(z[c + 3] * sc.x, f.w, sc.y);
-          }
-          const bool edge = tile0 + kTile > first_limit;
-          if (edge) {
-            const int4* li = reinterpret_cast<const int4*>(S.limit + col0);
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-              const int4 f = li[c / 4];
-              if (pos >= f.x) z[c] = -INFINITY;
-              if (pos >= f.y) z[c + 1] = -INFINITY;
-              if (pos >= f.z) z[c + 2] = -INFINITY;
-              if (pos >= f.w) z[c + 3] = -INFINITY;
+            for (int c = 0; c < kMine; ++c)
+              z[j][c] = j < 2 ? fmaf(z[j][c] * sc0.x, rs[c], sc0.y) : fmaf(z[j][c] * sc1.x, rs[c], sc1.y);
+          if (tile0 + kTile > first_limit) {
+            const int pos = tile0 + 32 * wq + r8;
+#pragma unroll
+            for (int c = 0; c < kMine; ++c) {
+              const int limit = S.limit[col0 + 8 * (c >> 1) + pair + (c & 1)];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (pos + 8 * j >= limit) z[j][c] = -INFINITY;
             }
           }
-          // ---- the tile's maximum of every row: over the warp's tokens, then over the warps
-          float top = -INFINITY;
+          // ---- the tile's maximum of every row: over the thread's tokens, the warp's, the group's
+          float top;
+          {
+            float m[kMine];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const float m = warp_max(z[c]);
-            if (lane == c) top = m;
+            for (int c = 0; c < kMine; ++c) m[c] = fmaxf(fmaxf(z[0][c], z[1][c]), fmaxf(z[2][c], z[3][c]));
+            top = reduce_columns<Max>(m, lane);
           }
-          if (lane < kCols) S.wmax[buf][g][warp & 3][lane] = top;
+          if (own < kCols) S.wmax[buf][g][wq][own] = top;
           group_sync<128>(g);
-          if (lane < kCols) {
+          if (own < kCols) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, S.wmax[buf][g][i][lane]);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, S.wmax[buf][g][i][own]);
             const float next = fmaxf(run, top);
             const float ref = next == -INFINITY ? 0.f : next;
-            bc.alpha[buf][lane] = ex2(run - ref);
-            bc.beta[buf][lane] = ex2(top - ref);
-            bc.mt[lane] = (top == -INFINITY ? 0.f : top) - 8.f;  // weights up to 2^8
+            bc.alpha[buf][own] = ex2(run - ref);
+            bc.beta[buf][own] = ex2(top - ref);
+            bc.mt[own] = (top == -INFINITY ? 0.f : top) - 8.f;  // weights up to 2^8
             run = next;
           }
           __syncwarp();
-          // ---- weights, their sum, their two e4m3 parts
-          const float4* mt = reinterpret_cast<const float4*>(bc.mt);
-          const float4* al = reinterpret_cast<const float4*>(bc.alpha[buf]);
-          const float4* be = reinterpret_cast<const float4*>(bc.beta[buf]);
-          uint32_t hi[kCols / 4], lo[kCols / 4];
+          // ---- weights, their sum, their two e4m3 parts (16 bits per token and pair of rows)
+          uint32_t hi[4][kBlocks], lo[4][kBlocks];
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 m4 = mt[c / 4], a4 = al[c / 4], b4 = be[c / 4];
-            const float w0 = ex2(z[c] - m4.x), w1 = ex2(z[c + 1] - m4.y), w2 = ex2(z[c + 2] - m4.z),
-                        w3 = ex2(z[c + 3] - m4.w);
-            l[c] = l[c] * a4.x + (b4.x * sc.z) * w0;
-            l[c + 1] = l[c + 1] * a4.y + (b4.y * sc.z) * w1;
-            l[c + 2] = l[c + 2] * a4.z + (b4.z * sc.z) * w2;
-            l[c + 3] = l[c + 3] * a4.w + (b4.w * sc.z) * w3;
-            const __half2 x0 = __floats2half2_rn(w0, w1), x1 = __floats2half2_rn(w2, w3);
-            const __nv_fp8x2_storage_t h0 = __nv_cvt_halfraw2_to_fp8x2(x0, __NV_SATFINITE, __NV_E4M3),
-                                       h1 = __nv_cvt_halfraw2_to_fp8x2(x1, __NV_SATFINITE, __NV_E4M3);
-            const __half2 y0 = __hsub2(x0, __half2(__nv_cvt_fp8x2_to_halfraw2(h0, __NV_E4M3))),
-                          y1 = __hsub2(x1, __half2(__nv_cvt_fp8x2_to_halfraw2(h1, __NV_E4M3)));
-            hi[c / 4] = h0 | (static_cast<uint32_t>(h1) << 16);
-            lo[c / 4] = __nv_cvt_halfraw2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
-                        (static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3)) << 16);
+          for (int b = 0; b < kBlocks; ++b) {
+            const float2 mt = *reinterpret_cast<const float2*>(bc.mt + 8 * b + pair);
+            const float2 al = *reinterpret_cast<const float2*>(bc.alpha[buf] + 8 * b + pair);
+            const float2 be = *reinterpret_cast<const float2*>(bc.beta[buf] + 8 * b + pair);
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float w0 = ex2(z[j][2 * b] - mt.x), w1 = ex2(z[j][2 * b + 1] - mt.y);
+              const float rv = j < 2 ? sc0.z : sc1.z;
+              s0 = fmaf(w0, rv, s0);
+              s1 = fmaf(w1, rv, s1);
+              const __half2 x = __floats2half2_rn(w0, w1);
+              const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+              hi[j][b] = h;
+              lo[j][b] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3))),
+                                                    __NV_SATFINITE, __NV_E4M3);
+            }
+            l[2 * b] = l[2 * b] * al.x + s0 * be.x;
+            l[2 * b + 1] = l[2 * b + 1] * al.y + s1 * be.y;
           }
           if (it > 0) bar_wait(&S.o_full[(it - 1) & 1], static_cast<uint32_t>((it - 1) >> 1) & 1, &S.failed);
 #pragma unroll
-          for (int c = 0; c < kCols / 16; ++c) {
-            const int off = (col0 / 16 + c) * (16 * kTile) + t * 16;
-            *reinterpret_cast<uint4*>(S.p[0] + off) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            *reinterpret_cast<uint4*>(S.p[1] + off) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+          for (int j = 0; j < 4; ++j) {
+            const int tok = 32 * wq + r8 + 8 * j;
+#pragma unroll
+            for (int b = 0; b + 1 < kBlocks; b += 2) {
+              const int off = (col0 / 16 + b / 2) * (16 * kTile) + tok * 16 + 2 * pair;
+              *reinterpret_cast<uint32_t*>(S.p[0] + off) = hi[j][b] | (hi[j][b + 1] << 16);
+              *reinterpret_cast<uint32_t*>(S.p[1] + off) = lo[j][b] | (lo[j][b + 1] << 16);
+            }
+            if constexpr (kBlocks & 1) {
+              const int off = (kBlocks / 2) * (16 * kTile) + tok * 16 + pair;
+              *reinterpret_cast<uint16_t*>(S.p[0] + off) = static_cast<uint16_t>(hi[j][kBlocks - 1]);
+              *reinterpret_cast<uint16_t*>(S.p[1] + off) = static_cast<uint16_t>(lo[j][kBlocks - 1]);
+            }
           }
           // ---- values that some row does not see: a zero weight times NaN is
           // NaN, so what no row sees is cleared, and a NaN that only some rows
           // see is taken out here and put back into their results
           if (g == 0 && tile0 + kTile > least) {
+            const int pos = tile0 + t;
             bar_wait(&S.v_full[vs], static_cast<uint32_t>(it / C::kV) & 1, &S.failed);
             __syncwarp();
             uint4* v = reinterpret_cast<uint4*>(S.v[vs] + t * kD);
@@ -747,55 +837,48 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
         }
         add_tile(it - 1);
 
-        // ---- the unit's end: sums over the tokens (threads) of every row
-        float lsum;
-        if constexpr (kCols == 32) {
-#pragma unroll
-          for (int s = 16; s > 0; s >>= 1)
-#pragma unroll
-            for (int c = 0; c < s; ++c) {
-              const float send = lane & s ? l[c] : l[c + s], keep = lane & s ? l[c + s] : l[c];
-              l[c] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-            }
-          lsum = l[0];
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
-#pragma unroll
-          for (int s = 8; s > 0; s >>= 1)
-#pragma unroll
-            for (int c = 0; c < s; ++c) {
-              const float send = lane & s ? l[c] : l[c + s], keep = lane & s ? l[c + s] : l[c];
-              l[c] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-            }
-          lsum = l[0];
-        }
-        if (lane < kCols) S.wsum[g][warp & 3][lane] = lsum;
+        // ---- the unit's end: sums over the tokens of every row
+        float lsum = reduce_columns<Sum>(l, lane);
+        if (own < kCols) S.wsum[g][wq][own] = lsum;
         group_sync<128>(g);
-        if (lane < kCols) {
+        if (own < kCols) {
           lsum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) lsum += S.wsum[g][i][lane];
-          if (S.row_scale[col0 + lane] != S.row_scale[col0 + lane]) lsum = S.row_scale[col0 + lane];
+          for (int i = 0; i < 4; ++i) lsum += S.wsum[g][i][own];
+          const float f = S.row_scale[col0 + own];
+          if (f != f) lsum = f;  // a row that is not finite
         }
-        const int nan_at = S.nan_at[unit & (C::kNan - 1)][t];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (nan_at < S.limit[col0 + c]) o[c] = __uint_as_float(0x7fc00000u);
-        uint16_t* out = p.out + static_cast<int64_t>(w.h) * p.G * kD + t;
-        auto store = [&](int c, float v) {
-          const int row = row0 + c;
-          const __nv_bfloat16 b = __float2bfloat16_rn(v);
-          out[(w.q0 + row / p.G) * p.out_stride + static_cast<int64_t>(row % p.G) * kD] =
-              *reinterpret_cast<const uint16_t*>(&b);
+        for (int j = 0; j < 4; ++j) {
+          const int nan_at = S.nan_at[unit & (C::kNan - 1)][32 * wq + r8 + 8 * j];
+#pragma unroll
+          for (int c = 0; c < kMine; ++c)
+            if (nan_at < S.limit[col0 + row_of_column<kBlocks>(c >> 1, lane) + (c & 1)])
+              o[j][c] = __uint_as_float(0x7fc00000u);
+        }
+        // A thread and its neighbour four lanes on hold channels d, d + 1 of the
+        // same two rows: each takes one row and writes both channels.
+        const bool odd = r8 & 1;
+        auto two_channels = [&](int j, int b) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? o[j][2 * b] : o[j][2 * b + 1], 4);
+          return odd ? make_float2(got, o[j][2 * b + 1]) : make_float2(o[j][2 * b], got);
         };
+        const int d0 = 32 * wq + (r8 & ~1);
         if (take == w.nt) {
-          if (lane < kCols) bc.mt[lane] = lsum == 0.f ? 0.f : 1.f / lsum;
+          if (own < kCols) bc.mt[own] = lsum == 0.f ? 0.f : 1.f / lsum;
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < rows) store(c, o[c] * bc.mt[c]);
-          __syncwarp();
+          for (int b = 0; b < kBlocks; ++b) {
+            const int c = row_of_column<kBlocks>(b, lane) + odd, row = row0 + c;
+            const float f = bc.mt[c];
+            uint16_t* out = p.out + (w.q0 + row / p.G) * p.out_stride +
+                            (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + d0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = two_channels(j, b);
+              if (c < rows) *reinterpret_cast<__nv_bfloat162*>(out + 8 * j) = __floats2bfloat162_rn(x.x * f, x.y * f);
+            }
+          }
         } else if (rows > 0) {
           // a part of the unit: a record for the CTA that arrives last
           const int64_t us = at - t0;
@@ -806,9 +889,15 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
           };
           float* rec = record(static_cast<int>(cta));
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (c < rows) rec[2 * kCols + c * kD + t] = o[c];
-          if ((warp & 3) == 0 && lane < kCols) rec[lane] = run, rec[kCols + lane] = lsum;
+          for (int b = 0; b < kBlocks; ++b) {
+            const int c = row_of_column<kBlocks>(b, lane) + odd;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = two_channels(j, b);
+              if (c < rows) *reinterpret_cast<float2*>(rec + 2 * kCols + c * kD + d0 + 8 * j) = x;
+            }
+          }
+          if (wq == 0 && own < kCols) rec[own] = run, rec[kCols + own] = lsum;
           __threadfence();
           group_sync<128>(g);
           if (t == 0) {
@@ -821,31 +910,57 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtasPerSm)
           group_sync<128>(g);
           if (S.last[g]) {
             __threadfence();
-            float m = -INFINITY, sum = 0.f;
-            if (lane < kCols) {
-              for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(record(c) + lane));
-              const float ref = m == -INFINITY ? 0.f : m;
-              for (int c = c0; c <= c1; ++c) sum += ex2(__ldcg(record(c) + lane) - ref) * __ldcg(record(c) + kCols + lane);
-              bc.mt[lane] = ref;
-              bc.alpha[0][lane] = sum == 0.f ? 0.f : 1.f / sum;
-            }
-            __syncwarp();
-            for (int c = 0; c < rows; ++c) {
-              float v = 0.f;
-              for (int i = c0; i <= c1; ++i) {
-                const float* r = record(i);
-                v += ex2(__ldcg(r + c) - bc.mt[c]) * __ldcg(r + 2 * kCols + c * kD + t);
+            // warp = every fourth row, lane = four channels; kJoin rows at a time, so
+            // that their loads are under way together
+            constexpr int kJoin = kCols >= 16 ? 4 : 2;
+            for (int c = wq; c < rows; c += 4 * kJoin) {
+              float top[kJoin], sum[kJoin];
+              float4 acc[kJoin];
+#pragma unroll
+              for (int i = 0; i < kJoin; ++i) top[i] = -INFINITY;
+              for (int part = c0 + lane; part <= c1; part += 32)
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i)
+                  if (c + 4 * i < rows) top[i] = fmaxf(top[i], __ldcg(record(part) + c + 4 * i));
+#pragma unroll
+              for (int i = 0; i < kJoin; ++i) {
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], s));
+                if (top[i] == -INFINITY) top[i] = 0.f;
+                sum[i] = 0.f;
+                acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
               }
-              store(c, v * bc.alpha[0][c]);
+#pragma unroll 4
+              for (int part = c0; part <= c1; ++part) {
+                const float* rp = record(part);
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i) {
+                  const int row = min(c + 4 * i, rows - 1);
+                  const float f = ex2(__ldcg(rp + row) - top[i]);
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(rp + 2 * kCols + row * kD) + lane);
+                  sum[i] += f * __ldcg(rp + kCols + row);
+                  acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < kJoin; ++i) {
+                const int row = row0 + c + 4 * i;
+                if (c + 4 * i >= rows) continue;
+                const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+                const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
+                                     y = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
+                *reinterpret_cast<uint2*>(p.out + (w.q0 + row / p.G) * p.out_stride +
+                                          (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + 4 * lane) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+              }
             }
-            __syncwarp();
           }
         }
         group_sync<128>(g);  // row_scale and limit are read: the next unit may write them
         left -= take;
         at += take;
         t0 = 0;
-        if (left > 0) next_unit<R>(p, w);
+        if (left > 0) next_unit<C>(p, w);
       }
     }
     // every product has ended before the accumulators are given back
@@ -866,12 +981,25 @@ std::mutex g_mutex;
 int g_sms[64];
 EncodeFn g_encode;
 
-template <int R>
+using Rows8 = Cfg<8, 1>;
+using Rows16 = Cfg<16, 1>;
+using Rows24 = Cfg<24, 1>;
+using Rows32 = Cfg<32, 1>;
+using Rows64 = Cfg<32, 2>;
+using Rows96 = Cfg<32, 3>;
+
+template <class C>
 constexpr size_t smem_bytes() {
-  constexpr size_t n = sizeof(Smem<R>) + 4 * Cfg<R>::kGroups * sizeof(Bcast<R>);
+  constexpr size_t n = sizeof(Smem<C>) + 4 * C::kGroups * sizeof(Bcast<C>);
   // an SM has 228 KB, of which each CTA's system part takes 1 KB
-  static_assert((n + 1024) * Cfg<R>::kCtasPerSm <= 228 * 1024 && n <= 227 * 1024, "shared memory");
+  static_assert((n + 1024) * C::kCtasPerSm <= 228 * 1024 && n <= 227 * 1024, "shared memory");
   return n;
+}
+
+template <class C>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(cache_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem_bytes<C>()));
 }
 
 cudaError_t setup(int* sms) {
@@ -887,10 +1015,9 @@ cudaError_t setup(int* sms) {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeFn>(fn);
-    const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if ((e = cudaFuncSetAttribute(cache_attention_kernel<16>, attr, smem_bytes<16>())) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(cache_attention_kernel<32>, attr, smem_bytes<32>())) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(cache_attention_kernel<64>, attr, smem_bytes<64>())) != cudaSuccess)
+    if ((e = allow_smem<Rows8>()) != cudaSuccess || (e = allow_smem<Rows16>()) != cudaSuccess ||
+        (e = allow_smem<Rows24>()) != cudaSuccess || (e = allow_smem<Rows32>()) != cudaSuccess ||
+        (e = allow_smem<Rows64>()) != cudaSuccess || (e = allow_smem<Rows96>()) != cudaSuccess)
       return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -902,28 +1029,30 @@ cudaError_t setup(int* sms) {
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
 
-// Rows of a tile: all the queries of a kv head in a single-token or
-// multi-token step, so that the cache is read once; 64 for more.
-int row_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
-template <int R>
-constexpr int64_t partial_bytes() {
-  return 2LL * (kMaxCtas / 2) * Cfg<R>::kCtasPerSm * Cfg<R>::kGroups * Cfg<R>::kPartial * 4;
+// Calls `f` with the variant for `rows` query rows per kv head and sequence: all
+// the queries of a single-token or multi-token step, so that the cache is read
+// once and no column is idle for more than 7 of 8 rows; 96 rows for prompts.
+template <class F>
+auto with_variant(int64_t rows, F f) {
+  if (rows <= 8) return f(Rows8{});
+  if (rows <= 16) return f(Rows16{});
+  if (rows <= 24) return f(Rows24{});
+  if (rows <= 32) return f(Rows32{});
+  if (rows <= 64) return f(Rows64{});
+  return f(Rows96{});
 }
 
-template <int R>
-cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, int sms, void* stream) {
-  return kda_internal_launch(cache_attention_kernel<R>, dim3(static_cast<unsigned>(sms * Cfg<R>::kCtasPerSm)),
-                             dim3(Cfg<R>::kThreads), smem_bytes<R>(), stream, p, k, v);
+template <class C>
+constexpr int64_t partial_bytes() {
+  return 2LL * (kMaxCtas / 2) * C::kCtasPerSm * C::kGroups * C::kPartial * 4;
 }
 
 }  // namespace
 
 extern "C" int64_t kda_cache_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t max_new) {
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads || max_new < 1) return -1;
-  const int r = row_tile(static_cast<int64_t>(max_new) * (num_q_heads / num_kv_heads));
-  return KDA_CACHE_ATTENTION_COUNTER_BYTES +
-         (r == 16 ? partial_bytes<16>() : r == 32 ? partial_bytes<32>() : partial_bytes<64>());
+  return KDA_CACHE_ATTENTION_COUNTER_BYTES + with_variant(static_cast<int64_t>(max_new) * (num_q_heads / num_kv_heads),
+                                                          [](auto c) { return partial_bytes<decltype(c)>(); });
 }
 
 extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream) {
@@ -987,10 +1116,11 @@ extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream)
   p.k_scale = a->k_scale, p.v_scale = a->v_scale, p.err = a->err_flag;
   p.counters = static_cast<int32_t*>(a->workspace);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + KDA_CACHE_ATTENTION_COUNTER_BYTES);
-  const int r = row_tile(static_cast<int64_t>(a->max_new) * p.G);
-  e = r == 16   ? launch<16>(p, maps[0], maps[1], sms, stream)
-      : r == 32 ? launch<32>(p, maps[0], maps[1], sms, stream)
-                : launch<64>(p, maps[0], maps[1], sms, stream);
+  e = with_variant(static_cast<int64_t>(a->max_new) * p.G, [&](auto c) {
+    using C = decltype(c);
+    return kda_internal_launch(cache_attention_kernel<C>, dim3(static_cast<unsigned>(sms * C::kCtasPerSm)),
+                               dim3(C::kThreads), smem_bytes<C>(), stream, p, maps[0], maps[1]);
+  });
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }
