@@ -54,6 +54,11 @@ constexpr int kTile = 128;                 // tokens per tile
 constexpr int kTileBytes = kTile * kD;     // of K, and of V
 constexpr int kMaxPages = 8;               // blocks of a tile, at block size 16
 constexpr int kMaxCtas = 304;              // 2 x 152
+// What beginning and ending a unit costs, in tiles: the work is dealt out by
+// tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
+constexpr int kUnitCost = 4;
+constexpr int kJoinFan = 8;                // parts that one CTA joins
+constexpr int kCounters = 456;             // of each kind: CTAs x groups, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -370,13 +375,40 @@ __device__ __forceinline__ void next_unit(const Params& p, Walk& w) {  // only c
   w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
 }
 template <class C>
-__device__ __forceinline__ int64_t seq_tiles(const Params& p, int i) {
+__device__ __forceinline__ int64_t seq_cost(const Params& p, int i) {
   Walk w;
   w.seq = i;
   if (!load_seq<C>(p, w)) return 0;
   int64_t s = 0;
-  for (int rt = 0; rt < w.rts; ++rt) s += tiles_of<C>(p, w.n, w.len, rt);
+  for (int rt = 0; rt < w.rts; ++rt) s += tiles_of<C>(p, w.n, w.len, rt) + kUnitCost;
   return s * p.Hkv;
+}
+// A CTA's share: the units it has tiles of, one after another.  Positions are
+// in cost; a unit's cost is kUnitCost, then its tiles.
+struct Share {
+  Walk w;
+  int64_t us, left;  // where the unit begins; cost left of the share, this unit's included
+  int off;           // where the share begins in the unit
+  int t0, take;      // the unit's tiles here
+  __device__ __forceinline__ int span() const {
+    return static_cast<int>(min(static_cast<int64_t>(kUnitCost + w.nt - off), left));
+  }
+  __device__ __forceinline__ void tiles() {
+    t0 = max(off - kUnitCost, 0);
+    take = max(off + span() - kUnitCost, 0) - t0;
+  }
+};
+template <class C>
+__device__ __forceinline__ bool next_share(const Params& p, Share& s) {  // false: the share is done
+  do {
+    s.left -= s.span();
+    if (s.left <= 0) return false;
+    s.us += kUnitCost + s.w.nt;
+    s.off = 0;
+    next_unit<C>(p, s.w);
+    s.tiles();
+  } while (s.take == 0);
+  return true;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -411,7 +443,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   int64_t mine = 0;
   bool bad = false;
   for (int i = tid; i < p.B; i += C::kThreads) {
-    mine += seq_tiles<C>(p, i);
+    mine += seq_cost<C>(p, i);
     const int a = p.cu[i], b = p.cu[i + 1];
     bad |= a < 0 || b < a || b > p.T;
   }
@@ -437,7 +469,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     for (int base = 0; base < p.B; base += C::kThreads) {
       __syncthreads();
       const int i = base + tid;
-      const int64_t t = i < p.B ? seq_tiles<C>(p, i) : 0;
+      const int64_t t = i < p.B ? seq_cost<C>(p, i) : 0;
       int64_t incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -458,28 +490,32 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         w.seq = i;
         load_seq<C>(p, w);
         int64_t off = begin - from;
-        int nt = tiles_of<C>(p, w.n, w.len, 0);
-        while (off >= static_cast<int64_t>(nt) * p.Hkv) {
-          off -= static_cast<int64_t>(nt) * p.Hkv;
-          nt = tiles_of<C>(p, w.n, w.len, ++w.rt);
+        int cost = tiles_of<C>(p, w.n, w.len, 0) + kUnitCost;
+        while (off >= static_cast<int64_t>(cost) * p.Hkv) {
+          off -= static_cast<int64_t>(cost) * p.Hkv;
+          cost = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
         }
         S.walk[0] = i;
         S.walk[1] = w.rt;
-        S.walk[2] = off / nt;
-        S.walk[3] = off % nt;
+        S.walk[2] = off / cost;
+        S.walk[3] = off % cost;
       }
       before += all;
       if (before > begin) break;
     }
     __syncthreads();
-    Walk w;
+    Share sh;
+    Walk& w = sh.w;
     w.seq = static_cast<int>(S.walk[0]);
     load_seq<C>(p, w);
     w.rt = static_cast<int>(S.walk[1]);
     w.h = static_cast<int>(S.walk[2]);
     w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
-    int t0 = static_cast<int>(S.walk[3]);
-    int64_t left = end - begin;
+    sh.off = static_cast<int>(S.walk[3]);
+    sh.us = begin - sh.off;
+    sh.left = end - begin;
+    sh.tiles();
+    bool more = sh.take > 0 || next_share<C>(p, sh);
 
     if (warp == 4 * C::kGroups) {
       // ================================================================ producer
@@ -487,12 +523,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       const int rows = p.bs >= kTile ? kTile : p.bs;     // rows of a copy
       struct Ref {
         int block, head, tok;
+        bool valid;
       };
-      int t = t0;  // next tile of the walk
-      bool more = true;
-      auto take = [&]() {  // the walk's next tile: this lane's block id in it
+      int t = sh.t0;       // next tile
+      auto take = [&]() {  // the next tile of the share: this lane's block id in it
         Ref r;
+        r.valid = more;
         r.block = -1;
+        r.head = r.tok = 0;
+        if (!more) return r;
         r.head = w.h;
         const int64_t pos = static_cast<int64_t>(t) * kTile + lane * rows;
         r.tok = p.bs > kTile ? static_cast<int>(pos % p.bs) : 0;
@@ -508,13 +547,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
           r.block = b;
         }
-        if (--left > 0) {
-          if (++t == w.nt) {
-            t = 0;
-            next_unit<C>(p, w);
-          }
-        } else {
-          more = false;
+        if (++t == sh.t0 + sh.take) {
+          more = next_share<C>(p, sh);
+          t = sh.t0;
         }
         return r;
       };
@@ -523,19 +558,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         const int64_t at = static_cast<int64_t>(r.block) * p.Hkv + r.head;
         return make_float2(p.k_scale[at], p.v_scale[at]);
       };
-      const int64_t count = left;
-      Ref a = take(), b = a;
-      if (more) b = take();
+      Ref a = take(), b = take();
       float2 sa = scales(a);
       bool ok = true;
-      int64_t k_sent = 0, v_sent = 0;
-      for (int64_t it = 0; it < count; ++it) {
-        const float2 sb = it + 1 < count ? scales(b) : make_float2(0.f, 0.f);
-        Ref c = b;
-        if (more) c = take();
-        const int ks = static_cast<int>(it % C::kK), vs = static_cast<int>(it % C::kV);
-        const int cs = static_cast<int>(it % (C::kV + 1));
-        const uint32_t kr = static_cast<uint32_t>(it / C::kK), vr = static_cast<uint32_t>(it / C::kV);
+      uint32_t k_sent = 0, v_sent = 0;
+      for (uint32_t it = 0; a.valid; ++it) {
+        const float2 sb = scales(b);
+        const Ref c = take();
+        const uint32_t ks = it % C::kK, vs = it % C::kV, cs = it % (C::kV + 1), kr = it / C::kK, vr = it / C::kV;
         if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
         if (lane < ppt) {
           const float sv = fmaxf(sa.y, 0x1p-64f);
@@ -555,25 +585,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         a = b, b = c, sa = sb;
       }
       if (!ok) {  // nothing may land in shared memory after the CTA is gone
-        for (int64_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
-          bar_drain(&S.k_full[j % C::kK], static_cast<uint32_t>(j / C::kK) & 1);
-        for (int64_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
-          bar_drain(&S.v_full[j % C::kV], static_cast<uint32_t>(j / C::kV) & 1);
+        for (uint32_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
+          bar_drain(&S.k_full[j % C::kK], (j / C::kK) & 1);
+        for (uint32_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
+          bar_drain(&S.v_full[j % C::kV], (j / C::kV) & 1);
       }
     } else if (warp == 4 * C::kGroups + 1) {
       // ======================================================== product issuer
       if (lane == 0) {
         constexpr uint32_t id_s = idesc(kN, false, false), id_o = idesc(kN, true, true);
-        int64_t it = 0;
-        uint32_t unit = 0;
+        uint32_t it = 0, unit = 0;
         bool ok = true;
-        auto weigh = [&](int64_t j) {  // O^T of tile j
-          const int st = static_cast<int>(j % C::kV);
-          ok = ok && bar_wait(&S.p_full, static_cast<uint32_t>(j & 1), &S.failed) &&
-               bar_wait(&S.v_full[st], static_cast<uint32_t>(j / C::kV) & 1, &S.failed);
+        auto weigh = [&](uint32_t j) {  // O^T of tile j
+          const uint32_t st = j % C::kV;
+          ok = ok && bar_wait(&S.p_full, j & 1, &S.failed) && bar_wait(&S.v_full[st], (j / C::kV) & 1, &S.failed);
           if (!ok) return;
           tc_after();
-          const uint32_t v = s32(S.v[st]), d = tmem + (2 + static_cast<uint32_t>(j & 1)) * kN;
+          const uint32_t v = s32(S.v[st]), d = tmem + (2 + (j & 1)) * kN;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -583,20 +611,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           commit(&S.v_empty[st]);
           commit(&S.o_full[j & 1]);
         };
-        int t = t0;
-        for (; left > 0 && ok; ++unit) {
-          const int take = static_cast<int>(min(static_cast<int64_t>(w.nt - t), left));
-          for (int k0 = 0; k0 < take && ok; ++k0, ++it) {
+        for (; more && ok; ++unit) {
+          for (int k0 = 0; k0 < sh.take && ok; ++k0, ++it) {
             if (k0 == 0) {
               // the rows of a new unit are in place only after the old unit's last tile is weighed
               if (it > 0) weigh(it - 1);
               ok = ok && bar_wait(&S.q_full, unit & 1, &S.failed);
             }
-            const int st = static_cast<int>(it % C::kK);
-            ok = ok && bar_wait(&S.k_full[st], static_cast<uint32_t>(it / C::kK) & 1, &S.failed);
+            const uint32_t st = it % C::kK;
+            ok = ok && bar_wait(&S.k_full[st], (it / C::kK) & 1, &S.failed);
             if (!ok) break;
             tc_after();
-            const uint32_t kk = s32(S.k[st]), d = tmem + static_cast<uint32_t>(it & 1) * kN;
+            const uint32_t kk = s32(S.k[st]), d = tmem + (it & 1) * kN;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -607,9 +633,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             commit(&S.k_empty[st]);
             if (k0 > 0) weigh(it - 1);
           }
-          left -= take;
-          t = 0;
-          if (left > 0) next_unit<C>(p, w);
+          more = next_share<C>(p, sh);
         }
         if (ok && it > 0) weigh(it - 1);
         commit(&S.done);
@@ -624,26 +648,30 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16) + col0;
       Bcast<C>& bc = bcast[warp];
       float o[4][kMine], l[kMine], rs[kMine];
-      int64_t it = 0;
-      uint32_t unit = 0;
-      int64_t at = begin;  // global index of the unit's first tile here
-      for (; left > 0; ++unit) {
-        const int take = static_cast<int>(min(static_cast<int64_t>(w.nt - t0), left));
+      uint32_t it = 0, unit = 0;
+      const int page0 = p.bs >= kTile ? 0 : 32 * wq / p.bs, page1 = p.bs >= kTile ? 0 : (32 * wq + 16) / p.bs;
+      // The rows of a unit in registers: 16 threads per row, 8 channels each.  They
+      // are asked for before the unit ahead of it ends.
+      uint4 v[kBlocks];
+      auto load_rows = [&](const Walk& u) {
+        const int row0 = u.rt * C::kRows + col0, rows = u.n * p.G - row0;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int c = 8 * i + (t >> 4), row = row0 + c;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (c < rows)
+            v[i] = *reinterpret_cast<const uint4*>(p.q + (u.q0 + row / p.G) * p.q_stride +
+                                                   (static_cast<int64_t>(u.h) * p.G + row % p.G) * kD + (t & 15) * 8);
+        }
+      };
+      if (more) load_rows(w);
+      for (; more; ++unit) {
+        const int t0 = sh.t0, take = sh.take;
         const int row0 = w.rt * C::kRows + col0;                // first of the group's query rows
         const int rows = min(max(w.n * p.G - row0, 0), kCols);  // rows that exist
         const int ctx = w.len - w.n;
-        // ---- the unit's rows: scaled to e4m3's range by a power of two per row, split in two parts.
-        // 16 threads per row, 8 channels each; all loads are under way before the first is used.
+        // ---- the unit's rows: scaled to e4m3's range by a power of two per row, split in two parts
         {
-          uint4 v[kBlocks];
-#pragma unroll
-          for (int i = 0; i < kBlocks; ++i) {
-            const int c = 8 * i + (t >> 4), row = row0 + c;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (c < rows)
-              v[i] = *reinterpret_cast<const uint4*>(p.q + (w.q0 + row / p.G) * p.q_stride +
-                                                     (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + (t & 15) * 8);
-          }
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
             const int c = 8 * i + (t >> 4), d = (t & 15) * 8;
@@ -706,11 +734,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           for (int j = 0; j < 4; ++j) o[j][c] = 0.f;
         }
 
-        auto add_tile = [&](int64_t i) {  // the products of tile i join the sums
-          bar_wait(&S.o_full[i & 1], static_cast<uint32_t>(i >> 1) & 1, &S.failed);
+        Share nx = sh;
+        const bool then = next_share<C>(p, nx);
+
+        auto add_tile = [&](uint32_t i) {  // the products of tile i join the sums
+          bar_wait(&S.o_full[i & 1], (i >> 1) & 1, &S.failed);
           tc_after();
           float v[4][kMine];
-          tm_ld<kBlocks>(lanes + (2 + static_cast<uint32_t>(i & 1)) * kN, v);
+          tm_ld<kBlocks>(lanes + (2 + (i & 1)) * kN, v);
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             const int row = row_of_column<kBlocks>(b, lane);
@@ -725,17 +756,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         };
 
         for (int k = 0; k < take; ++k, ++it) {
-          const int cs = static_cast<int>(it % (C::kV + 1)), vs = static_cast<int>(it % C::kV);
-          const int buf = static_cast<int>(it & 1);
+          const uint32_t cs = it % (C::kV + 1), vs = it % C::kV, buf = it & 1;
           const int tile0 = (t0 + k) * kTile;
-          bar_wait(&S.s_full[buf], static_cast<uint32_t>(it >> 1) & 1, &S.failed);
-          bar_wait(&S.sc_full[cs], static_cast<uint32_t>(it / (C::kV + 1)) & 1, &S.failed);
+          bar_wait(&S.s_full[buf], (it >> 1) & 1, &S.failed);
+          bar_wait(&S.sc_full[cs], (it / (C::kV + 1)) & 1, &S.failed);
           tc_after();
           float z[4][kMine];
-          tm_ld<kBlocks>(lanes + static_cast<uint32_t>(buf) * kN, z);
+          tm_ld<kBlocks>(lanes + buf * kN, z);
           // a block is at least 16 tokens: lanes 0 .. 15 lie in one, 16 .. 31 in one
-          const float4 sc0 = S.sc[cs][p.bs >= kTile ? 0 : 32 * wq / p.bs];
-          const float4 sc1 = S.sc[cs][p.bs >= kTile ? 0 : (32 * wq + 16) / p.bs];
+          const float4 sc0 = S.sc[cs][page0];
+          const float4 sc1 = S.sc[cs][page1];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -795,7 +825,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             l[2 * b] = l[2 * b] * al.x + s0 * be.x;
             l[2 * b + 1] = l[2 * b + 1] * al.y + s1 * be.y;
           }
-          if (it > 0) bar_wait(&S.o_full[(it - 1) & 1], static_cast<uint32_t>((it - 1) >> 1) & 1, &S.failed);
+          if (it > 0) bar_wait(&S.o_full[(it - 1) & 1], ((it - 1) >> 1) & 1, &S.failed);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int tok = 32 * wq + r8 + 8 * j;
@@ -816,7 +846,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           // see is taken out here and put back into their results
           if (g == 0 && tile0 + kTile > least) {
             const int pos = tile0 + t;
-            bar_wait(&S.v_full[vs], static_cast<uint32_t>(it / C::kV) & 1, &S.failed);
+            bar_wait(&S.v_full[vs], (it / C::kV) & 1, &S.failed);
             __syncwarp();
             uint4* v = reinterpret_cast<uint4*>(S.v[vs] + t * kD);
             uint32_t nan = 0;
@@ -835,6 +865,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           bar_arrive(&S.p_full);
           if (k > 0) add_tile(it - 1);
         }
+        if (then) load_rows(nx.w);
         add_tile(it - 1);
 
         // ---- the unit's end: sums over the tokens of every row
@@ -881,9 +912,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
         } else if (rows > 0) {
           // a part of the unit: a record for the CTA that arrives last
-          const int64_t us = at - t0;
-          const int c0 = static_cast<int>(((us + 1) * ctas - 1) / total);
-          const int c1 = static_cast<int>(((us + w.nt) * ctas - 1) / total);
+          const int64_t first = sh.us + kUnitCost;  // of the unit's tiles
+          const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
+          const int c1 = static_cast<int>(((first + w.nt) * ctas - 1) / total);
           auto record = [&](int c) {  // of CTA c: its tail for the unit's first part, else its head
             return p.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * C::kGroups + g) * C::kPartial;
           };
@@ -898,27 +929,31 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             }
           }
           if (wq == 0 && own < kCols) rec[own] = run, rec[kCols + own] = lsum;
-          __threadfence();
-          group_sync<128>(g);
-          if (t == 0) {
-            int32_t* n = p.counters + c0 * C::kGroups + g;
-            const int arrived = atomicAdd(n, 1);
-            S.last[g] = arrived == c1 - c0;
-            if (arrived == c1 - c0) *n = 0;
-            __threadfence();
-          }
-          group_sync<128>(g);
-          if (S.last[g]) {
-            __threadfence();
-            // warp = every fourth row, lane = four channels; kJoin rows at a time, so
-            // that their loads are under way together
+          // Whether this CTA is the last of `parts` to arrive at a counter, whose
+          // records it then sees; the counter is left at zero.
+          auto arrive = [&](int32_t* counter, int parts) {
+            group_sync<128>(g);
+            if (t == 0) {
+              __threadfence();
+              const bool is_last = atomicAdd(counter, 1) == parts - 1;
+              if (is_last) *counter = 0;
+              __threadfence();
+              S.last[g] = is_last;
+            }
+            group_sync<128>(g);
+            return S.last[g] != 0;
+          };
+          // Joins the records of CTAs from, from + step .. to in this order: into the
+          // first of them, or into the output.  Warp = every fourth row, lane = four
+          // channels; kJoin rows at a time, so that their loads are under way together.
+          auto join = [&](int from, int step, int to, bool into_out) {
             constexpr int kJoin = kCols >= 16 ? 4 : 2;
             for (int c = wq; c < rows; c += 4 * kJoin) {
               float top[kJoin], sum[kJoin];
               float4 acc[kJoin];
 #pragma unroll
               for (int i = 0; i < kJoin; ++i) top[i] = -INFINITY;
-              for (int part = c0 + lane; part <= c1; part += 32)
+              for (int part = from + lane * step; part <= to; part += 32 * step)
 #pragma unroll
                 for (int i = 0; i < kJoin; ++i)
                   if (c + 4 * i < rows) top[i] = fmaxf(top[i], __ldcg(record(part) + c + 4 * i));
@@ -926,41 +961,53 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               for (int i = 0; i < kJoin; ++i) {
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], s));
-                if (top[i] == -INFINITY) top[i] = 0.f;
                 sum[i] = 0.f;
                 acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
               }
 #pragma unroll 4
-              for (int part = c0; part <= c1; ++part) {
+              for (int part = from; part <= to; part += step) {
                 const float* rp = record(part);
 #pragma unroll
                 for (int i = 0; i < kJoin; ++i) {
                   const int row = min(c + 4 * i, rows - 1);
-                  const float f = ex2(__ldcg(rp + row) - top[i]);
+                  const float f = ex2(__ldcg(rp + row) - (top[i] == -INFINITY ? 0.f : top[i]));
                   const float4 x = __ldcg(reinterpret_cast<const float4*>(rp + 2 * kCols + row * kD) + lane);
                   sum[i] += f * __ldcg(rp + kCols + row);
                   acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
                 }
               }
+              __syncwarp();  // this warp has read the rows that it may now write
 #pragma unroll
               for (int i = 0; i < kJoin; ++i) {
-                const int row = row0 + c + 4 * i;
-                if (c + 4 * i >= rows) continue;
-                const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
-                const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
-                                     y = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
-                *reinterpret_cast<uint2*>(p.out + (w.q0 + row / p.G) * p.out_stride +
-                                          (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + 4 * lane) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+                const int cc = c + 4 * i, row = row0 + cc;
+                if (cc >= rows) continue;
+                if (into_out) {
+                  const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+                  const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
+                                       y = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
+                  *reinterpret_cast<uint2*>(p.out + (w.q0 + row / p.G) * p.out_stride +
+                                            (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + 4 * lane) =
+                      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+                } else {
+                  float* rp = record(from);
+                  reinterpret_cast<float4*>(rp + 2 * kCols + cc * kD)[lane] = acc[i];
+                  if (lane == 0) rp[cc] = top[i], rp[kCols + cc] = sum[i];
+                }
               }
             }
+          };
+          // Up to kJoinFan parts are joined by the last CTA to arrive; of more, every
+          // kJoinFan neighbours by the last of them, and those by the last of all.
+          const int fan = (static_cast<int>(cta) - c0) / kJoinFan, from = c0 + fan * kJoinFan;
+          const int to = min(from + kJoinFan - 1, c1), fans = (c1 - c0) / kJoinFan + 1;
+          if (arrive(p.counters + (fan ? kCounters : 0) + from * C::kGroups + g, to - from + 1)) {
+            join(from, 1, to, fans == 1);
+            if (fans > 1 && arrive(p.counters + 2 * kCounters + c0 * C::kGroups + g, fans)) join(c0, kJoinFan, c1, true);
           }
         }
         group_sync<128>(g);  // row_scale and limit are read: the next unit may write them
-        left -= take;
-        at += take;
-        t0 = 0;
-        if (left > 0) next_unit<C>(p, w);
+        sh = nx;
+        more = then;
       }
     }
     // every product has ended before the accumulators are given back
