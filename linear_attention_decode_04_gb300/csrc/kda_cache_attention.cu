@@ -57,13 +57,13 @@ constexpr int kMaxCtas = 304;              // 2 x 152
 // What beginning and ending a unit costs, in tiles: the work is dealt out by
 // tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
 constexpr int kUnitCost = 4;
-constexpr int kJoinFan = 8;                // parts that one CTA joins
-constexpr int kCounters = 456;             // of each kind: CTAs x groups, at most
+constexpr int kCounters = 4 * 456;         // of each kind: CTAs x warps that join, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Params {
   int B, T, Hq, Hkv, G, bs, num_blocks, max_blocks;
+  uint32_t g_mul;  // ceil(2^32 / G), or 0 where that is not exact for every row
   float scale;  // sm_scale * log2(e)
   const uint16_t* q;
   int64_t q_stride;
@@ -91,7 +91,8 @@ struct Cfg {
   static constexpr int kV = GROUPS > 2 ? 4 : GROUPS > 1 ? 5 : 3;
   static constexpr int kNan = GROUPS > 1 ? 4 : 1;
   static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
-  static constexpr int kPartial = COLS * (kD + 2);       // floats of a partial record
+  static constexpr int kPartial = COLS * (32 + 2);       // floats of a warp's partial record: maxima, sums, 32 channels
+  static constexpr int kJoinFan = 8;              // parts that one warp joins
   static constexpr int kBlocks = COLS / 8;               // 8-column blocks of a group's tensor-memory loads
   static constexpr int kMine = COLS / 4;                 // rows that a thread holds elements of
 };
@@ -101,22 +102,19 @@ struct alignas(1024) Smem {
   uint8_t p[2][C::kN * kTile];            // leading part, remainder; [row' / 16][token][row' % 16]
   uint8_t q[2][C::kN * kD];               // likewise; core matrices of 8 rows x 16 bytes
   uint8_t k[C::kK][kTileBytes], v[C::kV][kTileBytes];
-  uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], sc_full[C::kV + 1];
+  uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], sc_full[C::kV];
   uint64_t s_full[2], o_full[2], p_full, q_full, done;
-  // k_scale, log2(v_scale), 1 / v_scale of a tile's blocks.  One deeper than the
-  // V ring: written before the tile's V place is waited for, when the tile
-  // kV + 1 before it has been weighed.
-  float4 sc[C::kV + 1][kMaxPages];
+  float4 sc[C::kV][kMaxPages];            // k_scale, log2(v_scale), 1 / v_scale of a tile's blocks; lives as V does
   float row_scale[C::kRows];
   int limit[C::kRows];
   float wmax[2][C::kGroups][4][C::kCols];
   float wsum[C::kGroups][4][C::kCols];
   int nan_at[C::kNan][kD];                // per unit and channel: first position that holds a NaN value
-  int64_t walk[4];                        // where this CTA's tiles start
-  int64_t scan[C::kThreads / 32];
+  int64_t total;                          // cost of all work, for the few places that need it again
+  int walk[4];                            // where this CTA's tiles start
+  int64_t scan[C::kThreads / 32], beyond[C::kThreads / 32];
   uint32_t tmem;
   int failed;
-  int last[C::kGroups];
 };
 // Per warp, broadcast to its lanes: the tile's maxima, and the two factors per
 // row of the tile and of the one before.
@@ -339,11 +337,15 @@ struct Walk {
   int n, len, q0;        // the sequence's queries, length, first query row
   int rts, nt;           // its row tiles; tiles of the current unit
 };
+// row / G for row < n * G
+__device__ __forceinline__ int token_of(const Params& p, int row) {
+  return p.g_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.g_mul)) : row / p.G;
+}
 template <class C>
 __device__ __forceinline__ int tiles_of(const Params& p, int n, int len, int rt) {
   const int rows = n * p.G;
   const int last = min(rows, (rt + 1) * C::kRows) - 1;  // last query row of the tile
-  const int limit = len - n + last / p.G + 1;    // tokens it sees
+  const int limit = len - n + token_of(p, last) + 1;    // tokens it sees
   return limit <= kTile ? 1 : (limit + kTile - 1) / kTile;
 }
 template <class C>
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   if (tid == 0) {
     for (int i = 0; i < C::kK; ++i) bar_init(&S.k_full[i], 1), bar_init(&S.k_empty[i], 1);
     for (int i = 0; i < C::kV; ++i) bar_init(&S.v_full[i], 1), bar_init(&S.v_empty[i], 1);
-    for (int i = 0; i <= C::kV; ++i) bar_init(&S.sc_full[i], 1);
+    for (int i = 0; i < C::kV; ++i) bar_init(&S.sc_full[i], 1);
     for (int i = 0; i < 2; ++i) bar_init(&S.s_full[i], 1), bar_init(&S.o_full[i], 1);
     bar_init(&S.p_full, 128 * C::kGroups);
     bar_init(&S.q_full, 128 * C::kGroups);
@@ -440,78 +442,87 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   // ---- where this CTA's tiles lie: total, then the sequence they start in
-  int64_t mine = 0;
+  int64_t mine = 0, beyond = 0;  // cost of sequence tid, and of those past the first kThreads
   bool bad = false;
   for (int i = tid; i < p.B; i += C::kThreads) {
-    mine += seq_cost<C>(p, i);
+    const int64_t c = seq_cost<C>(p, i);
+    if (i == tid) mine = c;
+    else beyond += c;
     const int a = p.cu[i], b = p.cu[i + 1];
     bad |= a < 0 || b < a || b > p.T;
   }
   if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, KDA_DEVERR_SEQLENS);
-  int64_t x = mine;
+  auto warp_scan = [&](int64_t v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (lane == 0) S.scan[warp] = x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  int64_t incl = warp_scan(mine);
+  if (p.B > C::kThreads) beyond = warp_scan(beyond);
+  if (lane == 31) S.scan[warp] = incl, S.beyond[warp] = beyond;
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = S.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t total = 0;
+  int64_t prior = 0, all = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) total += S.scan[w];
-  // one tile at least for each CTA that takes part, so that every CTA between
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w < warp) prior += S.scan[w];
+    all += S.scan[w];
+    total += S.beyond[w];
+  }
+  total += all;
+  if (tid == 0) S.total = total;
+  // one position at least for each CTA that takes part, so that every CTA between
   // a unit's first and last leaves a part of it
   const int64_t cta = blockIdx.x, ctas = max(min(static_cast<int64_t>(gridDim.x), total), int64_t{1});
   const int64_t begin = cta < ctas ? cta * total / ctas : 0, end = cta < ctas ? (cta + 1) * total / ctas : 0;
   if (begin < end) {
-    int64_t before = 0;
-    for (int base = 0; base < p.B; base += C::kThreads) {
+    auto look = [&](int i, int64_t from, int64_t cost) {  // whether the share begins in sequence i
+      if (cost == 0 || begin < from || begin >= from + cost) return;
+      Walk w;
+      w.seq = i;
+      load_seq<C>(p, w);
+      int64_t off = begin - from;
+      int c = tiles_of<C>(p, w.n, w.len, 0) + kUnitCost;
+      while (off >= static_cast<int64_t>(c) * p.Hkv) {
+        off -= static_cast<int64_t>(c) * p.Hkv;
+        c = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
+      }
+      S.walk[0] = i;
+      S.walk[1] = w.rt;
+      S.walk[2] = static_cast<int>(off) / c;
+      S.walk[3] = static_cast<int>(off) % c;
+    };
+    look(tid, prior + incl - mine, mine);
+    for (int base = C::kThreads; all <= begin; base += C::kThreads) {  // larger batches
       __syncthreads();
       const int i = base + tid;
-      const int64_t t = i < p.B ? seq_cost<C>(p, i) : 0;
-      int64_t incl = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
+      mine = i < p.B ? seq_cost<C>(p, i) : 0;
+      incl = warp_scan(mine);
       if (lane == 31) S.scan[warp] = incl;
       __syncthreads();
-      int64_t prior = before, all = 0;
+      prior = all;
 #pragma unroll
       for (int w = 0; w < C::kThreads / 32; ++w) {
         if (w < warp) prior += S.scan[w];
         all += S.scan[w];
       }
-      const int64_t from = prior + incl - t;
-      if (t > 0 && begin >= from && begin < from + t) {
-        Walk w;
-        w.seq = i;
-        load_seq<C>(p, w);
-        int64_t off = begin - from;
-        int cost = tiles_of<C>(p, w.n, w.len, 0) + kUnitCost;
-        while (off >= static_cast<int64_t>(cost) * p.Hkv) {
-          off -= static_cast<int64_t>(cost) * p.Hkv;
-          cost = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
-        }
-        S.walk[0] = i;
-        S.walk[1] = w.rt;
-        S.walk[2] = off / cost;
-        S.walk[3] = off % cost;
-      }
-      before += all;
-      if (before > begin) break;
+      look(i, prior + incl - mine, mine);
     }
     __syncthreads();
     Share sh;
     Walk& w = sh.w;
-    w.seq = static_cast<int>(S.walk[0]);
+    w.seq = S.walk[0];
     load_seq<C>(p, w);
-    w.rt = static_cast<int>(S.walk[1]);
-    w.h = static_cast<int>(S.walk[2]);
+    w.rt = S.walk[1];
+    w.h = S.walk[2];
     w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
-    sh.off = static_cast<int>(S.walk[3]);
+    sh.off = S.walk[3];
     sh.us = begin - sh.off;
     sh.left = end - begin;
     sh.tiles();
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         const int64_t pos = static_cast<int64_t>(t) * kTile + lane * rows;
         r.tok = p.bs > kTile ? static_cast<int>(pos % p.bs) : 0;
         const int last = min(w.n * p.G, (w.rt + 1) * C::kRows) - 1;
-        const int limit = w.len - w.n + last / p.G + 1;
+        const int limit = w.len - w.n + token_of(p, last) + 1;
         if (lane < ppt && pos < limit) {
           const int64_t e = pos / p.bs;
           int b = -1;
@@ -565,15 +576,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       for (uint32_t it = 0; a.valid; ++it) {
         const float2 sb = scales(b);
         const Ref c = take();
-        const uint32_t ks = it % C::kK, vs = it % C::kV, cs = it % (C::kV + 1), kr = it / C::kK, vr = it / C::kV;
+        const uint32_t ks = it % C::kK, vs = it % C::kV, kr = it / C::kK, vr = it / C::kV;
         if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
-        if (lane < ppt) {
-          const float sv = fmaxf(sa.y, 0x1p-64f);
-          S.sc[cs][lane] = a.block < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                       : make_float4(sa.x, log2f(sv), 1.f / sv, 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&S.sc_full[cs]), bar_expect(&S.k_full[ks], kTileBytes);
+        if (lane == 0) bar_expect(&S.k_full[ks], kTileBytes);
         __syncwarp();
         if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
         ++k_sent;
@@ -582,6 +587,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         __syncwarp();
         if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
         ++v_sent;
+        if (lane < ppt) {
+          const float sv = fmaxf(sa.y, 0x1p-64f);
+          S.sc[vs][lane] = a.block < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                       : make_float4(sa.x, log2f(sv), 1.f / sv, 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&S.sc_full[vs]);
         a = b, b = c, sa = sb;
       }
       if (!ok) {  // nothing may land in shared memory after the CTA is gone
@@ -659,9 +671,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         for (int i = 0; i < kBlocks; ++i) {
           const int c = 8 * i + (t >> 4), row = row0 + c;
           v[i] = make_uint4(0, 0, 0, 0);
-          if (c < rows)
-            v[i] = *reinterpret_cast<const uint4*>(p.q + (u.q0 + row / p.G) * p.q_stride +
-                                                   (static_cast<int64_t>(u.h) * p.G + row % p.G) * kD + (t & 15) * 8);
+          if (c < rows) {
+            const int tok = token_of(p, row);
+            v[i] = *reinterpret_cast<const uint4*>(p.q + (u.q0 + tok) * p.q_stride +
+                                                   (static_cast<int64_t>(u.h) * p.G + row - tok * p.G) * kD + (t & 15) * 8);
+          }
         }
       };
       if (more) load_rows(w);
@@ -714,7 +728,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             if ((t & 15) == 0) {
               S.row_scale[col0 + c] = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale
                                              : __uint_as_float(0x7fc00000u);
-              S.limit[col0 + c] = c < rows ? ctx + (row0 + c) / p.G + 1 : 0;
+              S.limit[col0 + c] = c < rows ? ctx + token_of(p, row0 + c) + 1 : 0;
             }
           }
         }
@@ -722,9 +736,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         fence_async();
         bar_arrive(&S.q_full);
         group_sync<128>(g);
-        const int first_limit = ctx + row0 / p.G + 1;  // of the group's rows, the one that sees least
+        const int first_limit = ctx + token_of(p, row0) + 1;  // of the group's rows, the one that sees least
         const int tile_rows = min(w.n * p.G, (w.rt + 1) * C::kRows);
-        const int least = ctx + (w.rt * C::kRows) / p.G + 1, most = ctx + (tile_rows - 1) / p.G + 1;  // of all groups
+        const int least = ctx + token_of(p, w.rt * C::kRows) + 1, most = ctx + token_of(p, tile_rows - 1) + 1;  // of all groups
         float run = -INFINITY;  // running maximum of row `own`
 #pragma unroll
         for (int c = 0; c < kMine; ++c) {
@@ -733,9 +747,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j][c] = 0.f;
         }
-
-        Share nx = sh;
-        const bool then = next_share<C>(p, nx);
 
         auto add_tile = [&](uint32_t i) {  // the products of tile i join the sums
           bar_wait(&S.o_full[i & 1], (i >> 1) & 1, &S.failed);
@@ -756,16 +767,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         };
 
         for (int k = 0; k < take; ++k, ++it) {
-          const uint32_t cs = it % (C::kV + 1), vs = it % C::kV, buf = it & 1;
+          const uint32_t vs = it % C::kV, buf = it & 1;
           const int tile0 = (t0 + k) * kTile;
           bar_wait(&S.s_full[buf], (it >> 1) & 1, &S.failed);
-          bar_wait(&S.sc_full[cs], (it / (C::kV + 1)) & 1, &S.failed);
+          bar_wait(&S.sc_full[vs], (it / C::kV) & 1, &S.failed);
           tc_after();
           float z[4][kMine];
           tm_ld<kBlocks>(lanes + buf * kN, z);
           // a block is at least 16 tokens: lanes 0 .. 15 lie in one, 16 .. 31 in one
-          const float4 sc0 = S.sc[cs][page0];
-          const float4 sc1 = S.sc[cs][page1];
+          const float4 sc0 = S.sc[vs][page0];
+          const float4 sc1 = S.sc[vs][page1];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -852,10 +863,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             uint32_t nan = 0;
             if (pos >= most) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < 8; ++i) v[i ^ (t & 7)] = make_uint4(0, 0, 0, 0);  // 8 threads, 8 different banks
             } else if (pos >= least) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) nan |= nan_bytes(v[i].x) | nan_bytes(v[i].y) | nan_bytes(v[i].z) | nan_bytes(v[i].w);
+              for (int i = 0; i < 8; ++i) {
+                const uint4 u = v[i ^ (t & 7)];
+                nan |= nan_bytes(u.x) | nan_bytes(u.y) | nan_bytes(u.z) | nan_bytes(u.w);
+              }
             }
             if (__any_sync(0xffffffffu, nan != 0)) take_out_nan(S.v[vs] + t * kD, nan != 0, t, pos, S.nan_at[unit & (C::kNan - 1)]);
           }
@@ -865,6 +879,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           bar_arrive(&S.p_full);
           if (k > 0) add_tile(it - 1);
         }
+        Share nx = sh;
+        const bool then = next_share<C>(p, nx);
         if (then) load_rows(nx.w);
         add_tile(it - 1);
 
@@ -901,9 +917,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             const int c = row_of_column<kBlocks>(b, lane) + odd, row = row0 + c;
+            const int tok = token_of(p, row);
             const float f = bc.mt[c];
-            uint16_t* out = p.out + (w.q0 + row / p.G) * p.out_stride +
-                            (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + d0;
+            uint16_t* out = p.out + (w.q0 + tok) * p.out_stride +
+                            (static_cast<int64_t>(w.h) * p.G + row - tok * p.G) * kD + d0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 x = two_channels(j, b);
@@ -912,97 +929,96 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
         } else if (rows > 0) {
           // a part of the unit: a record for the CTA that arrives last
-          const int64_t first = sh.us + kUnitCost;  // of the unit's tiles
-          const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
-          const int c1 = static_cast<int>(((first + w.nt) * ctas - 1) / total);
+          const int64_t first = sh.us + kUnitCost, cost = S.total;  // first: of the unit's tiles
+          const int64_t parties = min(static_cast<int64_t>(gridDim.x), cost);
+          const int c0 = static_cast<int>(((first + 1) * parties - 1) / cost);
+          const int c1 = static_cast<int>(((first + w.nt) * parties - 1) / cost);
+          // Records belong to a warp, its 32 channels of all rows: the warps of a group
+          // join apart from one another, and none waits for the rest of its CTA.
           auto record = [&](int c) {  // of CTA c: its tail for the unit's first part, else its head
-            return p.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * C::kGroups + g) * C::kPartial;
+            return p.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * 4 * C::kGroups + 4 * g + wq) * C::kPartial;
           };
-          float* rec = record(static_cast<int>(cta));
+          float* rec = record(static_cast<int>(blockIdx.x));
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             const int c = row_of_column<kBlocks>(b, lane) + odd;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 x = two_channels(j, b);
-              if (c < rows) *reinterpret_cast<float2*>(rec + 2 * kCols + c * kD + d0 + 8 * j) = x;
+              if (c < rows) *reinterpret_cast<float2*>(rec + 2 * kCols + c * 32 + (r8 & ~1) + 8 * j) = x;
             }
           }
-          if (wq == 0 && own < kCols) rec[own] = run, rec[kCols + own] = lsum;
-          // Whether this CTA is the last of `parts` to arrive at a counter, whose
+          if (own < kCols) rec[own] = run, rec[kCols + own] = lsum;
+          // Joins the records of CTAs from, from + step .. to in this order, into the
+          // first of them or into the output: 8 lanes per row, four channels each.
+          auto join = [&](int from, int step, int to, bool into_out) {
+            const int sub = lane >> 3, l4 = lane & 7;
+            float top[kMine], sum[kMine];
+            float4 acc[kMine];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) top[i] = -INFINITY, sum[i] = 0.f, acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int part = from; part <= to; part += step) {
+              const float* rp = record(part);
+#pragma unroll
+              for (int i = 0; i < kMine; ++i) top[i] = fmaxf(top[i], __ldcg(rp + sub + 4 * i));
+            }
+#pragma unroll 2
+            for (int part = from; part <= to; part += step) {
+              const float* rp = record(part);
+#pragma unroll
+              for (int i = 0; i < kMine; ++i) {
+                const int row = sub + 4 * i;
+                const float f = ex2(__ldcg(rp + row) - (top[i] == -INFINITY ? 0.f : top[i]));
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(rp + 2 * kCols + row * 32) + l4);
+                sum[i] += f * __ldcg(rp + kCols + row);
+                acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
+              }
+            }
+            __syncwarp();  // the warp has read the record that it may now write
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+              const int cc = sub + 4 * i;
+              if (cc >= rows) continue;
+              if (into_out) {
+                const int row = row0 + cc, tok = token_of(p, row);
+                const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+                const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
+                                     y = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
+                *reinterpret_cast<uint2*>(p.out + (w.q0 + tok) * p.out_stride +
+                                          (static_cast<int64_t>(w.h) * p.G + row - tok * p.G) * kD + 32 * wq + 4 * l4) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+              } else {
+                float* rp = record(from);
+                reinterpret_cast<float4*>(rp + 2 * kCols + cc * 32)[l4] = acc[i];
+                if (l4 == 0) rp[cc] = top[i], rp[kCols + cc] = sum[i];
+              }
+            }
+          };
+          // Whether this warp is the last of `parts` to arrive at a counter, whose
           // records it then sees; the counter is left at zero.
           auto arrive = [&](int32_t* counter, int parts) {
-            group_sync<128>(g);
-            if (t == 0) {
-              __threadfence();
-              const bool is_last = atomicAdd(counter, 1) == parts - 1;
-              if (is_last) *counter = 0;
-              __threadfence();
-              S.last[g] = is_last;
+            __syncwarp();
+            int before = 0;
+            if (lane == 0) {
+              asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+              if (before == parts - 1) *counter = 0;
             }
-            group_sync<128>(g);
-            return S.last[g] != 0;
+            return __shfl_sync(0xffffffffu, before, 0) == parts - 1;
           };
-          // Joins the records of CTAs from, from + step .. to in this order: into the
-          // first of them, or into the output.  Warp = every fourth row, lane = four
-          // channels; kJoin rows at a time, so that their loads are under way together.
-          auto join = [&](int from, int step, int to, bool into_out) {
-            constexpr int kJoin = kCols >= 16 ? 4 : 2;
-            for (int c = wq; c < rows; c += 4 * kJoin) {
-              float top[kJoin], sum[kJoin];
-              float4 acc[kJoin];
-#pragma unroll
-              for (int i = 0; i < kJoin; ++i) top[i] = -INFINITY;
-              for (int part = from + lane * step; part <= to; part += 32 * step)
-#pragma unroll
-                for (int i = 0; i < kJoin; ++i)
-                  if (c + 4 * i < rows) top[i] = fmaxf(top[i], __ldcg(record(part) + c + 4 * i));
-#pragma unroll
-              for (int i = 0; i < kJoin; ++i) {
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], s));
-                sum[i] = 0.f;
-                acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              }
-#pragma unroll 4
-              for (int part = from; part <= to; part += step) {
-                const float* rp = record(part);
-#pragma unroll
-                for (int i = 0; i < kJoin; ++i) {
-                  const int row = min(c + 4 * i, rows - 1);
-                  const float f = ex2(__ldcg(rp + row) - (top[i] == -INFINITY ? 0.f : top[i]));
-                  const float4 x = __ldcg(reinterpret_cast<const float4*>(rp + 2 * kCols + row * kD) + lane);
-                  sum[i] += f * __ldcg(rp + kCols + row);
-                  acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
-                }
-              }
-              __syncwarp();  // this warp has read the rows that it may now write
-#pragma unroll
-              for (int i = 0; i < kJoin; ++i) {
-                const int cc = c + 4 * i, row = row0 + cc;
-                if (cc >= rows) continue;
-                if (into_out) {
-                  const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
-                  const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
-                                       y = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
-                  *reinterpret_cast<uint2*>(p.out + (w.q0 + row / p.G) * p.out_stride +
-                                            (static_cast<int64_t>(w.h) * p.G + row % p.G) * kD + 4 * lane) =
-                      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-                } else {
-                  float* rp = record(from);
-                  reinterpret_cast<float4*>(rp + 2 * kCols + cc * kD)[lane] = acc[i];
-                  if (lane == 0) rp[cc] = top[i], rp[kCols + cc] = sum[i];
-                }
-              }
-            }
-          };
-          // Up to kJoinFan parts are joined by the last CTA to arrive; of more, every
-          // kJoinFan neighbours by the last of them, and those by the last of all.
-          const int fan = (static_cast<int>(cta) - c0) / kJoinFan, from = c0 + fan * kJoinFan;
-          const int to = min(from + kJoinFan - 1, c1), fans = (c1 - c0) / kJoinFan + 1;
-          if (arrive(p.counters + (fan ? kCounters : 0) + from * C::kGroups + g, to - from + 1)) {
-            join(from, 1, to, fans == 1);
-            if (fans > 1 && arrive(p.counters + 2 * kCounters + c0 * C::kGroups + g, fans)) join(c0, kJoinFan, c1, true);
+          // Up to kJoinFan parts are joined by the last to arrive; of more, every fan
+          // of neighbours by the last of them, and those by the last of all.  (One
+          // place for both: code that runs once per unit costs instruction fetches.)
+          const int fan = (static_cast<int>(blockIdx.x) - c0) / C::kJoinFan, fans = (c1 - c0) / C::kJoinFan + 1;
+          int from = c0 + fan * C::kJoinFan, step = 1, to = min(from + C::kJoinFan - 1, c1);
+          int32_t* counter = p.counters + (fan ? kCounters : 0) + (from * C::kGroups + g) * 4 + wq;
+#pragma unroll 1
+          for (int n = to - from + 1; arrive(counter, n); n = fans) {
+            const bool all_parts = fans == 1 || step > 1;
+            join(from, step, to, all_parts);
+            if (all_parts) break;
+            from = c0, step = C::kJoinFan, to = c1;
+            counter = p.counters + 2 * kCounters + (c0 * C::kGroups + g) * 4 + wq;
           }
         }
         group_sync<128>(g);  // row_scale and limit are read: the next unit may write them
@@ -1091,7 +1107,7 @@ auto with_variant(int64_t rows, F f) {
 
 template <class C>
 constexpr int64_t partial_bytes() {
-  return 2LL * (kMaxCtas / 2) * C::kCtasPerSm * C::kGroups * C::kPartial * 4;
+  return 2LL * (kMaxCtas / 2) * C::kCtasPerSm * 4 * C::kGroups * C::kPartial * static_cast<int64_t>(sizeof(float));
 }
 
 }  // namespace
@@ -1156,6 +1172,8 @@ extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream)
   }
   Params p{};
   p.B = a->B, p.T = a->T, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.bs = bs;
+  // exact below 2^32 / G, and a row is below T * G
+  p.g_mul = p.G > 1 && static_cast<int64_t>(a->T) * p.G * p.G < (1LL << 32) ? static_cast<uint32_t>(((1ULL << 32) + p.G - 1) / p.G) : 0;
   p.num_blocks = a->num_blocks, p.max_blocks = a->max_blocks;
   p.scale = (a->sm_scale == 0.f ? 0.08838834764831845f : a->sm_scale) * kLog2e;
   p.q = a->q, p.q_stride = a->q_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;

@@ -11,7 +11,9 @@
 // never read.
 //
 // The weights are 64-bit integers in units of 2^-60, so sums are exact and
-// the token does not depend on how the row was split.
+// the token does not depend on how the row was split.  They are made from the
+// floats' bits with a 64-bit shift: the conversion instruction is several
+// times slower and would bound the kernel.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -35,8 +37,15 @@ struct Params {
   int32_t* err;
 };
 
+// floor(min(max(x, 0), 1) 2^60), NaN as 0.  With the mantissa at the top of 64
+// bits, x = m 2^(e - 190) for exponent field e, so the value is m >> (130 - e);
+// x <= 1 has e <= 127, and below 2^-60 nothing is left.
 __device__ __forceinline__ uint64_t fixed60(float x) {
-  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
+  const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
+  const uint32_t e = u >> 23;
+  const uint64_t m = static_cast<uint64_t>((u << 8) | 0x80000000u) << 32;
+  const uint32_t shift = 130u - e;
+  return shift < 64 ? m >> shift : 0;
 }
 
 // What a row's weights are made of: w = max(P - Q, 0) with Q from the draft's
@@ -70,8 +79,8 @@ __device__ __forceinline__ void cluster_barrier() {
 
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cluster, int part) {
-  __shared__ uint64_t cta_rest[kMaxCluster], cta_full[kMaxCluster];  // every CTA's sums, in every CTA
-  __shared__ uint64_t warp_rest[kWarps], warp_full[kWarps];
+  __shared__ uint64_t cta_sum[2][kMaxCluster];  // every CTA's sum, in every CTA; of the rest, of the row itself
+  __shared__ uint64_t warp_sums[kWarps], found[kWarps];
   __shared__ int verdict[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = blockIdx.x / cluster, rank = blockIdx.x - n * cluster;
@@ -121,50 +130,46 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cl
   const int64_t lo64 = static_cast<int64_t>(rank * kWarps + warp) * part;
   const int lo = static_cast<int>(lo64 < p.V ? lo64 : p.V);
   const int hi = static_cast<int>(lo64 + part < p.V ? lo64 + part : p.V);
-  uint64_t rest = 0, full = 0;
-#pragma unroll 4
-  for (int i = lo + 4 * lane; i < hi; i += 128) {
-    float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<VEC>(r.p, i, p.V, a);
-    if (r.q) load4<VEC>(r.q, i, p.V, b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rest += weight(r, a[j], b[j], i + j);
-      full += fixed60(a[j]);
-    }
-  }
-  rest = warp_sum(rest);
-  full = warp_sum(full);
-  if (lane == 0) warp_rest[warp] = rest, warp_full[warp] = full;
-  __syncthreads();
-  if (cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  if (warp == 0) {
-    const uint64_t a = warp_sum(lane < kWarps ? warp_rest[lane] : 0), b = warp_sum(lane < kWarps ? warp_full[lane] : 0);
-    if (cluster == 1) {
-      if (lane == 0) cta_rest[0] = a, cta_full[0] = b;
-    } else if (lane < cluster) {  // lane c tells CTA c
-      const uint32_t ra = static_cast<uint32_t>(__cvta_generic_to_shared(&cta_rest[rank])),
-                     fa = static_cast<uint32_t>(__cvta_generic_to_shared(&cta_full[rank]));
-      asm volatile(
-          "{\n\t.reg .b32 x;\n\tmapa.shared::cluster.u32 x, %0, %2;\n\tst.shared::cluster.u64 [x], %3;\n\t"
-          "mapa.shared::cluster.u32 x, %1, %2;\n\tst.shared::cluster.u64 [x], %4;\n\t}" ::"r"(ra), "r"(fa),
-          "r"(lane), "l"(a), "l"(b)
-          : "memory");
-    }
-  }
-  if (cluster > 1) cluster_barrier();  // no CTA reads another's memory behind this
-  else __syncthreads();
-  uint64_t total = 0;
-  for (int c = 0; c < cluster; ++c) total += cta_rest[c];
-  const bool fall_back = total == 0;
-  if (fall_back) {
-    for (int c = 0; c < cluster; ++c) total += cta_full[c];
-    r.q = nullptr, r.out = -1;
-  }
-  const uint64_t* cta_sum = fall_back ? cta_full : cta_rest;
-  const uint64_t* warp_part = fall_back ? warp_full : warp_rest;
   const float u = fmaxf(p.sample_u[n], 0.f);
   const uint64_t u31 = u < 1.f ? static_cast<uint64_t>(u * 0x1p31f) : 0x7fffffffu;
+  uint64_t total = 0, before = 0;  // of the whole row; ahead of this CTA
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {  // the second round where the rest has no mass: the row itself
+    uint64_t sum = 0;
+#pragma unroll 4
+    for (int i = lo + 4 * lane; i < hi; i += 128) {
+      float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+      load4<VEC>(r.p, i, p.V, a);
+      if (r.q) load4<VEC>(r.q, i, p.V, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += weight(r, a[j], b[j], i + j);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) warp_sums[warp] = sum;
+    __syncthreads();
+    if (cluster > 1 && round == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (warp == 0) {
+      const uint64_t s = warp_sum(lane < kWarps ? warp_sums[lane] : 0);
+      if (cluster == 1) {
+        if (lane == 0) cta_sum[round][0] = s;
+      } else if (lane < cluster) {  // lane c tells CTA c
+        asm volatile(
+            "{\n\t.reg .b32 x;\n\tmapa.shared::cluster.u32 x, %0, %1;\n\tst.shared::cluster.u64 [x], %2;\n\t}" ::"r"(
+                static_cast<uint32_t>(__cvta_generic_to_shared(&cta_sum[round][rank]))),
+            "r"(lane), "l"(s)
+            : "memory");
+      }
+    }
+    if (cluster > 1) cluster_barrier();  // no CTA reads another's memory behind this
+    else __syncthreads();
+    total = before = 0;
+    for (int c = 0; c < cluster; ++c) {
+      total += cta_sum[round][c];
+      if (c < rank) before += cta_sum[round][c];
+    }
+    if (total != 0 || !refused) break;
+    r.q = nullptr, r.out = -1;
+  }
   const uint64_t goal = __umul64hi(u31 << 33, total);  // floor(u31 total / 2^31)
   if (rank == 0) {
     if (tid < p.T && tid != k) p.tokens[static_cast<int64_t>(n) * p.T + tid] = tid < k ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + tid] : -1;
@@ -174,38 +179,51 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cl
       if (total == 0) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;
     }
   }
-  if (total == 0) return;
-  uint64_t before = 0;
-  for (int c = 0; c < rank; ++c) before += cta_sum[c];
-  for (int w = 0; w < warp; ++w) before += warp_part[w];
-  if (goal < before || goal >= before + warp_part[warp]) return;  // not this warp's part
-  for (int i0 = lo; i0 < hi; i0 += 128) {
-    const int i = i0 + 4 * lane;
-    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i < hi) {
-      load4<VEC>(r.p, i, p.V, a);
-      if (r.q) load4<VEC>(r.q, i, p.V, b);
+  // the warp in whose part the inversion ends
+  int owner = -1;
+  for (int w = 0; w < kWarps; ++w) {
+    if (owner < 0 && goal >= before) {
+      if (goal < before + warp_sums[w]) owner = w;
+      else before += warp_sums[w];
     }
-    uint64_t w[4], s = 0;
+  }
+  if (total == 0 || owner < 0) return;  // not this CTA's part
+  // That part once more, with all threads: each takes `each` tokens in a row.
+  const int64_t begin = static_cast<int64_t>(rank * kWarps + owner) * part;
+  const int each = (part + 4 * kThreads - 1) / (4 * kThreads) * 4;
+  const int last = static_cast<int>(begin + part < p.V ? begin + part : p.V);
+  const int64_t from64 = begin + static_cast<int64_t>(tid) * each;
+  const int from = static_cast<int>(from64 < last ? from64 : last), to = min(from + each, last);
+  uint64_t mine = 0;
+#pragma unroll 2
+  for (int i = from; i < to; i += 4) {
+    float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+    load4<VEC>(r.p, i, p.V, a);
+    if (r.q) load4<VEC>(r.q, i, p.V, b);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += w[j] = weight(r, a[j], b[j], i + j);
-    uint64_t x = s;
+    for (int j = 0; j < 4; ++j) mine += i + j < to ? weight(r, a[j], b[j], i + j) : 0;
+  }
+  uint64_t x = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) found[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += found[w];
+  before += x - mine;
+  if (goal < before || goal >= before + mine) return;
+  for (int i = from; i < to; i += 4) {  // one thread is left
+    float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+    load4<VEC>(r.p, i, p.V, a);
+    if (r.q) load4<VEC>(r.q, i, p.V, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t w = i + j < to ? weight(r, a[j], b[j], i + j) : 0;
+      if (w > 0 && goal >= before && goal < before + w) p.tokens[static_cast<int64_t>(n) * p.T + k] = i + j;
+      before += w;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + x > goal);
-    if (past) {
-      if (lane == __ffs(past) - 1) {
-        uint64_t c = before + x - s;
-        int j = 0;
-        while (j < 3 && (c += w[j]) <= goal) ++j;
-        p.tokens[static_cast<int64_t>(n) * p.T + k] = i + j;
-      }
-      return;
-    }
-    before += __shfl_sync(0xffffffffu, x, 31);
   }
 }
 
