@@ -22,12 +22,13 @@
  * src_slot is <= 0 is padding: tokens -1, num_accepted 0, next_slot 0, and
  * its rows are not read.
  *
- * The inversion is exact and independent of summation order: probabilities
- * enter in units of 2^-60, P = floor(min(max(p, 0), 1) * 2^60) (NaN counts
- * as 0), weights are integers, and x is the lowest index whose inclusive
- * running sum exceeds floor(floor(sample_u * 2^31) * total / 2^31).
- * Probabilities of a row sum to about 1 (at most 7); sample_u is taken into
- * [0, 1 - 2^-31], NaN as 0.  Where a row has no mass at all x is V - 1.
+ * The inversion does not depend on summation order: probabilities are taken
+ * into [0, 1] (NaN counts as 0), the weights max(p - q, 0), or p, are integers
+ * in units of 2^-60, exact wherever p and q are 0 or at least 2^-37 and else off by at
+ * most 3 units, and x is the lowest index whose inclusive running sum exceeds
+ * floor(floor(sample_u * 2^31) * total / 2^31).  Probabilities of a row sum
+ * to about 1 (at most 7); sample_u is taken into [0, 1 - 2^-31], NaN as 0.
+ * Where a row has no mass at all x is V - 1.
  */
 #ifndef KDA_VERIFY_H
 #define KDA_VERIFY_H

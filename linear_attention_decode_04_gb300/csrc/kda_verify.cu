@@ -3,17 +3,20 @@
 //
 // HBM bound on large batches (one row of target probabilities per sequence,
 // and one of the draft's where a draft was refused), latency bound on small
-// ones.  One cluster of CTAs per sequence: every CTA works out for itself
-// which draft is the first refused (a few gathers), sums its part of that one
-// row, and the CTAs exchange their sums through distributed shared memory;
-// the CTA, then the warp, in whose part the inversion ends reads that part
-// once more (out of L2) to find the token.  Rows that no sample needs are
-// never read.
+// ones.  One cluster of CTAs per sequence: every CTA works out for itself which
+// draft is the first refused (a few gathers), sums its part of that one row,
+// and the CTAs exchange their sums through distributed shared memory; the CTA
+// and warp in whose part the inversion ends have that part read once more (out
+// of L2) to find the token.  Rows that no sample needs are never read.
 //
-// The weights are 64-bit integers in units of 2^-60, so sums are exact and
-// the token does not depend on how the row was split.  They are made from the
-// floats' bits with a 64-bit shift: the conversion instruction is several
-// times slower and would bound the kernel.
+// The weights are integers in units of 2^-60, so sums are exact and the token
+// does not depend on how the row was split.  Making such integers from floats
+// with shifts or conversions bounds the kernel (the integer and conversion
+// pipes are the slow ones: 52 us where the loads alone took 37); instead every
+// weight is cut, with additions of a large constant and without error, into
+// multiples of 2^-20, 2^-41 and 2^-60, and each kind is summed in fp32 where
+// such sums are exact: the first because a row's mass is below 2^3, the
+// others for eight tokens at a time.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,8 +25,6 @@
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
 struct Params {
@@ -37,16 +38,40 @@ struct Params {
   int32_t* err;
 };
 
-// floor(min(max(x, 0), 1) 2^60), NaN as 0.  With the mantissa at the top of 64
-// bits, x = m 2^(e - 190) for exponent field e, so the value is m >> (130 - e);
-// x <= 1 has e <= 127, and below 2^-60 nothing is left.
-__device__ __forceinline__ uint64_t fixed60(float x) {
-  const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
-  const uint32_t e = u >> 23;
-  const uint64_t m = static_cast<uint64_t>((u << 8) | 0x80000000u) << 32;
-  const uint32_t shift = 130u - e;
-  return shift < 64 ? m >> shift : 0;
+__device__ __forceinline__ float clamp01(float x) { return __saturatef(x); }  // NaN as 0
+// x rounded to a multiple of 2^(E - 23), for |x| < 2^(E - 1): 1.5 * 2^E has its
+// last bit there.
+template <int E>
+__device__ __forceinline__ float multiple(float x) {
+  constexpr float c = E == 3 ? 12.f : E == -18 ? 0x1.8p-18f : 0x1.8p-37f;
+  static_assert(E == 3 || E == -18 || E == -37, "one of the three units");
+  return __fsub_rn(__fadd_rn(x, c), c);
 }
+// Sums of weights: `a` in multiples of 2^-20, b of 2^-41, c of 2^-60.
+struct Parts {
+  float a = 0.f, b = 0.f, c = 0.f;
+  __device__ __forceinline__ void low(float x) {  // |x| < 2^-19
+    const float h = multiple<-18>(x);
+    b += h;
+    c += multiple<-37>(x - h);
+  }
+  __device__ __forceinline__ void add(float x) {  // 0 <= x <= 1
+    const float h = multiple<3>(x);
+    a += h;
+    low(x - h);
+  }
+  // max(x - y, 0) for x, y in [0, 1]: d is the difference, e what its rounding left out
+  __device__ __forceinline__ void add_difference(float x, float y) {
+    const float z = fmaxf(x, y), d = z - y, e = (z - d) - y;
+    add(d);
+    low(e);
+  }
+  __device__ __forceinline__ uint64_t low_sum() const {
+    return (static_cast<uint64_t>(static_cast<int64_t>(__float2int_rn(b * 0x1p41f))) << 19) +
+           static_cast<uint64_t>(static_cast<int64_t>(__float2int_rn(c * 0x1p60f)));
+  }
+  __device__ __forceinline__ uint64_t sum() const { return (static_cast<uint64_t>(__float2uint_rn(a * 0x1p20f)) << 40) + low_sum(); }
+};
 
 // What a row's weights are made of: w = max(P - Q, 0) with Q from the draft's
 // row, or P with the refused token taken out, or P.
@@ -65,8 +90,9 @@ __device__ __forceinline__ void load4(const float* row, int i, int V, float (&x)
   }
 }
 __device__ __forceinline__ uint64_t weight(const Row& r, float p, float q, int i) {
-  const uint64_t P = fixed60(p), Q = fixed60(q);
-  return i == r.out ? 0 : P > Q ? P - Q : 0;
+  Parts w;
+  if (i != r.out) w.add_difference(clamp01(p), clamp01(q));
+  return w.sum();
 }
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
@@ -77,73 +103,194 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cluster, int part) {
+// Sum of this lane's share of the weights of tokens lo .. hi - 1 (lo a
+// multiple of 4), which the warp goes through four tokens a lane at a time.  DEPTH
+// loads per row are always on their way while the ones before are worked on:
+// the arithmetic takes about as long as the row takes to come.  The last
+// hi % 4 tokens come separately.
+template <bool VEC, int DEPTH>
+__device__ __forceinline__ uint64_t sum_weights(const Row& r, int lo, int hi, int first) {
+  constexpr int stride = 128;
+  const int full = lo + ((hi - lo) & ~3);
+  auto four = [&](const float* row, int i) {  // nothing past the end; tokens there weigh 0
+    if (i >= full) return make_float4(0.f, 0.f, 0.f, 0.f);
+    if (VEC) return *reinterpret_cast<const float4*>(row + i);
+    return make_float4(row[i], row[i + 1], row[i + 2], row[i + 3]);
+  };
+  uint64_t sum = 0;  // of the lower parts
+  float high = 0.f;
+  int i = lo + 4 * first;
+  float4 a[DEPTH], b[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) a[d] = four(r.p, i + d * stride);
+  if (r.q) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) b[d] = four(r.q, i + d * stride);
+    for (; i < full; i += DEPTH * stride) {
+      Parts w;
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const float4 x = a[d], y = b[d];
+        a[d] = four(r.p, i + (DEPTH + d) * stride);
+        b[d] = four(r.q, i + (DEPTH + d) * stride);
+        w.add_difference(clamp01(x.x), clamp01(y.x));
+        w.add_difference(clamp01(x.y), clamp01(y.y));
+        w.add_difference(clamp01(x.z), clamp01(y.z));
+        w.add_difference(clamp01(x.w), clamp01(y.w));
+        if (d & 1 || d + 1 == DEPTH) sum += w.low_sum(), w.b = w.c = 0.f;  // of eight tokens
+      }
+      high += w.a;
+    }
+  } else {
+    for (; i < full; i += DEPTH * stride) {
+      Parts w;
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const float4 x = a[d];
+        a[d] = four(r.p, i + (DEPTH + d) * stride);
+        w.add(clamp01(x.x));
+        w.add(clamp01(x.y));
+        w.add(clamp01(x.z));
+        w.add(clamp01(x.w));
+        if (d & 1 || d + 1 == DEPTH) sum += w.low_sum(), w.b = w.c = 0.f;
+      }
+      high += w.a;
+    }
+    if (first == 0 && r.out >= lo && r.out < full) {
+      Parts w;
+      w.add(clamp01(r.p[r.out]));
+      sum -= w.sum();
+    }
+  }
+  sum += static_cast<uint64_t>(__float2uint_rn(high * 0x1p20f)) << 40;
+  if (first < hi - full) sum += weight(r, r.p[full + first], r.q ? r.q[full + first] : 0.f, full + first);
+  return sum;
+}
+// All threads of the CTA: the token among begin .. end - 1 (`before` is the
+// weight ahead of them) at which the running sum passes `goal`, four tokens a
+// thread and a block of 4 * THREADS at a time.
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void search(const Row& r, int begin, int end, uint64_t before, uint64_t goal, int V,
+                                       int32_t* token) {
+  __shared__ uint64_t found[THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t block = begin; block < end; block += 4 * THREADS) {
+    const int i = static_cast<int>(min(block + 4 * tid, static_cast<int64_t>(end)));
+    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i < end) {
+      load4<VEC>(r.p, i, V, a);
+      if (r.q) load4<VEC>(r.q, i, V, b);
+    }
+    uint64_t w[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += w[j] = i + j < end ? weight(r, a[j], b[j], i + j) : 0;
+    uint64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) found[warp] = x;
+    __syncthreads();
+    uint64_t here = before;
+#pragma unroll
+    for (int u = 0; u < THREADS / 32; ++u) {
+      if (u < warp) here += found[u];
+      before += found[u];
+    }
+    here += x - mine;
+    if (goal >= here && goal < here + mine) {
+      int j = 0;
+      while (j < 3 && goal >= here + w[j]) here += w[j++];
+      *token = i + j;
+    }
+    if (goal < before) return;
+  }
+}
+// How many drafts of sequence n stand, and whether the next was refused (warp 0).
+__device__ __forceinline__ void judge(const Params& p, int n, bool report, int* verdict) {
+  const int lane = threadIdx.x & 31;
+  bool stands = false, drafted = false;
+  if (lane < p.T - 1) {
+    const int64_t at = static_cast<int64_t>(n) * (p.T - 1) + lane;
+    const int d = p.draft[at];
+    drafted = d >= 0 && d < p.V;
+    if (d >= p.V && report && p.err) atomicOr(p.err, KDA_DEVERR_TOKEN_RANGE);
+    if (drafted) {
+      const double u = p.accept_u[at];
+      const double q = p.probs ? p.probs[at * p.probs_stride + d] : 1.f;
+      stands = u * q < p.target[(static_cast<int64_t>(n) * p.T + lane) * p.target_stride + d];
+    }
+  }
+  const uint32_t s = __ballot_sync(0xffffffffu, stands), v = __ballot_sync(0xffffffffu, drafted);
+  if (lane == 0) {
+    const int k = __ffs(~s) - 1;  // leading drafts that stand; at most T - 1 < 32
+    verdict[0] = k;
+    verdict[1] = (v >> k) & 1;    // a draft stood at k and was refused
+  }
+}
+__device__ __forceinline__ Row row_of(const Params& p, int n, int k, bool refused) {
+  Row r;
+  r.p = p.target + (static_cast<int64_t>(n) * p.T + k) * p.target_stride;
+  r.q = refused && p.probs ? p.probs + (static_cast<int64_t>(n) * (p.T - 1) + k) * p.probs_stride : nullptr;
+  r.out = refused && !p.probs ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + k] : -1;
+  return r;
+}
+__device__ __forceinline__ void write_padding(const Params& p, int n) {
+  const int tid = threadIdx.x;
+  if (tid < p.T) p.tokens[static_cast<int64_t>(n) * p.T + tid] = -1;
+  if (tid == 0) {
+    p.accepted[n] = 0;
+    if (p.next) p.next[n] = 0;
+  }
+}
+__device__ __forceinline__ uint64_t goal_of(const Params& p, int n, uint64_t total) {  // floor(u31 total / 2^31)
+  const float u = fmaxf(p.sample_u[n], 0.f);
+  const uint64_t u31 = u < 1.f ? static_cast<uint64_t>(u * 0x1p31f) : 0x7fffffffu;
+  return __umul64hi(u31 << 33, total);
+}
+__device__ __forceinline__ void write_results(const Params& p, int n, int k, bool massless) {
+  const int tid = threadIdx.x;
+  if (tid < p.T && tid != k) p.tokens[static_cast<int64_t>(n) * p.T + tid] = tid < k ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + tid] : -1;
+  if (tid == 0) {
+    p.accepted[n] = k;
+    if (p.next) p.next[n] = p.slots[static_cast<int64_t>(n) * p.T + k];
+    if (massless) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;
+  }
+}
+
+// A warp's part of the row is `part` consecutive tokens.
+template <bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const Params p, int cluster, int part) {
+  constexpr int kWarps = THREADS / 32;
   __shared__ uint64_t cta_sum[2][kMaxCluster];  // every CTA's sum, in every CTA; of the rest, of the row itself
-  __shared__ uint64_t warp_sums[kWarps], found[kWarps];
+  __shared__ uint64_t warp_sums[kWarps];
   __shared__ int verdict[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = blockIdx.x / cluster, rank = blockIdx.x - n * cluster;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (p.src_slot && p.src_slot[n] <= 0) {  // the whole cluster leaves here
-    if (rank == 0) {
-      if (tid < p.T) p.tokens[static_cast<int64_t>(n) * p.T + tid] = -1;
-      if (tid == 0) {
-        p.accepted[n] = 0;
-        if (p.next) p.next[n] = 0;
-      }
-    }
+    if (rank == 0) write_padding(p, n);
     return;
   }
   // a CTA's memory may be written once that CTA has started: arrive here, wait
   // before the exchange
   if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  if (warp == 0) {
-    bool stands = false, drafted = false;
-    if (lane < p.T - 1) {
-      const int64_t at = static_cast<int64_t>(n) * (p.T - 1) + lane;
-      const int d = p.draft[at];
-      drafted = d >= 0 && d < p.V;
-      if (d >= p.V && rank == 0 && p.err) atomicOr(p.err, KDA_DEVERR_TOKEN_RANGE);
-      if (drafted) {
-        const double u = p.accept_u[at];
-        const double q = p.probs ? p.probs[at * p.probs_stride + d] : 1.f;
-        stands = u * q < p.target[(static_cast<int64_t>(n) * p.T + lane) * p.target_stride + d];
-      }
-    }
-    const uint32_t s = __ballot_sync(0xffffffffu, stands), v = __ballot_sync(0xffffffffu, drafted);
-    if (lane == 0) {
-      const int k = __ffs(~s) - 1;  // leading drafts that stand; at most T - 1 < 32
-      verdict[0] = k;
-      verdict[1] = (v >> k) & 1;    // a draft stood at k and was refused
-    }
-  }
+  if (warp == 0) judge(p, n, rank == 0, verdict);
   __syncthreads();
   const int k = verdict[0];
   const bool refused = verdict[1];
-  Row r;
-  r.p = p.target + (static_cast<int64_t>(n) * p.T + k) * p.target_stride;
-  r.q = refused && p.probs ? p.probs + (static_cast<int64_t>(n) * (p.T - 1) + k) * p.probs_stride : nullptr;
-  r.out = refused && !p.probs ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + k] : -1;
+  Row r = row_of(p, n, k, refused);
   // this warp's part of the row: `part` consecutive tokens
   const int64_t lo64 = static_cast<int64_t>(rank * kWarps + warp) * part;
   const int lo = static_cast<int>(lo64 < p.V ? lo64 : p.V);
   const int hi = static_cast<int>(lo64 + part < p.V ? lo64 + part : p.V);
-  const float u = fmaxf(p.sample_u[n], 0.f);
-  const uint64_t u31 = u < 1.f ? static_cast<uint64_t>(u * 0x1p31f) : 0x7fffffffu;
   uint64_t total = 0, before = 0;  // of the whole row; ahead of this CTA
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {  // the second round where the rest has no mass: the row itself
-    uint64_t sum = 0;
-#pragma unroll 4
-    for (int i = lo + 4 * lane; i < hi; i += 128) {
-      float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-      load4<VEC>(r.p, i, p.V, a);
-      if (r.q) load4<VEC>(r.q, i, p.V, b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum += weight(r, a[j], b[j], i + j);
-    }
+    uint64_t sum = sum_weights<VEC, 2>(r, lo, hi, lane);
     sum = warp_sum(sum);
     if (lane == 0) warp_sums[warp] = sum;
     __syncthreads();
@@ -170,15 +317,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cl
     if (total != 0 || !refused) break;
     r.q = nullptr, r.out = -1;
   }
-  const uint64_t goal = __umul64hi(u31 << 33, total);  // floor(u31 total / 2^31)
-  if (rank == 0) {
-    if (tid < p.T && tid != k) p.tokens[static_cast<int64_t>(n) * p.T + tid] = tid < k ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + tid] : -1;
-    if (tid == 0) {
-      p.accepted[n] = k;
-      if (p.next) p.next[n] = p.slots[static_cast<int64_t>(n) * p.T + k];
-      if (total == 0) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;
-    }
-  }
+  const uint64_t goal = goal_of(p, n, total);
+  if (rank == 0) write_results(p, n, k, total == 0);
   // the warp in whose part the inversion ends
   int owner = -1;
   for (int w = 0; w < kWarps; ++w) {
@@ -188,43 +328,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cl
     }
   }
   if (total == 0 || owner < 0) return;  // not this CTA's part
-  // That part once more, with all threads: each takes `each` tokens in a row.
   const int64_t begin = static_cast<int64_t>(rank * kWarps + owner) * part;
-  const int each = (part + 4 * kThreads - 1) / (4 * kThreads) * 4;
-  const int last = static_cast<int>(begin + part < p.V ? begin + part : p.V);
-  const int64_t from64 = begin + static_cast<int64_t>(tid) * each;
-  const int from = static_cast<int>(from64 < last ? from64 : last), to = min(from + each, last);
-  uint64_t mine = 0;
-#pragma unroll 2
-  for (int i = from; i < to; i += 4) {
-    float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<VEC>(r.p, i, p.V, a);
-    if (r.q) load4<VEC>(r.q, i, p.V, b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mine += i + j < to ? weight(r, a[j], b[j], i + j) : 0;
-  }
-  uint64_t x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) found[warp] = x;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) before += found[w];
-  before += x - mine;
-  if (goal < before || goal >= before + mine) return;
-  for (int i = from; i < to; i += 4) {  // one thread is left
-    float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<VEC>(r.p, i, p.V, a);
-    if (r.q) load4<VEC>(r.q, i, p.V, b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t w = i + j < to ? weight(r, a[j], b[j], i + j) : 0;
-      if (w > 0 && goal >= before && goal < before + w) p.tokens[static_cast<int64_t>(n) * p.T + k] = i + j;
-      before += w;
-    }
-  }
+  search<VEC, THREADS>(r, static_cast<int>(begin), static_cast<int>(begin + part < p.V ? begin + part : p.V), before, goal,
+                       p.V, p.tokens + static_cast<int64_t>(n) * p.T + k);
 }
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
@@ -252,20 +358,25 @@ extern "C" int kda_verify_draft(const KdaVerifyArgs* a, void* stream) {
       misaligned(a->slot_idx, 3) || misaligned(a->tokens, 3) || misaligned(a->num_accepted, 3) ||
       misaligned(a->next_slot, 3) || misaligned(a->err_flag, 3))
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer is not aligned as required");
-  const Params p{a->N, a->T, a->V, a->draft_tokens, a->target_probs, probs, a->target_row_stride, a->draft_row_stride,
-                 a->accept_u, a->sample_u, a->src_slot, a->slot_idx, a->tokens, a->num_accepted, a->next_slot,
-                 a->err_flag};
-  // CTAs per sequence: as many as are resident at once (four of 512 threads on
-  // each of 152 SMs), one on the largest batches
-  int cluster = kMaxCluster;
-  while (cluster > 1 && static_cast<int64_t>(a->N) * cluster > 4 * 152) cluster >>= 1;
-  const int parts = cluster * kWarps;
-  const int part = static_cast<int>((static_cast<int64_t>(a->V) + parts * 128LL - 1) / (parts * 128LL)) * 128;
   const bool vec = !misaligned(a->target_probs, 15) && a->target_row_stride % 4 == 0 &&
                    (!probs || (!misaligned(probs, 15) && a->draft_row_stride % 4 == 0));
-  const dim3 grid(static_cast<unsigned>(a->N) * cluster);
-  const cudaError_t e = kda_internal_launch_cluster(vec ? verify_kernel<true> : verify_kernel<false>, grid,
-                                                    dim3(kThreads), 0, stream, cluster, p, cluster, part);
+  const Params p{a->N, a->T, a->V, a->draft_tokens, a->target_probs, probs, a->target_row_stride, a->draft_row_stride,
+                 a->accept_u, a->sample_u, a->src_slot, a->slot_idx, a->tokens, a->num_accepted, a->next_slot, a->err_flag};
+  // CTAs per sequence: as many as are resident at once (1024 threads an SM: two
+  // of 512 threads while clusters of 8 of them fit, else four of 256), and on
+  // batches past that so many more that a CTA keeps about 16,384 tokens, for
+  // then sequences of unequal cost even out (256 x 131,072 tokens: 48 us with
+  // four, 52 with two or eight; 256 x 50,000: 19 with two, 22 with four).
+  const bool wide = static_cast<int64_t>(a->N) * kMaxCluster <= 2 * 152;
+  int cluster = kMaxCluster;
+  while (cluster > 1 && static_cast<int64_t>(a->N) * cluster > 4 * 152) cluster >>= 1;
+  while (cluster < kMaxCluster && a->V / (2 * cluster) > 16384) cluster <<= 1;
+  const int threads = wide ? 512 : 256, slices = cluster * (threads / 32);
+  const int part = static_cast<int>((static_cast<int64_t>(a->V) + slices * 128LL - 1) / (slices * 128LL)) * 128;
+  auto kernel = wide ? (vec ? verify_kernel<true, 512> : verify_kernel<false, 512>)
+                     : (vec ? verify_kernel<true, 256> : verify_kernel<false, 256>);
+  const cudaError_t e = kda_internal_launch_cluster(kernel, dim3(static_cast<unsigned>(a->N) * cluster), dim3(threads), 0,
+                                                    stream, cluster, p, cluster, part);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }

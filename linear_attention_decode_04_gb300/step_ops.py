@@ -464,7 +464,7 @@ class KdaVerifyDraftCall(_Call):
             accept_u=_p(accept_u) if drafts else None, sample_u=_p(sample_u), src_slot=_p(src_slot),
             slot_idx=_p(slot_idx), tokens=_p(self.tokens), num_accepted=_p(self.num_accepted),
             next_slot=_p(self.next_slot), err_flag=_p(err_flag))
-        own = (self.tokens, self.num_accepted) + (() if self.next_slot is None else (self.next_slot,))
+        own = tuple(t for t in (self.tokens, self.num_accepted, self.next_slot) if t is not None)
         self._prepare("kda_verify_draft", args, dev,
                       (draft_tokens, target_probs, accept_u, sample_u, draft_probs, src_slot, slot_idx, err_flag), own)
 
