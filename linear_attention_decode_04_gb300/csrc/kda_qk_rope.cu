@@ -3,12 +3,15 @@
 //
 // Bound by HBM on prompts (each row read once, each output written once) and
 // by latency on decode steps.  One launch holds two kinds of CTAs:
-//   - cache CTAs: a run of token rows that fall in one block, for one kv head
-//     and one of K / V.  The block's scale needs the largest value of all its
-//     new rows, so the run's rows stay in registers between the norm, the
-//     reduction and the rounding to e4m3; nothing is read twice.
-//   - query CTAs: one warp per token and group of heads; the token's sines
-//     and cosines are computed once for the warp's heads.
+//   - cache CTAs: some token rows for K or V of one or more kv heads.  Rows
+//     that go on in one block form a run; the block's scale needs the largest
+//     value of the whole run, so its rows stay in registers between the norm,
+//     the reduction and the rounding to e4m3, and nothing is read twice.  A
+//     short run (a decode or multi-token step) is one warp's work, a long one
+//     the CTA's, whose heads share the rows' sines and cosines.
+//   - query CTAs: one warp per token and group of heads.  The token's sines and
+//     cosines are computed once for the warp's heads and multiplied by the
+//     norm's weights, so that a row costs six multiply-adds per pair.
 // Eight lanes share a row of 128 channels, 16 channels each, as two 16-byte
 // loads: lane l holds the pairs 8l .. 8l + 7 of whichever pairing is used.
 //
@@ -28,11 +31,14 @@ namespace {
 
 constexpr int kD = KDA_HEAD_DIM;
 constexpr int kExpMin = -64, kExpMax = 119;  // range of the block scales' exponents
+constexpr int kMaxBlock = 256;               // largest block size
+constexpr int kTableRows = 64;               // largest block whose rows' sines the heads of a CTA share (32 KB)
 
 struct Params {
-  int T, Hq, Hkv, rot, bs, num_blocks, interleaved;
-  int cache_ctas, rows_per_cta;  // cache CTAs come first in the grid; rows each looks through
-  int q_heads, chunks, iters;    // heads that query CTAs write (q, and k with k_out); warps per token; row groups each
+  int T, Hq, Hkv, rot, bs, num_blocks;
+  int cache_ctas, rows_per_cta, heads_per_cta;  // cache CTAs come first in the grid; rows and heads of each
+  int q_groups, groups;          // groups of four heads that query CTAs write: of q; of q and, with k_out, k
+  int chunks, iters;             // warps per token; head groups each
   float eps;
   const uint16_t* qkv;
   int64_t qkv_stride;
@@ -77,35 +83,41 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 struct Runs {
   int c0, c1;
 };
-__device__ __forceinline__ Runs lane_runs(const Params& p, int l) {
-  if (p.interleaved) return {16 * l, 16 * l + 8};
-  const int half = p.rot >> 1, i = 8 * l;
+template <bool INTER>
+__device__ __forceinline__ Runs lane_runs(int rot, int l) {
+  if (INTER) return {16 * l, 16 * l + 8};
+  const int half = rot >> 1, i = 8 * l;
   if (i < half) return {i, i + half};
-  return {p.rot + (i - half), p.rot + (64 - half) + (i - half)};
+  return {rot + (i - half), rot + (64 - half) + (i - half)};
 }
 // Runs <-> pairs: the interleaved pairing takes neighbours.
-__device__ __forceinline__ Pairs to_pairs(const Params& p, const uint4& r0, const uint4& r1) {
-  float x[8], y[8];
-  unpack8(r0, x);
-  unpack8(r1, y);
+template <bool INTER>
+__device__ __forceinline__ Pairs to_pairs(const float (&x)[8], const float (&y)[8]) {
   Pairs q;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float ia = i < 4 ? x[2 * i & 7] : y[2 * i & 7], ib = i < 4 ? x[(2 * i + 1) & 7] : y[(2 * i + 1) & 7];
-    q.a[i] = p.interleaved ? ia : x[i];
-    q.b[i] = p.interleaved ? ib : y[i];
+    if (INTER) q.a[i] = i < 4 ? x[2 * i & 7] : y[2 * i & 7], q.b[i] = i < 4 ? x[(2 * i + 1) & 7] : y[(2 * i + 1) & 7];
+    else q.a[i] = x[i], q.b[i] = y[i];
   }
   return q;
 }
-__device__ __forceinline__ void to_runs(const Params& p, const Pairs& q, float (&x)[8], float (&y)[8]) {
+template <bool INTER>
+__device__ __forceinline__ Pairs to_pairs(const uint4& r0, const uint4& r1) {
+  float x[8], y[8];
+  unpack8(r0, x);
+  unpack8(r1, y);
+  return to_pairs<INTER>(x, y);
+}
+template <bool INTER>
+__device__ __forceinline__ void to_runs(const Pairs& q, float (&x)[8], float (&y)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float lo = i & 1 ? q.b[i >> 1] : q.a[i >> 1], hi = i & 1 ? q.b[4 + (i >> 1)] : q.a[4 + (i >> 1)];
-    x[i] = p.interleaved ? lo : q.a[i];
-    y[i] = p.interleaved ? hi : q.b[i];
+    if (INTER) x[i] = i & 1 ? q.b[i >> 1] : q.a[i >> 1], y[i] = i & 1 ? q.b[4 + (i >> 1)] : q.a[4 + (i >> 1)];
+    else x[i] = q.a[i], y[i] = q.b[i];
   }
 }
-__device__ __forceinline__ Pairs load_weight(const Params& p, const float* w, const Runs& r) {
+template <bool INTER>
+__device__ __forceinline__ Pairs load_weight(const float* w, const Runs& r) {
   float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -113,27 +125,18 @@ __device__ __forceinline__ Pairs load_weight(const Params& p, const float* w, co
     x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
     y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
   }
-  Pairs q;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float ia = i < 4 ? x[2 * i & 7] : y[2 * i & 7], ib = i < 4 ? x[(2 * i + 1) & 7] : y[(2 * i + 1) & 7];
-    q.a[i] = p.interleaved ? ia : x[i];
-    q.b[i] = p.interleaved ? ib : y[i];
-  }
-  return q;
+  return to_pairs<INTER>(x, y);
 }
 __device__ __forceinline__ float sum8(float v) {  // over the 8 lanes of a row
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ void norm_row(Pairs& x, const Pairs& w, float eps) {
+__device__ __forceinline__ float norm_factor(const Pairs& x, float eps) {
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], s));
-  const float r = rsqrtf(sum8(s) * (1.f / kD) + eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x.a[i] = x.a[i] * r * w.a[i], x.b[i] = x.b[i] * r * w.b[i];
+  return rsqrtf(sum8(s) * (1.f / kD) + eps);
 }
 struct Turn {
   float c[8], s[8];
@@ -148,14 +151,6 @@ __device__ __forceinline__ Turn turn_of(const Params& p, int pos, int l) {
     sincospif(x, &t.s[i], &t.c[i]);
   }
   return t;
-}
-__device__ __forceinline__ void rotate_row(Pairs& x, const Turn& t) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = x.a[i], b = x.b[i];
-    x.a[i] = a * t.c[i] - b * t.s[i];
-    x.b[i] = b * t.c[i] + a * t.s[i];
-  }
 }
 __device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
@@ -182,182 +177,309 @@ __device__ __forceinline__ float fit_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The rows t .. t + count - 1 fall in block `blk` from row `first` on.
-template <int THREADS, int ROWS>
-__device__ __forceinline__ void write_block(const Params& p, int t, int count, int blk, int first, int h, bool is_v,
-                                            float* red) {
-  constexpr int kGroups = THREADS / 8;
-  const int tid = threadIdx.x, l = tid & 7, g = tid >> 3;
-  const Runs run = lane_runs(p, l);
+// A run: `count` token rows from t on, in block `blk` from its row `first` on.
+struct Run {
+  int t, count, blk, first;
+};
+// Sines and cosines of a run's rows in shared memory: [row][4][lane], two pairs
+// of one lane each, so that eight lanes read 128 bytes in a row.
+__device__ __forceinline__ Turn turn_from(const float4* table, int row, int l) {
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = table[row * 32 + i * 8 + l];
+    t.c[2 * i] = v.x, t.s[2 * i] = v.y, t.c[2 * i + 1] = v.z, t.s[2 * i + 1] = v.w;
+  }
+  return t;
+}
+__device__ __forceinline__ void fill_table(const Params& p, const Run& u, float4* table, int threads) {
+  for (int e = threadIdx.x; e < u.count * 32; e += threads) {
+    const int row = e >> 5, pair = 8 * (e & 7) + 2 * ((e >> 3) & 3);
+    if (pair >= (p.rot >> 1)) continue;
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[u.t + row]));
+    float4 v;
+    sincospif(static_cast<float>(static_cast<int32_t>((pos * p.freqs[pair]) >> 32)) * 0x1p-31f, &v.y, &v.x);
+    sincospif(static_cast<float>(static_cast<int32_t>((pos * p.freqs[pair + 1]) >> 32)) * 0x1p-31f, &v.w, &v.z);
+    table[e] = v;
+  }
+}
+// Writes a run of at most GROUPS * ROWS rows of one head of K or V; group g of
+// the GROUPS that work on it (eight lanes each) takes rows g, g + GROUPS ...
+// `all_max` reduces a warp's maximum to that of all groups.  `table`: the rows'
+// sines and cosines, or null.
+template <int GROUPS, int ROWS, bool INTER, class Reduce>
+__device__ __forceinline__ void write_run(const Params& p, const Run& u, int h, bool is_v, int g, const float4* table,
+                                          Reduce all_max) {
+  const int l = threadIdx.x & 7;
+  const Runs run = lane_runs<INTER>(p.rot, l);
   const float* weight = is_v ? nullptr : p.k_weight;
   const bool rotated = !is_v && 8 * l < (p.rot >> 1);
-  const uint16_t* src = p.qkv + static_cast<int64_t>(t) * p.qkv_stride +
+  const uint16_t* src = p.qkv + static_cast<int64_t>(u.t) * p.qkv_stride +
                         static_cast<int64_t>(p.Hq + (is_v ? p.Hkv : 0) + h) * kD;
-  float* scale_at = (is_v ? p.v_scale : p.k_scale) + static_cast<int64_t>(blk) * p.Hkv + h;
-  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) + blk * p.block_stride + h * p.head_stride;
-  const float old = first > 0 ? *scale_at : 0.f;
-  Pairs x[ROWS];
+  float* scale_at = (is_v ? p.v_scale : p.k_scale) + static_cast<int64_t>(u.blk) * p.Hkv + h;
+  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) + u.blk * p.block_stride + h * p.head_stride;
+  uint4 r0[ROWS], r1[ROWS];
+  int pos[ROWS];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int j = g + r * kGroups;  // row of the run
-    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (j < count) {
+  for (int r = 0; r < ROWS; ++r) {  // everything that is needed from memory is asked for first
+    const int j = g + r * GROUPS;
+    r0[r] = r1[r] = make_uint4(0, 0, 0, 0);
+    pos[r] = 0;
+    if (j < u.count) {
       const uint16_t* row = src + static_cast<int64_t>(j) * p.qkv_stride;
-      r0 = *reinterpret_cast<const uint4*>(row + run.c0);
-      r1 = *reinterpret_cast<const uint4*>(row + run.c1);
+      r0[r] = *reinterpret_cast<const uint4*>(row + run.c0);
+      r1[r] = *reinterpret_cast<const uint4*>(row + run.c1);
+      if (rotated && !table) pos[r] = p.positions[u.t + j];
     }
-    x[r] = to_pairs(p, r0, r1);
   }
+  const float old = u.first > 0 ? *scale_at : 0.f;
+  Pairs x[ROWS];
   float amax = 0.f;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    const int j = g + r * kGroups;
-    if (r * kGroups < count) {  // whole warps leave together: count is the CTA's
-      if (weight) norm_row(x[r], load_weight(p, weight, run), p.eps);
-      if (rotated && j < count) rotate_row(x[r], turn_of(p, p.positions[t + j], l));
+    x[r] = to_pairs<INTER>(r0[r], r1[r]);
+    if (r * GROUPS < u.count) {  // the same for all threads of the run
+      if (weight) {
+        const Pairs w = load_weight<INTER>(weight, run);
+        const float f = norm_factor(x[r], p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[r].a[i] = x[r].a[i] * f * w.a[i], x[r].b[i] = x[r].b[i] * f * w.b[i];
+      }
+      if (rotated && g + r * GROUPS < u.count) {
+        const Turn t = table ? turn_from(table, g + r * GROUPS, l) : turn_of(p, pos[r], l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[r].a[i], b = x[r].b[i];
+          x[r].a[i] = a * t.c[i] - b * t.s[i];
+          x[r].b[i] = b * t.c[i] + a * t.s[i];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float u = fabsf(x[r].a[i]), v = fabsf(x[r].b[i]);
-        amax = fmaxf(amax, fmaxf(u <= FLT_MAX ? u : 0.f, v <= FLT_MAX ? v : 0.f));
+        amax = fmaxf(amax, fmaxf(fabsf(x[r].a[i]), fabsf(x[r].b[i])));  // passes over NaN
       }
     }
   }
+  if (__any_sync(0xffffffffu, amax > FLT_MAX)) {  // an infinity among them: it does not count
+    amax = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(x[r].a[i]), b = fabsf(x[r].b[i]);
+        amax = fmaxf(amax, fmaxf(a <= FLT_MAX ? a : 0.f, b <= FLT_MAX ? b : 0.f));
+      }
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
+  amax = all_max(amax);  // also: every thread of the run has read the old scale
   const float scale = fmaxf(old, fit_scale(amax));
   const float inv = 1.f / scale;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    const int j = g + r * kGroups;
-    if (j >= count) continue;
-    float u[8], v[8];
-    to_runs(p, x[r], u, v);
-    uint8_t* row = dst + (first + j) * p.token_stride;
+    const int j = g + r * GROUPS;
+    if (j >= u.count) continue;
+    float a[8], b[8];
+    to_runs<INTER>(x[r], a, b);
+    uint8_t* row = dst + (u.first + j) * p.token_stride;
     *reinterpret_cast<uint2*>(row + run.c0) =
-        make_uint2(e4m3x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv),
-                   e4m3x4(u[4] * inv, u[5] * inv, u[6] * inv, u[7] * inv));
+        make_uint2(e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv),
+                   e4m3x4(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv));
     *reinterpret_cast<uint2*>(row + run.c1) =
-        make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                   e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+        make_uint2(e4m3x4(b[0] * inv, b[1] * inv, b[2] * inv, b[3] * inv),
+                   e4m3x4(b[4] * inv, b[5] * inv, b[6] * inv, b[7] * inv));
   }
-  if (first > 0 && scale != old) {  // the older rows follow the scale
+  if (u.first > 0 && scale != old) {  // the older rows follow the scale
     const float ratio = old * inv;
-    for (int j = g; j < first; j += kGroups) {
+#pragma unroll 4
+    for (int j = g; j < u.first; j += GROUPS) {
       uint4* row = reinterpret_cast<uint4*>(dst + j * p.token_stride) + l;
       const uint4 v = *row;
       *row = make_uint4(rescale4(v.x, ratio), rescale4(v.y, ratio), rescale4(v.z, ratio), rescale4(v.w, ratio));
     }
   }
-  if (tid == 0) *scale_at = scale;
-  __syncthreads();  // red is free again
+  if (l == 0 && g == 0) *scale_at = scale;
 }
 
-template <int THREADS, int ROWS>
-__global__ void __launch_bounds__(THREADS) qk_rope_kernel(const Params p) {
-  __shared__ float red[THREADS / 32];
-  __shared__ int lead[THREADS];
-  __shared__ int leads, extent;
-  const int tid = threadIdx.x;
+// THREADS / 8 * ROWS is at least the block size.
+template <int THREADS, int ROWS, bool INTER>
+__global__ void __launch_bounds__(THREADS, ROWS > 2 ? 512 / THREADS : 768 / THREADS) qk_rope_kernel(const Params p) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (static_cast<int>(blockIdx.x) < p.cache_ctas) {
-    const int per_head = 2 * p.Hkv, unit = blockIdx.x % per_head, h = unit >> 1;
-    const int64_t base = static_cast<int64_t>(blockIdx.x / per_head) * p.rows_per_cta;
+    __shared__ float red[kWarps];
+    __shared__ int64_t slots[2 * kMaxBlock + 1];  // of the row before the CTA's rows, of them, and a block's worth behind
+    __shared__ Run run_of[kMaxBlock];
+    __shared__ int runs;
+    extern __shared__ float4 table[];
+    const int units = 2 * ((p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta), unit = blockIdx.x % units;
+    const int h0 = (unit >> 1) * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.Hkv);
+    const int base = static_cast<int>(blockIdx.x / units) * p.rows_per_cta;
     const bool is_v = unit & 1;
     const int64_t limit = static_cast<int64_t>(p.num_blocks) * p.bs;
-    if (tid == 0) leads = 0;
-    __syncthreads();
-    // rows that begin a run: the first of a block, or one whose slot does not follow the row before
-    if (tid < p.rows_per_cta && base + tid < p.T) {
-      const int t = static_cast<int>(base) + tid;
-      const int64_t s = p.slot_map[t];
+    const int seen = min(p.rows_per_cta + p.bs, p.T - base);
+    for (int i = tid; i <= seen; i += THREADS) {
+      const int64_t s = base + i > 0 ? p.slot_map[base + i - 1] : -1;
       if (s >= limit && unit == 0 && p.err) atomicOr(p.err, KDA_DEVERR_SLOT_RANGE);
-      if (s >= 0 && s < limit && (s % p.bs == 0 || t == 0 || p.slot_map[t - 1] != s - 1)) lead[atomicAdd(&leads, 1)] = t;
+      slots[i] = s >= limit ? -1 : s;
+    }
+    if (tid == 0) runs = 0;
+    __syncthreads();
+    // runs that begin here: at the first row of a block, or at a slot that does not follow the row before
+    const int rows = min(p.rows_per_cta, p.T - base);
+    for (int i = tid; i < rows; i += THREADS) {
+      const int64_t s = slots[i + 1];
+      if (s >= 0 && (s % p.bs == 0 || slots[i] != s - 1)) {
+        Run u;
+        u.t = base + i;
+        u.blk = static_cast<int>(s / p.bs);
+        u.first = static_cast<int>(s % p.bs);
+        u.count = 0;
+        run_of[atomicAdd(&runs, 1)] = u;
+      }
     }
     __syncthreads();
-    const int n = leads;
+    const int n = runs;
+    for (int i = warp; i < n; i += kWarps) {  // how far each goes on in its block
+      const Run u = run_of[i];
+      const int at = u.t - base + 1, most = min(p.bs - u.first, seen - at + 1);
+      const int64_t s = slots[at];
+      int count = 0;
+      while (count < most) {
+        const int j = count + lane;
+        const uint32_t on = __ballot_sync(0xffffffffu, j < most && slots[at + j] == s + j);
+        count += on == 0xffffffffu ? 32 : __ffs(~on) - 1;
+        if (on != 0xffffffffu) break;
+      }
+      __syncwarp();
+      if (lane == 0) run_of[i].count = count;
+    }
+    __syncthreads();
+    for (int i = warp; i < n; i += kWarps)
+      if (run_of[i].count <= 4 * ROWS)
+        for (int h = h0; h < h1; ++h)
+          write_run<4, ROWS, INTER>(p, run_of[i], h, is_v, lane >> 3, nullptr, [](float m) {
+            __syncwarp();
+            return m;
+          });
+    const bool shared = !is_v && p.rot > 0 && p.heads_per_cta > 1 && p.bs <= kTableRows;
     for (int i = 0; i < n; ++i) {
-      const int t = lead[i];
-      const int64_t s = p.slot_map[t];
-      const int blk = static_cast<int>(s / p.bs), first = static_cast<int>(s % p.bs);
-      // the run's length: the rows that go on in the same block (a run is at
-      // most a block, which is at most THREADS rows)
-      const int most = min(p.bs - first, p.T - t);
-      if (tid == 0) extent = most;
-      __syncthreads();
-      if (tid > 0 && tid < most && p.slot_map[t + tid] != s + tid) atomicMin(&extent, tid);
-      __syncthreads();
-      const int count = extent;
-      write_block<THREADS, ROWS>(p, t, count, blk, first, h, is_v, red);
+      if (run_of[i].count <= 4 * ROWS) continue;
+      if (shared) {
+        __syncthreads();  // the run before has been read
+        fill_table(p, run_of[i], table, THREADS);
+        __syncthreads();
+      }
+      for (int h = h0; h < h1; ++h)
+        write_run<THREADS / 8, ROWS, INTER>(p, run_of[i], h, is_v, tid >> 3, shared ? table : nullptr, [&](float m) {
+          __syncthreads();  // of the head before: `red` is free
+          if (lane == 0) red[warp] = m;
+          __syncthreads();
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red[w]);
+          return m;
+        });
     }
     return;
   }
-  // ---- queries (and k_out): warp = (token, chunk of heads), four heads at a time
-  const int warp = (blockIdx.x - p.cache_ctas) * (THREADS / 32) + (tid >> 5);
-  const int t = warp / p.chunks, chunk = warp - t * p.chunks;
+  // ---- queries (and k_out): warp = (token, chunk of head groups), four heads at a time
+  const int64_t work = static_cast<int64_t>(blockIdx.x - p.cache_ctas) * kWarps + warp;
+  const int t = static_cast<int>(work / p.chunks), chunk = static_cast<int>(work - static_cast<int64_t>(t) * p.chunks);
   if (t >= p.T) return;
-  const int l = tid & 7, sub = (tid & 31) >> 3;
-  const Runs run = lane_runs(p, l);
+  const int l = tid & 7, sub = lane >> 3;
+  const Runs run = lane_runs<INTER>(p.rot, l);
   const bool rotated = 8 * l < (p.rot >> 1);
   const uint16_t* src = p.qkv + static_cast<int64_t>(t) * p.qkv_stride;
-  Turn turn;
-  if (rotated) turn = turn_of(p, p.positions[t], l);
-  for (int it = 0; it < p.iters; ++it) {
-    const int h = (chunk * p.iters + it) * 4 + sub;
-    const bool live = h < p.q_heads;
-    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (live) {
-      r0 = *reinterpret_cast<const uint4*>(src + h * kD + run.c0);
-      r1 = *reinterpret_cast<const uint4*>(src + h * kD + run.c1);
+  const int from = chunk * p.iters, to = min(from + p.iters, p.groups);
+  // q's groups first, then k's: heads of a group are of one kind
+  auto head_of = [&](int i) { return i < p.q_groups ? 4 * i + sub : p.Hq + 4 * (i - p.q_groups) + sub; };
+  auto live_of = [&](int i) { return i < p.q_groups ? 4 * i + sub < p.Hq : 4 * (i - p.q_groups) + sub < p.Hkv; };
+  uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
+  if (live_of(from)) {
+    r0 = *reinterpret_cast<const uint4*>(src + head_of(from) * kD + run.c0);
+    r1 = *reinterpret_cast<const uint4*>(src + head_of(from) * kD + run.c1);
+  }
+  const int pos = p.positions[t];
+  // weights times cosines and sines: a' = f (a ac - b bs), b' = f (b bc + a as)
+  float ac[8], bs[8], bc[8], as[8];
+  const float* weight = nullptr;
+  for (int i = from; i < to; ++i) {
+    if (i == from || i == p.q_groups) {
+      weight = i < p.q_groups ? p.q_weight : p.k_weight;
+      Pairs w;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w.a[k] = w.b[k] = 1.f;
+      if (weight) w = load_weight<INTER>(weight, run);
+      Turn turn;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) turn.c[k] = 1.f, turn.s[k] = 0.f;
+      if (rotated) turn = turn_of(p, pos, l);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ac[k] = w.a[k] * turn.c[k], as[k] = w.a[k] * turn.s[k];
+        bc[k] = w.b[k] * turn.c[k], bs[k] = w.b[k] * turn.s[k];
+      }
     }
-    Pairs x = to_pairs(p, r0, r1);
-    const float* weight = h < p.Hq ? p.q_weight : p.k_weight;
-    if (p.q_weight || p.k_weight) {
-      Pairs y = x;
-      norm_row(y, weight ? load_weight(p, weight, run) : y, p.eps);
-      if (weight) x = y;
+    const Pairs x = to_pairs<INTER>(r0, r1);
+    const int h = head_of(i);
+    const bool live = live_of(i);
+    if (i + 1 < to) {  // the next group's rows, while this one's are worked on
+      r0 = r1 = make_uint4(0, 0, 0, 0);
+      if (live_of(i + 1)) {
+        r0 = *reinterpret_cast<const uint4*>(src + head_of(i + 1) * kD + run.c0);
+        r1 = *reinterpret_cast<const uint4*>(src + head_of(i + 1) * kD + run.c1);
+      }
     }
-    if (rotated) rotate_row(x, turn);
+    const float f = weight ? norm_factor(x, p.eps) : 1.f;
+    Pairs y;
+    if (rotated) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y.a[k] = f * (x.a[k] * ac[k] - x.b[k] * bs[k]);
+        y.b[k] = f * (x.b[k] * bc[k] + x.a[k] * as[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y.a[k] = f * (x.a[k] * ac[k]), y.b[k] = f * (x.b[k] * bc[k]);
+    }
     if (!live) continue;
     float u[8], v[8];
-    to_runs(p, x, u, v);
+    to_runs<INTER>(y, u, v);
     uint16_t* out = h < p.Hq ? p.q_out + t * p.q_stride + h * kD : p.k_out + t * p.k_stride + (h - p.Hq) * kD;
     *reinterpret_cast<uint4*>(out + run.c0) = pack8(u);
     *reinterpret_cast<uint4*>(out + run.c1) = pack8(v);
   }
 }
 
-// THREADS is at least the block size, ROWS * THREADS / 8 exactly.
 template <int THREADS, int ROWS>
-cudaError_t launch(Params& p, void* stream) {
+cudaError_t launch(Params& p, bool interleaved, void* stream) {
   constexpr int kWarps = THREADS / 32;
   int64_t cache_ctas = 0;
   if (p.k_cache) {
-    // rows looked through per CTA: one while the rows alone give enough CTAs
-    // to fill the card, up to a block's worth on prompts
-    const int64_t units = static_cast<int64_t>(p.T) * p.Hkv * 2;
-    int64_t rows = units / 8192;
-    rows = rows < 1 ? 1 : rows > p.bs ? p.bs : rows;
-    if (rows > THREADS) rows = THREADS;
-    p.rows_per_cta = static_cast<int>(rows);
-    cache_ctas = (p.T + rows - 1) / rows * p.Hkv * 2;
+    // rows per CTA: as few as fill half the card's room (three CTAs of 256
+    // threads an SM; fewer rows cost more CTAs than they help), up to a
+    // block's worth on prompts; then all heads that still leave it filled
+    const int64_t room = 152 * 768 / THREADS / 2, rows = static_cast<int64_t>(p.T) * p.Hkv * 2 / room;
+    p.rows_per_cta = static_cast<int>(rows < 1 ? 1 : rows > p.bs ? p.bs : rows);
+    const int64_t chunks = (static_cast<int64_t>(p.T) + p.rows_per_cta - 1) / p.rows_per_cta;
+    p.heads_per_cta = p.Hkv;
+    while (p.heads_per_cta > 1 && chunks * 2 * (p.Hkv / p.heads_per_cta) < room) p.heads_per_cta = (p.heads_per_cta + 1) / 2;
+    cache_ctas = chunks * 2 * ((p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta);
   }
   // warps per token: as many as there are groups of four heads while the
   // batch is small, one per token on prompts (the sines are then computed once)
-  const int groups = (p.q_heads + 3) / 4;
-  int64_t chunks = (static_cast<int64_t>(152) * 32 + p.T - 1) / p.T;
-  chunks = chunks < 1 ? 1 : chunks > groups ? groups : chunks;
-  p.iters = static_cast<int>((groups + chunks - 1) / chunks);
-  p.chunks = (groups + p.iters - 1) / p.iters;
+  int64_t chunks = (static_cast<int64_t>(152) * 24 + p.T - 1) / p.T;
+  chunks = chunks < 1 ? 1 : chunks > p.groups ? p.groups : chunks;
+  p.iters = static_cast<int>((p.groups + chunks - 1) / chunks);
+  p.chunks = (p.groups + p.iters - 1) / p.iters;
   const int64_t ctas = cache_ctas + (static_cast<int64_t>(p.T) * p.chunks + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   p.cache_ctas = static_cast<int>(cache_ctas);
-  return kda_internal_launch(qk_rope_kernel<THREADS, ROWS>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), 0,
-                             stream, p);
+  return kda_internal_launch(interleaved ? qk_rope_kernel<THREADS, ROWS, true> : qk_rope_kernel<THREADS, ROWS, false>,
+                             dim3(static_cast<unsigned>(ctas)), dim3(THREADS),
+                             p.k_cache && p.heads_per_cta > 1 && p.bs <= kTableRows ? p.bs * 512u : 0u, stream, p);
 }
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
@@ -402,8 +524,9 @@ extern "C" int kda_qk_rope(const KdaQkRopeArgs* a, void* stream) {
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer or stride is not aligned as required");
   Params p{};
   p.T = a->T, p.Hq = a->num_q_heads, p.Hkv = a->num_kv_heads, p.rot = a->rot_dim, p.bs = bs;
-  p.num_blocks = a->num_blocks, p.interleaved = (a->flags & KDA_ROPE_INTERLEAVED) != 0;
-  p.q_heads = a->num_q_heads + (a->k_out ? a->num_kv_heads : 0);
+  p.num_blocks = a->num_blocks;
+  p.q_groups = (a->num_q_heads + 3) / 4;
+  p.groups = p.q_groups + (a->k_out ? (a->num_kv_heads + 3) / 4 : 0);
   p.eps = a->eps;
   p.qkv = a->qkv, p.qkv_stride = a->qkv_row_stride;
   p.q_out = a->q_out, p.q_stride = a->q_row_stride, p.k_out = a->k_out, p.k_stride = a->k_row_stride;
@@ -412,12 +535,13 @@ extern "C" int kda_qk_rope(const KdaQkRopeArgs* a, void* stream) {
   p.block_stride = a->block_stride, p.head_stride = a->head_stride, p.token_stride = a->token_stride;
   p.k_scale = a->k_scale, p.v_scale = a->v_scale, p.slot_map = a->slot_map, p.err = a->err_flag;
   // a run of up to block_size rows stays in registers: rows per 8-lane group
+  const bool inter = (a->flags & KDA_ROPE_INTERLEAVED) != 0;
   cudaError_t e;
-  if (!cache || bs == 16) e = launch<128, 1>(p, stream);
-  else if (bs == 32) e = launch<128, 2>(p, stream);
-  else if (bs == 64) e = launch<128, 4>(p, stream);
-  else if (bs == 128) e = launch<256, 4>(p, stream);
-  else e = launch<256, 8>(p, stream);
+  if (!cache || bs == 64) e = launch<256, 2>(p, inter, stream);
+  else if (bs == 16) e = launch<128, 1>(p, inter, stream);
+  else if (bs == 32) e = launch<128, 2>(p, inter, stream);
+  else if (bs == 128) e = launch<256, 4>(p, inter, stream);
+  else e = launch<512, 4>(p, inter, stream);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }
