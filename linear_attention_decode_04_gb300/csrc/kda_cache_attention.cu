@@ -57,7 +57,7 @@ constexpr int kMaxCtas = 304;              // 2 x 152
 // What beginning and ending a unit costs, in tiles: the work is dealt out by
 // tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
 constexpr int kUnitCost = 4;
-constexpr int kCounters = 4 * 6 * 152;     // of each kind: CTAs x warps that join, at most
+constexpr int kCounters = 4 * 456;         // of each kind: CTAs x warps that join, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -90,7 +90,6 @@ struct Cfg {
   static constexpr int kK = GROUPS > 2 ? 3 : GROUPS > 1 ? 4 : kN > 16 ? 2 : 3;
   static constexpr int kV = GROUPS > 2 ? 4 : GROUPS > 1 ? 5 : 3;
   static constexpr int kNan = GROUPS > 1 ? 4 : 1;
-  static constexpr int kP = GROUPS > 2 ? 2 : 1;          // buffers of the weights
   static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
   static constexpr int kPartial = COLS * (32 + 2);       // floats of a warp's partial record: maxima, sums, 32 channels
   static constexpr int kJoinFan = 8;              // parts that one warp joins
@@ -100,12 +99,11 @@ struct Cfg {
 
 template <class C>
 struct alignas(1024) Smem {
-  uint8_t p[C::kP][2][C::kN * kTile];     // leading part, remainder; [row' / 16][token][row' % 16]
+  uint8_t p[2][C::kN * kTile];            // leading part, remainder; [row' / 16][token][row' % 16]
   uint8_t q[2][C::kN * kD];               // likewise; core matrices of 8 rows x 16 bytes
   uint8_t k[C::kK][kTileBytes], v[C::kV][kTileBytes];
   uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], sc_full[C::kV];
-  // p_full per tile parity: with two buffers a group may be done with a tile that another has not begun
-  uint64_t s_full[2], o_full[2], p_full[2], q_full, done;
+  uint64_t s_full[2], o_full[2], p_full, q_full, done;
   float4 sc[C::kV][kMaxPages];            // k_scale, log2(v_scale), 1 / v_scale of a tile's blocks; lives as V does
   float row_scale[C::kRows];
   int limit[C::kRows];
@@ -429,7 +427,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     for (int i = 0; i < C::kK; ++i) bar_init(&S.k_full[i], 1), bar_init(&S.k_empty[i], 1);
     for (int i = 0; i < C::kV; ++i) bar_init(&S.v_full[i], 1), bar_init(&S.v_empty[i], 1);
     for (int i = 0; i < C::kV; ++i) bar_init(&S.sc_full[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&S.s_full[i], 1), bar_init(&S.o_full[i], 1), bar_init(&S.p_full[i], 128 * C::kGroups);
+    for (int i = 0; i < 2; ++i) bar_init(&S.s_full[i], 1), bar_init(&S.o_full[i], 1);
+    bar_init(&S.p_full, 128 * C::kGroups);
     bar_init(&S.q_full, 128 * C::kGroups);
     bar_init(&S.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -611,7 +610,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         bool ok = true;
         auto weigh = [&](uint32_t j) {  // O^T of tile j
           const uint32_t st = j % C::kV;
-          ok = ok && bar_wait(&S.p_full[j & 1], (j >> 1) & 1, &S.failed) && bar_wait(&S.v_full[st], (j / C::kV) & 1, &S.failed);
+          ok = ok && bar_wait(&S.p_full, j & 1, &S.failed) && bar_wait(&S.v_full[st], (j / C::kV) & 1, &S.failed);
           if (!ok) return;
           tc_after();
           const uint32_t v = s32(S.v[st]), d = tmem + (2 + (j & 1)) * kN;
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < kTile / 32; ++k)
-              mma(d, sdesc(v + k * 32 * kD, 0, 1024, 2), sdesc(s32(S.p[j % C::kP][part]) + k * 512, 128, 2048, 0), id_o,
+              mma(d, sdesc(v + k * 32 * kD, 0, 1024, 2), sdesc(s32(S.p[part]) + k * 512, 128, 2048, 0), id_o,
                   part + k > 0);
           commit(&S.v_empty[st]);
           commit(&S.o_full[j & 1]);
@@ -837,22 +836,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             l[2 * b] = l[2 * b] * al.x + s0 * be.x;
             l[2 * b + 1] = l[2 * b + 1] * al.y + s1 * be.y;
           }
-          // one buffer: the tile before has to be weighed; two: the one before that was, when it was added
-          if (C::kP == 1 && it > 0) bar_wait(&S.o_full[(it - 1) & 1], ((it - 1) >> 1) & 1, &S.failed);
-          uint8_t(*weights)[C::kN * kTile] = S.p[it % C::kP];
+          if (it > 0) bar_wait(&S.o_full[(it - 1) & 1], ((it - 1) >> 1) & 1, &S.failed);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int tok = 32 * wq + r8 + 8 * j;
 #pragma unroll
             for (int b = 0; b + 1 < kBlocks; b += 2) {
               const int off = (col0 / 16 + b / 2) * (16 * kTile) + tok * 16 + 2 * pair;
-              *reinterpret_cast<uint32_t*>(weights[0] + off) = hi[j][b] | (hi[j][b + 1] << 16);
-              *reinterpret_cast<uint32_t*>(weights[1] + off) = lo[j][b] | (lo[j][b + 1] << 16);
+              *reinterpret_cast<uint32_t*>(S.p[0] + off) = hi[j][b] | (hi[j][b + 1] << 16);
+              *reinterpret_cast<uint32_t*>(S.p[1] + off) = lo[j][b] | (lo[j][b + 1] << 16);
             }
             if constexpr (kBlocks & 1) {
               const int off = (kBlocks / 2) * (16 * kTile) + tok * 16 + pair;
-              *reinterpret_cast<uint16_t*>(weights[0] + off) = static_cast<uint16_t>(hi[j][kBlocks - 1]);
-              *reinterpret_cast<uint16_t*>(weights[1] + off) = static_cast<uint16_t>(lo[j][kBlocks - 1]);
+              *reinterpret_cast<uint16_t*>(S.p[0] + off) = static_cast<uint16_t>(hi[j][kBlocks - 1]);
+              *reinterpret_cast<uint16_t*>(S.p[1] + off) = static_cast<uint16_t>(lo[j][kBlocks - 1]);
             }
           }
           // ---- values that some row does not see: a zero weight times NaN is
@@ -879,7 +876,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           __syncwarp();
           fence_async();
           tc_before();
-          bar_arrive(&S.p_full[buf]);
+          bar_arrive(&S.p_full);
           if (k > 0) add_tile(it - 1);
         }
         Share nx = sh;
