@@ -88,7 +88,7 @@ typedef struct KdaCacheAttentionArgs {
   int32_t* err_flag;           /* or NULL */
 } KdaCacheAttentionArgs;
 
-#define KDA_CACHE_ATTENTION_COUNTER_BYTES 24576
+#define KDA_CACHE_ATTENTION_COUNTER_BYTES 45056
 
 /* Workspace bytes of a call with these head counts and max_new; -1 for an
  * argument out of range.  It does not grow with B, T or the lengths. */

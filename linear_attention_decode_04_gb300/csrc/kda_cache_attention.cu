@@ -57,7 +57,7 @@ constexpr int kMaxCtas = 304;              // 2 x 152
 // What beginning and ending a unit costs, in tiles: the work is dealt out by
 // tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
 constexpr int kUnitCost = 4;
-constexpr int kCounters = 4 * 456;         // of each kind: CTAs x warps that join, at most
+constexpr int kCounters = 4 * 6 * 152;     // of each kind: CTAs x warps that join, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -1048,8 +1048,8 @@ using Rows8 = Cfg<8, 1>;
 using Rows16 = Cfg<16, 1>;
 using Rows24 = Cfg<24, 1>;
 using Rows32 = Cfg<32, 1>;
-using Rows64 = Cfg<32, 2>;
-using Rows96 = Cfg<32, 3>;
+using Rows64 = Cfg<16, 4>;
+using Rows96 = Cfg<16, 6>;
 
 template <class C>
 constexpr size_t smem_bytes() {
