@@ -37,7 +37,7 @@ extern "C" {
  * Arguments.  T = query rows of the batch, D = 128.
  *
  *   q, out      bf16 [T][row stride], Hq * D channels; 16-byte aligned, row
- *               strides multiples of 8
+ *               strides multiples of 8; they must not overlap
  *   cu_seqlens  int32 [B+1], cu_seqlens[0] = 0, non-decreasing, <= T; a
  *               sequence whose bounds break this is skipped and
  *               KDA_DEVERR_SEQLENS (kda_chunk_metadata.h) is set

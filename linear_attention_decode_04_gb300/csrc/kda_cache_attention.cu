@@ -62,7 +62,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Params {
-  int B, T, Hq, Hkv, G, bs, num_blocks, max_blocks;
+  int B, T, Hq, Hkv, G, bs_log2, num_blocks, max_blocks;
   uint32_t g_mul;  // ceil(2^32 / G), or 0 where that is not exact for every row
   float scale;  // sm_scale * log2(e)
   const uint16_t* q;
@@ -84,11 +84,13 @@ struct Cfg {
   static constexpr int kRows = COLS * GROUPS;            // query rows of a tile
   static constexpr int kN = (kRows + 15) / 16 * 16;      // width of the products
   static constexpr int kThreads = 128 * GROUPS + 64;
-  static constexpr int kCtasPerSm = GROUPS > 1 ? 1 : 2;
+  static constexpr int kCtasPerSm = kRows > 32 ? 1 : 2;
+  // a group's pairs of 8-column blocks share 16 columns of the weights
+  static_assert(COLS % 16 == 0 || COLS == 8 || GROUPS == 1, "groups");
   // Ring depths in tiles.  A K tile is free after its S product, about a tile's
   // time before its V tile is; at 32 rows two CTAs fit an SM with K two deep.
-  static constexpr int kK = GROUPS > 2 ? 3 : GROUPS > 1 ? 4 : kN > 16 ? 2 : 3;
-  static constexpr int kV = GROUPS > 2 ? 4 : GROUPS > 1 ? 5 : 3;
+  static constexpr int kK = kRows > 32 ? 3 : kN > 16 ? 2 : 3;
+  static constexpr int kV = kRows > 32 ? 4 : 3;
   static constexpr int kNan = GROUPS > 1 ? 4 : 1;
   static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
   static constexpr int kPartial = COLS * (32 + 2);       // floats of a warp's partial record: maxima, sums, 32 channels
@@ -495,8 +497,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       }
       S.walk[0] = i;
       S.walk[1] = w.rt;
-      S.walk[2] = static_cast<int>(off) / c;
-      S.walk[3] = static_cast<int>(off) % c;
+      S.walk[2] = static_cast<int>(off / c);
+      S.walk[3] = static_cast<int>(off % c);
     };
     look(tid, prior + incl - mine, mine);
     for (int base = C::kThreads; all <= begin; base += C::kThreads) {  // larger batches
@@ -530,8 +532,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 
     if (warp == 4 * C::kGroups) {
       // ================================================================ producer
-      const int ppt = p.bs >= kTile ? 1 : kTile / p.bs;  // blocks of a tile
-      const int rows = p.bs >= kTile ? kTile : p.bs;     // rows of a copy
+      const int log2 = p.bs_log2, rows = min(1 << log2, kTile), ppt = kTile / rows;  // rows of a copy, copies of a tile
       struct Ref {
         int block, head, tok;
         bool valid;
@@ -544,12 +545,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         r.head = r.tok = 0;
         if (!more) return r;
         r.head = w.h;
-        const int64_t pos = static_cast<int64_t>(t) * kTile + lane * rows;
-        r.tok = p.bs > kTile ? static_cast<int>(pos % p.bs) : 0;
+        const int pos = t * kTile + (lane < ppt ? lane * rows : 0);  // (lengths end below 2^31 - 256)
+        r.tok = pos & ((1 << log2) - 1);
         const int last = min(w.n * p.G, (w.rt + 1) * C::kRows) - 1;
         const int limit = w.len - w.n + token_of(p, last) + 1;
         if (lane < ppt && pos < limit) {
-          const int64_t e = pos / p.bs;
+          const int e = pos >> log2;
           int b = -1;
           if (e < p.max_blocks) b = p.table[w.seq * p.table_stride + e];
           if (b < 0 || b >= p.num_blocks) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       Bcast<C>& bc = bcast[warp];
       float o[4][kMine], l[kMine], rs[kMine];
       uint32_t it = 0, unit = 0;
-      const int page0 = p.bs >= kTile ? 0 : 32 * wq / p.bs, page1 = p.bs >= kTile ? 0 : (32 * wq + 16) / p.bs;
+      const int page0 = 32 * wq >> p.bs_log2, page1 = (32 * wq + 16) >> p.bs_log2;  // 0 for blocks of 128 and more
       // The rows of a unit in registers: 16 threads per row, 8 channels each.  They
       // are asked for before the unit ahead of it ends.
       uint4 v[kBlocks];
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               *reinterpret_cast<uint32_t*>(S.p[1] + off) = lo[j][b] | (lo[j][b + 1] << 16);
             }
             if constexpr (kBlocks & 1) {
-              const int off = (kBlocks / 2) * (16 * kTile) + tok * 16 + pair;
+              const int off = (col0 + 8 * (kBlocks - 1)) / 16 * (16 * kTile) + tok * 16 + (col0 + 8 * (kBlocks - 1)) % 16 + pair;
               *reinterpret_cast<uint16_t*>(S.p[0] + off) = static_cast<uint16_t>(hi[j][kBlocks - 1]);
               *reinterpret_cast<uint16_t*>(S.p[1] + off) = static_cast<uint16_t>(lo[j][kBlocks - 1]);
             }
@@ -1047,7 +1048,7 @@ EncodeFn g_encode;
 using Rows8 = Cfg<8, 1>;
 using Rows16 = Cfg<16, 1>;
 using Rows24 = Cfg<24, 1>;
-using Rows32 = Cfg<32, 1>;
+using Rows32 = Cfg<16, 2>;
 using Rows64 = Cfg<16, 4>;
 using Rows96 = Cfg<16, 6>;
 
@@ -1171,7 +1172,8 @@ extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream)
     if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
   }
   Params p{};
-  p.B = a->B, p.T = a->T, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.bs = bs;
+  p.B = a->B, p.T = a->T, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
+  while ((1 << p.bs_log2) < bs) ++p.bs_log2;
   // exact below 2^32 / G, and a row is below T * G
   p.g_mul = p.G > 1 && static_cast<int64_t>(a->T) * p.G * p.G < (1LL << 32) ? static_cast<uint32_t>(((1ULL << 32) + p.G - 1) / p.G) : 0;
   p.num_blocks = a->num_blocks, p.max_blocks = a->max_blocks;
