@@ -20,6 +20,11 @@
  *     slot_map[t]  = block_table[i][positions[t] / bs] * bs + positions[t] % bs
  *   rows t = cu_seqlens[B] .. T - 1 (padding of a captured step):
  *     positions[t] = 0, slot_map[t] = -1
+ * A request whose last step was cut back (drafted tokens that did not stand)
+ * still holds the blocks it was given for them.  With held_blocks, h_i takes
+ * the place of ceil(c_i / bs) above wherever it is larger, so that such blocks
+ * are used before the list; held_blocks_out[i] is the count after this step,
+ * the next step's h_i (blocks that the list did not have are not counted).
  */
 #ifndef KDA_BLOCK_TABLES_H
 #define KDA_BLOCK_TABLES_H
@@ -60,6 +65,8 @@ typedef struct KdaBlockTablesArgs {
   int32_t num_free;              /* entries of free_blocks */
   const int32_t* cached_lens;    /* [B] */
   const int32_t* new_lens;       /* [B] */
+  const int32_t* held_blocks;    /* [B] or NULL: table entries that hold blocks, see below */
+  int32_t* held_blocks_out;      /* [B] or NULL, another array than held_blocks */
   int32_t* block_table;          /* [B][block_table_stride] */
   int64_t block_table_stride;    /* elements, >= max_blocks */
   const int32_t* free_blocks;    /* [num_free] */

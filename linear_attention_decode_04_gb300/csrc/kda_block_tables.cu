@@ -24,7 +24,8 @@ constexpr int kTile = kThreads * kPer;
 
 struct Params {
   int B, max_blocks, bs, num_blocks, T, num_free;
-  const int32_t *cached, *fresh;
+  const int32_t *cached, *fresh, *held;
+  int32_t* held_out;
   int32_t* table;
   int64_t table_stride;
   const int32_t *free_blocks, *free_head;
@@ -46,10 +47,11 @@ __device__ __forceinline__ Request request(const Params& p, int i) {
   r.c = c < 0 ? 0 : c;
   r.n = r.bad ? 0 : n;
   // ceil without the overflow of c + bs - 1
-  const int have = r.c / p.bs + (r.c % p.bs != 0), end = (r.c + r.n) / p.bs + ((r.c + r.n) % p.bs != 0);
+  const int full = r.c / p.bs + (r.c % p.bs != 0), have = p.held ? max(full, p.held[i]) : full;
+  const int end = (r.c + r.n) / p.bs + ((r.c + r.n) % p.bs != 0);
   r.first = have;
   r.over = r.n > 0 && end > p.max_blocks;
-  r.need = min(end, p.max_blocks) - min(have, p.max_blocks);
+  r.need = max(min(end, p.max_blocks) - min(have, p.max_blocks), 0);
   return r;
 }
 
@@ -105,7 +107,13 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const Params p) 
       const int j = tid * kPer + k;
       tok_s[j] = ns;
       blk_s[j] = bo;
-      if (first_cta && base + j < p.B) p.cu[base + j] = static_cast<int32_t>(ns < 0x7fffffff ? ns : 0x7fffffff);
+      if (first_cta && base + j < p.B) {
+        p.cu[base + j] = static_cast<int32_t>(ns < 0x7fffffff ? ns : 0x7fffffff);
+        if (p.held_out) {  // what the request held, and of the new blocks those that the list had
+          const int64_t from = head + bo, got = from < 0 ? 0 : min(max(p.num_free - from, int64_t{0}), need[k]);
+          p.held_out[base + j] = min(request(p, base + j).first, p.max_blocks) + static_cast<int>(got);
+        }
+      }
       ns += n[k];
       bo += need[k];
     }
@@ -181,12 +189,15 @@ extern "C" int kda_block_tables(const KdaBlockTablesArgs* a, void* stream) {
     return kda_internal_fail(KDA_ERR_NULLPTR, "a required pointer is NULL");
   if (a->free_head == a->free_head_out)
     return kda_internal_fail(KDA_ERR_SHAPE, "free_head and free_head_out must be two words");
-  if (misaligned(a->cached_lens, 3) || misaligned(a->new_lens, 3) || misaligned(a->block_table, 3) ||
+  if (a->held_blocks && a->held_blocks == a->held_blocks_out)
+    return kda_internal_fail(KDA_ERR_SHAPE, "held_blocks and held_blocks_out must be two arrays");
+  if (misaligned(a->held_blocks, 3) || misaligned(a->held_blocks_out, 3) || misaligned(a->cached_lens, 3) || misaligned(a->new_lens, 3) || misaligned(a->block_table, 3) ||
       misaligned(a->free_blocks, 3) || misaligned(a->free_head, 3) || misaligned(a->free_head_out, 3) ||
       misaligned(a->cu_seqlens, 3) || misaligned(a->seq_lens, 3) || misaligned(a->positions, 3) ||
       misaligned(a->slot_map, 7) || misaligned(a->err_flag, 3))
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer is not aligned as required");
   const Params p{a->B, a->max_blocks, a->block_size, a->num_blocks, a->T, a->num_free, a->cached_lens, a->new_lens,
+                 a->held_blocks, a->held_blocks_out,
                  a->block_table, a->block_table_stride, a->free_blocks, a->free_head, a->free_head_out,
                  a->cu_seqlens, a->seq_lens, a->positions, a->slot_map, a->err_flag};
   const unsigned grid = a->T > kThreads ? static_cast<unsigned>((static_cast<int64_t>(a->T) + kThreads - 1) / kThreads) : 1u;

@@ -34,7 +34,8 @@ _i32, _i64, _u32, _f32, _ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, 
 class KdaBlockTablesArgs(ctypes.Structure):
     """Mirror of ``KdaBlockTablesArgs`` (field order and types must match)."""
     _fields_ = [("struct_size", _u32), ("B", _i32), ("max_blocks", _i32), ("block_size", _i32), ("num_blocks", _i32),
-                ("T", _i32), ("num_free", _i32), ("cached_lens", _ptr), ("new_lens", _ptr), ("block_table", _ptr),
+                ("T", _i32), ("num_free", _i32), ("cached_lens", _ptr), ("new_lens", _ptr), ("held_blocks", _ptr),
+                ("held_blocks_out", _ptr), ("block_table", _ptr),
                 ("block_table_stride", _i64), ("free_blocks", _ptr), ("free_head", _ptr), ("free_head_out", _ptr),
                 ("cu_seqlens", _ptr), ("seq_lens", _ptr), ("positions", _ptr), ("slot_map", _ptr), ("err_flag", _ptr)]
 
@@ -128,10 +129,14 @@ class KdaBlockTablesCall(_Call):
     in tensors that the call owns: ``cu_seqlens`` [B + 1], ``seq_lens`` [B],
     ``positions`` and ``slot_map`` (int64) [num_tokens], ``free_head_out``
     [1].  ``num_tokens`` is the row count of the step (the sum of the new
-    lengths, or a captured step's fixed size: the rows behind get slot -1)."""
+    lengths, or a captured step's fixed size: the rows behind get slot -1).
+    ``held_blocks`` int32 [B]: the table entries that already hold blocks,
+    where that may be more than the cached tokens need (a multi-token step
+    whose drafts did not all stand); ``held_blocks_out`` [B] is the count
+    after the call (also without ``held_blocks``)."""
 
     def __init__(self, cached_lens, new_lens, block_table, free_blocks, free_head=None, *, block_size: int,
-                 num_blocks: int, num_tokens: int, err_flag=None):
+                 num_blocks: int, num_tokens: int, held_blocks=None, err_flag=None):
         dev = block_table.device
         _check(block_table, "block_table", torch.int32, None)
         if block_table.dim() != 2 or block_table.shape[1] < 1 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
@@ -145,6 +150,8 @@ class KdaBlockTablesCall(_Call):
         _dense(free_blocks, "free_blocks")
         if free_head is not None:
             _shaped(free_head, "free_head", torch.int32, dev, (1,))
+        if held_blocks is not None:
+            _shaped(held_blocks, "held_blocks", torch.int32, dev, (B,))
         _err(err_flag, dev)
         stride = block_table.stride(0) if B > 1 else max(block_table.stride(0), M)
         if stride < M:
@@ -153,29 +160,32 @@ class KdaBlockTablesCall(_Call):
         self.cu_seqlens, self.seq_lens = torch.empty(B + 1, **i32), torch.empty(B, **i32)
         self.positions = torch.empty(int(num_tokens), **i32)
         self.slot_map = torch.empty(int(num_tokens), dtype=torch.int64, device=dev)
-        self.free_head_out = torch.empty(1, **i32)
-        own = (self.cu_seqlens, self.seq_lens, self.positions, self.slot_map, self.free_head_out)
+        self.free_head_out, self.held_blocks_out = torch.empty(1, **i32), torch.empty(B, **i32)
+        own = (self.cu_seqlens, self.seq_lens, self.positions, self.slot_map, self.free_head_out, self.held_blocks_out)
         args = KdaBlockTablesArgs(
             B=B, max_blocks=M, block_size=int(block_size), num_blocks=int(num_blocks), T=int(num_tokens),
             num_free=free_blocks.numel(), cached_lens=_p(cached_lens), new_lens=_p(new_lens),
+            held_blocks=_p(held_blocks), held_blocks_out=_p(self.held_blocks_out),
             block_table=_p(block_table), block_table_stride=stride, free_blocks=_p(free_blocks),
             free_head=_p(free_head), free_head_out=_p(self.free_head_out), cu_seqlens=_p(self.cu_seqlens),
             seq_lens=_p(self.seq_lens), positions=_p(self.positions), slot_map=_p(self.slot_map),
             err_flag=_p(err_flag))
         self._prepare("kda_block_tables", args, dev,
-                      (cached_lens, new_lens, block_table, free_blocks, free_head, err_flag), own)
+                      (cached_lens, new_lens, block_table, free_blocks, free_head, held_blocks, err_flag), own)
 
 
 def kda_block_tables(cached_lens, new_lens, block_table, free_blocks, free_head=None, *, block_size: int,
-                     num_blocks: int, num_tokens: int, err_flag=None, stream: torch.cuda.Stream | None = None):
+                     num_blocks: int, num_tokens: int, held_blocks=None, err_flag=None,
+                     stream: torch.cuda.Stream | None = None):
     """Build one step's metadata on the GPU; ``block_table`` is completed in
     place.  Returns ``(cu_seqlens, seq_lens, positions, slot_map,
-    free_head_out)`` as described on ``KdaBlockTablesCall``."""
+    free_head_out, held_blocks_out)`` as described on ``KdaBlockTablesCall``."""
     with torch.cuda.stream(stream):
         c = KdaBlockTablesCall(cached_lens, new_lens, block_table, free_blocks, free_head, block_size=block_size,
-                               num_blocks=num_blocks, num_tokens=num_tokens, err_flag=err_flag)
+                               num_blocks=num_blocks, num_tokens=num_tokens, held_blocks=held_blocks,
+                               err_flag=err_flag)
         c(stream)
-    return c.cu_seqlens, c.seq_lens, c.positions, c.slot_map, c.free_head_out
+    return c.cu_seqlens, c.seq_lens, c.positions, c.slot_map, c.free_head_out, c.held_blocks_out
 
 
 # ------------------------------------------------------------- norm and rotation

@@ -13,11 +13,11 @@ E4M3_MAX = 448.0
 SEQLENS, CAPACITY, SLOT_RANGE, TOKEN_RANGE = 4, 8, 1, 32
 
 
-def block_tables(cached, new, table, free, head, bs, num_blocks, T):
-    """Returns (table, cu, seq_lens, positions, slot_map, head_out, error bits)."""
+def block_tables(cached, new, table, free, head, bs, num_blocks, T, held=None):
+    """Returns (table, cu, seq_lens, positions, slot_map, head_out, held_out, error bits)."""
     table, err = np.array(table), 0
     B, M = table.shape
-    cu, lens, pos, slot = [0], [], [0] * T, [-1] * T
+    cu, lens, pos, slot, held_out = [0], [], [0] * T, [-1] * T, []
     at, t = head, 0
     for i in range(B):
         c, n = int(cached[i]), int(new[i])
@@ -25,12 +25,16 @@ def block_tables(cached, new, table, free, head, bs, num_blocks, T):
             err |= SEQLENS
             c, n = max(c, 0), 0
         first, end = -(-c // bs), -(-(c + n) // bs)
+        if held is not None:
+            first = max(first, int(held[i]))
+        has = min(first, M)
         if n > 0 and end > M:
             err |= CAPACITY
         got = {}
         for k in range(first, min(end, M)):
             if 0 <= at < len(free):
                 got[k] = int(free[at])
+                has += has == k
                 if not 0 <= got[k] < num_blocks:
                     got[k], err = -1, err | SLOT_RANGE
             else:
@@ -54,9 +58,10 @@ def block_tables(cached, new, table, free, head, bs, num_blocks, T):
             t += 1
         cu.append(t)
         lens.append(c + n)
+        held_out.append(has)
     if t > T:
         err |= CAPACITY
-    return table, cu, lens, pos, slot, min(at, max(len(free), head)), err
+    return table, cu, lens, pos, slot, min(at, max(len(free), head)), held_out, err
 
 
 def norm_rotate(x, w, pos, inv_freq, interleaved, eps):

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 
 def run(dev, cached, new, bs, *, T=None, M=None, num_blocks=None, free=None, head=0, seed=0, row_pad=0, table=None,
-        with_head=True):
+        with_head=True, held=None):
     rng = np.random.default_rng(seed)
     cached, new = np.asarray(cached, np.int32), np.asarray(new, np.int32)
     B = len(cached)
@@ -22,27 +22,28 @@ def run(dev, cached, new, bs, *, T=None, M=None, num_blocks=None, free=None, hea
         table = np.full((B, M), -5, np.int32)
         at = 0
         for b in range(B):
-            k = min(-(-max(int(cached[b]), 0) // bs), M)
+            k = min(max(-(-max(int(cached[b]), 0) // bs), 0 if held is None else held[b]), M)
             table[b, :k] = ids[at:at + k]
             at += k
         ids = ids[at:]
     free = ids if free is None else np.asarray(free, np.int32)
     T = max(0, int(np.maximum(new, 0).sum())) if T is None else T
-    want = R.block_tables(cached, new, table, free, head, bs, num_blocks, T)
+    want = R.block_tables(cached, new, table, free, head, bs, num_blocks, T, held)
     t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
     wide = torch.full((B, M + row_pad), -77, dtype=torch.int32, device=dev)
     wide[:, :M] = t(table)
     err = torch.zeros(1, dtype=torch.int32, device=dev)
     got = kda_block_tables(t(cached), t(new), wide[:, :M], t(free), torch.tensor([head], dtype=torch.int32, device=dev)
-                           if with_head else None, block_size=bs, num_blocks=num_blocks, num_tokens=T, err_flag=err)
+                           if with_head else None, held_blocks=None if held is None else t(np.asarray(held, np.int32)), block_size=bs, num_blocks=num_blocks, num_tokens=T, err_flag=err)
     torch.cuda.synchronize(dev)
     assert np.array_equal(wide[:, :M].cpu().numpy(), want[0])
     assert bool((wide[:, M:] == -77).all())
     for g, w in zip(got, want[1:5]):
         assert g.cpu().tolist() == list(w)
     assert got[4].item() == want[5]
-    assert err.item() == want[6]
-    return want[6]
+    assert got[5].cpu().tolist() == want[6]
+    assert err.item() == want[7]
+    return want[7]
 
 
 @pytest.mark.parametrize("bs", [1, 16, 24, 64, 256])
@@ -53,6 +54,16 @@ def test_random_batches(bs, cuda_device):
         new = rng.integers(0, 5, B) * (rng.random(B) < 0.9)
         new[rng.integers(0, B)] = 300
         assert run(cuda_device, rng.integers(0, 200, B), new, bs, seed=B, head=3, row_pad=2) == 0
+
+
+def test_held_blocks_are_used_before_the_list(cuda_device):
+    rng = np.random.default_rng(4)
+    for B in (3, 600, 2500):
+        cached, new = rng.integers(0, 100, B), rng.integers(0, 9, B)
+        held = [-(-int(c) // 16) + int(k) for c, k in zip(cached, rng.integers(-1, 3, B))]   # too few count as enough
+        assert run(cuda_device, cached, new, 16, held=held, M=12, num_blocks=20 * B + 40, seed=B) == 0
+    assert run(cuda_device, [10, 20], [40, 5], 16, held=[2, 2], free=[3], num_blocks=40) == R.CAPACITY
+    assert run(cuda_device, [10], [2], 16, held=[9], M=4, num_blocks=40) == 0                 # more than the row has
 
 
 def test_edges(cuda_device):
@@ -98,7 +109,7 @@ def test_graph_replay_follows_the_lengths(cuda_device):
     for _ in range(40):                                # several blocks per request, one token at a time
         g.replay()
         torch.cuda.synchronize(dev)
-        t, _, lens, pos, slot, h, err = R.block_tables(c, [1] * B, t, free.tolist(), h, bs, 200, B)
+        t, _, lens, pos, slot, h, _, err = R.block_tables(c, [1] * B, t, free.tolist(), h, bs, 200, B)
         assert err == 0 and call.slot_map.tolist() == slot and call.positions.tolist() == pos
         assert head.item() == h and np.array_equal(table.cpu().numpy(), t)
         c = np.asarray(lens)
