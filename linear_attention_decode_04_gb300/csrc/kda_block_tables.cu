@@ -24,6 +24,7 @@ constexpr int kTile = kThreads * kPer;
 
 struct Params {
   int B, max_blocks, bs, num_blocks, T, num_free;
+  int log2;  // of bs, or -1
   const int32_t *cached, *fresh, *held;
   int32_t* held_out;
   int32_t* table;
@@ -34,6 +35,8 @@ struct Params {
   int32_t* err;
 };
 
+// pos / bs: a shift for the usual sizes (a division takes some 40 instructions)
+__device__ __forceinline__ int block_of(const Params& p, int pos) { return p.log2 >= 0 ? pos >> p.log2 : pos / p.bs; }
 // A request's lengths with what is out of range taken out: new tokens,
 // first and number of new table entries.
 struct Request {
@@ -47,8 +50,9 @@ __device__ __forceinline__ Request request(const Params& p, int i) {
   r.c = c < 0 ? 0 : c;
   r.n = r.bad ? 0 : n;
   // ceil without the overflow of c + bs - 1
-  const int full = r.c / p.bs + (r.c % p.bs != 0), have = p.held ? max(full, p.held[i]) : full;
-  const int end = (r.c + r.n) / p.bs + ((r.c + r.n) % p.bs != 0);
+  const int cb = block_of(p, r.c), eb = block_of(p, r.c + r.n), full = cb + (r.c != cb * p.bs);
+  const int have = p.held ? max(full, p.held[i]) : full;
+  const int end = eb + (r.c + r.n != eb * p.bs);
   r.first = have;
   r.over = r.n > 0 && end > p.max_blocks;
   r.need = max(min(end, p.max_blocks) - min(have, p.max_blocks), 0);
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const Params p) 
       const int i = base + lo;
       const Request r = request(p, i);
       const int pos = r.c + static_cast<int>(row - tok_s[lo]);
-      const int page = pos / p.bs, at = pos - page * p.bs;
+      const int page = block_of(p, pos), at = pos - page * p.bs;
       int b = -1;
       if (page < p.max_blocks) {
         int32_t* entry = p.table + i * p.table_stride + page;
@@ -196,7 +200,10 @@ extern "C" int kda_block_tables(const KdaBlockTablesArgs* a, void* stream) {
       misaligned(a->cu_seqlens, 3) || misaligned(a->seq_lens, 3) || misaligned(a->positions, 3) ||
       misaligned(a->slot_map, 7) || misaligned(a->err_flag, 3))
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer is not aligned as required");
-  const Params p{a->B, a->max_blocks, a->block_size, a->num_blocks, a->T, a->num_free, a->cached_lens, a->new_lens,
+  int log2 = -1;
+  if ((a->block_size & (a->block_size - 1)) == 0)
+    for (log2 = 0; (1 << log2) < a->block_size;) ++log2;
+  const Params p{a->B, a->max_blocks, a->block_size, a->num_blocks, a->T, a->num_free, log2, a->cached_lens, a->new_lens,
                  a->held_blocks, a->held_blocks_out,
                  a->block_table, a->block_table_stride, a->free_blocks, a->free_head, a->free_head_out,
                  a->cu_seqlens, a->seq_lens, a->positions, a->slot_map, a->err_flag};

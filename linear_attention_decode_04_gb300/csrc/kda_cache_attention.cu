@@ -435,6 +435,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     bar_init(&S.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     S.failed = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
   __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -482,7 +484,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   // one position at least for each CTA that takes part, so that every CTA between
   // a unit's first and last leaves a part of it
   const int64_t cta = blockIdx.x, ctas = max(min(static_cast<int64_t>(gridDim.x), total), int64_t{1});
-  const int64_t begin = cta < ctas ? cta * total / ctas : 0, end = cta < ctas ? (cta + 1) * total / ctas : 0;
+  // (32-bit division where it is enough: 64-bit ones take longer than the scan)
+  auto share_of = [&](int64_t c) {
+    return total < (1 << 22) ? static_cast<int64_t>(static_cast<uint32_t>(c * total) / static_cast<uint32_t>(ctas))
+                             : c * total / ctas;
+  };
+  const int64_t begin = cta < ctas ? share_of(cta) : 0, end = cta < ctas ? share_of(cta + 1) : 0;
   if (begin < end) {
     auto look = [&](int i, int64_t from, int64_t cost) {  // whether the share begins in sequence i
       if (cost == 0 || begin < from || begin >= from + cost) return;
@@ -497,8 +504,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       }
       S.walk[0] = i;
       S.walk[1] = w.rt;
-      S.walk[2] = static_cast<int>(off / c);
-      S.walk[3] = static_cast<int>(off % c);
+      const bool small = off < 0x7fffffff;
+      S.walk[2] = small ? static_cast<int>(off) / c : static_cast<int>(off / c);
+      S.walk[3] = small ? static_cast<int>(off) % c : static_cast<int>(off % c);
     };
     look(tid, prior + incl - mine, mine);
     for (int base = C::kThreads; all <= begin; base += C::kThreads) {  // larger batches

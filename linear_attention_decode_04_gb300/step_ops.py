@@ -70,6 +70,9 @@ class KdaVerifyArgs(ctypes.Structure):
                 ("num_accepted", _ptr), ("next_slot", _ptr), ("err_flag", _ptr)]
 
 
+_current_raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
+
+
 def _p(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -98,12 +101,11 @@ class _Call:
         self._home = torch.cuda.current_stream(device).cuda_stream
 
     def __call__(self, stream: torch.cuda.Stream | None = None) -> None:
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        s = stream.cuda_stream
+        # the stream's handle alone: a Stream object takes 2 us to make, which is what a small call takes on the GPU
+        s = _current_raw_stream(self._index) if stream is None else stream.cuda_stream
         if s != self._home and self._own and not torch.cuda.is_current_stream_capturing():
             for t in self._own:
-                t.record_stream(stream)
+                t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
         if torch.cuda.current_device() == self._index:
             rc = self._fn(self._argp, s)
         else:
