@@ -113,7 +113,7 @@ struct alignas(1024) Smem {
   float wsum[C::kGroups][4][C::kCols];
   int nan_at[C::kNan][kD];                // per unit and channel: first position that holds a NaN value
   int64_t total;                          // cost of all work, for the few places that need it again
-  int walk[4];                            // where this CTA's tiles start
+  int walk[7];                            // where this CTA's tiles start
   int64_t scan[C::kThreads / 32], beyond[C::kThreads / 32];
   uint32_t tmem;
   int failed;
@@ -351,6 +351,10 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n, int len, int rt)
   return limit <= kTile ? 1 : (limit + kTile - 1) / kTile;
 }
 template <class C>
+__device__ __forceinline__ int rows_to_tiles(const Params& p, int n) {
+  return static_cast<int>((static_cast<int64_t>(n) * p.G + C::kRows - 1) / C::kRows);
+}
+template <class C>
 __device__ __forceinline__ bool load_seq(const Params& p, Walk& w) {  // false: nothing to do in this sequence
   if (w.seq < 0 || w.seq >= p.B) {  // cannot be; an empty end of the walk rather than a stray read
     w.q0 = w.n = w.len = w.rt = w.h = 0;
@@ -365,7 +369,7 @@ __device__ __forceinline__ bool load_seq(const Params& p, Walk& w) {  // false: 
   if (w.len > 0x7fffff00) w.len = 0x7fffff00;
   if (w.len < 0) w.len = 0;
   w.rt = w.h = 0;
-  w.rts = static_cast<int>((static_cast<int64_t>(w.n) * p.G + C::kRows - 1) / C::kRows);
+  w.rts = rows_to_tiles<C>(p, w.n);
   return w.n > 0;
 }
 template <class C>
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         c = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
       }
       S.walk[0] = i;
+      S.walk[4] = w.n, S.walk[5] = w.len, S.walk[6] = w.q0;
       S.walk[1] = w.rt;
       const bool small = off < 0x7fffffff;
       S.walk[2] = small ? static_cast<int>(off) / c : static_cast<int>(off / c);
@@ -528,7 +533,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     Share sh;
     Walk& w = sh.w;
     w.seq = S.walk[0];
-    load_seq<C>(p, w);
+    w.n = S.walk[4], w.len = S.walk[5], w.q0 = S.walk[6];
+    w.rts = rows_to_tiles<C>(p, w.n);
     w.rt = S.walk[1];
     w.h = S.walk[2];
     w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
@@ -959,29 +965,58 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
           if (own < kCols) rec[own] = run, rec[kCols + own] = lsum;
           // Joins the records of CTAs from, from + step .. to in this order, into the
-          // first of them or into the output: 8 lanes per row, four channels each.
+          // first of them or into the output: 8 lanes per row, four channels each.  Eight
+          // parts at a time: lane = part for the maxima and sums, so that they take one
+          // trip to memory, and the channels of four parts are on their way together.
           auto join = [&](int from, int step, int to, bool into_out) {
-            const int sub = lane >> 3, l4 = lane & 7;
+            constexpr int kAhead = C::kGroups > 1 ? 1 : kMine > 4 ? 2 : 4;
+            const int sub = lane >> 3, l4 = lane & 7, parts = (to - from) / step + 1;
             float top[kMine], sum[kMine];
             float4 acc[kMine];
 #pragma unroll
             for (int i = 0; i < kMine; ++i) top[i] = -INFINITY, sum[i] = 0.f, acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int part = from; part <= to; part += step) {
-              const float* rp = record(part);
-#pragma unroll
-              for (int i = 0; i < kMine; ++i) top[i] = fmaxf(top[i], __ldcg(rp + sub + 4 * i));
-            }
-#pragma unroll 2
-            for (int part = from; part <= to; part += step) {
-              const float* rp = record(part);
+#pragma unroll 1
+            for (int n0 = 0; n0 < parts; n0 += 8) {
+              const bool mine = n0 + l4 < parts;
+              const float* rm = record(from + min(n0 + l4, parts - 1) * step) + sub;
+              float f[kMine], part_sum[kMine];
 #pragma unroll
               for (int i = 0; i < kMine; ++i) {
-                const int row = sub + 4 * i;
-                const float f = ex2(__ldcg(rp + row) - (top[i] == -INFINITY ? 0.f : top[i]));
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(rp + 2 * kCols + row * 32) + l4);
-                sum[i] += f * __ldcg(rp + kCols + row);
-                acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
+                f[i] = mine ? __ldcg(rm + 4 * i) : -INFINITY;
+                part_sum[i] = mine ? __ldcg(rm + kCols + 4 * i) : 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < kMine; ++i) {
+                float next = fmaxf(top[i], f[i]);
+#pragma unroll
+                for (int s = 1; s < 8; s <<= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, s));
+                const float ref = next == -INFINITY ? 0.f : next, old = ex2(top[i] - ref);
+                f[i] = ex2(f[i] - ref);
+                float more_sum = f[i] * part_sum[i];
+#pragma unroll
+                for (int s = 1; s < 8; s <<= 1) more_sum += __shfl_xor_sync(0xffffffffu, more_sum, s);
+                top[i] = next;
+                sum[i] = sum[i] * old + more_sum;
+                acc[i].x *= old, acc[i].y *= old, acc[i].z *= old, acc[i].w *= old;
+              }
+#pragma unroll 1
+              for (int n = 0; n < 8 && n0 + n < parts; n += kAhead) {
+                float4 x[kAhead][kMine];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                  const float* rp = record(from + min(n0 + n + k, parts - 1) * step) + 2 * kCols + sub * 32;
+#pragma unroll
+                  for (int i = 0; i < kMine; ++i) x[k][i] = __ldcg(reinterpret_cast<const float4*>(rp + 128 * i) + l4);
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                  for (int i = 0; i < kMine; ++i) {
+                    const float w8 = __shfl_sync(0xffffffffu, f[i], (lane & 24) | (n + k));
+                    if (n0 + n + k >= parts) continue;  // the warp as one
+                    acc[i].x += w8 * x[k][i].x, acc[i].y += w8 * x[k][i].y;
+                    acc[i].z += w8 * x[k][i].z, acc[i].w += w8 * x[k][i].w;
+                  }
               }
             }
             __syncwarp();  // the warp has read the record that it may now write
