@@ -26,9 +26,10 @@
  * into [0, 1] (NaN counts as 0), the weights max(p - q, 0), or p, are integers
  * in units of 2^-60, exact wherever p and q are 0 or at least 2^-37 and else off by at
  * most 3 units, and x is the lowest index whose inclusive running sum exceeds
- * floor(floor(sample_u * 2^31) * total / 2^31).  Probabilities of a row sum
- * to about 1 (at most 7); sample_u is taken into [0, 1 - 2^-31], NaN as 0.
- * Where a row has no mass at all x is V - 1.
+ * floor(floor(sample_u * 2^31) * total / 2^31); sample_u is taken into
+ * [0, 1 - 2^-31], NaN as 0.  Probabilities of a row sum to about 1, at most
+ * 7 (of a row that sums to more x is some token in [0, V)).  Where a row has
+ * no mass at all x is V - 1.
  */
 #ifndef KDA_VERIFY_H
 #define KDA_VERIFY_H
@@ -61,7 +62,8 @@ typedef struct KdaVerifyArgs {
   const int32_t* slot_idx;     /* [N][T] or NULL, the multi-token step's */
   int32_t* tokens;             /* [N][T] */
   int32_t* num_accepted;       /* [N] */
-  int32_t* next_slot;          /* [N]; NULL exactly when slot_idx is */
+  int32_t* next_slot;          /* [N]; NULL exactly when slot_idx is; may be src_slot itself, no other
+                                * result may overlap an input */
   int32_t* err_flag;           /* or NULL */
 } KdaVerifyArgs;
 

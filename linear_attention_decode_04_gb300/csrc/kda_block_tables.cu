@@ -195,7 +195,14 @@ extern "C" int kda_block_tables(const KdaBlockTablesArgs* a, void* stream) {
     return kda_internal_fail(KDA_ERR_SHAPE, "free_head and free_head_out must be two words");
   if (a->held_blocks && a->held_blocks == a->held_blocks_out)
     return kda_internal_fail(KDA_ERR_SHAPE, "held_blocks and held_blocks_out must be two arrays");
-  if (misaligned(a->held_blocks, 3) || misaligned(a->held_blocks_out, 3) || misaligned(a->cached_lens, 3) || misaligned(a->new_lens, 3) || misaligned(a->block_table, 3) ||
+  // every CTA reads all lengths for itself, some after others have written
+  const void* const in[] = {a->cached_lens, a->new_lens, a->held_blocks, a->free_blocks, a->free_head};
+  const void* const results[] = {a->seq_lens, a->cu_seqlens, a->held_blocks_out, a->positions, a->block_table};
+  for (const void* x : in)
+    for (const void* y : results)
+      if (x && x == y) return kda_internal_fail(KDA_ERR_SHAPE, "a result may not take the place of an input");
+  if (misaligned(a->held_blocks, 3) || misaligned(a->held_blocks_out, 3) || misaligned(a->cached_lens, 3) ||
+      misaligned(a->new_lens, 3) || misaligned(a->block_table, 3) ||
       misaligned(a->free_blocks, 3) || misaligned(a->free_head, 3) || misaligned(a->free_head_out, 3) ||
       misaligned(a->cu_seqlens, 3) || misaligned(a->seq_lens, 3) || misaligned(a->positions, 3) ||
       misaligned(a->slot_map, 7) || misaligned(a->err_flag, 3))

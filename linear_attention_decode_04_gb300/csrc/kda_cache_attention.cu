@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll
           for (int i = 0; i < 4; ++i) lsum += S.wsum[g][i][own];
           const float f = S.row_scale[col0 + own];
-          if (f != f) lsum = f;  // a row that is not finite
+          if (f != f && S.limit[col0 + own] > 0) lsum = f;  // a row that is not finite (one that sees nothing stays zero)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1070,8 +1070,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         more = then;
       }
     }
-    // every product has ended before the accumulators are given back
-    if (warp == 0) bar_wait(&S.done, 0, &S.failed);
+    // every product has ended before the accumulators are given back, given up or not
+    if (warp == 0 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
   }
   tc_before();
   __syncthreads();
@@ -1186,6 +1186,7 @@ extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream)
   if (a->q_row_stride < width || a->out_row_stride < width || a->block_table_stride < a->max_blocks ||
       a->token_stride < kD || a->head_stride < kD || a->block_stride < kD)
     return kda_internal_fail(KDA_ERR_SHAPE, "a stride is smaller than the row");
+  if (a->q == a->out) return kda_internal_fail(KDA_ERR_SHAPE, "out may not be q");
   const int64_t need = kda_cache_attention_workspace_bytes(Hq, Hkv, a->max_new);
   if (a->workspace_bytes < need)
     return kda_internal_fail(KDA_ERR_SHAPE, "workspace of %lld bytes, %lld needed",

@@ -515,6 +515,10 @@ extern "C" int kda_qk_rope(const KdaQkRopeArgs* a, void* stream) {
     return kda_internal_fail(KDA_ERR_SHAPE, "a cache stride is smaller than a row");
   if (cache && a->k_out && a->k_out == a->qkv + static_cast<int64_t>(a->num_q_heads) * kD)
     return kda_internal_fail(KDA_ERR_SHAPE, "k_out may not be the k part of qkv when keys are cached");
+  // in place every warp writes the rows it has read, and only those
+  if ((a->q_out == a->qkv && a->q_row_stride != a->qkv_row_stride) ||
+      (a->k_out && a->k_out == a->qkv + static_cast<int64_t>(a->num_q_heads) * kD && a->k_row_stride != a->qkv_row_stride))
+    return kda_internal_fail(KDA_ERR_SHAPE, "an output in the place of its input needs the input's row stride");
   if (misaligned(a->qkv, 15) || (a->qkv_row_stride & 7) || misaligned(a->q_out, 15) || (a->q_row_stride & 7) ||
       misaligned(a->k_out, 15) || (a->k_out && (a->k_row_stride & 7)) || misaligned(a->positions, 3) ||
       misaligned(a->freqs, 7) || misaligned(a->q_weight, 15) || misaligned(a->k_weight, 15) ||

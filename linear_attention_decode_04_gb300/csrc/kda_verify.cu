@@ -203,7 +203,7 @@ __device__ __forceinline__ void search(const Row& r, int begin, int end, uint64_
     if (goal >= here && goal < here + mine) {
       int j = 0;
       while (j < 3 && goal >= here + w[j]) here += w[j++];
-      *token = i + j;
+      *token = min(i + j, end - 1);  // (past the end only where sums ran over)
     }
     if (goal < before) return;
   }
@@ -250,13 +250,12 @@ __device__ __forceinline__ uint64_t goal_of(const Params& p, int n, uint64_t tot
   const uint64_t u31 = u < 1.f ? static_cast<uint64_t>(u * 0x1p31f) : 0x7fffffffu;
   return __umul64hi(u31 << 33, total);
 }
-__device__ __forceinline__ void write_results(const Params& p, int n, int k, bool massless) {
+__device__ __forceinline__ void write_results(const Params& p, int n, int k) {
   const int tid = threadIdx.x;
   if (tid < p.T && tid != k) p.tokens[static_cast<int64_t>(n) * p.T + tid] = tid < k ? p.draft[static_cast<int64_t>(n) * (p.T - 1) + tid] : -1;
   if (tid == 0) {
     p.accepted[n] = k;
     if (p.next) p.next[n] = p.slots[static_cast<int64_t>(n) * p.T + k];
-    if (massless) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;
   }
 }
 
@@ -282,6 +281,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const P
   __syncthreads();
   const int k = verdict[0];
   const bool refused = verdict[1];
+  // the token of a row without mass, or of one whose sums run over; the barriers
+  // below put it before the one that is found
+  if (rank == 0 && tid == 0) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;
   Row r = row_of(p, n, k, refused);
   // this warp's part of the row: `part` consecutive tokens
   const int64_t lo64 = static_cast<int64_t>(rank * kWarps + warp) * part;
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const P
     r.q = nullptr, r.out = -1;
   }
   const uint64_t goal = goal_of(p, n, total);
-  if (rank == 0) write_results(p, n, k, total == 0);
+  if (rank == 0) write_results(p, n, k);
   // the warp in whose part the inversion ends
   int owner = -1;
   for (int w = 0; w < kWarps; ++w) {
@@ -358,6 +360,9 @@ extern "C" int kda_verify_draft(const KdaVerifyArgs* a, void* stream) {
       misaligned(a->slot_idx, 3) || misaligned(a->tokens, 3) || misaligned(a->num_accepted, 3) ||
       misaligned(a->next_slot, 3) || misaligned(a->err_flag, 3))
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer is not aligned as required");
+  if ((drafts && a->tokens == a->draft_tokens) || (a->src_slot && (a->tokens == a->src_slot || a->num_accepted == a->src_slot)) ||
+      (a->slot_idx && (a->next_slot == a->slot_idx || a->tokens == a->slot_idx)))
+    return kda_internal_fail(KDA_ERR_SHAPE, "a result may not take the place of an input (but next_slot of src_slot)");
   const bool vec = !misaligned(a->target_probs, 15) && a->target_row_stride % 4 == 0 &&
                    (!probs || (!misaligned(probs, 15) && a->draft_row_stride % 4 == 0));
   const Params p{a->N, a->T, a->V, a->draft_tokens, a->target_probs, probs, a->target_row_stride, a->draft_row_stride,

@@ -209,6 +209,17 @@ def test_nan_and_infinite_queries_and_keys(cuda_device):
     assert torch.equal(got.isnan().all(-1), bad) and torch.equal(got.isnan().any(-1), bad)
 
 
+@pytest.mark.parametrize("new", [3, 12])
+def test_rows_that_are_not_finite_and_see_nothing_are_zero(new, cuda_device):
+    c = Case(cuda_device, [1, 40], [new, 1], 8, 2, 16, seed=21)  # all but the first sequence's last query see nothing
+    c.q[0, 5] = float("nan")
+    c.q[1, 128 * 5 + 1] = float("inf")
+    t = c.tensors()
+    kda_cache_attention(*t, max_new=new)
+    got = t[-1].float().cpu()
+    assert (got[:new - 1] == 0).all() and not got.isnan().any() and (got[new - 1:new + 1] != 0).any(-1).all()
+
+
 def test_scales_of_very_different_size(cuda_device):
     # V scales from 2^-40 to 2^20 in one sequence, K scales that make logits of +-100 and of 1e-6
     c = Case(cuda_device, [700, 300], [2, 1], 8, 2, 16, seed=11)

@@ -156,3 +156,34 @@ def test_refusals(cuda_device):
         kda_verify_draft(d, p, u, su, draft_probs=t(2, 3, 8))
     with pytest.raises(ValueError, match="stride"):
         kda_verify_draft(d, t(2, 5, 9)[:, :4], u, su)
+
+
+@pytest.mark.parametrize("V", [7, 9, 130, 2048, 5000, 40000])
+@pytest.mark.parametrize("value", [1.0, 0.5, float("inf")])
+def test_rows_that_sum_to_more_still_give_a_token(value, V, cuda_device):
+    # softmax outputs by mistake unnormalised: which token is not defined, but one in range is written
+    N, T = 6, 2
+    p = torch.full((N, T, V), value, device=cuda_device)
+    draft = torch.full((N, 1), -1, dtype=torch.int32, device=cuda_device)
+    u = torch.zeros(N, 1, device=cuda_device)
+    su = torch.linspace(0, 1, N, device=cuda_device)
+    call = KdaVerifyDraftCall(draft, p, u, su)
+    call.tokens.fill_(-7)
+    call()
+    tok = call.tokens.cpu()
+    assert ((tok[:, 0] >= 0) & (tok[:, 0] < V)).all() and (tok[:, 1] == -1).all()
+
+
+@pytest.mark.parametrize("N, V", [(3, 40000), (400, 300)])
+def test_next_slot_in_the_place_of_src_slot(N, V, cuda_device):
+    # a captured loop keeps one array of slots; several CTAs a sequence, and one
+    x = inputs(N, 3, V, 5)
+    x["src"] = (np.arange(N) % 3).astype(np.int32)          # every third one is padding
+    want = R.verify(x["draft"], x["p"], x["u"], x["su"], x["q"], x["src"], x["slots"])
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(cuda_device)  # noqa: E731
+    src = t(x["src"])
+    call = KdaVerifyDraftCall(t(x["draft"]), t(x["p"]), t(x["u"]), t(x["su"]), draft_probs=t(x["q"]), src_slot=src,
+                              slot_idx=t(x["slots"]))
+    call.args.next_slot = src.data_ptr()
+    call()
+    assert src.tolist() == want[2] and call.num_accepted.tolist() == want[1] and call.tokens.tolist() == want[0]

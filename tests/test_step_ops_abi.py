@@ -135,6 +135,39 @@ def test_verify_codes(lib):
         assert call(**{n: 0x10002}) == ALIGN, n
 
 
+def test_results_in_the_place_of_inputs(lib):
+    # refused before any CUDA call; which places are allowed is tested on the GPU
+    names = ("cached_lens", "new_lens", "held_blocks", "free_blocks", "free_head", "free_head_out", "block_table",
+             "cu_seqlens", "seq_lens", "positions", "held_blocks_out", "slot_map")
+    at = {n: 0x10000 * (i + 1) for i, n in enumerate(names)}
+    call = caller(lib, "kda_block_tables", S.KdaBlockTablesArgs,
+                  dict(B=4, max_blocks=8, block_size=16, num_blocks=32, T=9, num_free=12, block_table_stride=8, **at))
+    for out, given in (("seq_lens", "cached_lens"), ("seq_lens", "new_lens"), ("held_blocks_out", "cached_lens"),
+                       ("held_blocks_out", "held_blocks"), ("cu_seqlens", "new_lens"), ("positions", "cached_lens"),
+                       ("free_head_out", "free_head"), ("block_table", "free_blocks")):
+        assert call(**{out: at[given]}) == SHAPE, out
+    names = ("qkv", "q_out", "positions", "freqs")
+    at = {n: 0x10000 * (i + 1) for i, n in enumerate(names)}
+    call = caller(lib, "kda_qk_rope", S.KdaQkRopeArgs,
+                  dict(T=4, num_q_heads=4, num_kv_heads=2, head_dim=128, rot_dim=64, qkv_row_stride=1024,
+                       q_row_stride=512, k_row_stride=256, **at))
+    assert call(q_out=at["qkv"]) == SHAPE
+    assert call(k_out=at["qkv"] + 4 * 256) == SHAPE
+    names = ("q", "out", "cu_seqlens", "seq_lens", "block_table", "k_cache", "v_cache", "k_scale", "v_scale", "workspace")
+    call = caller(lib, "kda_cache_attention", S.KdaCacheAttentionArgs,
+                  dict(B=3, T=7, num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=32, num_blocks=9, max_blocks=4,
+                       max_new=1, q_row_stride=1024, out_row_stride=1024, block_table_stride=4, block_stride=8192,
+                       head_stride=4096, token_stride=128, workspace_bytes=1 << 30,
+                       **{n: 0x10000 * (i + 1) for i, n in enumerate(names)}))
+    assert call(out=0x10000) == SHAPE
+    names = ("draft_tokens", "target_probs", "accept_u", "sample_u", "src_slot", "slot_idx", "tokens", "num_accepted",
+             "next_slot")
+    at = {n: 0x10000 * (i + 1) for i, n in enumerate(names)}
+    call = caller(lib, "kda_verify_draft", S.KdaVerifyArgs, dict(N=4, T=3, V=100, target_row_stride=100, **at))
+    for out, given in (("tokens", "draft_tokens"), ("next_slot", "slot_idx"), ("num_accepted", "src_slot")):
+        assert call(**{out: at[given]}) == SHAPE, out
+
+
 def test_host_tensors_are_refused(lib):
     i32, f32 = dict(dtype=torch.int32), dict(dtype=torch.float32)
     with pytest.raises(ValueError, match="CUDA"):
