@@ -60,7 +60,8 @@ extern "C" {
  *               ordered on one stream may share one.  After
  *               KDA_DEVERR_TIMEOUT they have to be cleared.
  *   max_new     the largest n_i the caller expects (>= 1): chooses the
- *               kernel's row tile, not the result
+ *               kernel and its row tile; the result stays the same up to
+ *               rounding
  */
 typedef struct KdaCacheAttentionArgs {
   uint32_t struct_size;        /* = sizeof(KdaCacheAttentionArgs) */

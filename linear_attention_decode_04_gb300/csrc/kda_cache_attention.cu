@@ -2,10 +2,18 @@
 // cache (definition in include/kda_cache_attention.h).
 //
 // Single tokens and multi-token steps are bound by HBM (the cache is read
-// once); prompt chunks by the softmax arithmetic and the tensor cores.
+// once); prompt chunks by the softmax between the two products.  There are
+// two kernels: one for up to 96 query rows per kv head and sequence, one
+// (at the end) for more.
 //
-// Products.  Both are formed transposed, so that the cache's codes are the
-// 128-row operand and the few queries the narrow one:
+// Measured on a GB300 against a copy's 6795 GB/s: 16 single tokens with 4,000
+// to 32,000 cached tokens each, 92 us (79 at a copy's rate); 64 sequences of 4
+// tokens, 64 q and 8 kv heads, 135 us (110); a small batch 7 us, of which the
+// launch, the plan and the trip to the first tile take most.  4 prompt chunks
+// of 515 tokens, 48 heads, 90 us; long ones reach 660 TFLOP/s of useful work.
+//
+// Products of the first kernel.  Both are formed transposed, so that the
+// cache's codes are the 128-row operand and the few queries the narrow one:
 //   S^T [token][row]   = K [token][d]   Q^T [d][row]      (128 x R, k = 128)
 //   O^T [d][row]       = V^T [d][token] P^T [token][row]  (128 x R, k = 128)
 // with R query rows (tokens x heads of one kv head).  K and V tiles of 128
@@ -30,8 +38,13 @@
 // depend on who is last).
 //
 // Roles.  One producer warp (block table and scales two tiles ahead, TMA
-// into a ring), one warp whose lane 0 issues the products, and one warpgroup
-// per 32 rows: thread = token of S^T, then channel of O^T.
+// into a ring), one warp whose lane 0 issues the products, and groups of one
+// warpgroup for 8, 16 or 24 query rows each (Cfg).  A thread holds 4 tokens of
+// a quarter of the group's rows, so a row's maximum takes shuffles and one trip
+// through shared memory per tile; up to 24 rows one group is enough (two CTAs
+// an SM hide one another's waits), above it several groups of 16 share the
+// tile: more warps hide the chain of one tile better than longer columns do
+// (64 sequences x 8 tokens x 64 heads: 244 us with groups of 16, 295 with 32).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,6 +55,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "kda_cache_attention.h"
 #include "kda_chunk_metadata.h"
@@ -56,6 +70,7 @@ constexpr int kMaxPages = 8;               // blocks of a tile, at block size 16
 constexpr int kMaxCtas = 304;              // 2 x 152
 // What beginning and ending a unit costs, in tiles: the work is dealt out by
 // tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
+// (Long prompts: 90 us with 4, 93 with 3 or 6, 101 with 2.)
 constexpr int kUnitCost = 4;
 constexpr int kCounters = 4 * 6 * 152;     // of each kind: CTAs x warps that join, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -94,9 +109,21 @@ struct Cfg {
   static constexpr int kNan = GROUPS > 1 ? 4 : 1;
   static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
   static constexpr int kPartial = COLS * (32 + 2);       // floats of a warp's partial record: maxima, sums, 32 channels
-  static constexpr int kJoinFan = 8;              // parts that one warp joins
+  // parts that one warp joins (16 long sequences: 92 us with 8, 94 with 16, 99 with all in one)
+  static constexpr int kJoinFan = 8;
   static constexpr int kBlocks = COLS / 8;               // 8-column blocks of a group's tensor-memory loads
   static constexpr int kMine = COLS / 4;                 // rows that a thread holds elements of
+};
+
+// The variant for prompts: two softmax warpgroups of 128 query rows each.  Four
+// warps beside them, producer, issuer and two that wait, so that whole warpgroups
+// can trade registers.
+struct Wide {
+  static constexpr int kGroups = 2, kRows = 256;
+  static constexpr int kThreads = 128 * kGroups + 128;
+  static constexpr int kCtasPerSm = 1, kK = 3, kV = 3;
+  static constexpr int kPartial = 32 * (kD + 2);         // floats of a warp's partial record: maxima, sums, 32 rows
+  static constexpr int kJoinFan = 8;
 };
 
 template <class C>
@@ -124,6 +151,21 @@ template <class C>
 struct alignas(16) Bcast {
   float mt[C::kCols];
   float alpha[2][C::kCols], beta[2][C::kCols];
+};
+
+struct alignas(1024) WideSmem {
+  uint8_t q[2][2][128 * kD], p[2][2][128 * kTile];  // [group][leading part, remainder], rows of 128 bytes, swizzled as K is
+  uint8_t k[Wide::kK][kTileBytes], v[Wide::kV][kTileBytes];
+  uint64_t k_full[Wide::kK], k_empty[Wide::kK], v_full[Wide::kV], v_empty[Wide::kV], sc_full[Wide::kV];
+  uint64_t s_full[2], o_full[2], p_full[2], q_full[2], done;
+  float4 sc[Wide::kV][kMaxPages];
+  int nan_at[kD];                         // of the unit, as above
+  int nan_seen;
+  int64_t total;
+  int walk[7];
+  int64_t scan[Wide::kThreads / 32], beyond[Wide::kThreads / 32];
+  uint32_t tmem;
+  int failed;
 };
 
 __device__ __forceinline__ uint32_t s32(const void* ptr) {
@@ -419,6 +461,183 @@ __device__ __forceinline__ bool next_share(const Params& p, Share& s) {  // fals
   return true;
 }
 
+// Where this CTA's tiles lie: the total, then the sequence they start in.  All
+// threads; false where the CTA has none.  The tensor memory that warp 0 asked for
+// is there afterwards.
+template <class C, class M>
+__device__ __forceinline__ bool plan(const Params& p, M& S, Share& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t mine = 0, beyond = 0;  // cost of sequence tid, and of those past the first kThreads
+  bool bad = false;
+  for (int i = tid; i < p.B; i += C::kThreads) {
+    const int64_t c = seq_cost<C>(p, i);
+    if (i == tid) mine = c;
+    else beyond += c;
+    const int a = p.cu[i], b = p.cu[i + 1];
+    bad |= a < 0 || b < a || b > p.T;
+  }
+  if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, KDA_DEVERR_SEQLENS);
+  auto warp_scan = [&](int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  int64_t incl = warp_scan(mine);
+  if (p.B > C::kThreads) beyond = warp_scan(beyond);
+  if (lane == 31) S.scan[warp] = incl, S.beyond[warp] = beyond;
+  tc_before();
+  __syncthreads();
+  tc_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t prior = 0, all = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w < warp) prior += S.scan[w];
+    all += S.scan[w];
+    total += S.beyond[w];
+  }
+  total += all;
+  if (tid == 0) S.total = total;
+  // one position at least for each CTA that takes part, so that every CTA between
+  // a unit's first and last leaves a part of it
+  const int64_t cta = blockIdx.x, ctas = max(min(static_cast<int64_t>(gridDim.x), total), int64_t{1});
+  // (32-bit division where it is enough: 64-bit ones take longer than the scan)
+  auto share_of = [&](int64_t c) {
+    return total < (1 << 22) ? static_cast<int64_t>(static_cast<uint32_t>(c * total) / static_cast<uint32_t>(ctas))
+                             : c * total / ctas;
+  };
+  const int64_t begin = cta < ctas ? share_of(cta) : 0, end = cta < ctas ? share_of(cta + 1) : 0;
+  if (begin >= end) return false;
+  auto look = [&](int i, int64_t from, int64_t cost) {  // whether the share begins in sequence i
+    if (cost == 0 || begin < from || begin >= from + cost) return;
+    Walk w;
+    w.seq = i;
+    load_seq<C>(p, w);
+    int64_t off = begin - from;
+    int c = tiles_of<C>(p, w.n, w.len, 0) + kUnitCost;
+    while (off >= static_cast<int64_t>(c) * p.Hkv) {
+      off -= static_cast<int64_t>(c) * p.Hkv;
+      c = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
+    }
+    S.walk[0] = i;
+    S.walk[4] = w.n, S.walk[5] = w.len, S.walk[6] = w.q0;
+    S.walk[1] = w.rt;
+    const bool small = off < 0x7fffffff;
+    S.walk[2] = small ? static_cast<int>(off) / c : static_cast<int>(off / c);
+    S.walk[3] = small ? static_cast<int>(off) % c : static_cast<int>(off % c);
+  };
+  look(tid, prior + incl - mine, mine);
+  for (int base = C::kThreads; all <= begin; base += C::kThreads) {  // larger batches
+    __syncthreads();
+    const int i = base + tid;
+    mine = i < p.B ? seq_cost<C>(p, i) : 0;
+    incl = warp_scan(mine);
+    if (lane == 31) S.scan[warp] = incl;
+    __syncthreads();
+    prior = all;
+#pragma unroll
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) prior += S.scan[w];
+      all += S.scan[w];
+    }
+    look(i, prior + incl - mine, mine);
+  }
+  __syncthreads();
+  Walk& w = sh.w;
+  w.seq = S.walk[0];
+  w.n = S.walk[4], w.len = S.walk[5], w.q0 = S.walk[6];
+  w.rts = rows_to_tiles<C>(p, w.n);
+  w.rt = S.walk[1];
+  w.h = S.walk[2];
+  w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
+  sh.off = S.walk[3];
+  sh.us = begin - sh.off;
+  sh.left = end - begin;
+  sh.tiles();
+  return true;
+}
+// One warp: tables and scales two tiles ahead, then the tiles into the rings.
+template <class C, class M>
+__device__ __forceinline__ void produce(const Params& p, M& S, Share& sh, bool more, const CUtensorMap& k_map,
+                                        const CUtensorMap& v_map) {
+  const int lane = threadIdx.x & 31;
+  Walk& w = sh.w;
+  const int log2 = p.bs_log2, rows = min(1 << log2, kTile), ppt = kTile / rows;  // rows of a copy, copies of a tile
+  struct Ref {
+    int block, head, tok;
+    bool valid;
+  };
+  int t = sh.t0;       // next tile
+  auto take = [&]() {  // the next tile of the share: this lane's block id in it
+    Ref r;
+    r.valid = more;
+    r.block = -1;
+    r.head = r.tok = 0;
+    if (!more) return r;
+    r.head = w.h;
+    const int pos = t * kTile + (lane < ppt ? lane * rows : 0);  // (lengths end below 2^31 - 256)
+    r.tok = pos & ((1 << log2) - 1);
+    const int last = min(w.n * p.G, (w.rt + 1) * C::kRows) - 1;
+    const int limit = w.len - w.n + token_of(p, last) + 1;
+    if (lane < ppt && pos < limit) {
+      const int e = pos >> log2;
+      int b = -1;
+      if (e < p.max_blocks) b = p.table[w.seq * p.table_stride + e];
+      if (b < 0 || b >= p.num_blocks) {
+        b = -1;
+        if (p.err) atomicOr(p.err, KDA_DEVERR_SLOT_RANGE);
+      }
+      r.block = b;
+    }
+    if (++t == sh.t0 + sh.take) {
+      more = next_share<C>(p, sh);
+      t = sh.t0;
+    }
+    return r;
+  };
+  auto scales = [&](const Ref& r) {
+    if (r.block < 0) return make_float2(0.f, 0.f);
+    const int64_t at = static_cast<int64_t>(r.block) * p.Hkv + r.head;
+    return make_float2(p.k_scale[at], p.v_scale[at]);
+  };
+  Ref a = take(), b = take();
+  float2 sa = scales(a);
+  bool ok = true;
+  uint32_t k_sent = 0, v_sent = 0;
+  for (uint32_t it = 0; a.valid; ++it) {
+    const float2 sb = scales(b);
+    const Ref c = take();
+    const uint32_t ks = it % C::kK, vs = it % C::kV, kr = it / C::kK, vr = it / C::kV;
+    if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
+    if (lane == 0) bar_expect(&S.k_full[ks], kTileBytes);
+    __syncwarp();
+    if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
+    ++k_sent;
+    if (vr > 0 && !(ok = bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed))) break;
+    if (lane == 0) bar_expect(&S.v_full[vs], kTileBytes);
+    __syncwarp();
+    if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
+    ++v_sent;
+    if (lane < ppt) {
+      const float sv = fmaxf(sa.y, 0x1p-64f);
+      S.sc[vs][lane] = a.block < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                   : make_float4(sa.x, log2f(sv), 1.f / sv, 0.f);
+    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(&S.sc_full[vs]);
+    a = b, b = c, sa = sb;
+  }
+  if (!ok) {  // nothing may land in shared memory after the CTA is gone
+    for (uint32_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
+      bar_drain(&S.k_full[j % C::kK], (j / C::kK) & 1);
+    for (uint32_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
+      bar_drain(&S.v_full[j % C::kV], (j / C::kV) & 1);
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
@@ -449,174 +668,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                  "n"(C::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // ---- where this CTA's tiles lie: total, then the sequence they start in
-  int64_t mine = 0, beyond = 0;  // cost of sequence tid, and of those past the first kThreads
-  bool bad = false;
-  for (int i = tid; i < p.B; i += C::kThreads) {
-    const int64_t c = seq_cost<C>(p, i);
-    if (i == tid) mine = c;
-    else beyond += c;
-    const int a = p.cu[i], b = p.cu[i + 1];
-    bad |= a < 0 || b < a || b > p.T;
-  }
-  if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, KDA_DEVERR_SEQLENS);
-  auto warp_scan = [&](int64_t v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    return v;
-  };
-  int64_t incl = warp_scan(mine);
-  if (p.B > C::kThreads) beyond = warp_scan(beyond);
-  if (lane == 31) S.scan[warp] = incl, S.beyond[warp] = beyond;
-  tc_before();
-  __syncthreads();
-  tc_after();
+  Share sh;
+  const bool any = plan<C>(p, S, sh);
   const uint32_t tmem = S.tmem;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t prior = 0, all = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) prior += S.scan[w];
-    all += S.scan[w];
-    total += S.beyond[w];
-  }
-  total += all;
-  if (tid == 0) S.total = total;
-  // one position at least for each CTA that takes part, so that every CTA between
-  // a unit's first and last leaves a part of it
-  const int64_t cta = blockIdx.x, ctas = max(min(static_cast<int64_t>(gridDim.x), total), int64_t{1});
-  // (32-bit division where it is enough: 64-bit ones take longer than the scan)
-  auto share_of = [&](int64_t c) {
-    return total < (1 << 22) ? static_cast<int64_t>(static_cast<uint32_t>(c * total) / static_cast<uint32_t>(ctas))
-                             : c * total / ctas;
-  };
-  const int64_t begin = cta < ctas ? share_of(cta) : 0, end = cta < ctas ? share_of(cta + 1) : 0;
-  if (begin < end) {
-    auto look = [&](int i, int64_t from, int64_t cost) {  // whether the share begins in sequence i
-      if (cost == 0 || begin < from || begin >= from + cost) return;
-      Walk w;
-      w.seq = i;
-      load_seq<C>(p, w);
-      int64_t off = begin - from;
-      int c = tiles_of<C>(p, w.n, w.len, 0) + kUnitCost;
-      while (off >= static_cast<int64_t>(c) * p.Hkv) {
-        off -= static_cast<int64_t>(c) * p.Hkv;
-        c = tiles_of<C>(p, w.n, w.len, ++w.rt) + kUnitCost;
-      }
-      S.walk[0] = i;
-      S.walk[4] = w.n, S.walk[5] = w.len, S.walk[6] = w.q0;
-      S.walk[1] = w.rt;
-      const bool small = off < 0x7fffffff;
-      S.walk[2] = small ? static_cast<int>(off) / c : static_cast<int>(off / c);
-      S.walk[3] = small ? static_cast<int>(off) % c : static_cast<int>(off % c);
-    };
-    look(tid, prior + incl - mine, mine);
-    for (int base = C::kThreads; all <= begin; base += C::kThreads) {  // larger batches
-      __syncthreads();
-      const int i = base + tid;
-      mine = i < p.B ? seq_cost<C>(p, i) : 0;
-      incl = warp_scan(mine);
-      if (lane == 31) S.scan[warp] = incl;
-      __syncthreads();
-      prior = all;
-#pragma unroll
-      for (int w = 0; w < C::kThreads / 32; ++w) {
-        if (w < warp) prior += S.scan[w];
-        all += S.scan[w];
-      }
-      look(i, prior + incl - mine, mine);
-    }
-    __syncthreads();
-    Share sh;
+  if (any) {
     Walk& w = sh.w;
-    w.seq = S.walk[0];
-    w.n = S.walk[4], w.len = S.walk[5], w.q0 = S.walk[6];
-    w.rts = rows_to_tiles<C>(p, w.n);
-    w.rt = S.walk[1];
-    w.h = S.walk[2];
-    w.nt = tiles_of<C>(p, w.n, w.len, w.rt);
-    sh.off = S.walk[3];
-    sh.us = begin - sh.off;
-    sh.left = end - begin;
-    sh.tiles();
     bool more = sh.take > 0 || next_share<C>(p, sh);
-
     if (warp == 4 * C::kGroups) {
       // ================================================================ producer
-      const int log2 = p.bs_log2, rows = min(1 << log2, kTile), ppt = kTile / rows;  // rows of a copy, copies of a tile
-      struct Ref {
-        int block, head, tok;
-        bool valid;
-      };
-      int t = sh.t0;       // next tile
-      auto take = [&]() {  // the next tile of the share: this lane's block id in it
-        Ref r;
-        r.valid = more;
-        r.block = -1;
-        r.head = r.tok = 0;
-        if (!more) return r;
-        r.head = w.h;
-        const int pos = t * kTile + (lane < ppt ? lane * rows : 0);  // (lengths end below 2^31 - 256)
-        r.tok = pos & ((1 << log2) - 1);
-        const int last = min(w.n * p.G, (w.rt + 1) * C::kRows) - 1;
-        const int limit = w.len - w.n + token_of(p, last) + 1;
-        if (lane < ppt && pos < limit) {
-          const int e = pos >> log2;
-          int b = -1;
-          if (e < p.max_blocks) b = p.table[w.seq * p.table_stride + e];
-          if (b < 0 || b >= p.num_blocks) {
-            b = -1;
-            if (p.err) atomicOr(p.err, KDA_DEVERR_SLOT_RANGE);
-          }
-          r.block = b;
-        }
-        if (++t == sh.t0 + sh.take) {
-          more = next_share<C>(p, sh);
-          t = sh.t0;
-        }
-        return r;
-      };
-      auto scales = [&](const Ref& r) {
-        if (r.block < 0) return make_float2(0.f, 0.f);
-        const int64_t at = static_cast<int64_t>(r.block) * p.Hkv + r.head;
-        return make_float2(p.k_scale[at], p.v_scale[at]);
-      };
-      Ref a = take(), b = take();
-      float2 sa = scales(a);
-      bool ok = true;
-      uint32_t k_sent = 0, v_sent = 0;
-      for (uint32_t it = 0; a.valid; ++it) {
-        const float2 sb = scales(b);
-        const Ref c = take();
-        const uint32_t ks = it % C::kK, vs = it % C::kV, kr = it / C::kK, vr = it / C::kV;
-        if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
-        if (lane == 0) bar_expect(&S.k_full[ks], kTileBytes);
-        __syncwarp();
-        if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
-        ++k_sent;
-        if (vr > 0 && !(ok = bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed))) break;
-        if (lane == 0) bar_expect(&S.v_full[vs], kTileBytes);
-        __syncwarp();
-        if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
-        ++v_sent;
-        if (lane < ppt) {
-          const float sv = fmaxf(sa.y, 0x1p-64f);
-          S.sc[vs][lane] = a.block < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                       : make_float4(sa.x, log2f(sv), 1.f / sv, 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&S.sc_full[vs]);
-        a = b, b = c, sa = sb;
-      }
-      if (!ok) {  // nothing may land in shared memory after the CTA is gone
-        for (uint32_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
-          bar_drain(&S.k_full[j % C::kK], (j / C::kK) & 1);
-        for (uint32_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
-          bar_drain(&S.v_full[j % C::kV], (j / C::kV) & 1);
-      }
+      produce<C>(p, S, sh, more, k_map, v_map);
     } else if (warp == 4 * C::kGroups + 1) {
       // ======================================================== product issuer
       if (lane == 0) {
@@ -1080,6 +1140,487 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
 }
 
+// ------------------------------------------------------------ the kernel, prompts
+// Here the query rows are many, so they are the 128-row operand:
+//   S [row][token] = Q [row][d] K^T,   O [row][d] = P [row][token] V
+// and a thread has a row of its own: its maximum, its sum and its 128 output
+// channels (in registers) take no exchange with others.  The scores are read
+// from tensor memory twice, for the maximum and for the weights, a row at 32
+// tokens a time.  Scales, parts and one accumulator per tile as above.  The
+// two warpgroups work on rows of their own, and one's arithmetic runs while
+// the other waits for its products.
+//
+// What bounds it: the chain weights -> products -> maximum -> weights of each
+// group (with next to no arithmetic left between them a tile still takes
+// 3,500 cycles for both groups; 5,400 with it, of which the tensor cores are
+// busy 2,100).  4,096 tokens behind 12,000, 64 heads: 2.17 ms (3.57 with the
+// kernel above; its threads exchange maxima over shared memory).  Measured and
+// left out: two threads per row (registers: 4.6 ms), products in halves of 64
+// tokens (2.45 ms), 64 tokens at a time (2.2 to 2.4 ms).
+//
+// Two floats in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tm_row(uint32_t addr, float (&r)[32]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// Two weights (or scaled queries) in two e4m3 parts each, 16 bits per part.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 v = __floats2half2_rn(x, y);
+  hi = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  lo = __nv_cvt_halfraw2_to_fp8x2(
+      __hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3))), __NV_SATFINITE,
+      __NV_E4M3);
+}
+
+// SCALES: scales that 32 tokens may have (2 for blocks of 16).
+template <int SCALES>
+__global__ void __launch_bounds__(Wide::kThreads, 1)
+    prompt_attention_kernel(const Params p, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap v_map) {
+  using C = Wide;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  WideSmem& S = *reinterpret_cast<WideSmem*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::kK; ++i) bar_init(&S.k_full[i], 1), bar_init(&S.k_empty[i], 1);
+    for (int i = 0; i < C::kV; ++i) bar_init(&S.v_full[i], 1), bar_init(&S.v_empty[i], 1);
+    for (int i = 0; i < C::kV; ++i) bar_init(&S.sc_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&S.s_full[i], 1), bar_init(&S.o_full[i], 1);
+      bar_init(&S.p_full[i], 128), bar_init(&S.q_full[i], 128);
+    }
+    bar_init(&S.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    S.failed = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
+  }
+  __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s32(&S.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  Share sh;
+  const bool any = plan<C>(p, S, sh);
+  const uint32_t tmem = S.tmem;
+  if (any) {
+    Walk& w = sh.w;
+    bool more = sh.take > 0 || next_share<C>(p, sh);
+    // groups that have rows of the unit
+    auto active = [&](const Walk& u) { return u.n * p.G - u.rt * C::kRows > 128 ? 2 : 1; };
+    if (warp >= 8) {
+      // 168 a thread at launch: 256 x 216 + 128 x 72 = 384 x 168.  (More for the rows
+      // and fewer here spills in the producer: 90 us against 94.)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (warp == 8) {
+        produce<C>(p, S, sh, more, k_map, v_map);
+      } else if (warp == 9) {
+        // ======================================================== product issuer
+        if (lane == 0) {
+          constexpr uint32_t id_s = idesc(128, false, false), id_o = idesc(128, false, true);
+          uint32_t it = 0, p_seen[2] = {0, 0}, units[2] = {0, 0};
+          bool ok = true;
+          auto weigh = [&](int g, uint32_t j) {  // O of group g for tile j, whose weights are there
+            const uint32_t v = s32(S.v[j % C::kV]), d = tmem + 256 + 128 * g;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < kTile / 32; ++k)
+                mma(d, sdesc(s32(S.p[g][part]) + k * 32, 0, 1024, 2), sdesc(v + k * 32 * kD, 0, 1024, 2), id_o, part + k > 0);
+            commit(&S.o_full[g]);
+          };
+          while (more && ok) {
+            const int groups = active(w);
+            for (int k0 = 0; k0 <= sh.take && ok; ++k0) {  // the scores of tile k0 and the sums of the one before
+              const uint32_t st = it % C::kK;
+              for (int g = 0; g < groups; ++g) {
+                ok = ok && (k0 > 0 ? bar_wait(&S.p_full[g], p_seen[g]++ & 1, &S.failed)
+                                   : bar_wait(&S.q_full[g], units[g]++ & 1, &S.failed));
+                if (k0 < sh.take && g == 0) ok = ok && bar_wait(&S.k_full[st], (it / C::kK) & 1, &S.failed);
+                if (!ok) break;
+                tc_after();
+                if (k0 < sh.take) {
+                  const uint32_t kk = s32(S.k[st]), d = tmem + 128 * g;
+#pragma unroll
+                  for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < kD / 32; ++k)
+                      mma(d, sdesc(s32(S.q[g][part]) + k * 32, 0, 1024, 2), sdesc(kk + k * 32, 0, 1024, 2), id_s, part + k > 0);
+                  commit(&S.s_full[g]);
+                  if (g == groups - 1) commit(&S.k_empty[st]);
+                }
+                if (k0 > 0) {
+                  if (g == 0) ok = bar_wait(&S.v_full[(it - 1) % C::kV], ((it - 1) / C::kV) & 1, &S.failed);
+                  if (!ok) break;
+                  weigh(g, it - 1);
+                  if (g == groups - 1) commit(&S.v_empty[(it - 1) % C::kV]);
+                }
+              }
+              if (k0 < sh.take) ++it;
+            }
+            more = next_share<C>(p, sh);
+          }
+          commit(&S.done);
+        }
+        __syncwarp();
+      }
+    } else {
+      // ================================================================ softmax
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      const int g = warp >> 2, wq = warp & 3, t = tid & 127;  // warpgroup, warp in it, row in it
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+      const uint32_t s_at = lanes + 128 * g, o_at = lanes + 256 + 128 * g;
+      uint8_t* const q_row = S.q[g][0] + t * 128;  // the remainders' row: 128 * kD bytes on
+      uint8_t* const p_row = S.p[g][0] + t * 128;
+      uint32_t it = 0, tiles = 0;                  // tiles of the share; of them those that this group took part in
+      for (; more; more = next_share<C>(p, sh)) {
+        const int t0 = sh.t0, take = sh.take, ctx = w.len - w.n;
+        const int row0 = w.rt * C::kRows, row = row0 + 128 * g + t;
+        const int tile_rows = min(w.n * p.G, row0 + C::kRows);  // end of the unit's rows
+        const int least = ctx + token_of(p, row0) + 1, most = ctx + token_of(p, tile_rows - 1) + 1;
+        const bool takes_part = g < active(w);
+        const bool live = row < tile_rows;
+        const int tok = token_of(p, min(row, tile_rows - 1));
+        const int limit = live ? ctx + tok + 1 : 0x7fffffff;  // a row that is not there: no masks, never written
+        const int64_t channel0 = (static_cast<int64_t>(w.h) * p.G + (row - tok * p.G)) * kD;
+        if (takes_part) {
+          // ---- the row: scaled to e4m3's range by a power of two, split in two parts
+          float rs;
+          {
+            uint4 u[16];
+            float amax = 0.f;
+            bool finite = true;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (w.q0 + tok) * p.q_stride + channel0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float a = fabsf(__uint_as_float(x[k] << 16)), b = fabsf(__uint_as_float(x[k] & 0xffff0000u));
+                finite &= a <= FLT_MAX && b <= FLT_MAX;
+                amax = fmaxf(amax, fmaxf(a, b));
+              }
+            }
+            // 2^e with amax 2^-e in (224, 448]
+            const uint32_t bits = __float_as_uint(amax);
+            int e = static_cast<int>(bits >> 23) - 126 - 9 + ((bits & 0x7fffffu) > 0x600000u);
+            e = min(max(e, -100), 119);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            rs = finite ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * p.scale : __uint_as_float(0x7fc00000u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint4 v = u[2 * i + (j >> 1)];
+                const uint32_t x = j & 1 ? v.z : v.x, y = j & 1 ? v.w : v.y;
+                uint32_t h0, l0, h1, l1;
+                split2(__uint_as_float(x << 16) * inv, __uint_as_float(x & 0xffff0000u) * inv, h0, l0);
+                split2(__uint_as_float(y << 16) * inv, __uint_as_float(y & 0xffff0000u) * inv, h1, l1);
+                hi[j] = h0 | (h1 << 16);
+                lo[j] = l0 | (l1 << 16);
+              }
+              const int at = (i ^ (t & 7)) * 16;
+              *reinterpret_cast<uint4*>(q_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(q_row + 128 * kD + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          if (g == 0) {
+            S.nan_at[t] = 0x7fffffff;
+            if (t == 0) S.nan_seen = 0;
+            group_sync<128>(0);
+          }
+          fence_async();
+          bar_arrive(&S.q_full[g]);
+          const int warp_least = __reduce_min_sync(0xffffffffu, limit);
+          uint64_t o[kD / 2];
+#pragma unroll
+          for (int c = 0; c < kD / 2; ++c) o[c] = 0;
+          float run = -INFINITY, l = 0.f;       // running maximum and sum of weights
+          float alpha = 0.f, beta = 0.f;        // of the tile whose products are not yet added
+          auto add_tile = [&](uint32_t j) {     // they join the sums
+            bar_wait(&S.o_full[g], j & 1, &S.failed);
+            tc_after();
+            const uint64_t a2 = pair_of(alpha, alpha), b2 = pair_of(beta, beta);
+            const bool grown = __any_sync(0xffffffffu, alpha != 1.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float x[32];
+              tm_row(o_at + 32 * c, x);
+              if (grown) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[16 * c + i] = mul2(o[16 * c + i], a2);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[16 * c + i] = fma2(pair_of(x[2 * i], x[2 * i + 1]), b2, o[16 * c + i]);
+            }
+          };
+          for (int k = 0;; ++k) {
+            const uint32_t j = tiles + k, vs = (it + k) % C::kV;
+            const int tile0 = (t0 + k) * kTile;
+            const bool masked = tile0 + kTile > warp_least;
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (k < take) {
+              bar_wait(&S.sc_full[vs], ((it + k) / C::kV) & 1, &S.failed);
+              bar_wait(&S.s_full[g], j & 1, &S.failed);
+              tc_after();
+              // ---- the tile's maximum.  (Loops over the chunks of 32 tokens, not unrolled: the
+              // loop's code has to stay in the instruction caches.)
+              auto maxima = [&](auto masks) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  float x[32];
+                  tm_row(s_at + 32 * c, x);
+                  const int sees = limit - tile0 - 32 * c;  // of the chunk's tokens
+#pragma unroll
+                  for (int part = 0; part < SCALES; ++part) {
+                    const float4 sc = S.sc[vs][(32 * c + 16 * part) >> p.bs_log2];
+                    const uint64_t f = pair_of(sc.x * rs, sc.x * rs), d = pair_of(sc.y, sc.y);
+#pragma unroll
+                    for (int i = 0; i < 16 / SCALES; ++i) {
+                      const int n = 16 * part + 2 * i;
+                      float2 z = both(fma2(pair_of(x[n], x[n + 1]), f, d));
+                      if (masks) {
+                        if (n >= sees) z.x = -INFINITY;
+                        if (n + 1 >= sees) z.y = -INFINITY;
+                      }
+                      m[i & 3] = fmaxf(m[i & 3], fmaxf(z.x, z.y));
+                    }
+                  }
+                }
+              };
+              if (masked) maxima(std::true_type{});
+              else maxima(std::false_type{});
+            }
+            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            if (k > 0) add_tile(j - 1);  // (also: the weights' place is free)
+            if (k == take) break;
+            const float next = fmaxf(run, top), ref = next == -INFINITY ? 0.f : next;
+            alpha = ex2(run - ref);
+            beta = ex2(top - ref);
+            run = next;
+            const float mt = (top == -INFINITY ? 0.f : top) - 8.f;  // weights up to 2^8
+            // ---- weights, their sum, their two e4m3 parts
+            float sum = 0.f;
+            auto weights = [&](auto masks) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float x[32];
+                tm_row(s_at + 32 * c, x);
+                const int sees = limit - tile0 - 32 * c;
+#pragma unroll
+                for (int part = 0; part < SCALES; ++part) {
+                  const float4 sc = S.sc[vs][(32 * c + 16 * part) >> p.bs_log2];
+                  const uint64_t f = pair_of(sc.x * rs, sc.x * rs), d = pair_of(sc.y - mt, sc.y - mt);
+                  uint64_t some = 0;
+#pragma unroll
+                  for (int half = part; half < 3 - SCALES + part; ++half) {  // 16 tokens
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      uint32_t h[2], r[2];
+#pragma unroll
+                      for (int e = 0; e < 2; ++e) {
+                        const int n = 16 * half + 4 * i + 2 * e;
+                        float2 z = both(fma2(pair_of(x[n], x[n + 1]), f, d));
+                        if (masks) {
+                          if (n >= sees) z.x = -INFINITY;
+                          if (n + 1 >= sees) z.y = -INFINITY;
+                        }
+                        const float w0 = ex2(z.x), w1 = ex2(z.y);
+                        some = add2(some, pair_of(w0, w1));
+                        split2(w0, w1, h[e], r[e]);
+                      }
+                      hi[i] = h[0] | (h[1] << 16);
+                      lo[i] = r[0] | (r[1] << 16);
+                    }
+                    const int at = ((2 * c + half) ^ (t & 7)) * 16;
+                    *reinterpret_cast<uint4*>(p_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(p_row + 128 * kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                  }
+                  const float2 two = both(some);
+                  sum = fmaf(two.x + two.y, sc.z, sum);
+                }
+              }
+            };
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
+            l = l * alpha + sum * beta;
+            // ---- values that some row does not see (as in the kernel above)
+            if (g == 0 && tile0 + kTile > least) {
+              const int pos = tile0 + t;
+              bar_wait(&S.v_full[vs], ((it + k) / C::kV) & 1, &S.failed);
+              __syncwarp();
+              uint4* v = reinterpret_cast<uint4*>(S.v[vs] + t * kD);
+              uint32_t nan = 0;
+              if (pos >= most) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i ^ (t & 7)] = make_uint4(0, 0, 0, 0);
+              } else if (pos >= least) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint4 u = v[i ^ (t & 7)];
+                  nan |= nan_bytes(u.x) | nan_bytes(u.y) | nan_bytes(u.z) | nan_bytes(u.w);
+                }
+              }
+              if (__any_sync(0xffffffffu, nan != 0)) {
+                if (nan) S.nan_seen = 1;
+                take_out_nan(S.v[vs] + t * kD, nan != 0, t, pos, S.nan_at);
+              }
+            }
+            __syncwarp();
+            fence_async();
+            tc_before();
+            bar_arrive(&S.p_full[g]);
+          }
+          tiles += take;
+          if (S.nan_seen) {
+#pragma unroll
+            for (int c = 0; c < kD / 2; ++c) {
+              float2 x = both(o[c]);
+              if (S.nan_at[2 * c] < limit) x.x = __uint_as_float(0x7fc00000u);
+              if (S.nan_at[2 * c + 1] < limit) x.y = __uint_as_float(0x7fc00000u);
+              o[c] = pair_of(x.x, x.y);
+            }
+          }
+          auto write_out = [&](float sum) {
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (w.q0 + tok) * p.out_stride + channel0);
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                uint32_t r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 x = both(o[4 * i + k]);
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x * f, x.y * f);
+                  r[k] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
+              }
+            }
+          };
+          if (take == w.nt) {
+            write_out(l);
+          } else {
+            // a part of the unit: a record for the warp that arrives last, as in the kernel
+            // above, but a thread's row is its own in every part
+            const int64_t first = sh.us + kUnitCost, cost = S.total;
+            const int64_t parties = min(static_cast<int64_t>(gridDim.x), cost);
+            const int c0 = static_cast<int>(((first + 1) * parties - 1) / cost);
+            const int c1 = static_cast<int>(((first + w.nt) * parties - 1) / cost);
+            auto record = [&](int c) {
+              return p.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * 4 * C::kGroups + 4 * g + wq) * C::kPartial;
+            };
+            auto write_record = [&](float* rec) {
+              rec[lane] = run, rec[32 + lane] = l;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 x = both(o[2 * i]), y = both(o[2 * i + 1]);
+                reinterpret_cast<float4*>(rec + 64)[32 * i + lane] = make_float4(x.x, x.y, y.x, y.y);
+              }
+            };
+            write_record(record(static_cast<int>(blockIdx.x)));
+            auto join = [&](int from, int step, int to) {
+              run = -INFINITY, l = 0.f;
+#pragma unroll
+              for (int c = 0; c < kD / 2; ++c) o[c] = 0;
+#pragma unroll 1
+              for (int c = from; c <= to; c += step) {
+                const float* rec = record(c);
+                const float pm = __ldcg(rec + lane), pl = __ldcg(rec + 32 + lane);
+                const float next = fmaxf(run, pm), ref = next == -INFINITY ? 0.f : next;
+                const float a = ex2(run - ref), b = ex2(pm - ref);
+                run = next;
+                l = l * a + pl * b;
+                const uint64_t a2 = pair_of(a, a), b2 = pair_of(b, b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + 64) + 32 * i + lane);
+                  o[2 * i] = fma2(pair_of(x.x, x.y), b2, mul2(o[2 * i], a2));
+                  o[2 * i + 1] = fma2(pair_of(x.z, x.w), b2, mul2(o[2 * i + 1], a2));
+                }
+              }
+            };
+            auto arrive = [&](int32_t* counter, int parts) {
+              __syncwarp();
+              int before = 0;
+              if (lane == 0) {
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+                if (before == parts - 1) *counter = 0;
+              }
+              return __shfl_sync(0xffffffffu, before, 0) == parts - 1;
+            };
+            const int fan = (static_cast<int>(blockIdx.x) - c0) / C::kJoinFan, fans = (c1 - c0) / C::kJoinFan + 1;
+            int from = c0 + fan * C::kJoinFan, step = 1, to = min(from + C::kJoinFan - 1, c1);
+            int32_t* counter = p.counters + (fan ? kCounters : 0) + (from * C::kGroups + g) * 4 + wq;
+#pragma unroll 1
+            for (int n = to - from + 1; arrive(counter, n); n = fans) {
+              const bool all_parts = fans == 1 || step > 1;
+              join(from, step, to);
+              if (all_parts) {
+                write_out(l);
+                break;
+              }
+              __syncwarp();
+              write_record(record(from));
+              from = c0, step = C::kJoinFan, to = c1;
+              counter = p.counters + 2 * kCounters + (c0 * C::kGroups + g) * 4 + wq;
+            }
+          }
+        }
+        it += take;
+        // both groups are behind the unit: what they share of it may be written anew
+        asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+      }
+    }
+    if (warp == 0 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  }
+  tc_before();
+  __syncthreads();
+  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+  __syncwarp();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
 // ------------------------------------------------------------------ host side
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1103,10 +1644,26 @@ constexpr size_t smem_bytes() {
   return n;
 }
 
+template <>
+constexpr size_t smem_bytes<Wide>() {
+  static_assert(sizeof(WideSmem) <= 227 * 1024, "shared memory");
+  return sizeof(WideSmem);
+}
+
+using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap);
+template <class C>
+constexpr Kernel kernel_of(bool two_scales) {
+  if constexpr (std::is_same<C, Wide>::value) return two_scales ? prompt_attention_kernel<2> : prompt_attention_kernel<1>;
+  else return cache_attention_kernel<C>;
+}
 template <class C>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(cache_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem_bytes<C>()));
+  for (bool two : {false, true}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel_of<C>(two), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem_bytes<C>()));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t setup(int* sms) {
@@ -1124,7 +1681,8 @@ cudaError_t setup(int* sms) {
     g_encode = reinterpret_cast<EncodeFn>(fn);
     if ((e = allow_smem<Rows8>()) != cudaSuccess || (e = allow_smem<Rows16>()) != cudaSuccess ||
         (e = allow_smem<Rows24>()) != cudaSuccess || (e = allow_smem<Rows32>()) != cudaSuccess ||
-        (e = allow_smem<Rows64>()) != cudaSuccess || (e = allow_smem<Rows96>()) != cudaSuccess)
+        (e = allow_smem<Rows64>()) != cudaSuccess || (e = allow_smem<Rows96>()) != cudaSuccess ||
+        (e = allow_smem<Wide>()) != cudaSuccess)
       return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -1138,7 +1696,9 @@ bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uint
 
 // Calls `f` with the variant for `rows` query rows per kv head and sequence: all
 // the queries of a single-token or multi-token step, so that the cache is read
-// once and no column is idle for more than 7 of 8 rows; 96 rows for prompts.
+// once and few columns are idle; the kernel for prompts from 97 on.  (64
+// sequences x 12 tokens x 64 heads, 96 rows: 215 us, 274 with the kernel for
+// prompts; 8 sequences x 16 tokens, 128 rows: 48 us in two tiles of 96, 44 with it.)
 template <class F>
 auto with_variant(int64_t rows, F f) {
   if (rows <= 8) return f(Rows8{});
@@ -1146,7 +1706,8 @@ auto with_variant(int64_t rows, F f) {
   if (rows <= 24) return f(Rows24{});
   if (rows <= 32) return f(Rows32{});
   if (rows <= 64) return f(Rows64{});
-  return f(Rows96{});
+  if (rows <= 96) return f(Rows96{});
+  return f(Wide{});
 }
 
 template <class C>
@@ -1229,7 +1790,7 @@ extern "C" int kda_cache_attention(const KdaCacheAttentionArgs* a, void* stream)
   p.partial = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + KDA_CACHE_ATTENTION_COUNTER_BYTES);
   e = with_variant(static_cast<int64_t>(a->max_new) * p.G, [&](auto c) {
     using C = decltype(c);
-    return kda_internal_launch(cache_attention_kernel<C>, dim3(static_cast<unsigned>(sms * C::kCtasPerSm)),
+    return kda_internal_launch(kernel_of<C>(bs == 16), dim3(static_cast<unsigned>(sms * C::kCtasPerSm)),
                                dim3(C::kThreads), smem_bytes<C>(), stream, p, maps[0], maps[1]);
   });
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));

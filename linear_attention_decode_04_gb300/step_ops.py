@@ -337,7 +337,8 @@ class KdaCacheAttentionCall(_Call):
                    fp32 [num_blocks, Hkv]
       num_q_heads  Hq, a multiple of Hkv; by default q's width / 128
       max_new      the most queries a sequence has in this call (host value,
-                   chooses the row tile; results do not depend on it)
+                   chooses the kernel's row tile; results are the same up to
+                   rounding)
       workspace    from ``cache_attention_workspace``; by default the call
                    makes its own, and the constructor then waits for the
                    current stream once"""

@@ -100,7 +100,8 @@ class Case:
                 a = torch.softmax(z, -1)
                 o = torch.einsum("hgl,hld->hgd", a, v[:, :lim])
                 av = torch.einsum("hgl,hld->hgd", a, v[:, :lim].abs())
-                e = (2.0 ** -18 + 2.0 ** -17) * sm * q[j].abs().amax(-1, keepdim=True) * k[:, :lim].abs().sum(-1).amax(-1)[:, None, None]
+                # the error of a logit is sm times that of q . k, so its bound has |sm| (a bound is not negative)
+                e = (2.0 ** -18 + 2.0 ** -17) * abs(sm) * q[j].abs().amax(-1, keepdim=True) * k[:, :lim].abs().sum(-1).amax(-1)[:, None, None]
                 e = e + 2.0 ** -21 * z.abs().amax(-1, keepdim=True)
                 pad = (-lim) % 128
                 tile = torch.nn.functional.pad(a * v[:, :lim].abs().amax(-1)[:, None], (0, pad)).view(Hkv, G, -1, 128)
@@ -440,3 +441,108 @@ def test_refusals(cuda_device):
     refuse(0, t[0], workspace=torch.zeros(100, dtype=torch.int32, device=cuda_device))
     with pytest.raises(ValueError):
         cache_attention_workspace(5, 2, 1, cuda_device)
+
+
+# The variant for prompts (two groups of 128 rows): chosen by a max_new of more than 96 rows per kv head.
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("Hq, Hkv", [(1, 1), (6, 2), (24, 3)])
+def test_prompt_variant_at_the_edges_of_its_rows(bs, Hq, Hkv, cuda_device):
+    # chunks that end below, at and above one group's and both groups' rows, from position 0 and behind cached tokens
+    G = Hq // Hkv
+    new = sorted({1, 127 // G, 128 // G, 128 // G + 1, 256 // G, 256 // G + 1})
+    lens = [n + c for n, c in zip(new, (0, 128, 1, 300, 127, 64, 5))]
+    c = Case(cuda_device, lens, new, Hq, Hkv, bs, seed=bs + G, row_pad=8, extra=2)
+    assert c.check(max_new=1000) < 4e-3
+
+
+def test_prompt_variant_joins_parts(cuda_device):
+    # one unit over most CTAs (two levels of joins), then some of a few parts each; the same bits every time
+    c = Case(cuda_device, [40000], [1], 4, 1, 64, seed=31)
+    assert c.check(max_new=1000) < 4e-3
+    c = Case(cuda_device, [9000, 3, 4100, 600], [40, 2, 33, 300], 12, 3, 16, seed=32)
+    ws = cache_attention_workspace(12, 3, 300, cuda_device)
+    t = c.tensors()
+    first = None
+    for _ in range(4):
+        kda_cache_attention(*t, max_new=300, workspace=ws)
+        first = t[-1].clone() if first is None else first
+        assert torch.equal(first, t[-1])
+    assert not ws[:11264].any()
+    assert c.compare(t[-1]) < 4e-3
+
+
+def test_prompt_variant_masks_and_values(cuda_device):
+    m = dict(max_new=1000)
+    c = Case(cuda_device, [0, 2, 5, 64, 0, 130], [1, 4, 0, 3, 5, 2], 8, 2, 16, seed=7, extra=1)
+    c.check(**m)
+    c.lens[4] = -3
+    c.check(**m)
+    c = Case(cuda_device, [700, 300], [2, 1], 8, 2, 16, seed=11)
+    g = torch.Generator().manual_seed(1)
+    c.vs = torch.exp2(torch.randint(-40, 20, c.vs.shape, generator=g).float())
+    c.check(**m)
+    c.ks = torch.exp2(torch.randint(-30, 1, c.ks.shape, generator=g).float())
+    c.check(**m)
+    c = Case(cuda_device, [4096], [1], 4, 1, 16, seed=13, outlier=True)
+    c.check(**m)
+    c = Case(cuda_device, [20000], [1], 4, 1, 16, seed=14)
+    c.k[:] = 0
+    c.k[c.table[0, 0].long(), 0, 0] = 0x38
+    c.ks[:] = 1.0
+    c.q[:] = 1.0
+    c.sm = 9.0 / 128
+    c.check(**m)
+    for scale_q, sm in ((30.0, 0.0), (1.0, -1.0), (1e4, 1e-5), (1e-30, 1e29)):
+        c = Case(cuda_device, [300, 129], [1, 3], 12, 4, 32, seed=12, scale_q=scale_q)
+        c.sm = sm
+        c.check(**m)
+
+
+@pytest.mark.parametrize("new", [4, 40])
+def test_prompt_variant_nan(new, cuda_device):
+    # NaN values that the last queries see, that all see; queries and keys that are not finite; in either group of rows
+    c = Case(cuda_device, [130, 260], [new, new], 12, 2, 16, seed=9)
+    c.v.view(torch.uint8)[c.table[0, 128 // 16].long(), 0, 0, 5] = 0x7f
+    c.v.view(torch.uint8)[c.table[0, 128 // 16].long(), 1, 0, 77] = 0xff
+    c.v.view(torch.uint8)[c.table[1, 0].long(), 0, 3, 9] = 0x7f
+    t = c.tensors()
+    t[0][new + 1, 128 * 3 + 7] = float("inf")
+    kda_cache_attention(*t, max_new=1000)
+    got = t[-1].cpu().double().view(c.T, 2, 6, 128)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[new - 2:new, 0, :, 5] = True
+    nan[new - 2:new, 1, :, 77] = True
+    nan[new:, 0, :, 9] = True
+    nan[new + 1, 0, 3] = True
+    assert torch.equal(got.isnan(), nan)
+    c.v = torch.where(c.v & 0x7f == 0x7f, torch.zeros_like(c.v), c.v)
+    want, tol = c.reference()
+    ok = (got - want.view_as(got)).abs() <= tol.view_as(got)
+    assert ok[~nan].all()
+
+
+def test_prompt_variant_bad_blocks_and_graph(cuda_device):
+    c = Case(cuda_device, [200, 90], [3, 40], 4, 2, 16, seed=18)
+    t = list(c.tensors())
+    want_err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    err = torch.zeros_like(want_err)
+    t[3] = t[3].clone()
+    t[3][0, 2], t[3][1, 5] = -1, 2 ** 30
+    u = list(t)
+    u[-1] = t[-1].clone()
+    kda_cache_attention(*t, max_new=1, err_flag=want_err)                # the other variant, tested above
+    ws = cache_attention_workspace(4, 2, 100, cuda_device)
+    call = KdaCacheAttentionCall(*u, max_new=100, err_flag=err, workspace=ws)
+    call()
+    assert err.item() == want_err.item() == R.SLOT_RANGE
+    assert (t[-1].float() - u[-1].float()).norm() <= 2.0 ** -7 * t[-1].float().norm()
+    first = u[-1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        u[-1].fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, u[-1])
+    assert not ws[:11264].any()
