@@ -6,11 +6,11 @@
 // two kernels: one for up to 96 query rows per kv head and sequence, one
 // (at the end) for more.
 //
-// Measured on a GB300 against a copy's 6795 GB/s: 16 single tokens with 4,000
-// to 32,000 cached tokens each, 92 us (79 at a copy's rate); 64 sequences of 4
-// tokens, 64 q and 8 kv heads, 135 us (110); a small batch 7 us, of which the
-// launch, the plan and the trip to the first tile take most.  4 prompt chunks
-// of 515 tokens, 48 heads, 90 us; long ones reach 660 TFLOP/s of useful work.
+// Measured on a GB300 against a copy's 6795 GB/s: one token behind 260,000
+// cached ones, 96 q and 8 kv heads, 91 us (78 at a copy's rate); 64 sequences of
+// 4 tokens behind 1,000 to 16,384, 48 heads, 135 us (110); a small batch 7 us, of
+// which the launch, the plan and the trip to the first tile take most.  4 prompt chunks
+// of 515 tokens, 48 heads, 90 us; long ones reach 860 TFLOP/s of useful work.
 //
 // Products of the first kernel.  Both are formed transposed, so that the
 // cache's codes are the 128-row operand and the few queries the narrow one:
@@ -109,7 +109,7 @@ struct Cfg {
   static constexpr int kNan = GROUPS > 1 ? 4 : 1;
   static constexpr int kTmemCols = kN > 64 ? 512 : 4 * kN;  // S and O, two buffers each; a power of two
   static constexpr int kPartial = COLS * (32 + 2);       // floats of a warp's partial record: maxima, sums, 32 channels
-  // parts that one warp joins (16 long sequences: 92 us with 8, 94 with 16, 99 with all in one)
+  // parts that one warp joins (one token behind 260,000: 92 us with 8, 94 with 16, 99 with all in one)
   static constexpr int kJoinFan = 8;
   static constexpr int kBlocks = COLS / 8;               // 8-column blocks of a group's tensor-memory loads
   static constexpr int kMine = COLS / 4;                 // rows that a thread holds elements of

@@ -15,6 +15,12 @@
 // Eight lanes share a row of 128 channels, 16 channels each, as two 16-byte
 // loads: lane l holds the pairs 8l .. 8l + 7 of whichever pairing is used.
 //
+// Measured on a GB300 (a copy runs at 6795 GB/s): 16,384 token rows, 48 q and 8
+// kv heads, blocks of 64, 97 us for 500 MB, 74 at a copy's rate; loads wait on
+// registers there (80 a thread, 24 warps an SM, DRAM 67% busy).  64 sequences of 4
+// tokens 6.8 us, 4 single tokens 3.7 us.  One CTA per block and head, without
+// the sharing of sines, took 155, 13 and 5.4.
+//
 // The angle is pos * freq modulo one turn in 64-bit integers (exact for any
 // position), of which the upper 32 bits go to sincospif as a fraction of a
 // half turn: the error is that of one fp32 rounding.

@@ -3,7 +3,11 @@
 //
 // HBM bound on large batches (one row of target probabilities per sequence,
 // and one of the draft's where a draft was refused), latency bound on small
-// ones.  One cluster of CTAs per sequence: every CTA works out for itself which
+// ones: measured on a GB300, 131,072 tokens, 256 sequences of 4 rows 49 us for
+// the 206 MB that are read (4.2 TB/s; sequences whose draft was refused read two
+// rows, the others one, and 1,024 CTAs are 1.7 times what is resident), one
+// sequence 6.6 us, of which the trips judge -> row -> exchange -> search take
+// most.  One cluster of CTAs per sequence: every CTA works out for itself which
 // draft is the first refused (a few gathers), sums its part of that one row,
 // and the CTAs exchange their sums through distributed shared memory; the CTA
 // and warp in whose part the inversion ends have that part read once more (out
