@@ -6,7 +6,7 @@
 // ones: measured on a GB300, 131,072 tokens, 256 sequences of 4 rows 49 us for
 // the 206 MB that are read (4.2 TB/s; sequences whose draft was refused read two
 // rows, the others one, and 1,024 CTAs are 1.7 times what is resident), one
-// sequence 6.6 us, of which the trips judge -> row -> exchange -> search take
+// sequence 6.6 us, of which the trips decide -> row -> exchange -> search take
 // most.  One cluster of CTAs per sequence: every CTA works out for itself which
 // draft is the first refused (a few gathers), sums its part of that one row,
 // and the CTAs exchange their sums through distributed shared memory; the CTA
@@ -213,7 +213,7 @@ __device__ __forceinline__ void search(const Row& r, int begin, int end, uint64_
   }
 }
 // How many drafts of sequence n stand, and whether the next was refused (warp 0).
-__device__ __forceinline__ void judge(const Params& p, int n, bool report, int* verdict) {
+__device__ __forceinline__ void decide(const Params& p, int n, bool report, int* outcome) {
   const int lane = threadIdx.x & 31;
   bool stands = false, drafted = false;
   if (lane < p.T - 1) {
@@ -230,8 +230,8 @@ __device__ __forceinline__ void judge(const Params& p, int n, bool report, int* 
   const uint32_t s = __ballot_sync(0xffffffffu, stands), v = __ballot_sync(0xffffffffu, drafted);
   if (lane == 0) {
     const int k = __ffs(~s) - 1;  // leading drafts that stand; at most T - 1 < 32
-    verdict[0] = k;
-    verdict[1] = (v >> k) & 1;    // a draft stood at k and was refused
+    outcome[0] = k;
+    outcome[1] = (v >> k) & 1;    // a draft stood at k and was refused
   }
 }
 __device__ __forceinline__ Row row_of(const Params& p, int n, int k, bool refused) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const P
   constexpr int kWarps = THREADS / 32;
   __shared__ uint64_t cta_sum[2][kMaxCluster];  // every CTA's sum, in every CTA; of the rest, of the row itself
   __shared__ uint64_t warp_sums[kWarps];
-  __shared__ int verdict[2];
+  __shared__ int outcome[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = blockIdx.x / cluster, rank = blockIdx.x - n * cluster;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -281,10 +281,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const P
   // a CTA's memory may be written once that CTA has started: arrive here, wait
   // before the exchange
   if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  if (warp == 0) judge(p, n, rank == 0, verdict);
+  if (warp == 0) decide(p, n, rank == 0, outcome);
   __syncthreads();
-  const int k = verdict[0];
-  const bool refused = verdict[1];
+  const int k = outcome[0];
+  const bool refused = outcome[1];
   // the token of a row without mass, or of one whose sums run over; the barriers
   // below put it before the one that is found
   if (rank == 0 && tid == 0) p.tokens[static_cast<int64_t>(n) * p.T + k] = p.V - 1;

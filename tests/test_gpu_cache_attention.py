@@ -546,3 +546,37 @@ def test_prompt_variant_bad_blocks_and_graph(cuda_device):
         torch.cuda.synchronize()
         assert torch.equal(first, u[-1])
     assert not ws[:11264].any()
+
+
+def test_prompt_variant_batches_and_heads(cuda_device):
+    # more sequences than threads, most without queries; more heads per kv head than a tile has rows
+    rng = np.random.default_rng(4)
+    lens, new = rng.integers(1, 40, 900).tolist(), rng.integers(0, 2, 900).tolist()
+    c = Case(cuda_device, lens, new, 2, 1, 16, seed=33)
+    assert c.check(max_new=100) < 4e-3
+    for Hq in (130, 300):
+        c = Case(cuda_device, [150, 40, 9], [2, 1, 3], Hq, 1, 32, seed=Hq)
+        assert c.check(max_new=3) < 4e-3
+        assert c.check(max_new=1) < 4e-3
+
+
+def test_both_kernels_share_a_workspace_and_run_side_by_side(cuda_device):
+    ws = cache_attention_workspace(12, 2, 300, cuda_device)
+    c = Case(cuda_device, [3000, 700, 10], [60, 200, 4], 12, 2, 64, seed=34)
+    d = Case(cuda_device, [9000, 500], [1, 2], 12, 2, 64, seed=35)
+    t, u = c.tensors(), d.tensors()
+    for _ in range(3):                                      # one after the other, the same workspace
+        kda_cache_attention(*t, max_new=300, workspace=ws)
+        kda_cache_attention(*u, max_new=2, workspace=ws)
+    assert c.compare(t[-1]) < 4e-3 and d.compare(u[-1]) < 4e-3
+    first, second = t[-1].clone(), u[-1].clone()
+    side = torch.cuda.Stream()
+    a, b = KdaCacheAttentionCall(*t, max_new=300), KdaCacheAttentionCall(*u, max_new=2)
+    again = KdaCacheAttentionCall(*t[:-1], torch.empty_like(first), max_new=300)
+    for _ in range(10):                                     # at the same time, a workspace each
+        a()
+        with torch.cuda.stream(side):
+            b(side)
+            again(side)
+    torch.cuda.synchronize()
+    assert torch.equal(first, t[-1]) and torch.equal(second, u[-1]) and torch.equal(first, again._keep[8])
