@@ -263,3 +263,42 @@ def test_refusals(cuda_device):
         kda_qk_rope(*args, **{**kw, "k_out": c.qkv[:, 512:768]})
     with pytest.raises(Exception, match="rot_dim"):
         kda_qk_rope(*args, **{**kw, "rope_freqs": torch.zeros(4, dtype=torch.int64, device=cuda_device)})
+
+
+@pytest.mark.parametrize("Hq, Hkv, bs, inter", [(22, 3, 16, False), (40, 1, 256, True), (33, 2, 64, False)])
+def test_large_batches_give_the_bits_of_small_ones(Hq, Hkv, bs, inter, cuda_device):
+    # every SM several times over, other splits of rows and heads over CTAs; the last group of heads not whole
+    T = 2 * 152 * 24 + 5
+    g = torch.Generator(device=cuda_device).manual_seed(Hq)
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * 128 + 64, device=cuda_device, generator=g).bfloat16()
+    w = torch.rand(2, 128, device=cuda_device, generator=g) + 0.5
+    pos = torch.randint(0, 10 ** 6, (T,), device=cuda_device, generator=g, dtype=torch.int32)
+    nb = -(-T // bs)
+    kw = dict(num_q_heads=Hq, num_kv_heads=Hkv, rope_freqs=rope_frequencies(96, 1e4, cuda_device), interleaved=inter,
+              q_weight=w[0], k_weight=w[1])
+
+    def run(rows):
+        n = rows.numel()
+        q, k = (torch.full((n, h * 128), 9.0, dtype=torch.bfloat16, device=cuda_device) for h in (Hq, Hkv))
+        cache = [torch.zeros(nb, Hkv, bs, 128, dtype=torch.uint8, device=cuda_device).view(torch.float8_e4m3fn) for _ in "kv"]
+        scale = [torch.zeros(nb, Hkv, device=cuda_device) for _ in "kv"]
+        err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+        kda_qk_rope(qkv[rows], pos[rows], q, k_out=k, k_cache=cache[0], v_cache=cache[1], k_scale=scale[0], v_scale=scale[1],
+                    slot_map=rows, err_flag=err, **kw)
+        assert err.item() == 0
+        return q, k, [c.view(torch.uint8) for c in cache], scale
+    rows = torch.arange(T, device=cuda_device)
+    q, k, cache, scale = run(rows)
+    # the same rows in small batches (tested above against 64 bits)
+    step = 2048
+    for t in range(0, T, step):
+        part = rows[t:t + step]
+        q2, k2, cache2, scale2 = run(part)
+        assert torch.equal(q[t:t + step], q2) and torch.equal(k[t:t + step], k2)
+        b0, b1 = t // bs, -(-min(t + step, T) // bs)
+        for a, b in zip(cache + scale, cache2 + scale2):
+            assert torch.equal(a[b0:b1], b[b0:b1])
+    # in place
+    x = qkv.clone()
+    kda_qk_rope(x, pos, x[:, :Hq * 128], **kw)
+    assert torch.equal(x[:, :Hq * 128], q) and torch.equal(x[:, Hq * 128:], qkv[:, Hq * 128:])
