@@ -92,7 +92,8 @@ typedef struct KdaCacheAttentionArgs {
 #define KDA_CACHE_ATTENTION_COUNTER_BYTES 45056
 
 /* Workspace bytes of a call with these head counts and max_new; -1 for an
- * argument out of range.  It does not grow with B, T or the lengths. */
+ * argument out of range.  It does not grow with B, T or the lengths, and a
+ * workspace for a larger max_new serves smaller ones (3 to 41 MB). */
 int64_t kda_cache_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t max_new);
 
 /*

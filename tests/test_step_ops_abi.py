@@ -206,3 +206,11 @@ def test_reference_rounds_like_torch():
     want = torch.from_numpy(np.clip(x, -448, 448)).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     got = R.e4m3_nearest(x.astype(np.float32).astype(np.float64))
     assert np.array_equal(got[:-1], want[:-1]) and got[-1] & 127 == 127
+
+
+def test_attention_workspace_grows_with_max_new(lib):
+    size = lib.kda_cache_attention_workspace_bytes
+    size.argtypes, size.restype = [ctypes.c_int32] * 3, ctypes.c_int64
+    for G in (1, 3, 8, 50):
+        sizes = [size(2 * G, 2, n) for n in range(1, 300)]
+        assert sizes == sorted(sizes) and sizes[-1] < 2 ** 26
