@@ -12,7 +12,7 @@
 // each new block is opened by exactly one row.
 //
 // Measured on a GB300, back to back: 64 requests 4.5 us, 1,024 requests
-// with 48,000 token rows 5.3 us (their bytes take 0.1 us: what is left is the
+// with 48,000 token rows 6.0 us (their bytes take 0.1 us: what is left is the
 // launch, two trips to memory and the scan).  Sizes that are powers of two are
 // shifted, not divided; sums are 64 bits wide, so that lengths whose total
 // passes 2^31 are found rather than wrapped.
