@@ -70,7 +70,9 @@ class KdaVerifyArgs(ctypes.Structure):
                 ("num_accepted", _ptr), ("next_slot", _ptr), ("err_flag", _ptr)]
 
 
-_current_raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
+# (Looked up without asking for a device: that would initialise the driver, and a process that imports the package
+# and then forks could not use CUDA in its children.)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _p(t: torch.Tensor | None):

@@ -5,6 +5,8 @@ import ctypes
 import math
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -214,3 +216,16 @@ def test_attention_workspace_grows_with_max_new(lib):
     for G in (1, 3, 8, 50):
         sizes = [size(2 * G, 2, n) for n in range(1, 300)]
         assert sizes == sorted(sizes) and sizes[-1] < 2 ** 26
+
+
+def test_import_leaves_cuda_to_forked_children():
+    # a server imports the package and then forks workers that use CUDA: importing must not initialise the driver, which
+    # marks every later fork as unable to.  A process of its own, so that no other test's use of CUDA counts.
+    code = ("import os, sys, torch\n"
+            "import linear_attention_decode_04_gb300\n"
+            "assert not torch.cuda.is_initialized()\n"
+            "pid = os.fork()\n"
+            "if pid == 0:\n"
+            "    os._exit(3 if torch.cuda._is_in_bad_fork() else 0)\n"
+            "sys.exit(os.waitstatus_to_exitcode(os.waitpid(pid, 0)[1]))\n")
+    assert subprocess.run([sys.executable, "-c", code], cwd=ROOT, timeout=300).returncode == 0
