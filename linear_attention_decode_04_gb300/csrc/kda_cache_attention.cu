@@ -1108,6 +1108,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
               if (before == parts - 1) *counter = 0;
             }
+            __syncwarp();  // what lane 0 acquired, the others may read (a shuffle passes the value, not the order)
             return __shfl_sync(0xffffffffu, before, 0) == parts - 1;
           };
           // Up to kJoinFan parts are joined by the last to arrive; of more, every fan
@@ -1587,6 +1588,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
                 asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
                 if (before == parts - 1) *counter = 0;
               }
+              __syncwarp();  // what lane 0 acquired, the others may read (as above)
               return __shfl_sync(0xffffffffu, before, 0) == parts - 1;
             };
             const int fan = (static_cast<int>(blockIdx.x) - c0) / C::kJoinFan, fans = (c1 - c0) / C::kJoinFan + 1;

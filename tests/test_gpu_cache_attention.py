@@ -580,3 +580,25 @@ def test_both_kernels_share_a_workspace_and_run_side_by_side(cuda_device):
             again(side)
     torch.cuda.synchronize()
     assert torch.equal(first, t[-1]) and torch.equal(second, u[-1]) and torch.equal(first, again._keep[8])
+
+
+COUNTERS = 45056 // 4        # KDA_CACHE_ATTENTION_COUNTER_BYTES
+# (query heads, kv heads, queries): 8, 16, 24, 32, 64 and 96 query rows per kv head, one variant each, and 120 for prompts
+VARIANTS = [(4, 2, 4), (8, 2, 4), (12, 2, 4), (16, 2, 4), (32, 2, 4), (24, 1, 4), (48, 2, 5)]
+
+
+@pytest.mark.parametrize("Hq, Hkv, new", VARIANTS)
+def test_every_row_tile_joins_many_parts(Hq, Hkv, new, cuda_device):
+    # units over more than eight CTAs (two levels of joins) beside short ones; the same bits every time, whichever part
+    # comes last, and the whole counter area is zero again
+    c = Case(cuda_device, [20000, 5, 2500], [new] * 3, Hq, Hkv, 64, seed=50 + Hq)
+    ws = cache_attention_workspace(Hq, Hkv, new, cuda_device)
+    t = c.tensors()
+    first = None
+    for _ in range(20):
+        t[-1].fill_(7.0)
+        kda_cache_attention(*t, max_new=new, workspace=ws)
+        first = t[-1].clone() if first is None else first
+        assert torch.equal(first, t[-1])
+        assert not ws[:COUNTERS].any()
+    assert c.compare(t[-1]) < 4e-3
