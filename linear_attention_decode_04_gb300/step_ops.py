@@ -88,8 +88,10 @@ def _shaped(t, name, dtype, device, shape):
 
 class _Call:
     """What the prepared calls share.  ``_own`` holds the tensors that the call
-    allocated: when it runs on another stream than they were made on, the
-    allocator is told, so that dropping the call early stays safe."""
+    allocated.  Their memory may have held others that work on the stream they
+    were made on still uses, and may hold others again once the call is
+    dropped: on another stream the first run therefore waits for that stream,
+    and the allocator is told of every run."""
 
     def _prepare(self, name: str, args: ctypes.Structure, device: torch.device, keep: tuple, own: tuple = ()):
         lib = load_library()
@@ -100,14 +102,20 @@ class _Call:
         args.struct_size = ctypes.sizeof(args)
         self.args, self._argp = args, ctypes.addressof(args)
         self._keep, self._own = keep, own
-        self._home = torch.cuda.current_stream(device).cuda_stream
+        self._home_stream = torch.cuda.current_stream(device)
+        self._home = self._home_stream.cuda_stream
+        self._ordered = set()  # streams that have waited for it
 
     def __call__(self, stream: torch.cuda.Stream | None = None) -> None:
         # the stream's handle alone: a Stream object takes 2 us to make, which is what a small call takes on the GPU
         s = _current_raw_stream(self._index) if stream is None else stream.cuda_stream
         if s != self._home and self._own and not torch.cuda.is_current_stream_capturing():
+            other = torch.cuda.current_stream(self.device) if stream is None else stream
+            if s not in self._ordered:
+                other.wait_stream(self._home_stream)
+                self._ordered.add(s)
             for t in self._own:
-                t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+                t.record_stream(other)
         if torch.cuda.current_device() == self._index:
             rc = self._fn(self._argp, s)
         else:
