@@ -605,18 +605,17 @@ __device__ __forceinline__ void produce(const Params& p, M& S, Share& sh, bool m
   };
   Ref a = take(), b = take();
   float2 sa = scales(a);
-  bool ok = true;
   uint32_t k_sent = 0, v_sent = 0;
   for (uint32_t it = 0; a.valid; ++it) {
     const float2 sb = scales(b);
     const Ref c = take();
     const uint32_t ks = it % C::kK, vs = it % C::kV, kr = it / C::kK, vr = it / C::kV;
-    if (kr > 0 && !(ok = bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed))) break;
+    if (kr > 0 && !bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed)) break;
     if (lane == 0) bar_expect(&S.k_full[ks], kTileBytes);
     __syncwarp();
     if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
     ++k_sent;
-    if (vr > 0 && !(ok = bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed))) break;
+    if (vr > 0 && !bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed)) break;
     if (lane == 0) bar_expect(&S.v_full[vs], kTileBytes);
     __syncwarp();
     if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
@@ -630,12 +629,11 @@ __device__ __forceinline__ void produce(const Params& p, M& S, Share& sh, bool m
     if (lane == 0) bar_arrive(&S.sc_full[vs]);
     a = b, b = c, sa = sb;
   }
-  if (!ok) {  // nothing may land in shared memory after the CTA is gone
-    for (uint32_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j)
-      bar_drain(&S.k_full[j % C::kK], (j / C::kK) & 1);
-    for (uint32_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j)
-      bar_drain(&S.v_full[j % C::kV], (j / C::kV) & 1);
-  }
+  // Nothing may land in shared memory after the CTA is gone.  (Where all went well the
+  // last copies have been waited for by who used them, or are about to be; where another
+  // role gave up, here or at the end, nobody else waits for them.)
+  for (uint32_t j = k_sent > C::kK ? k_sent - C::kK : 0; j < k_sent; ++j) bar_drain(&S.k_full[j % C::kK], (j / C::kK) & 1);
+  for (uint32_t j = v_sent > C::kV ? v_sent - C::kV : 0; j < v_sent; ++j) bar_drain(&S.v_full[j % C::kV], (j / C::kV) & 1);
 }
 
 // ---------------------------------------------------------------- the kernel
