@@ -606,16 +606,18 @@ __device__ __forceinline__ void produce(const Params& p, M& S, Share& sh, bool m
   Ref a = take(), b = take();
   float2 sa = scales(a);
   uint32_t k_sent = 0, v_sent = 0;
+  // The lanes leave together: one that gave up alone would leave the others at a __syncwarp().
+  auto gave_up = [&](uint64_t* empty, uint32_t parity) { return __any_sync(0xffffffffu, !bar_wait(empty, parity, &S.failed)); };
   for (uint32_t it = 0; a.valid; ++it) {
     const float2 sb = scales(b);
     const Ref c = take();
     const uint32_t ks = it % C::kK, vs = it % C::kV, kr = it / C::kK, vr = it / C::kV;
-    if (kr > 0 && !bar_wait(&S.k_empty[ks], (kr - 1) & 1, &S.failed)) break;
+    if (kr > 0 && gave_up(&S.k_empty[ks], (kr - 1) & 1)) break;
     if (lane == 0) bar_expect(&S.k_full[ks], kTileBytes);
     __syncwarp();
     if (lane < ppt) tma_tile(s32(S.k[ks]) + lane * rows * kD, &k_map, a.tok, a.head, a.block, &S.k_full[ks]);
     ++k_sent;
-    if (vr > 0 && !bar_wait(&S.v_empty[vs], (vr - 1) & 1, &S.failed)) break;
+    if (vr > 0 && gave_up(&S.v_empty[vs], (vr - 1) & 1)) break;
     if (lane == 0) bar_expect(&S.v_full[vs], kTileBytes);
     __syncwarp();
     if (lane < ppt) tma_tile(s32(S.v[vs]) + lane * rows * kD, &v_map, a.tok, a.head, a.block, &S.v_full[vs]);
