@@ -54,8 +54,9 @@ extern "C" {
  *                         is outside [0, num_blocks): treated as no block
  * Entries past max_blocks take nothing from the list, and *free_head_out
  * never passes num_free.  Blocks for tokens past row T are taken from the
- * list, but their table entries are not written.  No result may overlap an
- * input (seq_lens is not cached_lens, and so on) or another result.
+ * list, stored in the table and counted as held like the others.  No result
+ * may overlap an input (seq_lens is not cached_lens, and so on) or another
+ * result.
  */
 typedef struct KdaBlockTablesArgs {
   uint32_t struct_size;          /* = sizeof(KdaBlockTablesArgs) */

@@ -65,6 +65,18 @@ __device__ __forceinline__ Request request(const Params& p, int i) {
   return r;
 }
 
+// Entry f of the free list: a block, or -1 and the reason among `errors`.
+__device__ __forceinline__ int listed_block(const Params& p, int64_t f, int& errors) {
+  if (f < 0 || f >= p.num_free) {
+    errors |= KDA_DEVERR_CAPACITY;
+    return -1;
+  }
+  const int b = p.free_blocks[f];
+  if (b >= 0 && b < p.num_blocks) return b;
+  errors |= KDA_DEVERR_SLOT_RANGE;
+  return -1;
+}
+
 __global__ void __launch_bounds__(kThreads) block_tables_kernel(const Params p) {
   __shared__ int64_t tok_s[kTile + 1], blk_s[kTile];
   __shared__ int64_t warp_tok[kThreads / 32], warp_blk[kThreads / 32];
@@ -128,6 +140,18 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const Params p) 
       bo += need[k];
     }
     __syncthreads();
+    if (first_cta && tok + ntile > p.T) {
+      // blocks that rows past the end would open: taken and counted, so stored as well; a warp per request
+      for (int j = warp; j < min(kTile, p.B - base); j += kThreads / 32) {
+        if ((j + 1 < kTile ? tok_s[j + 1] : tok + ntile) <= p.T) continue;
+        const Request r = request(p, base + j);
+        for (int e = lane; e < r.need; e += 32) {
+          const int page = r.first + e;
+          if (tok_s[j] + (static_cast<int64_t>(page) * p.bs - r.c) >= p.T)
+            p.table[(base + j) * p.table_stride + page] = listed_block(p, head + blk_s[j] + e, errors);
+        }
+      }
+    }
     if (row >= tok && row < tok + ntile && row < p.T) {
       // the last request of the tile that starts at or before the row; it is
       // not empty, because the next one starts behind the row
@@ -145,13 +169,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(const Params p) 
       if (page < p.max_blocks) {
         int32_t* entry = p.table + i * p.table_stride + page;
         if (page >= r.first) {
-          const int64_t f = head + blk_s[lo] + (page - r.first);
-          if (f >= 0 && f < p.num_free) {
-            b = p.free_blocks[f];
-            if (b < 0 || b >= p.num_blocks) b = -1, errors |= KDA_DEVERR_SLOT_RANGE;
-          } else {
-            errors |= KDA_DEVERR_CAPACITY;
-          }
+          b = listed_block(p, head + blk_s[lo] + (page - r.first), errors);
           if (at == 0) *entry = b;
         } else {
           b = *entry;

@@ -113,3 +113,45 @@ def test_graph_replay_follows_the_lengths(cuda_device):
         assert err == 0 and call.slot_map.tolist() == slot and call.positions.tolist() == pos
         assert head.item() == h and np.array_equal(table.cpu().numpy(), t)
         c = np.asarray(lens)
+
+
+def steps_over_stale_tables(dev, cached, new, bs, Ts, M, free, num_blocks, head=0, held=None):
+    """Calls with T = each of ``Ts`` rows on the same requests, the held blocks and the list's head of one fed to the
+    next, over a table that is full of other requests' blocks.  A call's table, counts and head are those of a call with
+    room for every row, and its rows the first T of that call's."""
+    B, total = len(cached), sum(new)
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    table = np.full((B, M), 7, np.int32)
+    held = [-(-c // bs) for c in cached] if held is None else held
+    g = [t(cached), t(new), torch.from_numpy(table.copy()).to(dev), t(free)]
+    owners = []
+    for T in Ts:
+        want = R.block_tables(cached, new, table, free, head, bs, num_blocks, max(T, total), held)
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        got = kda_block_tables(*g, t([head]), held_blocks=t(held), block_size=bs, num_blocks=num_blocks, num_tokens=T,
+                               err_flag=err)
+        assert err.item() == want[7] | (R.CAPACITY if T < total else 0)
+        table, head, held = want[0], want[5], want[6]
+        assert np.array_equal(g[2].cpu().numpy(), table)
+        assert got[0].tolist() == want[1] and got[1].tolist() == want[2]
+        assert got[2].tolist() == want[3][:T] and got[3].tolist() == want[4][:T]
+        assert got[4].item() == head and got[5].tolist() == held
+        owners = got[3].tolist()
+    return owners
+
+
+def test_blocks_for_rows_past_the_end_are_in_the_table(cuda_device):
+    # a step with more tokens than rows, then the same requests with room for all: the blocks that the first took and
+    # counted as held are the ones that the second uses, not what the table held before
+    slots = steps_over_stale_tables(cuda_device, [0, 0], [16, 16], 16, [16, 32], 3, list(range(20, 30)), 40)
+    assert slots == [*range(20 * 16, 21 * 16), *range(21 * 16, 22 * 16)]
+    # requests cut in the middle and past the end, several blocks each, rows of no CTA; a list that runs out or names
+    # blocks that are not there
+    steps_over_stale_tables(cuda_device, [3, 0, 40, 15], [90, 0, 33, 600], 16, [0, 50, 95, 1000], 45, list(range(8, 99)), 100)
+    steps_over_stale_tables(cuda_device, [0, 5, 0], [40, 70, 64], 16, [41, 60, 200], 6, [9, 10, 11, 12, 13], 20)
+    steps_over_stale_tables(cuda_device, [0, 0], [20, 60], 16, [10, 80], 5, [9, 55, 10, -3, 11, 12], 20)
+    # tables that are too narrow, blocks held from an earlier step, batches over several tiles of the scan
+    steps_over_stale_tables(cuda_device, [0, 10], [100, 100], 24, [30, 200], 3, list(range(50)), 50, held=[1, 2])
+    rng = np.random.default_rng(11)
+    cached, new = rng.integers(0, 60, 2500).tolist(), rng.integers(0, 40, 2500).tolist()
+    steps_over_stale_tables(cuda_device, cached, new, 16, [700, sum(new) // 2, sum(new)], 8, list(range(20000)), 20000, head=5)
