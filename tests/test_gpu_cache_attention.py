@@ -602,3 +602,16 @@ def test_every_row_tile_joins_many_parts(Hq, Hkv, new, cuda_device):
         assert torch.equal(first, t[-1])
         assert not ws[:COUNTERS].any()
     assert c.compare(t[-1]) < 4e-3
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("Hq, Hkv, new", [(8, 1, 1), (6, 2, 5), (20, 2, 2), (10, 2, 5), (16, 2, 4), (11, 1, 3), (16, 2, 8),
+                                          (13, 1, 5), (24, 2, 8), (97, 1, 1)])
+def test_every_row_tile_at_every_block_size(bs, Hq, Hkv, new, cuda_device):
+    # 8, 15, 20, 25, 32, 33, 64, 65, 96 and 97 query rows per kv head: both ends of every variant's range, whose block
+    # scales and copies differ with the block size; lengths around a tile, several tiles, parts of several CTAs
+    lens = [max(n, new) for n in (new, 127, 128, 129, 1, 300, 3000)]
+    c = Case(cuda_device, lens, [new] * len(lens), Hq, Hkv, bs, seed=bs + Hq + new, row_pad=8, extra=2)
+    ws = cache_attention_workspace(Hq, Hkv, new, cuda_device)
+    assert c.check(ws=ws) < 4e-3
+    assert not ws[:COUNTERS].any()
