@@ -187,3 +187,49 @@ def test_next_slot_in_the_place_of_src_slot(N, V, cuda_device):
     call.args.next_slot = src.data_ptr()
     call()
     assert src.tolist() == want[2] and call.num_accepted.tolist() == want[1] and call.tokens.tolist() == want[0]
+
+
+class SharedRows:
+    """[n, t] rows that are rows of a small pool, read as an array by the reference."""
+
+    def __init__(self, pool, at):
+        self.pool, self.at, self.shape = pool, at, (*at.shape, pool.shape[1])
+
+    def __getitem__(self, i):
+        row = self.pool[self.at[i[0], i[1]]]
+        return row if len(i) == 2 else row[i[2]]
+
+
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("N, T, V, cluster", [(39, 2, 140001, 8), (80, 3, 140001, 8), (256, 4, 131072, 4), (310, 2, 40001, 2),
+                                              (700, 2, 16385, 1)])
+def test_large_batches_of_long_rows(N, T, V, cluster, probs, cuda_device):
+    # batches of more sequences than the 512-thread kernel takes, whose rows are long: clusters are made larger again
+    # (CTAs per sequence: the rule of the launch, repeated here), and a warp's part takes many trips
+    c = 8
+    while c > 1 and N * c > 4 * 152:
+        c //= 2
+    while c < 8 and V // (2 * c) > 16384:
+        c *= 2
+    assert N * 8 > 2 * 152 and c == cluster
+    rng = np.random.default_rng(N + T + V)
+    z = rng.normal(size=(7, V)) * 3
+
+    def softmax(x):
+        e = np.exp(x - x.max(-1, keepdims=True))
+        return (e / e.sum(-1, keepdims=True)).astype(np.float32)
+    pool, near = softmax(z), softmax(z + 0.6 * rng.normal(size=z.shape))
+    at = rng.integers(0, 7, (N, T))
+    # drafts from the draft model's rows by inversion; without them, the target's likely tokens
+    cum = np.cumsum((near if probs else pool).astype(np.float64), -1)
+    draft = np.array([[min(int(np.searchsorted(cum[at[n, t]], rng.random())), V - 1) for t in range(T - 1)]
+                      for n in range(N)], np.int32)
+    u, su = rng.random((N, T - 1), np.float32) * np.float32(1.0 if probs else 2e-3), rng.random(N, np.float32)
+    slots = (rng.permutation(N * T) + 1).astype(np.int32).reshape(N, T)
+    want = R.verify(draft, SharedRows(pool, at), u, su, SharedRows(near, at[:, :-1]) if probs else None, None, slots)
+    g = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(cuda_device)  # noqa: E731
+    rows = g(at)
+    tok, acc, nxt = kda_verify_draft(g(draft), g(pool)[rows], g(u), g(su), slot_idx=g(slots),
+                                     draft_probs=g(near)[rows[:, :-1]] if probs else None)
+    assert acc.tolist() == want[1] and tok.tolist() == want[0] and nxt.tolist() == want[2]
+    assert 0 < sum(want[1]) < N * (T - 1)               # drafts of both kinds were met
