@@ -615,3 +615,33 @@ def test_every_row_tile_at_every_block_size(bs, Hq, Hkv, new, cuda_device):
     ws = cache_attention_workspace(Hq, Hkv, new, cuda_device)
     assert c.check(ws=ws) < 4e-3
     assert not ws[:COUNTERS].any()
+
+
+@pytest.mark.parametrize("bs", [16, 128, 256])
+@pytest.mark.parametrize("Hq, Hkv, new", VARIANTS)
+def test_every_row_tile_masks_and_values(Hq, Hkv, new, bs, cuda_device):
+    # rows that see nothing, lengths of zero and below the queries; values that are not finite and that the last query
+    # alone, or all queries, see; a key that is NaN and only the last query sees; an infinite query
+    c = Case(cuda_device, [0, new - 2, new, 300, 133], [new] * 5, Hq, Hkv, bs, seed=70 + Hq + bs, extra=1)
+    c.check()
+    last = Hkv - 1
+    c.v[c.table[3, 299 // bs].long(), 0, 299 % bs, 5] = 0x7f                  # position 299 of 300: the last query's own
+    c.v[c.table[4, 2 // bs].long(), last, 2 % bs, 9] = 0xff                   # position 2: every query of the sequence
+    c.k[c.table[4, 132 // bs].long(), 0, 132 % bs, 8] = 0x7f                  # the last token of 133
+    c.q[3 * new, 128 * (Hq - 1) + 3] = float("inf")                           # first query, last head of the fourth
+    t = c.tensors()
+    kda_cache_attention(*t, max_new=new)
+    got = t[-1].cpu().double().view(c.T, Hkv, Hq // Hkv, 128)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[4 * new - 1, 0, :, 5] = True
+    nan[4 * new:5 * new, last, :, 9] = True
+    nan[5 * new - 1, 0] = True
+    nan[3 * new, last, -1] = True
+    assert torch.equal(got.isnan(), nan)
+    # all else is as if the values and the key were finite
+    c.v = torch.where(c.v & 0x7f == 0x7f, torch.zeros_like(c.v), c.v)
+    c.k = torch.where(c.k & 0x7f == 0x7f, torch.zeros_like(c.k), c.k)
+    c.q[3 * new, 128 * (Hq - 1) + 3] = 0.0
+    want, tol = c.reference()
+    ok = (got - want.view_as(got)).abs() <= tol.view_as(got)
+    assert ok[:c.cu[-1]][~nan[:c.cu[-1]]].all()
