@@ -11,8 +11,8 @@
 // from the free list.  The row that opens a block stores its table entry;
 // each new block is opened by exactly one row.
 //
-// Measured on a GB300, back to back: 64 requests 4.5 us, 1,024 requests
-// with 48,000 token rows 6.0 us (their bytes take 0.1 us: what is left is the
+// Measured on a GB300, back to back: 64 requests 4.4 to 4.7 us, 1,024 requests
+// with 48,000 token rows 5.7 to 6.1 us (their bytes take 0.1 us: what is left is the
 // launch, two trips to memory and the scan).  Sizes that are powers of two are
 // shifted, not divided; sums are 64 bits wide, so that lengths whose total
 // passes 2^31 are found rather than wrapped.

@@ -8,9 +8,11 @@
 //
 // Measured on a GB300 against a copy's 6795 GB/s: one token behind 260,000
 // cached ones, 96 q and 8 kv heads, 91 us (78 at a copy's rate); 64 sequences of
-// 4 tokens behind 1,000 to 16,384, 48 heads, 135 us (110); a small batch 7 us, of
+// 4 tokens behind 1,000 to 16,384, 48 heads, 134 us (110); a small batch 7 us, of
 // which the launch, the plan and the trip to the first tile take most.  4 prompt chunks
 // of 515 tokens, 48 heads, 90 us; long ones reach 860 TFLOP/s of useful work.
+// 33 to 96 rows are far from the copy's rate: 64 sequences of 8 tokens, 64 heads, 234
+// us (112); their variants share maxima between groups and spill registers.
 //
 // Products of the first kernel.  Both are formed transposed, so that the
 // cache's codes are the 128-row operand and the few queries the narrow one:
@@ -22,6 +24,14 @@
 // as an M-major one.  The narrow operand is split into two e4m3 parts (leading
 // and remainder), each a product of its own into the same accumulator; the
 // tensor cores have time for that, and no code of the cache is ever converted.
+// What that rounds: the parts end at e4m3's smallest step, 2^-9, below a largest
+// value of 2^8 (of a tile's weights) or 224 to 448 (of a query row).  So a weight is
+// off by 2^-8 of itself at most, or 2^-18 of its tile's largest; its rounding to
+// fp16 on the way (2^-12) is small beside that and lets conversions and the remainder's
+// subtraction work on pairs.  The output is rounded to bf16's 2^-8 in the end; a third part would cost
+// half as many products again for bits that are lost there.  The softmax sum adds the
+// unrounded weights: the roundings, as often up as down, then stay in the numerator
+// alone, where they average out, and no sum has to wait for the parts.
 //
 // Block scales.  k_scale multiplies S.  v_scale is folded into the weights:
 // with z = s + log2(v_scale) a token's weight is w = 2^(z - M), M the largest
@@ -44,7 +54,8 @@
 // through shared memory per tile; up to 24 rows one group is enough (two CTAs
 // an SM hide one another's waits), above it several groups of 16 share the
 // tile: more warps hide the chain of one tile better than longer columns do
-// (64 sequences x 8 tokens x 64 heads: 244 us with groups of 16, 295 with 32).
+// (64 sequences x 8 tokens x 64 heads: 244 us with groups of 16 when that was chosen,
+// 295 with 32).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,7 +81,11 @@ constexpr int kMaxPages = 8;               // blocks of a tile, at block size 16
 constexpr int kMaxCtas = 304;              // 2 x 152
 // What beginning and ending a unit costs, in tiles: the work is dealt out by
 // tiles + kUnitCost per unit, so that CTAs with many short units end with the rest.
-// (Long prompts: 90 us with 4, 93 with 3 or 6, 101 with 2.)
+// One value for all variants, measured with 2, 4 and 8: prompt chunks 101, 90 and 94 us;
+// 64 sequences behind 1,000 to 16,384 tokens, 8 rows 120, 121 and 124, 16 rows 117, 117
+// and 121, 24 rows 135, 134 and 137, 32 rows 163, 156 and 158, 64 rows 245, 234 and 246,
+// 96 rows 363, 339 and 343; one long sequence 91 with any.  Only many short units of few
+// rows want less: 500 sequences of 10 to 2,000 tokens, 8 rows, 114, 124 and 141.
 constexpr int kUnitCost = 4;
 constexpr int kCounters = 4 * 6 * 152;     // of each kind: CTAs x warps that join, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -1151,10 +1166,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 // two warpgroups work on rows of their own, and one's arithmetic runs while
 // the other waits for its products.
 //
-// What bounds it: the chain weights -> products -> maximum -> weights of each
-// group (with next to no arithmetic left between them a tile still takes
+// What bounds long chunks: the chain weights -> products -> maximum -> weights of
+// each group (with next to no arithmetic left between them a tile still takes
 // 3,500 cycles for both groups; 5,400 with it, of which the tensor cores are
-// busy 2,100).  4,096 tokens behind 12,000, 64 heads: 2.17 ms (3.57 with the
+// busy 2,100).  Short ones spend less than half their time there (4 chunks of up to
+// 515 tokens behind up to 4,100: 15 tiles an SM, some 40 of 90 us); by inference, not
+// by a profile, the rest is what beginning, cutting and joining their units costs.  4,096 tokens behind 12,000, 64 heads: 2.17 ms (3.57 with the
 // kernel above; its threads exchange maxima over shared memory).  Measured and
 // left out: two threads per row (registers: 4.6 ms), products in halves of 64
 // tokens (2.45 ms), 64 tokens at a time (2.2 to 2.4 ms).

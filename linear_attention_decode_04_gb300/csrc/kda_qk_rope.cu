@@ -19,11 +19,14 @@
 // kv heads, blocks of 64, 97 us for 500 MB, 74 at a copy's rate; loads wait on
 // registers there (80 a thread, 24 warps an SM, DRAM 67% busy).  64 sequences of 4
 // tokens 6.8 us, 4 single tokens 3.7 us.  One CTA per block and head, without
-// the sharing of sines, took 155, 13 and 5.4.
+// the sharing of sines, took 155, 13 and 5.4.  Without a cache, queries and keys
+// written as bf16: 87 us (69 at a copy's rate), and 4.4 and 2.7 us for 256 and 4 rows.
 //
 // The angle is pos * freq modulo one turn in 64-bit integers (exact for any
 // position), of which the upper 32 bits go to sincospif as a fraction of a
-// half turn: the error is that of one fp32 rounding.
+// half turn.  Rounding that to fp32 is off by at most 2^-25 of a half turn, and the
+// sines are fp32's: a sine or cosine is off by less than 2^-22, where the outputs are
+// rounded to 2^-8 (bf16) or 2^-4 (e4m3) of themselves.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

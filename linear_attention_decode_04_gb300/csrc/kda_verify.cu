@@ -5,9 +5,12 @@
 // and one of the draft's where a draft was refused), latency bound on small
 // ones: measured on a GB300, 131,072 tokens, 256 sequences of 4 rows 49 us for
 // the 206 MB that are read (4.2 TB/s; sequences whose draft was refused read two
-// rows, the others one, and 1,024 CTAs are 1.7 times what is resident), one
-// sequence 6.6 us, of which the trips decide -> row -> exchange -> search take
-// most.  One cluster of CTAs per sequence: every CTA works out for itself which
+// rows, the others one).  The loads alone took 37 us, a copy would take 30: what is
+// missing is most likely bytes in flight, two 16-byte loads per row and thread, in the
+// registers that the arithmetic needs too.  That 1,024 CTAs are 1.7 times what is
+// resident is not it: CTAs that take rows from a counter were no faster.  One sequence
+// takes 6.6 to 7.6 us from card to card, of which the trips decide -> row -> exchange ->
+// search take most.  One cluster of CTAs per sequence: every CTA works out for itself which
 // draft is the first refused (a few gathers), sums its part of that one row,
 // and the CTAs exchange their sums through distributed shared memory; the CTA
 // and warp in whose part the inversion ends have that part read once more (out

@@ -415,7 +415,8 @@ def kda_cache_attention(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, 
                         max_new: int = 1, num_q_heads: int | None = None, sm_scale: float = 0.0, workspace=None,
                         err_flag=None, stream: torch.cuda.Stream | None = None) -> None:
     """Causal attention of the batch's queries over the 8-bit paged cache, to
-    ``out`` (see ``KdaCacheAttentionCall``)."""
+    ``out`` (see ``KdaCacheAttentionCall``).  Without ``workspace`` every call
+    makes and clears one of 3 to 41 MB: a loop keeps one."""
     with torch.cuda.stream(stream):
         KdaCacheAttentionCall(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, out,
                               max_new=max_new, num_q_heads=num_q_heads, sm_scale=sm_scale, workspace=workspace,

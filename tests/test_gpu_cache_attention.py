@@ -140,6 +140,8 @@ def test_one_tile(cuda_device):
 @pytest.mark.parametrize("Hq, Hkv, new", [(4, 4, 1), (12, 4, 1), (16, 2, 2), (24, 2, 2), (48, 8, 4), (33, 11, 3), (32, 1, 8)])
 def test_steps(bs, Hq, Hkv, new, cuda_device):
     # every row tile (16, 32, 64 rows, and several tiles of 64); lengths around the 128 tokens of a tile
+    # (that was with the first kernel's tiles: these are now 1, 3, 16, 24, 24, 9 and 256 rows, the variants of 8, 16 and 24
+    # rows and the one for prompts; test_every_row_tile_at_every_block_size has all variants)
     lens = [new, 127, 128, 129, 1, 300, 1025]
     lens = [max(n, new) for n in lens]
     c = Case(cuda_device, lens, [new] * len(lens), Hq, Hkv, bs, seed=bs + Hq, row_pad=8, extra=2)
@@ -328,6 +330,7 @@ def test_bad_starts_are_skipped(cuda_device):
 
 def test_max_new_does_not_change_the_result(cuda_device):
     # row tiles of 16, 32 and 64 rows, larger and smaller than the sequences' queries
+    # (now 8, 32 and 64 rows, and the variant for prompts)
     c = Case(cuda_device, [300, 200], [5, 2], 12, 2, 16, seed=20)
     for m in (1, 5, 8, 40):
         assert c.check(max_new=m) < 4e-3

@@ -54,6 +54,7 @@ def check(dev, x, row_pad=0, flat=False):
                                      (2, 4, 50001), (80, 3, 300), (160, 3, 300), (310, 2, 129), (700, 2, 64)])
 def test_matches_exact_arithmetic(N, T, V, probs, cuda_device):
     # every cluster size (by N), parts that end inside a warp's range, unaligned rows (odd V)
+    # (of batches whose rows are short where N is large: test_large_batches_of_long_rows has the others)
     check(cuda_device, inputs(N, T, V, N + T + V, probs))
 
 
