@@ -140,7 +140,7 @@ def prepare(case, seed):
             from linear_attention_decode_04_gb300 import KdaLinearCall
             s["call"] = KdaLinearCall(s["x"], s["weight"], s["out"], x_scale=s["x_scale"],
                                       weight_scale=s["weight_scale"], bias=s["bias"], residual=s["residual"],
-                                      activation=case["act"])
+                                      activation=case["act"], early_weight=True)
         return s
     B, T, V = case["B"], case["T"], case["V"]
     dt = torch.float32 if case["bits"] == 32 else torch.bfloat16
