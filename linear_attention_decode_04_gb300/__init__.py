@@ -1,7 +1,8 @@
 """GB300-native fused KDA (Kimi Delta Attention) single-token decode step and
 chunked varlen prefill, and the operators of a serving step around them
 (block tables, q/k norm with rotation and 8-bit cache write, attention over
-that cache, verification of drafted tokens).
+that cache, verification of drafted tokens; residual addition with norm and
+8-bit output, matrix products with fused epilogues, log probabilities).
 
 The compute lives in one hand-written CUDA library (``csrc/``) behind a C ABI
 (``include/kda_decode.h``); ``kda_decode`` here only marshals torch tensors
@@ -39,4 +40,12 @@ from .step_ops import (  # noqa: F401
     kda_qk_rope,
     kda_verify_draft,
     rope_frequencies,
+)
+from .layer_ops import (  # noqa: F401
+    KdaAddNormCall,
+    KdaLinearCall,
+    KdaLogprobsCall,
+    kda_add_norm,
+    kda_linear,
+    kda_logprobs,
 )

@@ -1,0 +1,201 @@
+// kda_add_norm.cu -- residual addition, root-mean-square norm and 8-bit
+// output (definition in include/kda_add_norm.h).
+//
+// A CTA per row: the row stays in registers from its load to its codes, so
+// that every byte crosses HBM once.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_add_norm.h"
+#include "kda_internal.h"
+
+namespace {
+
+constexpr float kMaxCode = 448.f;       // largest e4m3 value
+constexpr float kScaleFloor = 0x1p-100f;
+
+struct Params {
+  int T, D;
+  float eps;
+  const uint16_t *x, *residual;
+  int64_t x_stride, residual_stride;
+  const float* weight;
+  uint16_t *residual_out, *out;
+  int64_t residual_out_stride, out_stride;
+  uint8_t* out_q;
+  int64_t out_q_stride;
+  float* out_scale;
+};
+
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint2 codes(const float (&f)[8], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// A thread holds VECS pieces of 8 channels, blockDim.x pieces apart.
+template <int VECS, bool NORM>
+__global__ void __launch_bounds__(1024) add_norm_kernel(const Params p) {
+  __shared__ float sums[32];
+  __shared__ uint32_t tops[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, n = p.D / 8;
+  const int64_t t = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float h[VECS][8];
+  {
+    uint4 a[VECS], b[VECS];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = tid + i * blockDim.x;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (c < n) {
+        a[i] = reinterpret_cast<const uint4*>(p.x + t * p.x_stride)[c];
+        if (p.residual) b[i] = reinterpret_cast<const uint4*>(p.residual + t * p.residual_stride)[c];
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      float r[8];
+      unpack(a[i], h[i]);
+      unpack(b[i], r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[i][k] += r[k];
+        sum = fmaf(h[i][k], h[i][k], sum);
+      }
+    }
+    if (NORM) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) sums[warp] = sum;
+    }
+  }
+  __syncthreads();  // (also: the whole row is read before any of it is written)
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int c = tid + i * blockDim.x;
+    if (c < n && p.residual_out) reinterpret_cast<uint4*>(p.residual_out + t * p.residual_out_stride)[c] = pack(h[i]);
+  }
+  if (NORM) {
+    float sum = lane < warps ? sums[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float f = 1.f / sqrtf(sum / static_cast<float>(p.D) + p.eps);
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = tid + i * blockDim.x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] *= f;
+      if (c < n && p.weight) {
+        const float4 u = reinterpret_cast<const float4*>(p.weight)[2 * c], v = reinterpret_cast<const float4*>(p.weight)[2 * c + 1];
+        h[i][0] *= u.x, h[i][1] *= u.y, h[i][2] *= u.z, h[i][3] *= u.w;
+        h[i][4] *= v.x, h[i][5] *= v.y, h[i][6] *= v.z, h[i][7] *= v.w;
+      }
+    }
+  }
+  if (p.out) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = tid + i * blockDim.x;
+      if (c < n) reinterpret_cast<uint4*>(p.out + t * p.out_stride)[c] = pack(h[i]);
+    }
+  }
+  if (!p.out_q) return;
+  uint32_t top = 0;  // as bit patterns: NaN above infinity above everything else
+#pragma unroll
+  for (int i = 0; i < VECS; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(h[i][k]) & 0x7fffffffu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0);
+  const float amax = top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) : __uint_as_float(0x7fc00000u);
+  const float inv = kMaxCode / amax;
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int c = tid + i * blockDim.x;
+    if (c < n) reinterpret_cast<uint2*>(p.out_q + t * p.out_q_stride)[c] = codes(h[i], inv);
+  }
+  if (tid == 0) p.out_scale[t] = amax / kMaxCode;
+}
+
+bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
+
+template <bool NORM>
+auto kernel_of(int vecs) {
+  return vecs == 1 ? add_norm_kernel<1, NORM> : vecs == 2 ? add_norm_kernel<2, NORM>
+       : vecs == 3 ? add_norm_kernel<3, NORM> : add_norm_kernel<4, NORM>;
+}
+
+}  // namespace
+
+extern "C" int kda_add_norm(const KdaAddNormArgs* a, void* stream) {
+  kda_internal_clear_error();
+  if (!a) return kda_internal_fail(KDA_ERR_NULLPTR, "args is NULL");
+  if (a->struct_size != sizeof(KdaAddNormArgs))
+    return kda_internal_fail(KDA_ERR_ABI, "struct_size %u, library expects %zu", a->struct_size, sizeof(KdaAddNormArgs));
+  if (a->flags & ~KDA_ADD_NORM_NO_NORM) return kda_internal_fail(KDA_ERR_FLAGS, "unknown flags 0x%x", a->flags);
+  const bool norm = !(a->flags & KDA_ADD_NORM_NO_NORM);
+  if (!norm && a->weight) return kda_internal_fail(KDA_ERR_FLAGS, "a weight without the norm");
+  if (a->T < 0 || a->D < 8 || a->D % 8 || a->D > KDA_ADD_NORM_MAX_D || !(a->eps >= 0.f))
+    return kda_internal_fail(KDA_ERR_SHAPE, "T=%d D=%d eps=%g (D a multiple of 8 up to %d)", a->T, a->D,
+                             static_cast<double>(a->eps), KDA_ADD_NORM_MAX_D);
+  if (a->T == 0) return KDA_OK;
+  if (!a->x || (!a->out && !a->out_q && !a->residual_out) || (a->out_q != nullptr) != (a->out_scale != nullptr))
+    return kda_internal_fail(KDA_ERR_NULLPTR, "x and a result are required; out_q and out_scale go together");
+  if (a->x_row_stride < a->D || (a->residual && a->residual_row_stride < a->D) ||
+      (a->residual_out && a->residual_out_row_stride < a->D) || (a->out && a->out_row_stride < a->D) ||
+      (a->out_q && a->out_q_row_stride < a->D))
+    return kda_internal_fail(KDA_ERR_SHAPE, "a row stride is smaller than the row");
+  if (misaligned(a->x, 15) || (a->x_row_stride & 7) || (a->residual && (misaligned(a->residual, 15) || (a->residual_row_stride & 7))) ||
+      (a->residual_out && (misaligned(a->residual_out, 15) || (a->residual_out_row_stride & 7))) ||
+      (a->out && (misaligned(a->out, 15) || (a->out_row_stride & 7))) ||
+      (a->out_q && (misaligned(a->out_q, 7) || (a->out_q_row_stride & 7))) || misaligned(a->weight, 15) ||
+      misaligned(a->out_scale, 3))
+    return kda_internal_fail(KDA_ERR_ALIGN, "a pointer or stride is not aligned as required");
+  // a result in the place of an input has to have its rows in the same places
+  const auto races = [](const void* r, int64_t rs, const void* i, int64_t is) { return r && r == i && rs != is; };
+  if (races(a->residual_out, a->residual_out_row_stride, a->x, a->x_row_stride) ||
+      races(a->residual_out, a->residual_out_row_stride, a->residual, a->residual_row_stride) ||
+      races(a->out, a->out_row_stride, a->x, a->x_row_stride) ||
+      races(a->out, a->out_row_stride, a->residual, a->residual_row_stride) || (a->out && a->out == a->residual_out) ||
+      (a->out_q && (static_cast<const void*>(a->out_q) == a->x || static_cast<const void*>(a->out_q) == a->residual ||
+                    static_cast<const void*>(a->out_q) == a->out || static_cast<const void*>(a->out_q) == a->residual_out)))
+    return kda_internal_fail(KDA_ERR_SHAPE, "a result stands in the place of another or, with another stride, of an input");
+  const Params p{a->T, a->D, a->eps, a->x, a->residual, a->x_row_stride, a->residual_row_stride, a->weight,
+                 a->residual_out, a->out, a->residual_out_row_stride, a->out_row_stride, a->out_q, a->out_q_row_stride,
+                 a->out_scale};
+  // up to 256 threads with one to three pieces each, then more threads
+  const int n = a->D / 8;
+  int vecs = (n + 255) / 256;
+  if (vecs > 4) vecs = 4;
+  const int threads = ((n + vecs - 1) / vecs + 31) / 32 * 32;
+  const cudaError_t e = kda_internal_launch(norm ? kernel_of<true>(vecs) : kernel_of<false>(vecs),
+                                            dim3(static_cast<unsigned>(a->T)), dim3(threads), 0, stream, p);
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+  return KDA_OK;
+}

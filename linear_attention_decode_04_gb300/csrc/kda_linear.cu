@@ -1,0 +1,420 @@
+// kda_linear.cu -- matrix products with scales, bias, activation and residual
+// in the epilogue (definition in include/kda_linear.h).
+//
+// Products are formed transposed, Y^T [channel][row] = W [channel][k] X^T: 128
+// channels are the wide side of a tile and the rows of x, of which a decode
+// step has few, the narrow one (16 to 256 columns).  Tiles of W and X go to
+// shared memory by TMA (128 bytes of k, 128-byte swizzle), tcgen05 multiplies
+// them as they are, and a thread of the epilogue has a channel of its own, with
+// its scale and bias in registers.
+//
+// A gated tile holds 64 channels of each half, 16 and 16 in turn, so that a
+// warp's 32 lanes have both halves of 16 results.
+//
+// Few tiles: the CTAs of a cluster share one tile, each with a range of k, and
+// add their parts up over distributed shared memory in a fixed order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "kda_internal.h"
+#include "kda_linear.h"
+#include "kda_tc.cuh"
+
+namespace {
+
+constexpr int kTileN = 128;                // channels of a tile
+constexpr int kBlock = 128;                // bytes of k per stage
+constexpr int kThreads = 192;              // four warps of the epilogue, producer, issuer
+constexpr int kMaxSplit = 8;
+
+struct Params {
+  int M, N, K, width;          // width: channels of out
+  int m_tiles, tiles, blocks;  // row tiles, tiles, blocks of k
+  int act;
+  bool out_f32, early;
+  const float *x_scale, *w_scale, *bias;
+  const uint16_t* residual;
+  int64_t res_stride;
+  void* out;
+  int64_t out_stride;
+  int32_t* err;
+};
+
+// ROWS of x per tile.
+template <int ROWS>
+struct Cfg {
+  static constexpr int kStageBytes = (kTileN + ROWS) * kBlock;
+  static constexpr int kStages = 200 * 1024 / kStageBytes;
+  static constexpr int kTmemCols = 2 * ROWS;  // two accumulators; a power of two from 32 on
+};
+
+template <class C>
+struct alignas(1024) Smem {
+  uint8_t stage[C::kStages][C::kStageBytes];
+  uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int failed;
+};
+
+__device__ __forceinline__ float sigmoid_times(float y) { return y / (1.f + __expf(-y)); }
+__device__ __forceinline__ float activate(float y, int act) {
+  if (act == KDA_ACT_SILU) return sigmoid_times(y);
+  if (act == KDA_ACT_GELU) return 0.5f * y * erfcf(y * -0.70710678118654752f);  // (1 + erf loses the lower tail)
+  return y;
+}
+__device__ __forceinline__ void store(const Params& p, int64_t m, int n, float y) {
+  if (p.residual) y += __uint_as_float(static_cast<uint32_t>(p.residual[m * p.res_stride + n]) << 16);
+  if (p.out_f32) static_cast<float*>(p.out)[m * p.out_stride + n] = y;
+  else static_cast<__nv_bfloat16*>(p.out)[m * p.out_stride + n] = __float2bfloat16_rn(y);
+}
+// A thread's channel: of weight (scale, bias) and of out.
+template <bool GATED>
+struct Channel {
+  int out;
+  bool live;
+  float scale, bias;
+  __device__ __forceinline__ Channel(const Params& p, int n_tile, int wq, int lane) {
+    int n;
+    if (GATED) {
+      out = n_tile * (kTileN / 2) + 16 * wq + (lane & 15);
+      n = (lane >> 4) * p.width + out;
+    } else {
+      n = out = n_tile * kTileN + 32 * wq + lane;
+    }
+    live = out < p.width;
+    scale = live && p.w_scale ? p.w_scale[n] : 1.f;
+    bias = live && p.bias ? p.bias[n] : 0.f;
+  }
+};
+// Two neighbouring rows m, m + 1 of a thread's channel, from their sums.
+template <bool GATED>
+__device__ __forceinline__ void finish(const Params& p, const Channel<GATED>& c, int lane, int m, float a0, float a1, float s0,
+                                       float s1) {
+  const float y0 = fmaf(a0 * s0, c.scale, c.bias), y1 = fmaf(a1 * s1, c.scale, c.bias);
+  if (GATED) {  // the lower 16 lanes have the first half's values and finish row m, the upper ones the second half's and row m + 1
+    const bool up = lane >> 4;
+    const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
+    const float y = up ? sigmoid_times(got) * y1 : sigmoid_times(y0) * got;
+    if (c.live && m + up < p.M) store(p, m + up, c.out, y);
+  } else {
+    if (c.live && m < p.M) store(p, m, c.out, activate(y0, p.act));
+    if (c.live && m + 1 < p.M) store(p, m + 1, c.out, activate(y1, p.act));
+  }
+}
+
+template <int ROWS, bool E4M3, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int split) {
+  using C = Cfg<ROWS>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<C>& S = *reinterpret_cast<Smem<C>*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int first = blockIdx.x / split, rank = blockIdx.x - first * split, step = gridDim.x / split;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
+    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 128);
+    bar_init(&S.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    S.failed = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&w_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
+  }
+  __syncwarp();
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = S.tmem;
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split), span = k1 - k0;
+  const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;  // tiles of this CTA
+  if (warp == 4) {
+    // ================================================================ producer
+    if (lane == 0) {
+      const int64_t total = static_cast<int64_t>(mine) * span;
+      auto weights = [&](uint32_t st, int tile, int k) {
+        const int nt = tile / p.m_tiles;
+        const uint32_t dst = s32(S.stage[st]);
+        if (GATED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tma_3d(dst + i * 32 * kBlock, &w_map, k * kBlock, nt * (kTileN / 2) + 16 * i, 0, &S.full[st]);
+        } else {
+          tma_2d(dst, &w_map, k * kBlock, nt * kTileN, &S.full[st]);
+        }
+      };
+      auto rows = [&](uint32_t st, int tile, int k) {
+        tma_2d(s32(S.stage[st]) + kTileN * kBlock, &x_map, k * kBlock, (tile % p.m_tiles) * ROWS, &S.full[st]);
+      };
+      int64_t ahead = 0;  // stages whose weights were asked for before the kernel ahead ended
+      if (p.early) {
+        int tile = first, k = k0;
+        for (; ahead < total && ahead < C::kStages; ++ahead) {
+          bar_expect(&S.full[ahead], C::kStageBytes);
+          weights(static_cast<uint32_t>(ahead), tile, k);
+          if (++k == k1) k = k0, tile += step;
+        }
+      }
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      int tile = first, k = k0;
+      int64_t it = 0;
+      for (; it < total; ++it) {
+        const uint32_t st = static_cast<uint32_t>(it % C::kStages), round = static_cast<uint32_t>(it / C::kStages);
+        if (it >= ahead) {
+          if (round > 0 && !bar_wait(&S.empty[st], (round - 1) & 1, &S.failed)) break;
+          bar_expect(&S.full[st], C::kStageBytes);
+          weights(st, tile, k);
+        }
+        rows(st, tile, k);
+        if (++k == k1) k = k0, tile += step;
+      }
+      // nothing may land in shared memory after the CTA is gone, whoever gave up
+      for (int64_t j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+        bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ========================================================== product issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_k(E4M3, kTileN, ROWS);
+      bool ok = true;
+      int64_t it = 0;
+      for (int i = 0; i < mine && ok; ++i) {
+        const uint32_t buf = i & 1;
+        if (i >= 2) ok = bar_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
+        tc_after();
+        for (int k = 0; k < span && ok; ++k, ++it) {
+          const uint32_t st = static_cast<uint32_t>(it % C::kStages);
+          ok = bar_wait(&S.full[st], static_cast<uint32_t>(it / C::kStages) & 1, &S.failed);
+          if (!ok) break;
+          tc_after();
+          const uint32_t w = s32(S.stage[st]), x = w + kTileN * kBlock;
+#pragma unroll
+          for (int j = 0; j < kBlock / 32; ++j)
+            mma_1cta<E4M3>(tmem + buf * ROWS, sdesc128(w + 32 * j), sdesc128(x + 32 * j), id, k + j > 0);
+          commit(&S.empty[st]);
+        }
+        if (ok) commit(&S.acc_full[buf]);
+      }
+      commit(&S.done);
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ epilogue
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t buf = i & 1;
+      const int tile = first + i * step, nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
+      const Channel<GATED> c(p, nt, warp, lane);
+      bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
+      tc_after();
+#pragma unroll 1
+      for (int col = 0; col < ROWS; col += 16) {
+        float a[16];
+        tm_cols(lanes + buf * ROWS + col, a);
+        if (split > 1) {
+          float* part = reinterpret_cast<float*>(raw) + col * kTileN + tid;  // [column][channel], where the stages were
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[j * kTileN] = a[j];
+        } else if (m0 + col < p.M) {
+          const int row = m0 + col + (lane & 15);
+          const float s = p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            finish<GATED>(p, c, lane, m0 + col + j, a[j], a[j + 1], __shfl_sync(0xffffffffu, s, j), __shfl_sync(0xffffffffu, s, j + 1));
+        }
+      }
+      tc_before();
+      bar_arrive(&S.acc_empty[buf]);
+    }
+  }
+  if (split > 1) {
+    // ---- the parts of the cluster's CTAs: each adds up its share of the columns
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp < 4 && mine > 0) {
+      const int nt = first / p.m_tiles, m0 = (first - nt * p.m_tiles) * ROWS;
+      const Channel<GATED> c(p, nt, warp, lane);
+      uint32_t from[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from[r]) : "r"(s32(raw) + 4 * tid), "r"(r < split ? r : 0));
+      for (int col = rank * (ROWS / split); col < (rank + 1) * (ROWS / split) && m0 + col < p.M; col += 2) {
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) {
+          if (r < split) {
+            float v0, v1;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v0) : "r"(from[r] + col * kTileN * 4) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v1) : "r"(from[r] + (col + 1) * kTileN * 4) : "memory");
+            a0 += v0, a1 += v1;
+          }
+        }
+        const int m = m0 + col;
+        finish<GATED>(p, c, lane, m, a0, a1, p.x_scale ? p.x_scale[m] : 1.f, p.x_scale && m + 1 < p.M ? p.x_scale[m + 1] : 1.f);
+      }
+    }
+    __syncwarp();
+    cluster_arrive();  // nobody reads this CTA's memory any more
+    cluster_wait();
+  }
+  // every product has ended before the accumulators are given back, given up or not
+  if (warp == 5 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  tc_before();
+  __syncthreads();
+  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+  __syncwarp();
+  if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::mutex g_mutex;
+int g_sms[64];
+EncodeFn g_encode;
+
+using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap, int);
+template <int ROWS>
+Kernel kernel_of(bool e4m3, bool gated) {
+  return e4m3 ? (gated ? linear_kernel<ROWS, true, true> : linear_kernel<ROWS, true, false>)
+              : (gated ? linear_kernel<ROWS, false, true> : linear_kernel<ROWS, false, false>);
+}
+template <int ROWS>
+constexpr size_t smem_bytes() {
+  static_assert(sizeof(Smem<Cfg<ROWS>>) <= 227 * 1024 && ROWS * kTileN * 4 <= Cfg<ROWS>::kStages * Cfg<ROWS>::kStageBytes, "shared memory");
+  return sizeof(Smem<Cfg<ROWS>>);
+}
+// Calls `f` with the number of rows per tile as a constant.
+template <class F>
+auto with_rows(int M, F f) {
+  if (M <= 16) return f(std::integral_constant<int, 16>{});
+  if (M <= 32) return f(std::integral_constant<int, 32>{});
+  if (M <= 64) return f(std::integral_constant<int, 64>{});
+  if (M <= 128) return f(std::integral_constant<int, 128>{});
+  return f(std::integral_constant<int, 256>{});
+}
+
+cudaError_t setup(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!g_sms[dev]) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeFn>(fn);
+    for (int rows = 16; rows <= 256; rows *= 2)
+      for (int v = 0; v < 4; ++v) {
+        e = with_rows(rows, [&](auto r) {
+          return cudaFuncSetAttribute(kernel_of<r.value>(v & 1, v >> 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(smem_bytes<r.value>()));
+        });
+        if (e != cudaSuccess) return e;
+      }
+    int n = 0;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    g_sms[dev] = n;
+  }
+  *sms = g_sms[dev];
+  return cudaSuccess;
+}
+
+bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
+
+}  // namespace
+
+extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
+  kda_internal_clear_error();
+  if (!a) return kda_internal_fail(KDA_ERR_NULLPTR, "args is NULL");
+  if (a->struct_size != sizeof(KdaLinearArgs))
+    return kda_internal_fail(KDA_ERR_ABI, "struct_size %u, library expects %zu", a->struct_size, sizeof(KdaLinearArgs));
+  if (a->flags & ~(KDA_LINEAR_E4M3 | KDA_LINEAR_OUT_F32 | KDA_LINEAR_EARLY_WEIGHT))
+    return kda_internal_fail(KDA_ERR_FLAGS, "unknown flags 0x%x", a->flags);
+  const bool e4m3 = a->flags & KDA_LINEAR_E4M3, f32 = a->flags & KDA_LINEAR_OUT_F32;
+  const bool gated = a->activation == KDA_ACT_SILU_GATED;
+  constexpr int kMost = 1 << 24;
+  if (a->M < 0 || a->N < 1 || a->N > kMost || a->K < 1 || a->K > kMost || a->activation < 0 ||
+      a->activation > KDA_ACT_SILU_GATED || (gated && a->N % 2))
+    return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d K=%d activation=%d", a->M, a->N, a->K, a->activation);
+  if (a->M == 0) return KDA_OK;
+  if (!a->x || !a->weight || !a->out || (a->x_scale != nullptr) != e4m3 || (a->weight_scale != nullptr) != e4m3)
+    return kda_internal_fail(KDA_ERR_NULLPTR, "a required pointer is NULL (x_scale and weight_scale go with e4m3, and only with it)");
+  const int width = gated ? a->N / 2 : a->N;
+  if (a->x_row_stride < a->K || a->weight_row_stride < a->K || a->out_row_stride < width ||
+      (a->residual && a->residual_row_stride < width) || a->x_row_stride >= 1LL << 32 || a->weight_row_stride >= 1LL << 32)
+    return kda_internal_fail(KDA_ERR_SHAPE, "a row stride is smaller than the row, or 2^32 elements and more");
+  const int64_t each = e4m3 ? 15 : 7;
+  if (misaligned(a->x, 15) || misaligned(a->weight, 15) || (a->x_row_stride & each) || (a->weight_row_stride & each) ||
+      misaligned(a->x_scale, 3) || misaligned(a->weight_scale, 3) || misaligned(a->bias, 3) || misaligned(a->residual, 1) ||
+      misaligned(a->out, f32 ? 3 : 1) || misaligned(a->err_flag, 3))
+    return kda_internal_fail(KDA_ERR_ALIGN, "a pointer or stride is not aligned as required");
+  if (a->out == a->x || a->out == a->weight ||
+      (a->out == a->residual && (f32 || a->out_row_stride != a->residual_row_stride)))
+    return kda_internal_fail(KDA_ERR_SHAPE, "out may take the place of a bf16 residual of the same stride, and of nothing else");
+  int sms = 0;
+  cudaError_t e = setup(&sms);
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "setup: %s", cudaGetErrorString(e));
+  const cuuint64_t size = e4m3 ? 1 : 2;
+  const cuuint64_t k_bytes = static_cast<cuuint64_t>(a->K) * size;
+  const cuuint64_t w_pitch = static_cast<cuuint64_t>(a->weight_row_stride) * size, x_pitch = static_cast<cuuint64_t>(a->x_row_stride) * size;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const int rows = with_rows(a->M, [](auto r) { return static_cast<int>(r.value); });
+  CUtensorMap w_map, x_map;
+  CUresult r;
+  {
+    // gated: the two halves are a dimension of their own, a copy takes 16 rows of each
+    const cuuint64_t dims[3] = {k_bytes, static_cast<cuuint64_t>(width), 2};
+    const cuuint64_t strides[2] = {w_pitch, w_pitch * static_cast<cuuint64_t>(width)};
+    const cuuint32_t box[3] = {kBlock, static_cast<cuuint32_t>(gated ? 16 : kTileN), 2};
+    r = g_encode(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 3 : 2, const_cast<void*>(a->weight), dims, strides, box, ones,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (r == CUDA_SUCCESS) {
+    const cuuint64_t dims[2] = {k_bytes, static_cast<cuuint64_t>(a->M)};
+    const cuuint64_t strides[1] = {x_pitch};
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(rows)};
+    r = g_encode(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a->x), dims, strides, box, ones,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
+  Params p{};
+  p.M = a->M, p.N = a->N, p.K = a->K, p.width = width;
+  const int tile_width = gated ? kTileN / 2 : kTileN;
+  const int64_t m_tiles = (static_cast<int64_t>(a->M) + rows - 1) / rows, n_tiles = (static_cast<int64_t>(width) + tile_width - 1) / tile_width;
+  if (m_tiles * n_tiles > 0x7fffffff / kMaxSplit) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
+  p.m_tiles = static_cast<int>(m_tiles), p.tiles = static_cast<int>(m_tiles * n_tiles);
+  p.blocks = static_cast<int>((k_bytes + kBlock - 1) / kBlock);
+  p.act = a->activation, p.out_f32 = f32, p.early = a->flags & KDA_LINEAR_EARLY_WEIGHT;
+  p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
+  p.residual = a->residual, p.res_stride = a->residual_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
+  p.err = a->err_flag;
+  // few tiles: up to eight CTAs share one, while all of them are resident and each has a block of k
+  int split = 1;
+  while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;
+  const unsigned grid = static_cast<unsigned>(split > 1 ? p.tiles * split : (p.tiles < sms ? p.tiles : sms));
+  e = with_rows(a->M, [&](auto r) {
+    return kda_internal_launch_cluster(kernel_of<r.value>(e4m3, gated), dim3(grid), dim3(kThreads), smem_bytes<r.value>(), stream,
+                                       static_cast<unsigned>(split), p, w_map, x_map, split);
+  });
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+  return KDA_OK;
+}
