@@ -31,12 +31,13 @@ constexpr int kTileN = 128;                // channels of a tile
 constexpr int kBlock = 128;                // bytes of k per stage
 constexpr int kThreads = 192;              // four warps of the epilogue, producer, issuer
 constexpr int kMaxSplit = 8;
+constexpr int kPitch = 80;                 // bytes between rows of results in shared memory
 
 struct Params {
   int M, N, K, width;          // width: channels of out
   int m_tiles, tiles, blocks;  // row tiles, tiles, blocks of k
   int act;
-  bool out_f32, early;
+  bool out_f32, early, vec_out, vec_res;  // vec: rows in 16-byte pieces
   const float *x_scale, *w_scale, *bias;
   const uint16_t* residual;
   int64_t res_stride;
@@ -56,54 +57,244 @@ struct Cfg {
 template <class C>
 struct alignas(1024) Smem {
   uint8_t stage[C::kStages][C::kStageBytes];
+  alignas(16) uint8_t rows[4][32 * kPitch];  // of the warps of the epilogue
   uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int failed;
 };
 
 __device__ __forceinline__ float sigmoid_times(float y) { return y / (1.f + __expf(-y)); }
+// (1 + erf loses gelu's lower tail)
+__device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(y * -0.70710678118654752f); }
 __device__ __forceinline__ float activate(float y, int act) {
-  if (act == KDA_ACT_SILU) return sigmoid_times(y);
-  if (act == KDA_ACT_GELU) return 0.5f * y * erfcf(y * -0.70710678118654752f);  // (1 + erf loses the lower tail)
-  return y;
+  return act == KDA_ACT_SILU ? sigmoid_times(y) : act == KDA_ACT_GELU ? gelu(y) : y;
 }
-__device__ __forceinline__ void store(const Params& p, int64_t m, int n, float y) {
-  if (p.residual) y += __uint_as_float(static_cast<uint32_t>(p.residual[m * p.res_stride + n]) << 16);
-  if (p.out_f32) static_cast<float*>(p.out)[m * p.out_stride + n] = y;
-  else static_cast<__nv_bfloat16*>(p.out)[m * p.out_stride + n] = __float2bfloat16_rn(y);
+__device__ __forceinline__ float of_bf16(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-// A thread's channel: of weight (scale, bias) and of out.
+
+// ---- A warp's part of a tile: 32 accumulator lanes, which are 32 channels of
+// out, or gated 16 of them (their two halves 16 lanes apart), as fragments: a
+// thread has lanes r8 + 8 j and pairs of neighbouring rows.  Rows of 32 channels
+// of bf16 results go through shared memory, 80 bytes apart so that the eight
+// rows of a matrix lie in different banks, and from there to memory 16 bytes a
+// thread; residuals come the same way.
 template <bool GATED>
-struct Channel {
-  int out;
-  bool live;
-  float scale, bias;
-  __device__ __forceinline__ Channel(const Params& p, int n_tile, int wq, int lane) {
-    int n;
-    if (GATED) {
-      out = n_tile * (kTileN / 2) + 16 * wq + (lane & 15);
-      n = (lane >> 4) * p.width + out;
-    } else {
-      n = out = n_tile * kTileN + 32 * wq + lane;
+struct Epilogue {
+  static constexpr int kWidth = GATED ? 16 : 32;  // channels of out
+  static constexpr int kParts = kWidth / 8;       // 16-byte pieces of a row
+  const Params& p;
+  uint8_t* stage;                                 // 32 rows of the warp's own
+  int lane, n0;
+  float scale[4], bias[4];
+
+  __device__ __forceinline__ Epilogue(const Params& q, uint8_t* st, int n_tile, int wq, int ln)
+      : p(q), stage(st), lane(ln), n0(n_tile * (GATED ? kTileN / 2 : kTileN) + wq * kWidth) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + (lane >> 2) + 8 * (GATED ? j & 1 : j), n = GATED ? c + (j >> 1) * p.width : c;
+      const bool live = c < p.width;
+      scale[j] = live && p.w_scale ? p.w_scale[n] : 1.f;
+      bias[j] = live && p.bias ? p.bias[n] : 0.f;
     }
-    live = out < p.width;
-    scale = live && p.w_scale ? p.w_scale[n] : 1.f;
-    bias = live && p.bias ? p.bias[n] : 0.f;
+  }
+  // this thread's row of the matrices of 8-row block b (gated: of b and b + 1)
+  __device__ __forceinline__ uint32_t matrix(int b) const {
+    const int m = lane >> 3;
+    return s32(stage) + (8 * (GATED ? b + (m >> 1) : b) + (lane & 7)) * kPitch + (GATED ? m & 1 : m) * 16;
+  }
+  // Rows m0 .. m0 + 8 BLOCKS - 1 between memory and the stage.
+  template <int BLOCKS>
+  __device__ __forceinline__ void fetch(int m0) {
+    const bool vec = p.vec_res && n0 + kWidth <= p.width;
+    if (vec) {
+      constexpr int kRows = 32 / kParts, kTrips = 8 * BLOCKS / kRows;  // rows per trip
+      uint4 v[kTrips];
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i) {
+        const int m = m0 + i * kRows + lane / kParts;
+        v[i] = m < p.M ? *reinterpret_cast<const uint4*>(p.residual + m * p.res_stride + n0 + lane % kParts * 8) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i)
+        *reinterpret_cast<uint4*>(stage + (i * kRows + lane / kParts) * kPitch + lane % kParts * 16) = v[i];
+    } else {
+      constexpr int kRows = 32 / kWidth, kTrips = 8 * BLOCKS / kRows;
+      const int c = n0 + lane % kWidth;
+      uint16_t v[kTrips];
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i) {
+        const int m = m0 + i * kRows + lane / kWidth;
+        v[i] = m < p.M && c < p.width ? p.residual[m * p.res_stride + c] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i)
+        *reinterpret_cast<uint16_t*>(stage + (i * kRows + lane / kWidth) * kPitch + lane % kWidth * 2) = v[i];
+    }
+    __syncwarp();
+  }
+  template <int BLOCKS>
+  __device__ __forceinline__ void put(int m0) {
+    __syncwarp();
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    if (p.vec_out && n0 + kWidth <= p.width) {
+      constexpr int kRows = 32 / kParts, kTrips = 8 * BLOCKS / kRows;
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i) {
+        const int m = m0 + i * kRows + lane / kParts;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * kRows + lane / kParts) * kPitch + lane % kParts * 16);
+        if (m < p.M) *reinterpret_cast<uint4*>(out + m * p.out_stride + n0 + lane % kParts * 8) = v;
+      }
+    } else {
+      constexpr int kRows = 32 / kWidth, kTrips = 8 * BLOCKS / kRows;
+      const int c = n0 + lane % kWidth;
+#pragma unroll
+      for (int i = 0; i < kTrips; ++i) {
+        const int m = m0 + i * kRows + lane / kWidth;
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(stage + (i * kRows + lane / kWidth) * kPitch + lane % kWidth * 2);
+        if (m < p.M && c < p.width) out[m * p.out_stride + c] = v;
+      }
+    }
+    __syncwarp();
+  }
+  // Rows m0 .. m0 + 8 BLOCKS - 1 from their sums.
+  template <int BLOCKS>
+  __device__ __forceinline__ void rows(int m0, float (&z)[4][2 * BLOCKS]) {
+    if (n0 >= p.width) return;
+    if (p.residual) fetch<BLOCKS>(m0);
+    const int a = 2 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) {
+      const int m = m0 + 8 * b + a;
+      const float s0 = p.x_scale && m < p.M ? p.x_scale[m] : 1.f, s1 = p.x_scale && m + 1 < p.M ? p.x_scale[m + 1] : 1.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[j][2 * b] = fmaf(z[j][2 * b] * s0, scale[j], bias[j]);
+        z[j][2 * b + 1] = fmaf(z[j][2 * b + 1] * s1, scale[j], bias[j]);
+      }
+    }
+    if (GATED) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = sigmoid_times(z[j][i]) * z[j + 2][i];
+    } else if (p.act == KDA_ACT_SILU) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = sigmoid_times(z[j][i]);
+    } else if (p.act == KDA_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = gelu(z[j][i]);
+    }
+    if (p.residual) {
+#pragma unroll
+      for (int b = 0; b < BLOCKS; b += GATED ? 2 : 1) {
+        uint32_t r[4];
+        load_transposed(matrix(b), r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = GATED ? k & 1 : k, i = 2 * (GATED ? b + (k >> 1) : b);
+          z[j][i] += of_bf16(r[k] & 0xffffu);
+          z[j][i + 1] += of_bf16(r[k] >> 16);
+        }
+      }
+      __syncwarp();
+    }
+    if (p.out_f32) {  // eight neighbouring channels of four rows at a time: whole sectors
+      float* out = static_cast<float*>(p.out);
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int m = m0 + 8 * b + a + e;
+#pragma unroll
+          for (int j = 0; j < (GATED ? 2 : 4); ++j) {
+            const int c = n0 + (lane >> 2) + 8 * j;
+            if (m < p.M && c < p.width) out[m * p.out_stride + c] = z[j][2 * b + e];
+          }
+        }
+    } else {
+#pragma unroll
+      for (int b = 0; b < BLOCKS; b += GATED ? 2 : 1) {
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = GATED ? k & 1 : k, i = 2 * (GATED ? b + (k >> 1) : b);
+          r[k] = pack_bf16(z[j][i], z[j][i + 1]);
+        }
+        store_transposed(matrix(b), r);
+      }
+      put<BLOCKS>(m0);
+    }
   }
 };
-// Two neighbouring rows m, m + 1 of a thread's channel, from their sums.
-template <bool GATED>
-__device__ __forceinline__ void finish(const Params& p, const Channel<GATED>& c, int lane, int m, float a0, float a1, float s0,
-                                       float s1) {
-  const float y0 = fmaf(a0 * s0, c.scale, c.bias), y1 = fmaf(a1 * s1, c.scale, c.bias);
-  if (GATED) {  // the lower 16 lanes have the first half's values and finish row m, the upper ones the second half's and row m + 1
-    const bool up = lane >> 4;
-    const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-    const float y = up ? sigmoid_times(got) * y1 : sigmoid_times(y0) * got;
-    if (c.live && m + up < p.M) store(p, m + up, c.out, y);
-  } else {
-    if (c.live && m < p.M) store(p, m, c.out, activate(y0, p.act));
-    if (c.live && m + 1 < p.M) store(p, m + 1, c.out, activate(y1, p.act));
+
+// A tile shared by the CTAs of a cluster: this CTA's share of the rows, from all
+// their sums.  A thread has one accumulator lane and pairs of rows.
+template <int ROWS, bool GATED>
+__device__ __forceinline__ void join_parts(const Params& p, uint8_t* raw, int tile, int rank, int split) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
+  const int c = GATED ? nt * (kTileN / 2) + 16 * warp + (lane & 15) : nt * kTileN + tid;  // of out
+  const int n = GATED ? c + (lane >> 4) * p.width : c;
+  const bool live = c < p.width;
+  const float scale = live && p.w_scale ? p.w_scale[n] : 1.f, bias = live && p.bias ? p.bias[n] : 0.f;
+  constexpr int kAhead = 4;  // pairs of rows whose parts are on their way together
+  const int pairs = ROWS / 2 / split, end = min((rank + 1) * pairs, (p.M - m0 + 1) / 2);
+  for (int q0 = rank * pairs; q0 < end; q0 += kAhead) {
+    float2 a[kAhead];
+    float res[kAhead][2], xs[kAhead][2];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      a[k] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int m = m0 + 2 * (q0 + k) + e;
+        const bool there = q0 + k < end && m < p.M;
+        xs[k][e] = p.x_scale && there ? p.x_scale[m] : 1.f;
+        // (gated: lanes 0 .. 15 finish the even row, 16 .. 31 the odd one)
+        res[k][e] = p.residual && there && live && (!GATED || e == lane >> 4) ? of_bf16(p.residual[m * p.res_stride + c]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {
+      if (r < split) {
+        uint32_t from;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(s32(raw) + 8 * tid), "r"(r));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          float2 v;
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(from + min(q0 + k, end - 1) * (8 * kTileN)) : "memory");
+          a[k].x += v.x, a[k].y += v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (q0 + k >= end) break;
+      float y[2] = {fmaf(a[k].x * xs[k][0], scale, bias), fmaf(a[k].y * xs[k][1], scale, bias)};
+      const bool up = GATED && lane >> 4;
+      if (GATED) {
+        const float got = __shfl_xor_sync(0xffffffffu, up ? y[0] : y[1], 16);
+        if (up) y[1] = sigmoid_times(got) * y[1];
+        else y[0] = sigmoid_times(y[0]) * got;
+      } else {
+        y[0] = activate(y[0], p.act), y[1] = activate(y[1], p.act);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t m = m0 + 2 * (q0 + k) + e;
+        if (m >= p.M || !live || (GATED && up != (e == 1))) continue;
+        const float v = y[e] + res[k][e];
+        if (p.out_f32) static_cast<float*>(p.out)[m * p.out_stride + c] = v;
+        else static_cast<__nv_bfloat16*>(p.out)[m * p.out_stride + c] = __float2bfloat16_rn(v);
+      }
+    }
   }
 }
 
@@ -215,23 +406,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
       const int tile = first + i * step, nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
-      const Channel<GATED> c(p, nt, warp, lane);
+      constexpr int kBlocks = ROWS < 32 ? 2 : 4;
+      Epilogue<GATED> e(p, S.rows[warp], nt, warp, lane);
       bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
       tc_after();
 #pragma unroll 1
-      for (int col = 0; col < ROWS; col += 16) {
-        float a[16];
-        tm_cols(lanes + buf * ROWS + col, a);
-        if (split > 1) {
-          float* part = reinterpret_cast<float*>(raw) + col * kTileN + tid;  // [column][channel], where the stages were
+      for (int col = 0; col < ROWS && m0 + col < p.M; col += 8 * kBlocks) {
+        float z[4][2 * kBlocks];
+        tm_fragments<kBlocks>(lanes + buf * ROWS + col, z);
+        if (split > 1) {  // [column pair][channel], where the stages were
+          float2* part = reinterpret_cast<float2*>(raw) + (col / 2 + (lane & 3)) * kTileN + 32 * warp + (lane >> 2);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[j * kTileN] = a[j];
-        } else if (m0 + col < p.M) {
-          const int row = m0 + col + (lane & 15);
-          const float s = p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
+          for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            finish<GATED>(p, c, lane, m0 + col + j, a[j], a[j + 1], __shfl_sync(0xffffffffu, s, j), __shfl_sync(0xffffffffu, s, j + 1));
+            for (int j = 0; j < 4; ++j) part[4 * b * kTileN + 8 * j] = make_float2(z[j][2 * b], z[j][2 * b + 1]);
+        } else {
+          e.template rows<kBlocks>(m0 + col, z);
         }
       }
       tc_before();
@@ -244,26 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_arrive();
     cluster_wait();
     if (warp < 4 && mine > 0) {
-      const int nt = first / p.m_tiles, m0 = (first - nt * p.m_tiles) * ROWS;
-      const Channel<GATED> c(p, nt, warp, lane);
-      uint32_t from[kMaxSplit];
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from[r]) : "r"(s32(raw) + 4 * tid), "r"(r < split ? r : 0));
-      for (int col = rank * (ROWS / split); col < (rank + 1) * (ROWS / split) && m0 + col < p.M; col += 2) {
-        float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {
-          if (r < split) {
-            float v0, v1;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v0) : "r"(from[r] + col * kTileN * 4) : "memory");
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v1) : "r"(from[r] + (col + 1) * kTileN * 4) : "memory");
-            a0 += v0, a1 += v1;
-          }
-        }
-        const int m = m0 + col;
-        finish<GATED>(p, c, lane, m, a0, a1, p.x_scale ? p.x_scale[m] : 1.f, p.x_scale && m + 1 < p.M ? p.x_scale[m + 1] : 1.f);
-      }
+      join_parts<ROWS, GATED>(p, raw, first, rank, split);
     }
     __syncwarp();
     cluster_arrive();  // nobody reads this CTA's memory any more
@@ -407,6 +578,8 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
   p.residual = a->residual, p.res_stride = a->residual_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
   p.err = a->err_flag;
+  p.vec_out = !f32 && !misaligned(a->out, 15) && a->out_row_stride % 8 == 0;
+  p.vec_res = !misaligned(a->residual, 15) && a->residual_row_stride % 8 == 0;
   // few tiles: up to eight CTAs share one, while all of them are resident and each has a block of k
   int split = 1;
   while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;

@@ -97,16 +97,53 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(s32(b))
       : "memory");
 }
-// 16 or 32 consecutive columns of this thread's lane.
-__device__ __forceinline__ void tm_cols(uint32_t addr, float (&r)[16]) {
+// 8 * BLOCKS consecutive columns of this warp's 32 lanes as fragments: thread i
+// gets of block b, in r[j][2b], r[j][2b + 1], lane i / 4 + 8 j, columns 8 b +
+// 2 (i % 4) and the next.  The load writes the registers of all 32 threads, so
+// the warp has to be together; load and wait are one statement, so that nothing
+// can come between them.
+template <int BLOCKS>
+__device__ __forceinline__ void tm_fragments(uint32_t addr, float (&r)[4][2 * BLOCKS]) {
+  static_assert(BLOCKS == 2 || BLOCKS == 4, "16 or 32 columns");
   __syncwarp();
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-      : "r"(addr)
-      : "memory");
+  const uint32_t up = addr + (16u << 16);  // the upper 16 lanes
+  if constexpr (BLOCKS == 2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
+          "=f"(r[1][3]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]), "=f"(r[2][3]),
+          "=f"(r[3][2]), "=f"(r[3][3])
+        : "r"(addr), "r"(up)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+        "[%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
+          "=f"(r[1][3]), "=f"(r[0][4]), "=f"(r[0][5]), "=f"(r[1][4]), "=f"(r[1][5]), "=f"(r[0][6]), "=f"(r[0][7]),
+          "=f"(r[1][6]), "=f"(r[1][7]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]),
+          "=f"(r[2][3]), "=f"(r[3][2]), "=f"(r[3][3]), "=f"(r[2][4]), "=f"(r[2][5]), "=f"(r[3][4]), "=f"(r[3][5]),
+          "=f"(r[2][6]), "=f"(r[2][7]), "=f"(r[3][6]), "=f"(r[3][7])
+        : "r"(addr), "r"(up)
+        : "memory");
+  }
+}
+// Four 8 x 8 matrices of 16-bit values between fragments and rows of 16 bytes
+// in shared memory, transposed; thread i has the address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
