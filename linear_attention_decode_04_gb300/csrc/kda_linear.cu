@@ -449,6 +449,174 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
 }
 
+// ------------------------------------------------------- the kernel, many rows
+// 256 rows of x and 256 channels: a pair of CTAs forms one product, each with
+// 128 channels of the weights and half of the rows in its shared memory, so that
+// a tile's operands are read once per pair.  An accumulator's 256 columns are in
+// both CTAs' tensor memory, each with its own channels, twice: a tile's results
+// are written while the next one's products run.
+template <int ROWS>
+struct PairCfg {
+  static constexpr int kStageBytes = (kTileN + ROWS / 2) * kBlock;
+  static constexpr int kStages = 200 * 1024 / kStageBytes;
+  static constexpr int kTmemCols = 2 * ROWS;
+};
+// Tiles go through the channels for a group of row tiles at a time, so that what
+// runs at once shares both operands in L2.
+constexpr int kGroup = 10;
+struct TileAt {
+  int nt, mt;
+  __device__ __forceinline__ TileAt(const Params& p, int tile) {
+    const int groups = (p.m_tiles + kGroup - 1) / kGroup, size = (p.m_tiles + groups - 1) / groups;
+    const int n_tiles = p.tiles / p.m_tiles, g = tile / (size * n_tiles), first = g * size;
+    const int here = min(size, p.m_tiles - first), r = tile - first * n_tiles;
+    nt = r / here;
+    mt = first + r - nt * here;
+  }
+};
+
+template <int ROWS, bool E4M3, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int) {
+  using C = PairCfg<ROWS>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<C>& S = *reinterpret_cast<Smem<C>*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x & 1, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
+    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 8);  // the warps of both epilogues
+    bar_init(&S.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    S.failed = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&w_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
+  }
+  __syncwarp();
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_before();
+  __syncthreads();
+  cluster_arrive();  // the other CTA's barriers are there
+  cluster_wait();
+  tc_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = S.tmem;
+  const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
+  if (warp == 4) {
+    // ================================================================ producer
+    if (lane == 0) {
+      const int64_t total = static_cast<int64_t>(mine) * p.blocks;
+      auto expect = [&](uint32_t st) {  // both CTAs' copies count at the even one
+        if (rank == 0) bar_expect(&S.full[st], 2 * C::kStageBytes);
+      };
+      auto weights = [&](uint32_t st, int nt, int k) {
+        const uint32_t dst = s32(S.stage[st]), b = in_cta(&S.full[st], 0);
+        if (GATED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tma_3d_pair(dst + i * 32 * kBlock, &w_map, k * kBlock, (2 * nt + rank) * (kTileN / 2) + 16 * i, 0, b);
+        } else {
+          tma_2d_pair(dst, &w_map, k * kBlock, (2 * nt + rank) * kTileN, b);
+        }
+      };
+      auto rows = [&](uint32_t st, int mt, int k) {
+        tma_2d_pair(s32(S.stage[st]) + kTileN * kBlock, &x_map, k * kBlock, mt * ROWS + rank * (ROWS / 2), in_cta(&S.full[st], 0));
+      };
+      int64_t ahead = 0;  // stages whose weights were asked for before the kernel ahead ended
+      if (p.early) {
+        int tile = first, k = 0;
+        for (; ahead < total && ahead < C::kStages; ++ahead) {
+          expect(static_cast<uint32_t>(ahead));
+          weights(static_cast<uint32_t>(ahead), TileAt(p, tile).nt, k);
+          if (++k == p.blocks) k = 0, tile += step;
+        }
+      }
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      int64_t it = 0;
+      bool ok = true;
+      for (int i = 0; i < mine && ok; ++i) {
+        const TileAt at(p, first + i * step);
+        for (int k = 0; k < p.blocks; ++k, ++it) {
+          const uint32_t st = static_cast<uint32_t>(it % C::kStages), round = static_cast<uint32_t>(it / C::kStages);
+          if (it >= ahead) {
+            if (round > 0 && !bar_wait(&S.empty[st], (round - 1) & 1, &S.failed)) {
+              ok = false;
+              break;
+            }
+            expect(st);
+            weights(st, at.nt, k);
+          }
+          rows(st, at.mt, k);
+        }
+      }
+      // nothing may land in either CTA's memory after it is gone, whoever gave up
+      if (rank == 0)
+        for (int64_t j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+          bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ========================================================== product issuer
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id = idesc_k(E4M3, 2 * kTileN, ROWS);
+      bool ok = true;
+      int64_t it = 0;
+      for (int i = 0; i < mine && ok; ++i) {
+        const uint32_t buf = i & 1;
+        if (i >= 2) ok = bar_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
+        tc_after();
+        for (int k = 0; k < p.blocks && ok; ++k, ++it) {
+          const uint32_t st = static_cast<uint32_t>(it % C::kStages);
+          ok = bar_wait(&S.full[st], static_cast<uint32_t>(it / C::kStages) & 1, &S.failed);
+          if (!ok) break;
+          tc_after();
+          const uint32_t w = s32(S.stage[st]), x = w + kTileN * kBlock;
+#pragma unroll
+          for (int j = 0; j < kBlock / 32; ++j)
+            mma_2cta<E4M3>(tmem + buf * ROWS, sdesc128(w + 32 * j), sdesc128(x + 32 * j), id, k + j > 0);
+          commit_both(&S.empty[st]);
+        }
+        if (ok) commit_both(&S.acc_full[buf]);
+      }
+      commit_both(&S.done);
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ epilogue
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t buf = i & 1;
+      const TileAt at(p, first + i * step);
+      const int m0 = at.mt * ROWS;
+      Epilogue<GATED> e(p, S.rows[warp], 2 * at.nt + rank, warp, lane);
+      bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
+      tc_after();
+#pragma unroll 1
+      for (int col = 0; col < ROWS && m0 + col < p.M; col += 32) {
+        float z[4][8];
+        tm_fragments<4>(lanes + buf * ROWS + col, z);
+        e.template rows<4>(m0 + col, z);
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_at(in_cta(&S.acc_empty[buf], 0));
+    }
+  }
+  // every product has ended, in both CTAs' memory, before either leaves, given up or not
+  if (warp == 5 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  tc_before();
+  __syncthreads();
+  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+}
+
 // ------------------------------------------------------------------ host side
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -458,25 +626,26 @@ int g_sms[64];
 EncodeFn g_encode;
 
 using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap, int);
+struct Variant {
+  int rows, box;     // rows of a tile; rows of x per copy
+  bool pair;
+  Kernel kernel[4];  // bf16, e4m3, and both gated
+  size_t smem;
+};
 template <int ROWS>
-Kernel kernel_of(bool e4m3, bool gated) {
-  return e4m3 ? (gated ? linear_kernel<ROWS, true, true> : linear_kernel<ROWS, true, false>)
-              : (gated ? linear_kernel<ROWS, false, true> : linear_kernel<ROWS, false, false>);
+Variant single() {
+  using M = Smem<Cfg<ROWS>>;
+  static_assert(sizeof(M) <= 227 * 1024 && ROWS * kTileN * 4 <= sizeof(M::stage), "shared memory");
+  return {ROWS, ROWS, false, {linear_kernel<ROWS, false, false>, linear_kernel<ROWS, true, false>, linear_kernel<ROWS, false, true>, linear_kernel<ROWS, true, true>}, sizeof(M)};
 }
 template <int ROWS>
-constexpr size_t smem_bytes() {
-  static_assert(sizeof(Smem<Cfg<ROWS>>) <= 227 * 1024 && ROWS * kTileN * 4 <= Cfg<ROWS>::kStages * Cfg<ROWS>::kStageBytes, "shared memory");
-  return sizeof(Smem<Cfg<ROWS>>);
+Variant pair() {
+  using M = Smem<PairCfg<ROWS>>;
+  static_assert(sizeof(M) <= 227 * 1024, "shared memory");
+  return {ROWS, ROWS / 2, true, {linear_pair_kernel<ROWS, false, false>, linear_pair_kernel<ROWS, true, false>, linear_pair_kernel<ROWS, false, true>, linear_pair_kernel<ROWS, true, true>}, sizeof(M)};
 }
-// Calls `f` with the number of rows per tile as a constant.
-template <class F>
-auto with_rows(int M, F f) {
-  if (M <= 16) return f(std::integral_constant<int, 16>{});
-  if (M <= 32) return f(std::integral_constant<int, 32>{});
-  if (M <= 64) return f(std::integral_constant<int, 64>{});
-  if (M <= 128) return f(std::integral_constant<int, 128>{});
-  return f(std::integral_constant<int, 256>{});
-}
+const Variant kVariants[] = {single<16>(), single<32>(), single<64>(), single<128>(), pair<256>()};
+const Variant& variant_of(int M) { return kVariants[M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : M <= 128 ? 3 : 4]; }
 
 cudaError_t setup(int* sms) {
   int dev = 0;
@@ -491,14 +660,9 @@ cudaError_t setup(int* sms) {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeFn>(fn);
-    for (int rows = 16; rows <= 256; rows *= 2)
-      for (int v = 0; v < 4; ++v) {
-        e = with_rows(rows, [&](auto r) {
-          return cudaFuncSetAttribute(kernel_of<r.value>(v & 1, v >> 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem_bytes<r.value>()));
-        });
-        if (e != cudaSuccess) return e;
-      }
+    for (const Variant& v : kVariants)
+      for (const Kernel k : v.kernel)
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem))) != cudaSuccess) return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     g_sms[dev] = n;
@@ -546,7 +710,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const cuuint64_t k_bytes = static_cast<cuuint64_t>(a->K) * size;
   const cuuint64_t w_pitch = static_cast<cuuint64_t>(a->weight_row_stride) * size, x_pitch = static_cast<cuuint64_t>(a->x_row_stride) * size;
   const cuuint32_t ones[3] = {1, 1, 1};
-  const int rows = with_rows(a->M, [](auto r) { return static_cast<int>(r.value); });
+  const Variant& v = variant_of(a->M);
   CUtensorMap w_map, x_map;
   CUresult r;
   {
@@ -561,7 +725,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   if (r == CUDA_SUCCESS) {
     const cuuint64_t dims[2] = {k_bytes, static_cast<cuuint64_t>(a->M)};
     const cuuint64_t strides[1] = {x_pitch};
-    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(rows)};
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(v.box)};
     r = g_encode(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a->x), dims, strides, box, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -569,8 +733,8 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
   Params p{};
   p.M = a->M, p.N = a->N, p.K = a->K, p.width = width;
-  const int tile_width = gated ? kTileN / 2 : kTileN;
-  const int64_t m_tiles = (static_cast<int64_t>(a->M) + rows - 1) / rows, n_tiles = (static_cast<int64_t>(width) + tile_width - 1) / tile_width;
+  const int tile_width = (gated ? kTileN / 2 : kTileN) * (v.pair ? 2 : 1);
+  const int64_t m_tiles = (static_cast<int64_t>(a->M) + v.rows - 1) / v.rows, n_tiles = (static_cast<int64_t>(width) + tile_width - 1) / tile_width;
   if (m_tiles * n_tiles > 0x7fffffff / kMaxSplit) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
   p.m_tiles = static_cast<int>(m_tiles), p.tiles = static_cast<int>(m_tiles * n_tiles);
   p.blocks = static_cast<int>((k_bytes + kBlock - 1) / kBlock);
@@ -582,12 +746,12 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   p.vec_res = !misaligned(a->residual, 15) && a->residual_row_stride % 8 == 0;
   // few tiles: up to eight CTAs share one, while all of them are resident and each has a block of k
   int split = 1;
-  while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;
-  const unsigned grid = static_cast<unsigned>(split > 1 ? p.tiles * split : (p.tiles < sms ? p.tiles : sms));
-  e = with_rows(a->M, [&](auto r) {
-    return kda_internal_launch_cluster(kernel_of<r.value>(e4m3, gated), dim3(grid), dim3(kThreads), smem_bytes<r.value>(), stream,
-                                       static_cast<unsigned>(split), p, w_map, x_map, split);
-  });
+  if (!v.pair)
+    while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;
+  const int cluster = v.pair ? 2 : split, resident = v.pair ? sms / 2 : sms;
+  const unsigned grid = static_cast<unsigned>((split > 1 || p.tiles < resident ? p.tiles : resident) * cluster);
+  e = kda_internal_launch_cluster(v.kernel[(gated ? 2 : 0) + (e4m3 ? 1 : 0)], dim3(grid), dim3(kThreads), v.smem, stream,
+                                  static_cast<unsigned>(cluster), p, w_map, x_map, split);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }
