@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kTileN = 128;                // channels of a tile
 constexpr int kBlock = 128;                // bytes of k per stage
-constexpr int kThreads = 192;              // four warps of the epilogue, producer, issuer
 constexpr int kMaxSplit = 8;
 constexpr int kPitch = 80;                 // bytes between rows of results in shared memory
 
@@ -52,12 +51,14 @@ struct Cfg {
   static constexpr int kStageBytes = (kTileN + ROWS) * kBlock;
   static constexpr int kStages = 200 * 1024 / kStageBytes;
   static constexpr int kTmemCols = 2 * ROWS;  // two accumulators; a power of two from 32 on
+  // A warpgroup of the epilogue per 32 rows, up to two; then producer and issuer.
+  static constexpr int kGroups = ROWS > 32 ? 2 : 1, kThreads = 128 * kGroups + 64;
 };
 
 template <class C>
 struct alignas(1024) Smem {
   uint8_t stage[C::kStages][C::kStageBytes];
-  alignas(16) uint8_t rows[4][32 * kPitch];  // of the warps of the epilogue
+  alignas(16) uint8_t rows[4 * C::kGroups][32 * kPitch];  // of the warps of the epilogue
   uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int failed;
@@ -238,7 +239,7 @@ struct Epilogue {
 // their sums.  A thread has one accumulator lane and pairs of rows.
 template <int ROWS, bool GATED>
 __device__ __forceinline__ void join_parts(const Params& p, uint8_t* raw, int tile, int rank, int split) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane = tid & 31, warp = tid >> 5;
   const int nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
   const int c = GATED ? nt * (kTileN / 2) + 16 * warp + (lane & 15) : nt * kTileN + tid;  // of out
   const int n = GATED ? c + (lane >> 4) * p.width : c;
@@ -246,7 +247,7 @@ __device__ __forceinline__ void join_parts(const Params& p, uint8_t* raw, int ti
   const float scale = live && p.w_scale ? p.w_scale[n] : 1.f, bias = live && p.bias ? p.bias[n] : 0.f;
   constexpr int kAhead = 4;  // pairs of rows whose parts are on their way together
   const int pairs = ROWS / 2 / split, end = min((rank + 1) * pairs, (p.M - m0 + 1) / 2);
-  for (int q0 = rank * pairs; q0 < end; q0 += kAhead) {
+  for (int q0 = rank * pairs + kAhead * group; q0 < end; q0 += kAhead * Cfg<ROWS>::kGroups) {
     float2 a[kAhead];
     float res[kAhead][2], xs[kAhead][2];
 #pragma unroll
@@ -299,7 +300,7 @@ __device__ __forceinline__ void join_parts(const Params& p, uint8_t* raw, int ti
 }
 
 template <int ROWS, bool E4M3, bool GATED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     linear_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int split) {
   using C = Cfg<ROWS>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = blockIdx.x / split, rank = blockIdx.x - first * split, step = gridDim.x / split;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 128);
+    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 128 * C::kGroups);
     bar_init(&S.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     S.failed = 0;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
   }
   __syncwarp();
-  if (warp == 5) {
+  if (warp == 4 * C::kGroups + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
   const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split), span = k1 - k0;
   const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;  // tiles of this CTA
-  if (warp == 4) {
+  if (warp == 4 * C::kGroups) {
     // ================================================================ producer
     if (lane == 0) {
       const int64_t total = static_cast<int64_t>(mine) * span;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 4 * C::kGroups + 1) {
     // ========================================================== product issuer
     if (lane == 0) {
       constexpr uint32_t id = idesc_k(E4M3, kTileN, ROWS);
@@ -402,20 +403,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ================================================================ epilogue
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int wq = warp & 3, group = warp >> 2;  // the warp's quarter of the lanes; its group, which takes every kGroups-th 32 rows
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
       const int tile = first + i * step, nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
       constexpr int kBlocks = ROWS < 32 ? 2 : 4;
-      Epilogue<GATED> e(p, S.rows[warp], nt, warp, lane);
+      Epilogue<GATED> e(p, S.rows[warp], nt, wq, lane);
       bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
       tc_after();
 #pragma unroll 1
-      for (int col = 0; col < ROWS && m0 + col < p.M; col += 8 * kBlocks) {
+      for (int col = 8 * kBlocks * group; col < ROWS && m0 + col < p.M; col += 8 * kBlocks * C::kGroups) {
         float z[4][2 * kBlocks];
         tm_fragments<kBlocks>(lanes + buf * ROWS + col, z);
         if (split > 1) {  // [column pair][channel], where the stages were
-          float2* part = reinterpret_cast<float2*>(raw) + (col / 2 + (lane & 3)) * kTileN + 32 * warp + (lane >> 2);
+          float2* part = reinterpret_cast<float2*>(raw) + (col / 2 + (lane & 3)) * kTileN + 32 * wq + (lane >> 2);
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    if (warp < 4 && mine > 0) {
+    if (warp < 4 * C::kGroups && mine > 0) {
       join_parts<ROWS, GATED>(p, raw, first, rank, split);
     }
     __syncwarp();
@@ -441,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait();
   }
   // every product has ended before the accumulators are given back, given up or not
-  if (warp == 5 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  if (warp == 4 * C::kGroups + 1 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
   tc_before();
   __syncthreads();
   if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
   __syncwarp();
-  if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+  if (warp == 4 * C::kGroups + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
 }
 
 // ------------------------------------------------------- the kernel, many rows
@@ -460,6 +462,7 @@ struct PairCfg {
   static constexpr int kStageBytes = (kTileN + ROWS / 2) * kBlock;
   static constexpr int kStages = 200 * 1024 / kStageBytes;
   static constexpr int kTmemCols = 2 * ROWS;
+  static constexpr int kGroups = 2, kThreads = 128 * kGroups + 64;
 };
 // Tiles go through the channels for a group of row tiles at a time, so that what
 // runs at once shares both operands in L2.
@@ -476,7 +479,7 @@ struct TileAt {
 };
 
 template <int ROWS, bool E4M3, bool GATED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PairCfg<ROWS>::kThreads, 1)
     linear_pair_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int) {
   using C = PairCfg<ROWS>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = blockIdx.x & 1, first = blockIdx.x >> 1, step = gridDim.x >> 1;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 8);  // the warps of both epilogues
+    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 8 * C::kGroups);  // the warps of both epilogues
     bar_init(&S.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     S.failed = 0;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
   }
   __syncwarp();
-  if (warp == 5) {
+  if (warp == 4 * C::kGroups + 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = S.tmem;
   const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
-  if (warp == 4) {
+  if (warp == 4 * C::kGroups) {
     // ================================================================ producer
     if (lane == 0) {
       const int64_t total = static_cast<int64_t>(mine) * p.blocks;
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 4 * C::kGroups + 1) {
     // ========================================================== product issuer
     if (lane == 0 && rank == 0) {
       constexpr uint32_t id = idesc_k(E4M3, 2 * kTileN, ROWS);
@@ -587,16 +590,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ================================================================ epilogue
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int wq = warp & 3, group = warp >> 2;  // the warp's quarter of the lanes; its group, which takes every kGroups-th 32 rows
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
       const TileAt at(p, first + i * step);
       const int m0 = at.mt * ROWS;
-      Epilogue<GATED> e(p, S.rows[warp], 2 * at.nt + rank, warp, lane);
+      Epilogue<GATED> e(p, S.rows[warp], 2 * at.nt + rank, wq, lane);
       bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
       tc_after();
 #pragma unroll 1
-      for (int col = 0; col < ROWS && m0 + col < p.M; col += 32) {
+      for (int col = 32 * group; col < ROWS && m0 + col < p.M; col += 32 * C::kGroups) {
         float z[4][8];
         tm_fragments<4>(lanes + buf * ROWS + col, z);
         e.template rows<4>(m0 + col, z);
@@ -607,14 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   // every product has ended, in both CTAs' memory, before either leaves, given up or not
-  if (warp == 5 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  if (warp == 4 * C::kGroups + 1 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
   tc_before();
   __syncthreads();
   if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+  if (warp == 4 * C::kGroups + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
 }
 
 // ------------------------------------------------------------------ host side
@@ -631,18 +635,19 @@ struct Variant {
   bool pair;
   Kernel kernel[4];  // bf16, e4m3, and both gated
   size_t smem;
+  int threads;
 };
 template <int ROWS>
 Variant single() {
   using M = Smem<Cfg<ROWS>>;
   static_assert(sizeof(M) <= 227 * 1024 && ROWS * kTileN * 4 <= sizeof(M::stage), "shared memory");
-  return {ROWS, ROWS, false, {linear_kernel<ROWS, false, false>, linear_kernel<ROWS, true, false>, linear_kernel<ROWS, false, true>, linear_kernel<ROWS, true, true>}, sizeof(M)};
+  return {ROWS, ROWS, false, {linear_kernel<ROWS, false, false>, linear_kernel<ROWS, true, false>, linear_kernel<ROWS, false, true>, linear_kernel<ROWS, true, true>}, sizeof(M), Cfg<ROWS>::kThreads};
 }
 template <int ROWS>
 Variant pair() {
   using M = Smem<PairCfg<ROWS>>;
   static_assert(sizeof(M) <= 227 * 1024, "shared memory");
-  return {ROWS, ROWS / 2, true, {linear_pair_kernel<ROWS, false, false>, linear_pair_kernel<ROWS, true, false>, linear_pair_kernel<ROWS, false, true>, linear_pair_kernel<ROWS, true, true>}, sizeof(M)};
+  return {ROWS, ROWS / 2, true, {linear_pair_kernel<ROWS, false, false>, linear_pair_kernel<ROWS, true, false>, linear_pair_kernel<ROWS, false, true>, linear_pair_kernel<ROWS, true, true>}, sizeof(M), PairCfg<ROWS>::kThreads};
 }
 const Variant kVariants[] = {single<16>(), single<32>(), single<64>(), single<128>(), pair<256>()};
 const Variant& variant_of(int M) { return kVariants[M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : M <= 128 ? 3 : 4]; }
@@ -750,7 +755,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
     while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;
   const int cluster = v.pair ? 2 : split, resident = v.pair ? sms / 2 : sms;
   const unsigned grid = static_cast<unsigned>((split > 1 || p.tiles < resident ? p.tiles : resident) * cluster);
-  e = kda_internal_launch_cluster(v.kernel[(gated ? 2 : 0) + (e4m3 ? 1 : 0)], dim3(grid), dim3(kThreads), v.smem, stream,
+  e = kda_internal_launch_cluster(v.kernel[(gated ? 2 : 0) + (e4m3 ? 1 : 0)], dim3(grid), dim3(static_cast<unsigned>(v.threads)), v.smem, stream,
                                   static_cast<unsigned>(cluster), p, w_map, x_map, split);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
