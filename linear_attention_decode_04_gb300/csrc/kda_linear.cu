@@ -5,20 +5,23 @@
 // channels are the wide side of a tile and the rows of x, of which a decode
 // step has few, the narrow one (16 to 256 columns).  Tiles of W and X go to
 // shared memory by TMA (128 bytes of k, 128-byte swizzle), tcgen05 multiplies
-// them as they are, and a thread of the epilogue has a channel of its own, with
-// its scale and bias in registers.
+// them as they are, and each of the tile's two accumulators is written out while
+// the next tile's products run in the other.  With many rows two CTAs form one
+// product of 256 channels, each with its half of the channels and of the rows in
+// its own shared memory, so that a pair reads a tile's operands once.
 //
-// A gated tile holds 64 channels of each half, 16 and 16 in turn, so that a
-// warp's 32 lanes have both halves of 16 results.
+// A gated tile has two operands of 128 channels, one of each half, and an
+// accumulator for each, so that a thread has both factors of its results.
 //
-// Few tiles: the CTAs of a cluster share one tile, each with a range of k, and
-// add their parts up over distributed shared memory in a fixed order.
+// Few tiles: the CTAs (or pairs) of a cluster share one tile, each with a range
+// of k, and add their parts up over distributed shared memory in a fixed order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "kda_internal.h"
@@ -27,14 +30,16 @@
 
 namespace {
 
-constexpr int kTileN = 128;                // channels of a tile
+constexpr int kTileN = 128;                // channels of a CTA's tile
 constexpr int kBlock = 128;                // bytes of k per stage
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 4;
+constexpr int kMaxStages = 12;
 constexpr int kPitch = 80;                 // bytes between rows of results in shared memory
 
 struct Params {
   int M, N, K, width;          // width: channels of out
-  int m_tiles, tiles, blocks;  // row tiles, tiles, blocks of k
+  int m_tiles, n_tiles, blocks;  // row tiles, channel tiles (of a CTA or pair), blocks of k
+  int split, stages;           // CTAs (or pairs) per tile, ring depth
   int act;
   bool out_f32, early, vec_out, vec_res;  // vec: rows in 16-byte pieces
   const float *x_scale, *w_scale, *bias;
@@ -45,30 +50,56 @@ struct Params {
   int32_t* err;
 };
 
+// A gate's two halves: in two accumulators, or 16 and 16 channels in turn in one.
+constexpr int kNoGate = 0, kTwoSums = 1, kInterleaved = 2;
+
 // ROWS of x per tile.
-template <int ROWS>
+template <int ROWS, int GATE, bool PAIR>
 struct Cfg {
-  static constexpr int kStageBytes = (kTileN + ROWS) * kBlock;
-  static constexpr int kStages = 200 * 1024 / kStageBytes;
-  static constexpr int kTmemCols = 2 * ROWS;  // two accumulators; a power of two from 32 on
-  // A warpgroup of the epilogue per 32 rows, up to two; then producer and issuer.
-  static constexpr int kGroups = ROWS > 32 ? 2 : 1, kThreads = 128 * kGroups + 64;
+  static constexpr int kAcc = GATE == kTwoSums ? 2 : 1;
+  static constexpr int kChannels = GATE == kInterleaved ? kTileN / 2 : kTileN;  // of out, of a CTA
+  static constexpr int kUnroll = PAIR || ROWS > 64 ? 4 : 2;  // blocks of eight rows that a warp writes at a time
+  static constexpr int kWeightBytes = kAcc * kTileN * kBlock, kXRows = PAIR ? ROWS / 2 : ROWS;
+  static constexpr int kStageBytes = kWeightBytes + kXRows * kBlock;
+  static constexpr int kCols = kAcc * ROWS;      // accumulator columns of a tile, of which there are two sets
+  static constexpr int kTmemCols = 2 * kCols;    // a power of two from 32 on
+  // One CTA takes an SM's shared memory; where a short range of k leaves room, the next call's CTAs start beside it.
+  static constexpr int kCtasPerSm = PAIR || ROWS > 64 ? 1 : 2;
+  // warpgroups that write results; then a warp that copies weights, one that copies rows, and the issuer
+  static constexpr int kGroups = kCtasPerSm == 1 ? 2 : 1, kThreads = 128 * kGroups + 96;
+  // sums of a tile that several CTAs share: in the stages, when its products have ended, lie a CTA's own and those sent to it
+  static constexpr int kPartBytes = kCols / 2 * (kTileN * 8 + 64 * kMaxSplit);
+  static_assert(kTmemCols * kCtasPerSm <= 512, "tensor memory");
 };
 
+// Shared memory: the stages, then this.
 template <class C>
-struct alignas(1024) Smem {
-  uint8_t stage[C::kStages][C::kStageBytes];
-  alignas(16) uint8_t rows[4 * C::kGroups][32 * kPitch];  // of the warps of the epilogue
-  uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], done;
+struct Head {
+  alignas(16) uint8_t rows[4 * C::kGroups][8 * C::kUnroll * kPitch];  // of the warps that write results
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], joined, done;
   uint32_t tmem;
   int failed;
 };
 
-__device__ __forceinline__ float sigmoid_times(float y) { return y / (1.f + __expf(-y)); }
-// (1 + erf loses gelu's lower tail)
-__device__ __forceinline__ float gelu(float y) { return 0.5f * y * erfcf(y * -0.70710678118654752f); }
-__device__ __forceinline__ float activate(float y, int act) {
-  return act == KDA_ACT_SILU ? sigmoid_times(y) : act == KDA_ACT_GELU ? gelu(y) : y;
+__device__ __forceinline__ float sigmoid_times(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+// y (1 + erf(y / sqrt 2)) / 2 with erfc(x) = t e^(-x^2 + P(t)), t = 1 / (1 + x / 2),
+// P of degree 9: Numerical Recipes' erfcc (Press et al., section 6.2), off by 1.2e-7
+// of itself at any x >= 0, so that the lower tail keeps its digits; -x^2 rounded
+// adds x^2 2^-23.
+__device__ __forceinline__ float gelu(float y) {
+  const float x = fabsf(y) * 0.70710678118654752f, t = __fdividef(1.f, fmaf(0.5f, x, 1.f));
+  float q = 0.17087277f;
+  q = fmaf(q, t, -0.82215223f);
+  q = fmaf(q, t, 1.48851587f);
+  q = fmaf(q, t, -1.13520398f);
+  q = fmaf(q, t, 0.27886807f);
+  q = fmaf(q, t, -0.18628806f);
+  q = fmaf(q, t, 0.09678418f);
+  q = fmaf(q, t, 0.37409196f);
+  q = fmaf(q, t, 1.00002368f);
+  q = fmaf(q, t, -1.26551223f);
+  const float half = 0.5f * t * __expf(fmaf(-x, x, q));  // the normal distribution's lower tail
+  return y * (y > 0.f ? 1.f - half : half);
 }
 __device__ __forceinline__ float of_bf16(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -76,394 +107,159 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ---- A warp's part of a tile: 32 accumulator lanes, which are 32 channels of
-// out, or gated 16 of them (their two halves 16 lanes apart), as fragments: a
-// thread has lanes r8 + 8 j and pairs of neighbouring rows.  Rows of 32 channels
-// of bf16 results go through shared memory, 80 bytes apart so that the eight
-// rows of a matrix lie in different banks, and from there to memory 16 bytes a
-// thread; residuals come the same way.
-template <bool GATED>
+// ---- A warp's part of a tile: 32 accumulator lanes, which are 32 channels or,
+// interleaved, both halves of 16, BLOCKS times eight rows at a time, as fragments:
+// a thread has lanes r8 + 8 j and two neighbouring rows of each block.  bf16
+// results go through shared memory as four 8 x 8 matrices (eight rows of 32
+// channels, or 16 of 16), rows 80 bytes apart so that they lie in different banks,
+// and from there to memory 16 bytes a thread; residuals come the same way, a trip
+// ahead.  (A loop of few instructions: in a short launch all of them are fetched
+// for the first time, which with 32 rows unrolled took longer than the products of
+// a small matrix.)
+template <int GATE, int BLOCKS>
 struct Epilogue {
-  static constexpr int kWidth = GATED ? 16 : 32;  // channels of out
-  static constexpr int kParts = kWidth / 8;       // 16-byte pieces of a row
+  static constexpr int kAcc = GATE == kTwoSums ? 2 : 1;
+  static constexpr int kWidth = GATE == kInterleaved ? 16 : 32;      // channels of out
+  static constexpr int kRows = 256 / kWidth, kSets = 8 * BLOCKS / kRows;  // rows of four matrices; sets of them
+  static constexpr int kParts = kWidth / 8;                          // 16-byte pieces of a row
   const Params& p;
-  uint8_t* stage;                                 // 32 rows of the warp's own
+  uint8_t* stage;                                                    // 8 BLOCKS rows of the warp's own
   int lane, n0;
-  float scale[4], bias[4];
+  float scale[kAcc][4], bias[kAcc][4];
 
-  __device__ __forceinline__ Epilogue(const Params& q, uint8_t* st, int n_tile, int wq, int ln)
-      : p(q), stage(st), lane(ln), n0(n_tile * (GATED ? kTileN / 2 : kTileN) + wq * kWidth) {
+  __device__ __forceinline__ Epilogue(const Params& q, uint8_t* st, int channel0, int ln) : p(q), stage(st), lane(ln), n0(channel0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + (lane >> 2) + 8 * (GATED ? j & 1 : j), n = GATED ? c + (j >> 1) * p.width : c;
-      const bool live = c < p.width;
-      scale[j] = live && p.w_scale ? p.w_scale[n] : 1.f;
-      bias[j] = live && p.bias ? p.bias[n] : 0.f;
-    }
-  }
-  // this thread's row of the matrices of 8-row block b (gated: of b and b + 1)
-  __device__ __forceinline__ uint32_t matrix(int b) const {
-    const int m = lane >> 3;
-    return s32(stage) + (8 * (GATED ? b + (m >> 1) : b) + (lane & 7)) * kPitch + (GATED ? m & 1 : m) * 16;
-  }
-  // Rows m0 .. m0 + 8 BLOCKS - 1 between memory and the stage.
-  template <int BLOCKS>
-  __device__ __forceinline__ void fetch(int m0) {
-    const bool vec = p.vec_res && n0 + kWidth <= p.width;
-    if (vec) {
-      constexpr int kRows = 32 / kParts, kTrips = 8 * BLOCKS / kRows;  // rows per trip
-      uint4 v[kTrips];
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i) {
-        const int m = m0 + i * kRows + lane / kParts;
-        v[i] = m < p.M ? *reinterpret_cast<const uint4*>(p.residual + m * p.res_stride + n0 + lane % kParts * 8) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i)
-        *reinterpret_cast<uint4*>(stage + (i * kRows + lane / kParts) * kPitch + lane % kParts * 16) = v[i];
-    } else {
-      constexpr int kRows = 32 / kWidth, kTrips = 8 * BLOCKS / kRows;
-      const int c = n0 + lane % kWidth;
-      uint16_t v[kTrips];
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i) {
-        const int m = m0 + i * kRows + lane / kWidth;
-        v[i] = m < p.M && c < p.width ? p.residual[m * p.res_stride + c] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i)
-        *reinterpret_cast<uint16_t*>(stage + (i * kRows + lane / kWidth) * kPitch + lane % kWidth * 2) = v[i];
-    }
-    __syncwarp();
-  }
-  template <int BLOCKS>
-  __device__ __forceinline__ void put(int m0) {
-    __syncwarp();
-    uint16_t* out = static_cast<uint16_t*>(p.out);
-    if (p.vec_out && n0 + kWidth <= p.width) {
-      constexpr int kRows = 32 / kParts, kTrips = 8 * BLOCKS / kRows;
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i) {
-        const int m = m0 + i * kRows + lane / kParts;
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * kRows + lane / kParts) * kPitch + lane % kParts * 16);
-        if (m < p.M) *reinterpret_cast<uint4*>(out + m * p.out_stride + n0 + lane % kParts * 8) = v;
-      }
-    } else {
-      constexpr int kRows = 32 / kWidth, kTrips = 8 * BLOCKS / kRows;
-      const int c = n0 + lane % kWidth;
-#pragma unroll
-      for (int i = 0; i < kTrips; ++i) {
-        const int m = m0 + i * kRows + lane / kWidth;
-        const uint16_t v = *reinterpret_cast<const uint16_t*>(stage + (i * kRows + lane / kWidth) * kPitch + lane % kWidth * 2);
-        if (m < p.M && c < p.width) out[m * p.out_stride + c] = v;
-      }
-    }
-    __syncwarp();
-  }
-  // Rows m0 .. m0 + 8 BLOCKS - 1 from their sums.
-  template <int BLOCKS>
-  __device__ __forceinline__ void rows(int m0, float (&z)[4][2 * BLOCKS]) {
-    if (n0 >= p.width) return;
-    if (p.residual) fetch<BLOCKS>(m0);
-    const int a = 2 * (lane & 3);
-#pragma unroll
-    for (int b = 0; b < BLOCKS; ++b) {
-      const int m = m0 + 8 * b + a;
-      const float s0 = p.x_scale && m < p.M ? p.x_scale[m] : 1.f, s1 = p.x_scale && m + 1 < p.M ? p.x_scale[m + 1] : 1.f;
+    for (int h = 0; h < kAcc; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        z[j][2 * b] = fmaf(z[j][2 * b] * s0, scale[j], bias[j]);
-        z[j][2 * b + 1] = fmaf(z[j][2 * b + 1] * s1, scale[j], bias[j]);
+        const int c = n0 + (lane >> 2) + 8 * (GATE == kInterleaved ? j & 1 : j), n = c + (GATE == kInterleaved ? j >> 1 : h) * p.width;
+        const bool live = c < p.width;
+        scale[h][j] = live && p.w_scale ? p.w_scale[n] : 1.f;
+        bias[h][j] = live && p.bias ? p.bias[n] : 0.f;
+      }
+  }
+  __device__ __forceinline__ bool whole() const { return n0 + kWidth <= p.width; }
+  // block and fragment of matrix k of set s
+  __device__ __forceinline__ static constexpr int block_of(int s, int k) { return GATE == kInterleaved ? 2 * s + (k >> 1) : s; }
+  __device__ __forceinline__ static constexpr int lane_of(int k) { return GATE == kInterleaved ? k & 1 : k; }
+  // this thread's row of set s
+  __device__ __forceinline__ uint32_t matrix(int s) const {
+    const int k = lane >> 3, row = GATE == kInterleaved ? 8 * (k >> 1) + (lane & 7) : lane & 7;
+    return s32(stage) + (s * kRows + row) * kPitch + (GATE == kInterleaved ? k & 1 : k) * 16;
+  }
+  // The residuals of the sets from row m on: 16 bytes of a row, or eight rows of a channel.
+  __device__ __forceinline__ void fetch(int m, uint4 (&res)[kSets]) const {
+    if (!p.residual || n0 >= p.width) return;
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      if (p.vec_res && whole()) {
+        const int at = m + s * kRows + lane / kParts;
+        res[s] = at < p.M ? *reinterpret_cast<const uint4*>(p.residual + at * p.res_stride + n0 + lane % kParts * 8) : make_uint4(0, 0, 0, 0);
+      } else {
+        uint32_t v[8];
+        const int row = m + s * kRows + lane / kWidth, c = n0 + lane % kWidth;
+        const uint16_t* at = p.residual + row * p.res_stride + c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, at += p.res_stride * (32 / kWidth)) v[i] = row + i * (32 / kWidth) < p.M && c < p.width ? *at : 0;
+        res[s] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
       }
     }
-    if (GATED) {
+  }
+  // Rows m .. m + 8 BLOCKS - 1 from their sums (kTwoSums: those of the second half in `u`).
+  __device__ __forceinline__ void rows(int m, float (&z)[BLOCKS][4][2], float (&u)[BLOCKS][4][2], const uint4 (&res)[kSets]) const {
+    if (n0 >= p.width) return;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int b = 0; b < BLOCKS; ++b) {
+      const int m0 = m + 8 * b + 2 * (lane & 3);
+      const float s[2] = {p.x_scale && m0 < p.M ? p.x_scale[m0] : 1.f, p.x_scale && m0 + 1 < p.M ? p.x_scale[m0 + 1] : 1.f};
 #pragma unroll
-        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = sigmoid_times(z[j][i]) * z[j + 2][i];
-    } else if (p.act == KDA_ACT_SILU) {
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+          z[b][j][e] = fmaf(z[b][j][e] * s[e], scale[0][j], bias[0][j]);
+          if constexpr (GATE == kTwoSums) z[b][j][e] = sigmoid_times(z[b][j][e]) * fmaf(u[b][j][e] * s[e], scale[1][j], bias[1][j]);
+        }
+        if constexpr (GATE == kInterleaved)
 #pragma unroll
-        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = sigmoid_times(z[j][i]);
-    } else if (p.act == KDA_ACT_GELU) {
+          for (int j = 0; j < 2; ++j) z[b][j][e] = sigmoid_times(z[b][j][e]) * z[b][j + 2][e];
+      }
+    }
+    if constexpr (GATE == kNoGate) {
+      if (p.act == KDA_ACT_SILU) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 8 * BLOCKS; ++i) z[i >> 3][(i >> 1) & 3][i & 1] = sigmoid_times(z[i >> 3][(i >> 1) & 3][i & 1]);
+      } else if (p.act == KDA_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 2 * BLOCKS; ++i) z[j][i] = gelu(z[j][i]);
+        for (int i = 0; i < 8 * BLOCKS; ++i) z[i >> 3][(i >> 1) & 3][i & 1] = gelu(z[i >> 3][(i >> 1) & 3][i & 1]);
+      }
     }
     if (p.residual) {
 #pragma unroll
-      for (int b = 0; b < BLOCKS; b += GATED ? 2 : 1) {
+      for (int s = 0; s < kSets; ++s) {
+        if (p.vec_res && whole()) {
+          *reinterpret_cast<uint4*>(stage + (s * kRows + lane / kParts) * kPitch + lane % kParts * 16) = res[s];
+        } else {
+          const uint32_t w[4] = {res[s].x, res[s].y, res[s].z, res[s].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint16_t*>(stage + (s * kRows + lane / kWidth + i * (32 / kWidth)) * kPitch + lane % kWidth * 2) =
+                static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) {
         uint32_t r[4];
-        load_transposed(matrix(b), r);
+        load_transposed(matrix(s), r);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int j = GATED ? k & 1 : k, i = 2 * (GATED ? b + (k >> 1) : b);
-          z[j][i] += of_bf16(r[k] & 0xffffu);
-          z[j][i + 1] += of_bf16(r[k] >> 16);
+          float(&v)[2] = z[block_of(s, k)][lane_of(k)];
+          v[0] += of_bf16(r[k] & 0xffffu), v[1] += of_bf16(r[k] >> 16);
         }
       }
       __syncwarp();
     }
     if (p.out_f32) {  // eight neighbouring channels of four rows at a time: whole sectors
-      float* out = static_cast<float*>(p.out);
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b)
+      for (int b = 0; b < BLOCKS; ++b) {
+        const int m0 = m + 8 * b + 2 * (lane & 3);
+        float* out = static_cast<float*>(p.out) + m0 * p.out_stride + n0 + (lane >> 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int m = m0 + 8 * b + a + e;
+        for (int e = 0; e < 2; ++e, out += p.out_stride)
 #pragma unroll
-          for (int j = 0; j < (GATED ? 2 : 4); ++j) {
-            const int c = n0 + (lane >> 2) + 8 * j;
-            if (m < p.M && c < p.width) out[m * p.out_stride + c] = z[j][2 * b + e];
-          }
-        }
-    } else {
-#pragma unroll
-      for (int b = 0; b < BLOCKS; b += GATED ? 2 : 1) {
-        uint32_t r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = GATED ? k & 1 : k, i = 2 * (GATED ? b + (k >> 1) : b);
-          r[k] = pack_bf16(z[j][i], z[j][i + 1]);
-        }
-        store_transposed(matrix(b), r);
+          for (int j = 0; j < kParts; ++j)
+            if (m0 + e < p.M && n0 + (lane >> 2) + 8 * j < p.width) out[8 * j] = z[b][j][e];
       }
-      put<BLOCKS>(m0);
-    }
-  }
-};
-
-// A tile shared by the CTAs of a cluster: this CTA's share of the rows, from all
-// their sums.  A thread has one accumulator lane and pairs of rows.
-template <int ROWS, bool GATED>
-__device__ __forceinline__ void join_parts(const Params& p, uint8_t* raw, int tile, int rank, int split) {
-  const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane = tid & 31, warp = tid >> 5;
-  const int nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
-  const int c = GATED ? nt * (kTileN / 2) + 16 * warp + (lane & 15) : nt * kTileN + tid;  // of out
-  const int n = GATED ? c + (lane >> 4) * p.width : c;
-  const bool live = c < p.width;
-  const float scale = live && p.w_scale ? p.w_scale[n] : 1.f, bias = live && p.bias ? p.bias[n] : 0.f;
-  constexpr int kAhead = 4;  // pairs of rows whose parts are on their way together
-  const int pairs = ROWS / 2 / split, end = min((rank + 1) * pairs, (p.M - m0 + 1) / 2);
-  for (int q0 = rank * pairs + kAhead * group; q0 < end; q0 += kAhead * Cfg<ROWS>::kGroups) {
-    float2 a[kAhead];
-    float res[kAhead][2], xs[kAhead][2];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      a[k] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int m = m0 + 2 * (q0 + k) + e;
-        const bool there = q0 + k < end && m < p.M;
-        xs[k][e] = p.x_scale && there ? p.x_scale[m] : 1.f;
-        // (gated: lanes 0 .. 15 finish the even row, 16 .. 31 the odd one)
-        res[k][e] = p.residual && there && live && (!GATED || e == lane >> 4) ? of_bf16(p.residual[m * p.res_stride + c]) : 0.f;
-      }
+      return;
     }
 #pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r) {
-      if (r < split) {
-        uint32_t from;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(s32(raw) + 8 * tid), "r"(r));
+    for (int s = 0; s < kSets; ++s) {
+      uint32_t r[4];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          float2 v;
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(from + min(q0 + k, end - 1) * (8 * kTileN)) : "memory");
-          a[k].x += v.x, a[k].y += v.y;
-        }
-      }
+      for (int k = 0; k < 4; ++k) r[k] = pack_bf16(z[block_of(s, k)][lane_of(k)][0], z[block_of(s, k)][lane_of(k)][1]);
+      store_transposed(matrix(s), r);
     }
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (q0 + k >= end) break;
-      float y[2] = {fmaf(a[k].x * xs[k][0], scale, bias), fmaf(a[k].y * xs[k][1], scale, bias)};
-      const bool up = GATED && lane >> 4;
-      if (GATED) {
-        const float got = __shfl_xor_sync(0xffffffffu, up ? y[0] : y[1], 16);
-        if (up) y[1] = sigmoid_times(got) * y[1];
-        else y[0] = sigmoid_times(y[0]) * got;
+    for (int s = 0; s < kSets; ++s) {
+      if (p.vec_out && whole()) {
+        const int at = m + s * kRows + lane / kParts;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + (s * kRows + lane / kParts) * kPitch + lane % kParts * 16);
+        if (at < p.M) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_stride + n0 + lane % kParts * 8) = v;
       } else {
-        y[0] = activate(y[0], p.act), y[1] = activate(y[1], p.act);
-      }
+        const int row = s * kRows + lane / kWidth, c = n0 + lane % kWidth;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + (m + row) * p.out_stride + c;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t m = m0 + 2 * (q0 + k) + e;
-        if (m >= p.M || !live || (GATED && up != (e == 1))) continue;
-        const float v = y[e] + res[k][e];
-        if (p.out_f32) static_cast<float*>(p.out)[m * p.out_stride + c] = v;
-        else static_cast<__nv_bfloat16*>(p.out)[m * p.out_stride + c] = __float2bfloat16_rn(v);
-      }
-    }
-  }
-}
-
-template <int ROWS, bool E4M3, bool GATED>
-__global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
-    linear_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int split) {
-  using C = Cfg<ROWS>;
-  extern __shared__ __align__(1024) uint8_t raw[];
-  Smem<C>& S = *reinterpret_cast<Smem<C>*>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = blockIdx.x / split, rank = blockIdx.x - first * split, step = gridDim.x / split;
-  if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 128 * C::kGroups);
-    bar_init(&S.done, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    S.failed = 0;
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&w_map) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
-  }
-  __syncwarp();
-  if (warp == 4 * C::kGroups + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  tc_before();
-  __syncthreads();
-  tc_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = S.tmem;
-  const int k0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
-  const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split), span = k1 - k0;
-  const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;  // tiles of this CTA
-  if (warp == 4 * C::kGroups) {
-    // ================================================================ producer
-    if (lane == 0) {
-      const int64_t total = static_cast<int64_t>(mine) * span;
-      auto weights = [&](uint32_t st, int tile, int k) {
-        const int nt = tile / p.m_tiles;
-        const uint32_t dst = s32(S.stage[st]);
-        if (GATED) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tma_3d(dst + i * 32 * kBlock, &w_map, k * kBlock, nt * (kTileN / 2) + 16 * i, 0, &S.full[st]);
-        } else {
-          tma_2d(dst, &w_map, k * kBlock, nt * kTileN, &S.full[st]);
-        }
-      };
-      auto rows = [&](uint32_t st, int tile, int k) {
-        tma_2d(s32(S.stage[st]) + kTileN * kBlock, &x_map, k * kBlock, (tile % p.m_tiles) * ROWS, &S.full[st]);
-      };
-      int64_t ahead = 0;  // stages whose weights were asked for before the kernel ahead ended
-      if (p.early) {
-        int tile = first, k = k0;
-        for (; ahead < total && ahead < C::kStages; ++ahead) {
-          bar_expect(&S.full[ahead], C::kStageBytes);
-          weights(static_cast<uint32_t>(ahead), tile, k);
-          if (++k == k1) k = k0, tile += step;
+        for (int i = 0; i < 8; ++i, out += p.out_stride * (32 / kWidth)) {
+          const uint16_t v = *reinterpret_cast<const uint16_t*>(stage + (row + i * (32 / kWidth)) * kPitch + lane % kWidth * 2);
+          if (m + row + i * (32 / kWidth) < p.M && c < p.width) *out = v;
         }
       }
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      int tile = first, k = k0;
-      int64_t it = 0;
-      for (; it < total; ++it) {
-        const uint32_t st = static_cast<uint32_t>(it % C::kStages), round = static_cast<uint32_t>(it / C::kStages);
-        if (it >= ahead) {
-          if (round > 0 && !bar_wait(&S.empty[st], (round - 1) & 1, &S.failed)) break;
-          bar_expect(&S.full[st], C::kStageBytes);
-          weights(st, tile, k);
-        }
-        rows(st, tile, k);
-        if (++k == k1) k = k0, tile += step;
-      }
-      // nothing may land in shared memory after the CTA is gone, whoever gave up
-      for (int64_t j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
-        bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
     }
     __syncwarp();
-  } else if (warp == 4 * C::kGroups + 1) {
-    // ========================================================== product issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_k(E4M3, kTileN, ROWS);
-      bool ok = true;
-      int64_t it = 0;
-      for (int i = 0; i < mine && ok; ++i) {
-        const uint32_t buf = i & 1;
-        if (i >= 2) ok = bar_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
-        tc_after();
-        for (int k = 0; k < span && ok; ++k, ++it) {
-          const uint32_t st = static_cast<uint32_t>(it % C::kStages);
-          ok = bar_wait(&S.full[st], static_cast<uint32_t>(it / C::kStages) & 1, &S.failed);
-          if (!ok) break;
-          tc_after();
-          const uint32_t w = s32(S.stage[st]), x = w + kTileN * kBlock;
-#pragma unroll
-          for (int j = 0; j < kBlock / 32; ++j)
-            mma_1cta<E4M3>(tmem + buf * ROWS, sdesc128(w + 32 * j), sdesc128(x + 32 * j), id, k + j > 0);
-          commit(&S.empty[st]);
-        }
-        if (ok) commit(&S.acc_full[buf]);
-      }
-      commit(&S.done);
-    }
-    __syncwarp();
-  } else {
-    // ================================================================ epilogue
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int wq = warp & 3, group = warp >> 2;  // the warp's quarter of the lanes; its group, which takes every kGroups-th 32 rows
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
-    for (int i = 0; i < mine; ++i) {
-      const uint32_t buf = i & 1;
-      const int tile = first + i * step, nt = tile / p.m_tiles, m0 = (tile - nt * p.m_tiles) * ROWS;
-      constexpr int kBlocks = ROWS < 32 ? 2 : 4;
-      Epilogue<GATED> e(p, S.rows[warp], nt, wq, lane);
-      bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
-      tc_after();
-#pragma unroll 1
-      for (int col = 8 * kBlocks * group; col < ROWS && m0 + col < p.M; col += 8 * kBlocks * C::kGroups) {
-        float z[4][2 * kBlocks];
-        tm_fragments<kBlocks>(lanes + buf * ROWS + col, z);
-        if (split > 1) {  // [column pair][channel], where the stages were
-          float2* part = reinterpret_cast<float2*>(raw) + (col / 2 + (lane & 3)) * kTileN + 32 * wq + (lane >> 2);
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[4 * b * kTileN + 8 * j] = make_float2(z[j][2 * b], z[j][2 * b + 1]);
-        } else {
-          e.template rows<kBlocks>(m0 + col, z);
-        }
-      }
-      tc_before();
-      bar_arrive(&S.acc_empty[buf]);
-    }
   }
-  if (split > 1) {
-    // ---- the parts of the cluster's CTAs: each adds up its share of the columns
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    if (warp < 4 * C::kGroups && mine > 0) {
-      join_parts<ROWS, GATED>(p, raw, first, rank, split);
-    }
-    __syncwarp();
-    cluster_arrive();  // nobody reads this CTA's memory any more
-    cluster_wait();
-  }
-  // every product has ended before the accumulators are given back, given up or not
-  if (warp == 4 * C::kGroups + 1 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
-  tc_before();
-  __syncthreads();
-  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
-  __syncwarp();
-  if (warp == 4 * C::kGroups + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
-}
-
-// ------------------------------------------------------- the kernel, many rows
-// 256 rows of x and 256 channels: a pair of CTAs forms one product, each with
-// 128 channels of the weights and half of the rows in its shared memory, so that
-// a tile's operands are read once per pair.  An accumulator's 256 columns are in
-// both CTAs' tensor memory, each with its own channels, twice: a tile's results
-// are written while the next one's products run.
-template <int ROWS>
-struct PairCfg {
-  static constexpr int kStageBytes = (kTileN + ROWS / 2) * kBlock;
-  static constexpr int kStages = 200 * 1024 / kStageBytes;
-  static constexpr int kTmemCols = 2 * ROWS;
-  static constexpr int kGroups = 2, kThreads = 128 * kGroups + 64;
 };
+
 // Tiles go through the channels for a group of row tiles at a time, so that what
 // runs at once shares both operands in L2.
 constexpr int kGroup = 10;
@@ -471,154 +267,297 @@ struct TileAt {
   int nt, mt;
   __device__ __forceinline__ TileAt(const Params& p, int tile) {
     const int groups = (p.m_tiles + kGroup - 1) / kGroup, size = (p.m_tiles + groups - 1) / groups;
-    const int n_tiles = p.tiles / p.m_tiles, g = tile / (size * n_tiles), first = g * size;
-    const int here = min(size, p.m_tiles - first), r = tile - first * n_tiles;
+    const int g = tile / (size * p.n_tiles), first = g * size;
+    const int here = min(size, p.m_tiles - first), r = tile - first * p.n_tiles;
     nt = r / here;
     mt = first + r - nt * here;
   }
 };
 
-template <int ROWS, bool E4M3, bool GATED>
-__global__ void __launch_bounds__(PairCfg<ROWS>::kThreads, 1)
-    linear_pair_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, int) {
-  using C = PairCfg<ROWS>;
+// ---- A tile shared by the CTAs (or pairs) of a cluster.  Each finishes a share of
+// the channels: it gets the others' sums of them, and adds them up in the order of
+// the CTAs.  Sums are kept as [half][pair of rows][channel], a pair of rows 64
+// bytes longer than its channels so that four of them lie in different banks.
+template <class C>
+struct Parts {
+  int channels, pitch, bytes;  // of a share: channels; bytes of a pair of rows, and of all
+  __device__ __forceinline__ explicit Parts(int split) : channels(kTileN / split), pitch(channels * 8 + 64), bytes(C::kCols / 2 * pitch) {}
+  // of lane channel c (of the share) and pair of rows q
+  __device__ __forceinline__ uint8_t* at(uint8_t* part, int h, int q, int c) const { return part + (h * (C::kCols / C::kAcc / 2) + q) * pitch + c * 8; }
+};
+
+// Clusters of split CTAs, or split pairs.  A pair's even CTA issues the products
+// of both and counts the copies of both; its odd one copies its half and writes its
+// own channels' results.
+template <int ROWS, bool E4M3, int GATE, bool PAIR>
+__global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GATE, PAIR>::kCtasPerSm)
+    linear_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
+  using C = Cfg<ROWS, GATE, PAIR>;
+  constexpr int kPair = PAIR ? 2 : 1, kCopies = 4 * C::kGroups, kIssuer = kCopies + 2;
   extern __shared__ __align__(1024) uint8_t raw[];
-  Smem<C>& S = *reinterpret_cast<Smem<C>*>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x & 1, first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], 8 * C::kGroups);  // the warps of both epilogues
-    bar_init(&S.done, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    S.failed = 0;
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&w_map) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
+  Head<C>& S = *reinterpret_cast<Head<C>*>(raw + p.stages * C::kStageBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, to the compiler too)
+  const int log2 = (PAIR ? 1 : 0) + p.split / 2;  // CTAs of a cluster (split is 1, 2 or 4)
+  const int in_cluster = blockIdx.x & ((1 << log2) - 1), half = in_cluster % kPair, share = in_cluster / kPair;
+  const int first = blockIdx.x >> log2, step = gridDim.x >> log2;
+  const uint32_t even = in_cluster - half;  // the CTA whose barriers count
+  if (warp == kCopies) {  // (so that its first copies need wait for nothing else)
+    if (lane == 0) {
+      for (int i = 0; i < p.stages; ++i) bar_init(&S.full[i], 2), bar_init(&S.empty[i], 1);  // (full: both kinds of copies)
+      for (int i = 0; i < 2; ++i) bar_init(&S.acc_full[i], 1), bar_init(&S.acc_empty[i], kPair * 4 * C::kGroups);  // warps
+      bar_init(&S.joined, 1), bar_init(&S.done, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      S.failed = 0;
+      if (p.split > 1) bar_expect(&S.joined, (p.split - 1) * Parts<C>(p.split).bytes);
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&w_map) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&x_map) : "memory");
+    }
+    __syncwarp();
+  } else if (warp == kIssuer) {
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
   }
-  __syncwarp();
-  if (warp == 4 * C::kGroups + 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  if (PAIR) {  // the other CTA's barriers are there
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
   }
-  tc_before();
-  __syncthreads();
-  cluster_arrive();  // the other CTA's barriers are there
-  cluster_wait();
+  if (warp == kCopies) asm volatile("barrier.cta.arrive 1, %0;" ::"n"(C::kThreads) : "memory");
+  else asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kThreads) : "memory");
   tc_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = S.tmem;
-  const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
-  if (warp == 4 * C::kGroups) {
-    // ================================================================ producer
-    if (lane == 0) {
-      const int64_t total = static_cast<int64_t>(mine) * p.blocks;
-      auto expect = [&](uint32_t st) {  // both CTAs' copies count at the even one
-        if (rank == 0) bar_expect(&S.full[st], 2 * C::kStageBytes);
+  const uint32_t tmem = warp == kCopies ? 0 : S.tmem;
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.blocks) * share / p.split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (share + 1) / p.split);
+  const int tiles = p.m_tiles * p.n_tiles, mine = first < tiles ? (tiles - first + step - 1) / step : 0;  // tiles of this cluster
+  // columns of the products of a row tile: fewer in one that ends early
+  auto columns = [&](int mt) { return min(ROWS, (p.M - mt * ROWS + 16 * kPair - 1) / (16 * kPair) * (16 * kPair)); };
+  if (warp == kCopies || warp == kCopies + 1) {
+    // ================================================== copies: weights, rows of x
+    // (Two warps: one issuing both took longer for them than a short tile's products.)
+    const int span = k1 - k0;
+    const int64_t total = static_cast<int64_t>(mine) * span;
+    auto produce = [&](uint32_t bytes, bool early, auto copy) {
+      auto expect = [&](int st) {
+        if (half == 0) bar_expect(&S.full[st], kPair * bytes);
       };
-      auto weights = [&](uint32_t st, int nt, int k) {
-        const uint32_t dst = s32(S.stage[st]), b = in_cta(&S.full[st], 0);
-        if (GATED) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tma_3d_pair(dst + i * 32 * kBlock, &w_map, k * kBlock, (2 * nt + rank) * (kTileN / 2) + 16 * i, 0, b);
-        } else {
-          tma_2d_pair(dst, &w_map, k * kBlock, (2 * nt + rank) * kTileN, b);
-        }
-      };
-      auto rows = [&](uint32_t st, int mt, int k) {
-        tma_2d_pair(s32(S.stage[st]) + kTileN * kBlock, &x_map, k * kBlock, mt * ROWS + rank * (ROWS / 2), in_cta(&S.full[st], 0));
-      };
-      int64_t ahead = 0;  // stages whose weights were asked for before the kernel ahead ended
-      if (p.early) {
-        int tile = first, k = 0;
-        for (; ahead < total && ahead < C::kStages; ++ahead) {
-          expect(static_cast<uint32_t>(ahead));
-          weights(static_cast<uint32_t>(ahead), TileAt(p, tile).nt, k);
-          if (++k == p.blocks) k = 0, tile += step;
-        }
-      }
+      // the first round of the ring, a stage per lane: places are worked out side by side
+      const bool fills = lane < p.stages && lane < total;
+      const TileAt start(p, fills ? first + lane / span * step : 0);
+      const int start_k = k0 + lane % span;
+      if (fills) expect(lane);
+      __syncwarp();
+      if (early && fills) copy(lane, start, start_k);  // before the kernel ahead has ended
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      int64_t it = 0;
+      if (!early && fills) copy(lane, start, start_k);
+      __syncwarp();
+      int64_t it = total < p.stages ? total : p.stages;
+      int i = static_cast<int>(it) / span, k = k0 + static_cast<int>(it) % span, st = 0;
+      uint32_t parity = 0;
       bool ok = true;
-      for (int i = 0; i < mine && ok; ++i) {
+      for (; i < mine && ok; ++i, k = k0) {
         const TileAt at(p, first + i * step);
-        for (int k = 0; k < p.blocks; ++k, ++it) {
-          const uint32_t st = static_cast<uint32_t>(it % C::kStages), round = static_cast<uint32_t>(it / C::kStages);
-          if (it >= ahead) {
-            if (round > 0 && !bar_wait(&S.empty[st], (round - 1) & 1, &S.failed)) {
-              ok = false;
-              break;
-            }
+        for (; k < k1; ++k, ++it) {
+          ok = warp_wait(&S.empty[st], parity, &S.failed);
+          if (!ok) break;
+          if (elect()) {
             expect(st);
-            weights(st, at.nt, k);
+            copy(st, at, k);
           }
-          rows(st, at.mt, k);
+          __syncwarp();
+          if (++st == p.stages) st = 0, parity ^= 1;
         }
       }
       // nothing may land in either CTA's memory after it is gone, whoever gave up
-      if (rank == 0)
-        for (int64_t j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
-          bar_drain(&S.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1);
+      if (half == 0 && lane == 0)
+        for (int64_t j = it > p.stages ? it - p.stages : 0; j < it; ++j)
+          bar_drain(&S.full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1);
+      __syncwarp();
+    };
+    if (warp == kCopies) {
+      produce(C::kWeightBytes, p.early, [&](int st, const TileAt& at, int k) {
+        const uint32_t dst = s32(raw) + st * C::kStageBytes;
+        const int x = k * kBlock, y = (kPair * at.nt + half) * C::kChannels;
+        if constexpr (GATE == kInterleaved) {
+          static_assert(PAIR, "the map has the halves as a dimension");
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tma_3d_pair(dst + i * 32 * kBlock, &w_map, x, y + 16 * i, 0, in_cta(&S.full[st], even));
+        } else {
+#pragma unroll
+          for (int h = 0; h < C::kAcc; ++h) {
+            if constexpr (PAIR) tma_2d_pair(dst + h * kTileN * kBlock, &w_map, x, y + h * p.width, in_cta(&S.full[st], even));
+            else tma_2d(dst + h * kTileN * kBlock, &w_map, x, y + h * p.width, &S.full[st]);
+          }
+        }
+      });
+    } else {
+      produce(C::kXRows * kBlock, false, [&](int st, const TileAt& at, int k) {
+        const uint32_t dst = s32(raw) + st * C::kStageBytes + C::kWeightBytes;
+        const int x = k * kBlock, y = at.mt * ROWS + (PAIR ? half * columns(at.mt) / 2 : 0);
+        if constexpr (PAIR) tma_2d_pair(dst, &x_map, x, y, in_cta(&S.full[st], even));
+        else tma_2d(dst, &x_map, x, y, &S.full[st]);
+      });
     }
-    __syncwarp();
-  } else if (warp == 4 * C::kGroups + 1) {
+  } else if (warp == kIssuer) {
     // ========================================================== product issuer
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t id = idesc_k(E4M3, 2 * kTileN, ROWS);
+    if (half == 0) {
       bool ok = true;
-      int64_t it = 0;
+      int st = 0;
+      uint32_t round = 0;
+      const uint64_t desc = sdesc128(s32(raw));
+      auto signal = [&](uint64_t* b) {
+        if constexpr (PAIR) commit_both(b, even);
+        else commit(b);
+      };
       for (int i = 0; i < mine && ok; ++i) {
-        const uint32_t buf = i & 1;
-        if (i >= 2) ok = bar_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
+        const uint32_t buf = i & 1, id = idesc_k(E4M3, kPair * kTileN, columns(TileAt(p, first + i * step).mt));
+        if (i >= 2) ok = warp_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
         tc_after();
-        for (int k = 0; k < p.blocks && ok; ++k, ++it) {
-          const uint32_t st = static_cast<uint32_t>(it % C::kStages);
-          ok = bar_wait(&S.full[st], static_cast<uint32_t>(it / C::kStages) & 1, &S.failed);
+        for (int k = k0; k < k1 && ok; ++k) {
+          ok = warp_wait(&S.full[st], round & 1, &S.failed);
           if (!ok) break;
           tc_after();
-          const uint32_t w = s32(S.stage[st]), x = w + kTileN * kBlock;
+          if (elect()) {
+            // (descriptors count in 16 bytes, and no address carries out of their field)
+            const uint64_t w = desc + static_cast<uint32_t>(st * (C::kStageBytes / 16)), x = w + C::kWeightBytes / 16;
 #pragma unroll
-          for (int j = 0; j < kBlock / 32; ++j)
-            mma_2cta<E4M3>(tmem + buf * ROWS, sdesc128(w + 32 * j), sdesc128(x + 32 * j), id, k + j > 0);
-          commit_both(&S.empty[st]);
+            for (int j = 0; j < kBlock / 32; ++j)
+#pragma unroll
+              for (int h = 0; h < C::kAcc; ++h) {
+                const uint64_t a = w + h * kTileN * kBlock / 16 + 2 * j, b = x + 2 * j;
+                const uint32_t d = tmem + buf * C::kCols + h * ROWS;
+                if constexpr (PAIR) mma_2cta<E4M3>(d, a, b, id, k > k0 || j > 0);
+                else mma_1cta<E4M3>(d, a, b, id, k > k0 || j > 0);
+              }
+            signal(&S.empty[st]);
+            if (k == k1 - 1) signal(&S.acc_full[buf]);
+          }
+          __syncwarp();
+          if (++st == p.stages) st = 0, ++round;
         }
-        if (ok) commit_both(&S.acc_full[buf]);
       }
-      commit_both(&S.done);
+      if (elect()) signal(&S.done);
     }
     __syncwarp();
   } else {
-    // ================================================================ epilogue
+    // ================================================================= results
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int wq = warp & 3, group = warp >> 2;  // the warp's quarter of the lanes; its group, which takes every kGroups-th 32 rows
+    const int wq = warp & 3, group = warp >> 2;  // the warp's quarter of the lanes; its group, which takes every kGroups-th block of rows
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    const Parts<C> part(p.split);
+    uint8_t* const sent = raw + p.split * part.bytes;  // what the others send
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
       const TileAt at(p, first + i * step);
       const int m0 = at.mt * ROWS;
-      Epilogue<GATED> e(p, S.rows[warp], 2 * at.nt + rank, wq, lane);
-      bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);
+      using E = Epilogue<GATE, C::kUnroll>;
+      const int channel0 = (kPair * at.nt + half) * C::kChannels;
+      E e(p, S.rows[warp], channel0 + wq * E::kWidth, lane);
+      constexpr int kStep = 8 * C::kUnroll;
+      uint4 ahead[E::kSets] = {};
+      if (p.split == 1) e.fetch(m0 + kStep * group, ahead);
+      if (p.x_scale && lane < ROWS / 32 + 1 && m0 + 32 * lane < p.M) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.x_scale + m0 + 32 * lane));
+      if (lane == 0) bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);  // (one lane: polls are not free for the issuer)
+      __syncwarp();
       tc_after();
+      if (p.split == 1) {
 #pragma unroll 1
-      for (int col = 32 * group; col < ROWS && m0 + col < p.M; col += 32 * C::kGroups) {
-        float z[4][8];
-        tm_fragments<4>(lanes + buf * ROWS + col, z);
-        e.template rows<4>(m0 + col, z);
+        for (int col = kStep * group; col < ROWS && m0 + col < p.M; col += kStep * C::kGroups) {
+          float z[C::kUnroll][4][2], u[C::kUnroll][4][2];
+          tm_fragments(lanes + buf * C::kCols + col, z);
+          if constexpr (GATE == kTwoSums) tm_fragments(lanes + buf * C::kCols + ROWS + col, u);
+          uint4 res[E::kSets];
+#pragma unroll
+          for (int i = 0; i < E::kSets; ++i) res[i] = ahead[i];
+          if (col + kStep * C::kGroups < ROWS) e.fetch(m0 + col + kStep * C::kGroups, ahead);
+          e.rows(m0 + col, z, u, res);
+        }
+      } else {  // this CTA's sums, where the stages were
+        uint8_t* const to = raw + (32 * wq / part.channels) * part.bytes;
+#pragma unroll 1
+        for (int col = 8 * group; col < ROWS && m0 + col < p.M; col += 8 * C::kGroups)
+#pragma unroll
+          for (int h = 0; h < C::kAcc; ++h) {
+            float z[1][4][2];
+            tm_fragments(lanes + buf * C::kCols + h * ROWS + col, z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float2*>(part.at(to, h, col / 2 + (lane & 3), 32 * wq % part.channels + (lane >> 2) + 8 * j)) = make_float2(z[0][j][0], z[0][j][1]);
+          }
       }
       tc_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_at(in_cta(&S.acc_empty[buf], 0));
+      if (lane == 0) {
+        if constexpr (PAIR) bar_arrive_at(in_cta(&S.acc_empty[buf], even));
+        else bar_arrive(&S.acc_empty[buf]);
+      }
+      if constexpr (GATE == kInterleaved) continue;  // (never split)
+      else if (p.split > 1) {  // (this cluster's only tile)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        cluster_arrive();  // its stages are free
+        cluster_wait();    // and so are the others', and all of its own sums are in place
+        if (tid < p.split && tid != share) {
+          const uint32_t cta = tid * kPair + half;
+          send(in_cta(sent + share * part.bytes, cta), raw + tid * part.bytes, part.bytes, in_cta(&S.joined, cta));
+        }
+        __syncwarp();
+        // blocks of 32 channels and a few rows, a warp each
+        const int wide = part.channels / 32, cb = warp % wide * 32;
+        using Own = Epilogue<GATE, 1>;
+        const Own own(p, S.rows[warp], channel0 + share * part.channels + cb, lane);
+        if (lane == 0) bar_wait(&S.joined, 0, &S.failed);
+        __syncwarp();
+#pragma unroll 1
+        for (int block = warp; block < wide * (ROWS / 8); block += 4 * C::kGroups) {
+          const int col = block / wide * 8;
+          if (m0 + col >= p.M) break;
+          uint4 res[1] = {};
+          own.fetch(m0 + col, res);
+          float s[2][1][4][2] = {};
+#pragma unroll 1
+          for (int r = 0; r < p.split; ++r)
+#pragma unroll
+            for (int h = 0; h < C::kAcc; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 v = *reinterpret_cast<const float2*>(
+                    part.at((r == share ? raw : sent) + r * part.bytes, h, col / 2 + (lane & 3), cb + (lane >> 2) + 8 * j));
+                s[h][0][j][0] += v.x, s[h][0][j][1] += v.y;
+              }
+          own.rows(m0 + col, s[0], s[1], res);
+        }
+      }
     }
   }
-  // every product has ended, in both CTAs' memory, before either leaves, given up or not
-  if (warp == 4 * C::kGroups + 1 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  if (p.split > 1 && warp >= 4 * C::kGroups) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+  // every product has ended before the accumulators are given back, and in a pair before either CTA leaves, given up or not
+  if (warp == kIssuer && lane == 0 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
+  __syncwarp();
   tc_before();
   __syncthreads();
   if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
   __syncwarp();
-  cluster_arrive();
-  cluster_wait();
-  if (warp == 4 * C::kGroups + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+  // (what a CTA sent is read from its memory until the others have it)
+  if (PAIR || p.split > 1) {
+    cluster_arrive();
+    cluster_wait();
+    // where sums were given up on, they may still be on their way here
+    if (p.split > 1 && S.failed && tid < 32) bar_drain(&S.joined, 0);
+  }
+  if (warp == kIssuer) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kTmemCols));
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -629,28 +568,31 @@ std::mutex g_mutex;
 int g_sms[64];
 EncodeFn g_encode;
 
-using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap, int);
+using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap);
+// What a kernel takes, with and without the gate, for bf16 and e4m3.
 struct Variant {
-  int rows, box;     // rows of a tile; rows of x per copy
-  bool pair;
-  Kernel kernel[4];  // bf16, e4m3, and both gated
-  size_t smem;
+  int rows, x_rows, channels;  // rows of a tile; of x per copy; channels of out per tile
+  bool pair, interleaved;
+  Kernel kernel[2];  // bf16, e4m3
   int threads;
+  int stage_bytes, part_bytes, head_bytes;
+  float start, block, join;  // us, see plan_of
 };
-template <int ROWS>
-Variant single() {
-  using M = Smem<Cfg<ROWS>>;
-  static_assert(sizeof(M) <= 227 * 1024 && ROWS * kTileN * 4 <= sizeof(M::stage), "shared memory");
-  return {ROWS, ROWS, false, {linear_kernel<ROWS, false, false>, linear_kernel<ROWS, true, false>, linear_kernel<ROWS, false, true>, linear_kernel<ROWS, true, true>}, sizeof(M), Cfg<ROWS>::kThreads};
+template <int ROWS, int GATE, bool PAIR>
+Variant variant(float start, float block, float join) {
+  using C = Cfg<ROWS, GATE, PAIR>;
+  return {ROWS, C::kXRows, C::kChannels * (PAIR ? 2 : 1), PAIR, GATE == kInterleaved, {linear_kernel<ROWS, false, GATE, PAIR>, linear_kernel<ROWS, true, GATE, PAIR>},
+          C::kThreads, C::kStageBytes, C::kPartBytes, static_cast<int>(sizeof(Head<C>)), start, block, join};
 }
-template <int ROWS>
-Variant pair() {
-  using M = Smem<PairCfg<ROWS>>;
-  static_assert(sizeof(M) <= 227 * 1024, "shared memory");
-  return {ROWS, ROWS / 2, true, {linear_pair_kernel<ROWS, false, false>, linear_pair_kernel<ROWS, true, false>, linear_pair_kernel<ROWS, false, true>, linear_pair_kernel<ROWS, true, true>}, sizeof(M), PairCfg<ROWS>::kThreads};
-}
-const Variant kVariants[] = {single<16>(), single<32>(), single<64>(), single<128>(), pair<256>()};
-const Variant& variant_of(int M) { return kVariants[M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : M <= 128 ? 3 : 4]; }
+constexpr int kPlain = 6, kGatedVariants = 5;
+const Variant kVariants[kPlain + kGatedVariants] = {
+    variant<16, kNoGate, false>(4.5f, .146f, .6f), variant<32, kNoGate, false>(4.7f, .17f, 1.f),
+    variant<64, kNoGate, false>(5.3f, .22f, 1.6f), variant<128, kNoGate, false>(6.f, .246f, 4.f),
+    variant<128, kNoGate, true>(6.3f, .195f, 3.f), variant<256, kNoGate, true>(7.2f, .26f, 0.f),
+    variant<16, kTwoSums, false>(4.8f, .26f, 1.f), variant<32, kTwoSums, false>(5.f, .28f, 1.5f),
+    variant<64, kTwoSums, false>(5.8f, .33f, 2.5f), variant<128, kTwoSums, false>(7.f, .4f, 0.f),
+    variant<256, kInterleaved, true>(8.f, .3f, 0.f)};
+constexpr int kSmemLimit = 227 * 1024;  // of a CTA
 
 cudaError_t setup(int* sms) {
   int dev = 0;
@@ -667,13 +609,50 @@ cudaError_t setup(int* sms) {
     g_encode = reinterpret_cast<EncodeFn>(fn);
     for (const Variant& v : kVariants)
       for (const Kernel k : v.kernel)
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem))) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit)) != cudaSuccess) return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     g_sms[dev] = n;
   }
   *sms = g_sms[dev];
   return cudaSuccess;
+}
+
+// What a call runs with: the variant, CTAs (or pairs) that share a tile, ring depth.
+struct Plan {
+  const Variant* variant;
+  int split, stages;
+};
+int64_t tiles_of(int n, int size) { return (static_cast<int64_t>(n) + size - 1) / size; }
+// The variant and split with the least expected time, in us: what a launch takes
+// from its start to its first product and from its last to its results, waves of
+// tiles at a time per block of k each, the weights from HBM meanwhile, and what joining takes each time a tile is shared by twice as many.  Measured on
+// these shapes, with e4m3 (the other choice in brackets): 4 x 4,608 x 2,048 6.2 us in
+// two parts (6.8 whole), 64 x 4,096 x 4,096 10.5 in two and 10.2 in four (12.3 whole),
+// 64 x 18,432 x 6,144 22.4 whole (31.7 in two); 256 x 2,048 x 2,048 8.4 with pairs and
+// tiles of 128 rows (11.5 with 256, 9.0 with 64 rows and one CTA); bf16, 512 x 4,096 x
+// 4,096, 18.9 with pairs and 128 rows (23.6 with 256, 21.8 with 128 and one CTA).
+Plan plan_of(int M, int width, int blocks, bool gated, double bytes, int sms) {
+  Plan best{nullptr, 1, 0};
+  double least = 0;
+  for (int i = gated ? kPlain : 0; i < (gated ? kPlain + kGatedVariants : kPlain); ++i) {
+    const Variant& v = kVariants[i];
+    const int most = std::min((kSmemLimit - v.head_bytes) / v.stage_bytes, kMaxStages);
+    const int64_t tiles = tiles_of(width, v.channels) * tiles_of(M, v.rows), at_once = v.pair ? sms / 2 : sms;
+    for (int split = 1, log2 = 0; split <= kMaxSplit; split *= 2, ++log2) {
+      if (split > 1 && (v.interleaved || tiles * split > at_once || split > blocks || 2 * v.part_bytes > most * v.stage_bytes)) break;
+      const int64_t waves = (tiles * split + at_once - 1) / at_once;
+      // (of the waves' time and the weights' the shorter hides behind the longer but for some three tenths)
+      const double compute = static_cast<double>(waves) * tiles_of(blocks, split) * v.block, memory = bytes / 6.5e6;
+      const double us = v.start + std::max(compute, memory) + .3 * std::min(compute, memory) + log2 * v.join;
+      if (best.variant && us >= least) continue;
+      // no more stages than there is to copy, but room for the sums of a tile in parts
+      const int64_t copies = waves * tiles_of(blocks, split), sums = split > 1 ? tiles_of(2 * v.part_bytes, v.stage_bytes) : 1;
+      best = {&v, split, static_cast<int>(std::min<int64_t>(most, std::max(copies, sums)))};
+      least = us;
+    }
+  }
+  return best;
 }
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
@@ -715,22 +694,30 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const cuuint64_t k_bytes = static_cast<cuuint64_t>(a->K) * size;
   const cuuint64_t w_pitch = static_cast<cuuint64_t>(a->weight_row_stride) * size, x_pitch = static_cast<cuuint64_t>(a->x_row_stride) * size;
   const cuuint32_t ones[3] = {1, 1, 1};
-  const Variant& v = variant_of(a->M);
+  const int blocks = static_cast<int>((k_bytes + kBlock - 1) / kBlock);
+  const Plan plan = plan_of(a->M, width, blocks, gated, static_cast<double>(k_bytes) * a->N, sms);
+  const Variant& v = *plan.variant;
   CUtensorMap w_map, x_map;
   CUresult r;
-  {
-    // gated: the two halves are a dimension of their own, a copy takes 16 rows of each
+  if (v.interleaved) {  // a copy takes 16 channels of each half
     const cuuint64_t dims[3] = {k_bytes, static_cast<cuuint64_t>(width), 2};
     const cuuint64_t strides[2] = {w_pitch, w_pitch * static_cast<cuuint64_t>(width)};
-    const cuuint32_t box[3] = {kBlock, static_cast<cuuint32_t>(gated ? 16 : kTileN), 2};
-    r = g_encode(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 3 : 2, const_cast<void*>(a->weight), dims, strides, box, ones,
+    const cuuint32_t box[3] = {kBlock, 16, 2};
+    r = g_encode(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a->weight), dims, strides, box, ones,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t dims[2] = {k_bytes, static_cast<cuuint64_t>(a->N)};
+    const cuuint64_t strides[1] = {w_pitch};
+    const cuuint32_t box[2] = {kBlock, kTileN};
+    r = g_encode(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a->weight), dims, strides, box, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   if (r == CUDA_SUCCESS) {
     const cuuint64_t dims[2] = {k_bytes, static_cast<cuuint64_t>(a->M)};
     const cuuint64_t strides[1] = {x_pitch};
-    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(v.box)};
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(v.x_rows)};
     r = g_encode(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a->x), dims, strides, box, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -738,25 +725,21 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
   Params p{};
   p.M = a->M, p.N = a->N, p.K = a->K, p.width = width;
-  const int tile_width = (gated ? kTileN / 2 : kTileN) * (v.pair ? 2 : 1);
-  const int64_t m_tiles = (static_cast<int64_t>(a->M) + v.rows - 1) / v.rows, n_tiles = (static_cast<int64_t>(width) + tile_width - 1) / tile_width;
-  if (m_tiles * n_tiles > 0x7fffffff / kMaxSplit) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
-  p.m_tiles = static_cast<int>(m_tiles), p.tiles = static_cast<int>(m_tiles * n_tiles);
-  p.blocks = static_cast<int>((k_bytes + kBlock - 1) / kBlock);
+  const int64_t m_tiles = tiles_of(a->M, v.rows), n_tiles = tiles_of(width, v.channels);
+  if (m_tiles * n_tiles > 0x7fffffff / 16) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
+  p.m_tiles = static_cast<int>(m_tiles), p.n_tiles = static_cast<int>(n_tiles), p.blocks = blocks;
+  p.split = plan.split, p.stages = plan.stages;
   p.act = a->activation, p.out_f32 = f32, p.early = a->flags & KDA_LINEAR_EARLY_WEIGHT;
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
   p.residual = a->residual, p.res_stride = a->residual_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
   p.err = a->err_flag;
   p.vec_out = !f32 && !misaligned(a->out, 15) && a->out_row_stride % 8 == 0;
   p.vec_res = !misaligned(a->residual, 15) && a->residual_row_stride % 8 == 0;
-  // few tiles: up to eight CTAs share one, while all of them are resident and each has a block of k
-  int split = 1;
-  if (!v.pair)
-    while (split < kMaxSplit && static_cast<int64_t>(p.tiles) * split * 2 <= sms && split * 2 <= p.blocks) split *= 2;
-  const int cluster = v.pair ? 2 : split, resident = v.pair ? sms / 2 : sms;
-  const unsigned grid = static_cast<unsigned>((split > 1 || p.tiles < resident ? p.tiles : resident) * cluster);
-  e = kda_internal_launch_cluster(v.kernel[(gated ? 2 : 0) + (e4m3 ? 1 : 0)], dim3(grid), dim3(static_cast<unsigned>(v.threads)), v.smem, stream,
-                                  static_cast<unsigned>(cluster), p, w_map, x_map, split);
+  const int cluster = plan.split * (v.pair ? 2 : 1);
+  const int64_t clusters = plan.split > 1 ? m_tiles * n_tiles : std::min<int64_t>(m_tiles * n_tiles, sms / cluster);
+  e = kda_internal_launch_cluster(v.kernel[e4m3], dim3(static_cast<unsigned>(clusters * cluster)), dim3(static_cast<unsigned>(v.threads)),
+                                  static_cast<size_t>(v.head_bytes + plan.stages * v.stage_bytes), stream,
+                                  static_cast<unsigned>(cluster), p, w_map, x_map);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }

@@ -48,6 +48,19 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, int* fail
     }
   }
 }
+// One lane of a warp that is together.  (Code that whole warps run, with one lane
+// elected for an instruction, keeps its operands in uniform registers: a product
+// takes 40 cycles to issue that way, 60 in code of one lane, and a wait ahead of
+// four of them 50 more against 250.)
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// bar_wait for a warp that is together, which leaves it together.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* failed) {
+  return __all_sync(0xffffffffu, bar_wait(b, parity, failed));
+}
 // The same without regard to others that gave up: for copies already on their way.
 __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
   uint64_t t0, now;
@@ -91,12 +104,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(s32(b))
       : "memory");
 }
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* b) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(s32(b))
-      : "memory");
-}
 // ---- two CTAs as one: products of 256 rows whose halves, and those of the
 // other operand, lie in both CTAs' shared memory, at the same places; the even
 // CTA issues them and its barriers count the copies of both.
@@ -108,10 +115,16 @@ __device__ __forceinline__ uint32_t in_cta(const void* ptr, uint32_t rank) {
 __device__ __forceinline__ void bar_arrive_at(uint32_t b) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
-__device__ __forceinline__ void commit_both(uint64_t* b) {
+// Shared memory of this CTA to that of another of the cluster, whose barrier counts the bytes.
+__device__ __forceinline__ void send(uint32_t dst, const void* src, uint32_t bytes, uint32_t b) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(s32(src)), "r"(bytes), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ void commit_both(uint64_t* b, uint32_t even) {  // at the same place in the even CTA and the next
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s32(b)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3u << even))
       : "memory");
 }
 template <bool E4M3>
@@ -143,24 +156,32 @@ __device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(b)
       : "memory");
 }
-// 8 * BLOCKS consecutive columns of this warp's 32 lanes as fragments: thread i
-// gets of block b, in r[j][2b], r[j][2b + 1], lane i / 4 + 8 j, columns 8 b +
-// 2 (i % 4) and the next.  The load writes the registers of all 32 threads, so
-// the warp has to be together; load and wait are one statement, so that nothing
-// can come between them.
+// 8 BLOCKS consecutive columns of this warp's 32 lanes as fragments: thread i gets,
+// in r[b][j], lane i / 4 + 8 j, columns 8 b + 2 (i % 4) and the next.  The load
+// writes the registers of all 32 threads, so the warp has to be together; load and
+// wait are one statement, so that nothing can come between them.
 template <int BLOCKS>
-__device__ __forceinline__ void tm_fragments(uint32_t addr, float (&r)[4][2 * BLOCKS]) {
-  static_assert(BLOCKS == 2 || BLOCKS == 4, "16 or 32 columns");
+__device__ __forceinline__ void tm_fragments(uint32_t addr, float (&r)[BLOCKS][4][2]) {
+  static_assert(BLOCKS == 1 || BLOCKS == 2 || BLOCKS == 4, "8, 16 or 32 columns");
   __syncwarp();
   const uint32_t up = addr + (16u << 16);  // the upper 16 lanes
-  if constexpr (BLOCKS == 2) {
+  if constexpr (BLOCKS == 1) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%9];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0][0][0]), "=f"(r[0][0][1]), "=f"(r[0][1][0]), "=f"(r[0][1][1]), "=f"(r[0][2][0]), "=f"(r[0][2][1]),
+          "=f"(r[0][3][0]), "=f"(r[0][3][1])
+        : "r"(addr), "r"(up)
+        : "memory");
+  } else if constexpr (BLOCKS == 2) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
-          "=f"(r[1][3]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]), "=f"(r[2][3]),
-          "=f"(r[3][2]), "=f"(r[3][3])
+        : "=f"(r[0][0][0]), "=f"(r[0][0][1]), "=f"(r[0][1][0]), "=f"(r[0][1][1]), "=f"(r[1][0][0]), "=f"(r[1][0][1]),
+          "=f"(r[1][1][0]), "=f"(r[1][1][1]), "=f"(r[0][2][0]), "=f"(r[0][2][1]), "=f"(r[0][3][0]), "=f"(r[0][3][1]),
+          "=f"(r[1][2][0]), "=f"(r[1][2][1]), "=f"(r[1][3][0]), "=f"(r[1][3][1])
         : "r"(addr), "r"(up)
         : "memory");
   } else {
@@ -169,11 +190,12 @@ __device__ __forceinline__ void tm_fragments(uint32_t addr, float (&r)[4][2 * BL
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
         "[%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0][0]), "=f"(r[0][1]), "=f"(r[1][0]), "=f"(r[1][1]), "=f"(r[0][2]), "=f"(r[0][3]), "=f"(r[1][2]),
-          "=f"(r[1][3]), "=f"(r[0][4]), "=f"(r[0][5]), "=f"(r[1][4]), "=f"(r[1][5]), "=f"(r[0][6]), "=f"(r[0][7]),
-          "=f"(r[1][6]), "=f"(r[1][7]), "=f"(r[2][0]), "=f"(r[2][1]), "=f"(r[3][0]), "=f"(r[3][1]), "=f"(r[2][2]),
-          "=f"(r[2][3]), "=f"(r[3][2]), "=f"(r[3][3]), "=f"(r[2][4]), "=f"(r[2][5]), "=f"(r[3][4]), "=f"(r[3][5]),
-          "=f"(r[2][6]), "=f"(r[2][7]), "=f"(r[3][6]), "=f"(r[3][7])
+        : "=f"(r[0][0][0]), "=f"(r[0][0][1]), "=f"(r[0][1][0]), "=f"(r[0][1][1]), "=f"(r[1][0][0]), "=f"(r[1][0][1]),
+          "=f"(r[1][1][0]), "=f"(r[1][1][1]), "=f"(r[2][0][0]), "=f"(r[2][0][1]), "=f"(r[2][1][0]), "=f"(r[2][1][1]),
+          "=f"(r[3][0][0]), "=f"(r[3][0][1]), "=f"(r[3][1][0]), "=f"(r[3][1][1]), "=f"(r[0][2][0]), "=f"(r[0][2][1]),
+          "=f"(r[0][3][0]), "=f"(r[0][3][1]), "=f"(r[1][2][0]), "=f"(r[1][2][1]), "=f"(r[1][3][0]), "=f"(r[1][3][1]),
+          "=f"(r[2][2][0]), "=f"(r[2][2][1]), "=f"(r[2][3][0]), "=f"(r[2][3][1]), "=f"(r[3][2][0]), "=f"(r[3][2][1]),
+          "=f"(r[3][3][0]), "=f"(r[3][3][1])
         : "r"(addr), "r"(up)
         : "memory");
   }

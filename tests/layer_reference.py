@@ -37,12 +37,14 @@ def linear(x, weight, x_scale=None, weight_scale=None, bias=None, residual=None,
     err = mag * (x.shape[1] / 16 + 1) * 2.0 ** -22
     half = weight.shape[0] // 2
     sig = torch.sigmoid(y)
-    # activations: their slopes are below 1.13; the exponential is off by 2^-18, erfc by 2^-20, relative to the result
+    # activations: their slopes are below 1.13; silu's exponential is off by 2^-18; gelu's erfc by 1.2e-7 < 2^-22, its
+    # exponent -y^2 / 2 and what is added to it (below 2) by three roundings of their sum, the exponential of the exact
+    # exponent's rounded multiple of log2 e by as much again, and four more roundings: all relative to the result
     if activation == "silu":
         y, err = y * sig, 1.13 * err + (y * sig).abs() * 2.0 ** -18
     elif activation == "gelu":
         g = y * 0.5 * torch.special.erfc(-y / math.sqrt(2))
-        y, err = g, 1.13 * err + g.abs() * 2.0 ** -20 + 2.0 ** -126
+        y, err = g, 1.13 * err + g.abs() * (2.0 ** -20 + (y.square() / 2 + 2) * 2.0 ** -21) + 2.0 ** -126
     elif activation == "silu_gated":
         g = (y * sig)[:, :half]
         e = 1.13 * err[:, :half] + g.abs() * 2.0 ** -18
