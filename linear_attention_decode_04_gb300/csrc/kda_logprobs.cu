@@ -1,32 +1,44 @@
 // kda_logprobs.cu -- log probabilities of given tokens, entropy and likeliest
 // alternatives (definition in include/kda_logprobs.h).
 //
-// One pass over the logits: every thread keeps the largest logit m of its
-// elements, s = sum e^(x - m) and t = sum (x - m) e^(x - m), from which lse and
-// entropy follow (lse = m + log s, entropy = log s - t / s), and counts the
-// logits ahead of the given token's.  The top alternatives cost next to nothing
-// in that pass: the num_top-th largest of the threads' largest elements bounds
-// the num_top-th largest element from below, and only the threads whose largest
-// element reaches it can hold one that does.  Those (at most num_top of a CTA)
-// have their elements read once more, out of L2.
+// One pass over the logits, which a warp of its own copies to shared memory in a
+// ring: every thread keeps the largest logit m of its elements, s = sum 2^y and t =
+// sum y 2^y with y = x log2 e - c and c = m log2 e as rounded, from which lse and
+// entropy follow (lse = ln 2 (c + log2 s), entropy = ln 2 (log2 s - t / s)).  y is one
+// fused operation, so neither c's rounding nor a large logit costs digits.  The top
+// alternatives cost little beside that pass: the num_top-th largest of the threads'
+// largest logits bounds the num_top-th largest logit from below, and of a thread's
+// elements, in two halves, only those can reach it whose half's largest does.  The
+// threads know where that one is and what comes next in the half, so that some num_top
+// pieces of 32 bytes are read once more; the whole half only where two of its pieces
+// reach the bound.
 //
-// Orders are those of 64-bit keys, the logit's bits in an order-preserving
-// form above the complement of the index: keys differ, so ties go to the lower
-// index and results do not depend on how a row was split.
+// Orders are those of 64-bit keys, the logit's bits in an order-preserving form
+// above the complement of the index: keys differ, so ties go to the lower index and
+// results do not depend on how a row was split.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "kda_internal.h"
 #include "kda_logprobs.h"
+#include "kda_tc.cuh"
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kAllThreads = kThreads + 32;  // that sum, and a warp that copies
+constexpr int kVecs = 4;                   // 16-byte pieces of a stage, per thread
+constexpr int kStageBytes = kThreads * kVecs * 16, kStages = 3;
+constexpr int kCtasPerSm = 4;
+constexpr int kHalves = 2;                 // of a thread's elements, by their place in a batch
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
-constexpr int kList = 1024;                // elements that a CTA lists as candidates
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kList = 1024;                 // elements that a CTA lists as candidates
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLeast = -200.f;           // of y: 2^y is 0 in fp32 from -150 on, and y 2^y is too where x is -infinity
+constexpr float kFar = 1e7f;               // from here on m log2 e is rounded by whole numbers: elements are taken relative to m itself
 
 struct Params {
   int R, V, top;
@@ -46,15 +58,25 @@ struct Sums {
   float m, s, t;
 };
 struct Shared {
-  uint64_t keys[kWarps][32];
-  uint64_t list[kList];
-  uint64_t best[kMaxCluster][kMaxTop];     // every CTA's alternatives, in the cluster's first CTA
-  Sums sums[kMaxCluster];
-  int count[kMaxCluster];
+  union {
+    alignas(128) uint8_t stage[kStages][kStageBytes];
+    struct {                               // when the row has been seen
+      uint64_t list[kList];
+      int spot[kThreads * kHalves];        // pieces that are read again: the first vector of each
+      int16_t half[kThreads * kHalves];    // halves that are
+    };
+  };
+  uint64_t full[kStages], empty[kStages];
+  uint64_t best[kMaxTop];
+  uint64_t round[kWarps + 1];
   Sums warp_sums[kWarps];
   int warp_count[kWarps];
-  int owner[kMaxTop];                      // threads whose elements are read again
-  int owners, listed;
+  uint32_t warp_bound[kWarps];
+  int spots, halves, listed, failed;
+  // in a cluster's first CTA: what every CTA has of the row
+  uint64_t part_top[kMaxCluster][kMaxTop];
+  Sums part_sums[kMaxCluster];
+  int part_count[kMaxCluster];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -62,30 +84,81 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = a.m == r.m ? 0.f : a.m - r.m, db = b.m == r.m ? 0.f : b.m - r.m;
-  const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);  // 0 from -infinity, where s and t are 0
-  r.s = a.s * fa + b.s * fb;
-  r.t = (a.t + fmaxf(da, -1e30f) * a.s) * fa + (b.t + fmaxf(db, -1e30f) * b.s) * fb;
+// Two floats in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ Sums warp_join(Sums v) {
+__device__ __forceinline__ float2 both(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float one_from(float x, float limit) {  // 1 where x >= limit, else 0
+  float r;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(limit));
+  return r;
+}
+__device__ __forceinline__ float float_above(float x) {  // the next higher float; NaN, which nothing reaches, of infinity
+  const int b = __float_as_int(x + 0.f);
+  return __int_as_float(b >= 0 ? b + 1 : b - 1);
+}
+__device__ __forceinline__ float at_least(float y) {  // NaN stays NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kLeast));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Sums whose largest is m are relative to c = m log2 e as rounded where |m| < kFar, to m log2 e itself further out, to 0
+// where there is nothing.  (c is rounded wherever it is used: fused into a difference it would be another one.)
+__device__ __forceinline__ bool is_near(float m) { return fabsf(m) < kFar || m == -INFINITY; }
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e); }
+// log2 of an element relative to that, and of m itself.
+__device__ __forceinline__ float relative(float x, float m) { return is_near(m) ? fmaf(x, kLog2e, -reference(m)) : (x - m) * kLog2e; }
+__device__ __forceinline__ float residue(float m) { return fabsf(m) < kFar ? fmaf(m, kLog2e, -reference(m)) : 0.f; }
+// The exponent that takes sums from largest m to largest `to` >= m.
+__device__ __forceinline__ float shift(float m, float to) {
+  if (m == to) return 0.f;
+  return m > -INFINITY ? fmaxf(fmaf(m - to, kLog2e, residue(to) - residue(m)), kLeast) : kLeast;
+}
+__device__ __forceinline__ Sums scaled(Sums a, float to) {
+  const float y = shift(a.m, to), f = ex2(y);
+  return Sums{to, a.s * f, (a.t + y * a.s) * f};
+}
+// Over the warp's lanes, in all of them.
+__device__ __forceinline__ Sums warp_sum(Sums v) {
+  float m = v.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  v = scaled(v, m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Sums w;
-    w.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-    w.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-    w.t = __shfl_xor_sync(0xffffffffu, v.t, o);
-    v = join(v, w);
+    v.s += __shfl_xor_sync(0xffffffffu, v.s, o);
+    v.t += __shfl_xor_sync(0xffffffffu, v.t, o);
   }
   return v;
 }
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // (-0 and 0 are equal)
+  return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
 __device__ __forceinline__ uint64_t key_of(float x, int i) {
-  uint32_t b = __float_as_uint(x + 0.f);   // (-0 and 0 are equal)
-  b ^= b >> 31 ? 0xffffffffu : 0x80000000u;
-  return static_cast<uint64_t>(b) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
+  return static_cast<uint64_t>(order_of(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
 }
 __device__ __forceinline__ float logit_of(uint64_t key) {
   uint32_t b = static_cast<uint32_t>(key >> 32);
@@ -93,51 +166,30 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
   return __uint_as_float(b);
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
-__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-// One step of a bitonic network over the warp's lanes.
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int distance, bool descending, int lane) {
-  const uint64_t w = __shfl_xor_sync(0xffffffffu, v, distance);
-  return ((lane & distance) == 0) == descending ? max64(v, w) : (v < w ? v : w);
-}
-__device__ __forceinline__ uint64_t warp_sort(uint64_t v, int lane) {  // descending over the lanes
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int d = size / 2; d > 0; d >>= 1) v = exchange(v, d, (lane & size) == 0 || size == 32, lane);
-  return v;
-}
-__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b_reversed, int lane) {  // the 32 largest of both
-  uint64_t v = max64(a, b_reversed);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = exchange(v, d, true, lane);
-  return v;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-// The row as vectors of 16 bytes from the boundary at or below its start: vector
-// j holds elements j * W - shift and on.
+// A row: `head` elements up to the first 16-byte boundary, whole vectors of W, and
+// `tail` elements.
 template <bool BF16>
 struct Row {
   static constexpr int W = BF16 ? 8 : 4;
-  const char* base;
-  int shift, V;
-  __device__ __forceinline__ Row(const Params& p, int r) {
-    const char* at = static_cast<const char*>(p.logits) + static_cast<int64_t>(r) * p.stride * (16 / W);
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
-    base = at - off;
-    shift = static_cast<int>(off) / (16 / W);
-    V = p.V;
+  const char* base;  // of the row
+  int V, head, vectors, tail;
+  __device__ __forceinline__ Row(const Params& p, int r) : V(p.V) {
+    base = static_cast<const char*>(p.logits) + static_cast<int64_t>(r) * p.stride * (16 / W);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u);
+    head = min(off ? (16 - off) / (16 / W) : 0, V);
+    vectors = (V - head) / W;
+    tail = V - head - vectors * W;
   }
-  __device__ __forceinline__ int vectors() const { return static_cast<int>((static_cast<int64_t>(V) + shift + W - 1) / W); }
   __device__ __forceinline__ float at(int i) const {
-    if (BF16) return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[shift + i]) << 16);
-    return reinterpret_cast<const float*>(base)[shift + i];
+    if (BF16) return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base)[i]) << 16);
+    return reinterpret_cast<const float*>(base)[i];
   }
-  __device__ __forceinline__ int first(int j) const { return j * W - shift; }
-  __device__ __forceinline__ bool whole(int j) const { return first(j) >= 0 && first(j) + W <= V; }
-  __device__ __forceinline__ uint4 load(int j) const { return reinterpret_cast<const uint4*>(base)[j]; }
+  __device__ __forceinline__ int first(int j) const { return head + j * W; }  // element of vector j
+  __device__ __forceinline__ const char* vector(int j) const { return base + static_cast<int64_t>(head) * (16 / W) + static_cast<int64_t>(j) * 16; }
+  // the element of the row's ends that a thread of the first CTA has, or -1: those of the head, then those of the tail
+  __device__ __forceinline__ int edge(int thread) const {
+    return thread < head ? thread : thread < head + tail ? V - tail + thread - head : -1;
+  }
   __device__ __forceinline__ static void values(uint4 u, float (&x)[W]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -148,57 +200,22 @@ struct Row {
   }
 };
 
-// What a thread has seen: its sums, the first batch of vectors that held its
-// largest element, and how many logits were ahead of the token's.
-struct Seen {
-  Sums sums{-INFINITY, 0.f, 0.f};
-  int batch = -1;
-  int ahead = 0;
-};
-constexpr int kBatch = 4;  // vectors
-
-__device__ __forceinline__ void see_one(Seen& s, float x, int i, int batch, float given, int token) {
-  if (x > s.sums.m) {
-    s.sums = join(s.sums, Sums{x, 0.f, 0.f});
-    s.batch = batch;
-  } else if (s.batch < 0) {
-    s.batch = batch;  // -infinity (or NaN) so far
-  }
-  const float d = x - (s.sums.m == -INFINITY ? 0.f : s.sums.m), e = ex2(d * kLog2e);
-  s.sums.s += e;
-  s.sums.t = fmaf(fmaxf(d, -1e30f), e, s.sums.t);
-  s.ahead += x > given || (x == given && i < token);
-}
-template <int N>
-__device__ __forceinline__ void see(Seen& s, const float (&x)[N], int batch) {
-  float top = x[0];
-#pragma unroll
-  for (int k = 1; k < N; ++k) top = fmaxf(top, x[k]);
-  if (top > s.sums.m) {
-    s.sums = join(s.sums, Sums{top, 0.f, 0.f});
-    s.batch = batch;
-  } else if (s.batch < 0) {
-    s.batch = batch;
-  }
-  const float ref = s.sums.m == -INFINITY ? 0.f : s.sums.m;
-  float sum = 0.f, weighted = 0.f;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float d = x[k] - ref, e = ex2(d * kLog2e);
-    sum += e;
-    weighted = fmaf(fmaxf(d, -1e30f), e, weighted);
-  }
-  s.sums.s += sum;
-  s.sums.t += weighted;
-}
-
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p, int cluster) {
+__global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const Params p, int cluster) {
   using Row = Row<BF16>;
   constexpr int W = Row::W;
-  __shared__ Shared S;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kStageVecs = kThreads * kVecs;
+  constexpr int kBatch = 16 / W, kHalf = kBatch / kHalves;  // vectors of 16 elements, of half of them
+  constexpr int kBatches = kVecs / kBatch;                   // of a stage, per thread
+  extern __shared__ __align__(128) uint8_t raw[];
+  Shared& S = *reinterpret_cast<Shared*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int r = blockIdx.x / cluster, rank = blockIdx.x - r * cluster;
+  if (tid == kThreads) {
+    for (int i = 0; i < kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], kWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 0) S.spots = S.halves = S.listed = S.failed = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int token = p.tokens ? p.tokens[r] : 0;
@@ -213,199 +230,347 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p, i
     return;
   }
   const Row row(p, r);
+  // this CTA's vectors: whole stages, the last of the row's perhaps short
+  const int64_t stages_all = (static_cast<int64_t>(row.vectors) + kStageVecs - 1) / kStageVecs;
+  const int64_t stages = (stages_all + cluster - 1) / cluster;
+  const int begin = static_cast<int>(min(rank * stages * kStageVecs, static_cast<int64_t>(row.vectors)));
+  const int end = static_cast<int>(min((rank + 1) * stages * kStageVecs, static_cast<int64_t>(row.vectors)));
+  const int fills = (end - begin + kStageVecs - 1) / kStageVecs;  // stages that hold any
+  __syncthreads();
+  if (cluster > 1) cluster_arrive();  // a CTA's memory may be written once it has arrived here
   const float given = p.tokens ? row.at(token) : INFINITY;
-  if (tid == 0) S.owners = S.listed = 0;
-  // this CTA's vectors: whole batches of all threads, so that a thread's elements are easily found again
-  const int vectors = row.vectors(), per_batch = kThreads * kBatch;
-  const int batches = static_cast<int>((vectors + static_cast<int64_t>(per_batch) * cluster - 1) / (static_cast<int64_t>(per_batch) * cluster));
-  const int64_t begin64 = static_cast<int64_t>(rank) * batches * per_batch;
-  const int begin = static_cast<int>(begin64 < vectors ? begin64 : vectors);
-  const int end = static_cast<int>(begin64 + static_cast<int64_t>(batches) * per_batch < vectors ? begin64 + static_cast<int64_t>(batches) * per_batch : vectors);
-  // vector k of batch b of a thread
-  auto vector_of = [&](int thread, int b, int k) { return begin + (b * kBatch + k) * kThreads + thread; };
-  Seen seen;
-  for (int b = 0; b < batches; ++b) {
-    if (vector_of(0, b, 0) >= end) break;
-    const int j0 = vector_of(tid, b, 0), j1 = vector_of(tid, b, kBatch - 1);
-    if (row.first(j0) >= 0 && j1 < end && row.first(j1) + W <= row.V) {
-      uint4 u[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) u[k] = row.load(vector_of(tid, b, k));
-      float x[kBatch * W];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        float y[W];
-        Row::values(u[k], y);
-        const int i0 = row.first(vector_of(tid, b, k));
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          x[k * W + e] = y[e];
-          seen.ahead += y[e] > given || (y[e] == given && i0 + e < token);
-        }
+  Sums mine{-INFINITY, 0.f, 0.f};
+  int ahead = 0;
+  // of each half: the largest element, the batch that it is in, and the largest of the other batches
+  float largest[kHalves] = {-INFINITY, -INFINITY}, second[kHalves] = {-INFINITY, -INFINITY};
+  int at[kHalves] = {0, 0};
+  const int edge = rank == 0 ? row.edge(tid) : -1;
+  const float edge_x = edge >= 0 ? row.at(edge) : -INFINITY;
+  if (warp == kWarps) {
+    // ================================================================== copies
+    bool ok = true;
+    int b = 0;
+    for (; b < fills; ++b) {
+      const int st = b % kStages;
+      if (b >= kStages) ok = warp_wait(&S.empty[st], (b / kStages - 1) & 1, &S.failed);
+      if (!ok) break;
+      if (elect()) {
+        const int from = begin + b * kStageVecs, n = min(kStageVecs, end - from) * 16;
+        bar_expect(&S.full[st], n);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(s32(S.stage[st])),
+                     "l"(row.vector(from)), "r"(n), "r"(s32(&S.full[st]))
+                     : "memory");
       }
-      see(seen, x, b);
-    } else {
-      for (int k = 0; k < kBatch; ++k) {
-        const int j = vector_of(tid, b, k);
-        if (j >= end) break;
-        for (int e = 0; e < W; ++e) {
-          const int i = row.first(j) + e;
-          if (i >= 0 && i < row.V) see_one(seen, row.at(i), i, b, given, token);
-        }
-      }
+      __syncwarp();
     }
-  }
-  // ---- the CTA's sums
-  {
-    const Sums w = warp_join(seen.sums);
-    const int n = __reduce_add_sync(0xffffffffu, seen.ahead);
-    if (lane == 0) S.warp_sums[warp] = w, S.warp_count[warp] = n;
-  }
-  // ---- the bound: the top-th largest of the threads' largest elements
-  uint64_t mine = 0;
-  if (p.top > 0) {
-    if (seen.batch >= 0) {
-      const float m = seen.sums.m;
-      int at = -1;
-      for (int k = 0; k < kBatch && at < 0; ++k) {
-        const int j = vector_of(tid, seen.batch, k);
-        if (j >= end) break;
-        for (int e = 0; e < W; ++e) {
-          const int i = row.first(j) + e;
-          if (at < 0 && i >= 0 && i < row.V && row.at(i) == m) at = i;
-        }
-      }
-      if (at >= 0) mine = key_of(m, at);  // (none where every element is NaN: such a row has no result)
-    }
-    uint64_t v = warp_sort(mine, lane);
-    S.keys[warp][lane] = v;
-    __syncthreads();
+    // nothing may land in shared memory after the CTA is gone, whoever gave up
+    if (lane == 0)
+      for (int j = b > kStages ? b - kStages : 0; j < b; ++j) bar_drain(&S.full[j % kStages], (j / kStages) & 1);
+    __syncwarp();
+  } else {
+    // ==================================================================== sums
+    float c = 0.f;  // the reference
+    const float above = float_above(given);
+    // 16 elements: the largest of their halves, then their sums relative to the thread's largest
+    auto see = [&](const uint64_t (&x)[8], int batch, auto index) {
+      float top[kHalves];
 #pragma unroll
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
-      if (warp < half) {
-        v = warp_merge(v, S.keys[warp + half][31 - lane], lane);
-        S.keys[warp][lane] = v;
+      for (int h = 0; h < kHalves; ++h) {
+        top[h] = max3(fmaxf(both(x[4 * h]).x, both(x[4 * h]).y), both(x[4 * h + 1]).x, both(x[4 * h + 1]).y);
+        top[h] = max3(max3(top[h], both(x[4 * h + 2]).x, both(x[4 * h + 2]).y), both(x[4 * h + 3]).x, both(x[4 * h + 3]).y);
+        second[h] = fmaxf(second[h], fminf(top[h], largest[h]));
+        if (top[h] > largest[h]) largest[h] = top[h], at[h] = batch;
       }
-      __syncthreads();
-    }
-    const uint64_t bound = S.keys[0][p.top - 1];
-    if (mine != 0 && mine >= bound) S.owner[atomicAdd(&S.owners, 1)] = tid;
-    __syncthreads();
-    // ---- the elements at or above it, of the threads that can have any
-    const int owners = S.owners;
-    auto scan = [&](auto f) {  // f(key) for the owners' elements, a warp per owner and lanes over its batches' vectors
-      for (int o = warp; o < owners; o += kWarps) {
-        const int thread = S.owner[o];
-        for (int q = lane; q < batches * kBatch; q += 32) {
-          const int j = vector_of(thread, q / kBatch, q % kBatch);
-          if (j >= end) continue;
-          for (int e = 0; e < W; ++e) {
-            const int i = row.first(j) + e;
-            if (i >= 0 && i < row.V) {
-              const float x = row.at(i);
-              if (x == x) f(key_of(x, i));
+      const float most = fmaxf(top[0], top[1]);
+      if (most > mine.m) {
+        mine = scaled(mine, most);
+        c = reference(most);
+      }
+      // logits ahead of the given one: x >= given of tokens of a lower index, x >= the float above it of others.
+      // (A token drawn from the row has hundreds ahead of it: many warps have one among a few hundred elements.)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (top[h] >= given) {
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k) {
+            const int i = index(h * kHalf + k);  // of the vector's first element
+            const float from = i + W <= token ? given : above;
+            uint64_t n = 0;
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) {
+              const float2 v = both(x[(h * kHalf + k) * (W / 2) + e]);
+              n = add2(n, pair_of(one_from(v.x, from), one_from(v.y, from)));
+              if (i < token && token < i + W) {  // (the token's own vector: equal ones ahead of it)
+                ahead += v.x == given && i + 2 * e < token;
+                ahead += v.y == given && i + 2 * e + 1 < token;
+              }
             }
+            ahead += static_cast<int>(both(n).x + both(n).y);
+          }
+        }
+      }
+      const uint64_t log2e = pair_of(kLog2e, kLog2e), c2 = pair_of(-c, -c);
+      uint64_t s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t y = fma2(x[k], log2e, c2), e = pair_of(ex2(both(y).x), ex2(both(y).y));
+        s[k & 1] = add2(s[k & 1], e);
+        t[k & 1] = fma2(y, e, t[k & 1]);
+      }
+      float2 s2 = both(add2(s[0], s[1])), t2 = both(add2(t[0], t[1]));
+      // y 2^y is NaN where y is -infinity (ruled out, or that far below), and y is not y where the largest is far out:
+      // once more, with care
+      if (!(t2.x + t2.y == t2.x + t2.y) || !is_near(mine.m)) {
+        s2 = t2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float y0 = at_least(relative(both(x[k]).x, mine.m)), y1 = at_least(relative(both(x[k]).y, mine.m));
+          const float e0 = ex2(y0), e1 = ex2(y1);
+          s2.x += e0, s2.y += e1;
+          t2.x = fmaf(y0, e0, t2.x), t2.y = fmaf(y1, e1, t2.y);
+        }
+      }
+      mine.s += s2.x + s2.y;
+      mine.t += t2.x + t2.y;
+    };
+    for (int b = 0; b < fills; ++b) {
+      const int st = b % kStages, from = begin + b * kStageVecs;
+      bar_wait(&S.full[st], (b / kStages) & 1, &S.failed);
+      uint4 u[kVecs];
+      const uint4* const in = reinterpret_cast<const uint4*>(S.stage[st]) + tid;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) u[k] = in[k * kThreads];
+      const int left = end - from - tid;  // vectors of the slice from this thread's first on
+      if (left <= (kVecs - 1) * kThreads) {
+        const uint32_t out = BF16 ? 0xff80ff80u : 0xff800000u;  // -infinity: not there
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+          if (k * kThreads >= left) u[k] = make_uint4(out, out, out, out);
+      }
+#pragma unroll
+      for (int k0 = 0; k0 < kVecs; k0 += kBatch) {
+        uint64_t x[8];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          float v[W];
+          Row::values(u[k0 + k], v);
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) x[k * (W / 2) + i] = pair_of(v[2 * i], v[2 * i + 1]);
+        }
+        // (what is not there counts for nothing even where the token itself is ruled out: its index is past the row's)
+        see(x, b * kBatches + k0 / kBatch, [&](int k) { const int j = from + (k0 + k) * kThreads + tid; return j < end ? row.first(j) : 0x7fffff00; });
+      }
+      // (Only now: every lane's pieces have arrived in its registers, as they have been used.  An arrival right behind the
+      // loads let copies overtake some of them.)
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.empty[st]);
+    }
+    if (edge >= 0) {
+      if (edge_x > mine.m) mine = scaled(mine, edge_x);
+      const float y = at_least(relative(edge_x, mine.m)), e = ex2(y);
+      mine.s += e;
+      mine.t += y * e;
+      ahead += edge_x > given || (edge_x == given && edge < token);
+    }
+    // ---- the warp's sums, and its share of the bound: each of eight warps has an eighth of num_top threads whose largest
+    // elements reach the least of the warps' bounds
+    const Sums w = warp_sum(mine);
+    const int n = __reduce_add_sync(0xffffffffu, ahead);
+    uint32_t left = order_of(mine.m), bound = 0;
+    for (int k = 0; k < (p.top + kWarps - 1) / kWarps; ++k) {
+      bound = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
+    }
+    if (lane == 0) S.warp_sums[warp] = w, S.warp_count[warp] = n, S.warp_bound[warp] = bound;
+  }
+  __syncthreads();
+  if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+  if (p.top > 0) {
+    uint32_t bound = S.warp_bound[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bound = min(bound, S.warp_bound[w]);
+    // (-infinity, which threads without elements have too, is left to the end: it would let all ruled-out tokens pass)
+    const float least = fmaxf(logit_of(static_cast<uint64_t>(bound) << 32), -3.4028235e38f);
+    if (warp < kWarps) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (second[h] >= least) S.half[atomicAdd(&S.halves, 1)] = static_cast<int16_t>(h * kThreads + tid);
+        else if (largest[h] >= least) S.spot[atomicAdd(&S.spots, 1)] = begin + (at[h] * kBatch + h * kHalf) * kThreads + tid;
+      }
+    }
+    auto list = [&](uint64_t key) {
+      const int n = atomicAdd(&S.listed, 1);
+      if (n < kList) S.list[n] = key;
+    };
+    if (edge >= 0 && edge_x >= least) list(key_of(edge_x, edge));
+    __syncthreads();
+    // ---- the elements at or above it
+    const int spots = S.spots * kHalf, vecs = fills * kBatches * kHalf, all = spots + S.halves * vecs;  // vectors; of a half
+    auto scan = [&](float from, auto f) {  // f(key) for those from a value on
+      constexpr int kAhead = 4;
+      for (int q0 = tid; q0 < all; q0 += kAhead * kAllThreads) {
+        uint4 u[kAhead];
+        int where[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int q = q0 + a * kAllThreads;
+          where[a] = end;
+          if (q < spots) {
+            where[a] = S.spot[q / kHalf] + q % kHalf * kThreads;
+          } else if (q < all) {
+            const int o = (q - spots) / vecs, k = q - spots - o * vecs, who = S.half[o];
+            where[a] = begin + (k / kHalf * kBatch + who / kThreads * kHalf + k % kHalf) * kThreads + who % kThreads;
+          }
+          if (where[a] < end) u[a] = *reinterpret_cast<const uint4*>(row.vector(where[a]));
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          if (where[a] >= end) continue;
+          float x[W], top = -INFINITY;
+          Row::values(u[a], x);
+#pragma unroll
+          for (int e = 0; e < W; ++e) top = fmaxf(top, x[e]);
+          if (top >= from) {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+              if (x[e] >= from) f(key_of(x[e], row.first(where[a]) + e));
           }
         }
       }
     };
-    scan([&](uint64_t key) {
-      if (key >= bound) {
-        const int n = atomicAdd(&S.listed, 1);
-        if (n < kList) S.list[n] = key;
-      }
-    });
+    scan(least, list);
     __syncthreads();
-    uint64_t* best = S.best[rank];
-    if (S.listed <= kList) {
-      const int n = S.listed;
-      if (tid < p.top && tid >= n) best[tid] = 0;
-      for (int c = tid; c < n; c += kThreads) {
+    const int n = S.listed;
+    if (n <= kList) {
+      if (tid < p.top && tid >= n) S.best[tid] = 0;
+      for (int c = tid; c < n; c += kAllThreads) {
         const uint64_t key = S.list[c];
-        int ahead = 0;
-        for (int k = 0; k < n; ++k) ahead += S.list[k] > key;
-        if (ahead < p.top) best[ahead] = key;
+        int before = 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) before += S.list[k] > key;
+        if (before < p.top) S.best[before] = key;
+      }
+      // fewer than asked for are above -infinity: then the first of those that are not, which most are
+      if (warp == 0 && n < p.top) {
+        __syncwarp();
+        const int64_t inner = static_cast<int64_t>(end - begin) * W, edges = rank == 0 ? row.head + row.tail : 0;
+        int have = n;
+        for (int64_t q0 = 0; q0 < inner + edges && have < p.top; q0 += 32) {  // head, slice, tail
+          const int64_t q = q0 + lane, h = rank == 0 ? row.head : 0;
+          const int i = q < h ? static_cast<int>(q) : q < h + inner ? static_cast<int>(row.first(begin) + (q - h))
+                      : q < inner + edges ? static_cast<int>(row.V - row.tail + (q - h - inner)) : -1;
+          const bool out = i >= 0 && row.at(i) == -INFINITY;
+          const uint32_t ruled = __ballot_sync(0xffffffffu, out);
+          const int rank_of = have + __popc(ruled & ((1u << lane) - 1));
+          if (out && rank_of < p.top) S.best[rank_of] = key_of(-INFINITY, i);
+          have += __popc(ruled);
+        }
       }
     } else {
-      // many elements of few threads reach the bound (rows in order, say): one alternative after another
+      // many elements of few threads reach the bound (rows in order, say), or many are equal: one alternative after another
       uint64_t last = ~0ull;
-      for (int n = 0; n < p.top; ++n) {
+      for (int k = 0; k < p.top; ++k) {
         uint64_t top = 0;
-        scan([&](uint64_t key) {
-          if (key < last) top = max64(top, key);
-        });
+        auto below = [&](uint64_t key) {
+          if (key < last && key > top) top = key;
+        };
+        scan(least, below);
+        if (edge >= 0 && edge_x >= least) below(key_of(edge_x, edge));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max64(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) S.keys[0][warp] = top;
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t other = __shfl_xor_sync(0xffffffffu, top, o);
+          if (other > top) top = other;
+        }
+        if (lane == 0) S.round[warp] = top;
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) top = max64(top, S.keys[0][w]);
-        if (tid == 0) best[n] = top;
+        for (int w = 0; w <= kWarps; ++w)
+          if (S.round[w] > top) top = S.round[w];
+        if (tid == 0) S.best[k] = top;
         last = top;
         __syncthreads();
       }
     }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    Sums w = lane < kWarps ? S.warp_sums[lane] : Sums{-INFINITY, 0.f, 0.f};
-    w = warp_join(w);
-    const int n = __reduce_add_sync(0xffffffffu, lane < kWarps ? S.warp_count[lane] : 0);
-    if (lane == 0) S.sums[rank] = w, S.count[rank] = n;
-  }
-  if (cluster > 1) {
     __syncthreads();
-    cluster_barrier();  // every CTA has its results
-    if (rank == 0) {
-      auto remote = [&](const void* at, int cta) {
-        uint32_t a;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "r"(cta));
-        return a;
-      };
-      for (int c = 1 + warp; c < cluster; c += kWarps) {
-        if (lane < p.top) {
-          uint64_t v;
-          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(&S.best[c][lane], c)) : "memory");
-          S.best[c][lane] = v;
-        }
-        if (lane < 4) {
-          const void* at = lane == 0 ? static_cast<const void*>(&S.sums[c].m) : lane == 1 ? &S.sums[c].s : lane == 2 ? &S.sums[c].t : static_cast<const void*>(&S.count[c]);
-          uint32_t v;
-          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(at, c)) : "memory");
-          *const_cast<uint32_t*>(static_cast<const uint32_t*>(at)) = v;
-        }
-      }
+  }
+  if (warp != 0) {  // the rest is one warp's
+    if (cluster > 1) {
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
     }
-    cluster_barrier();  // read: the others may leave
+    return;
+  }
+  Sums all = warp_sum(lane < kWarps ? S.warp_sums[lane] : Sums{-INFINITY, 0.f, 0.f});
+  int before = __reduce_add_sync(0xffffffffu, lane < kWarps ? S.warp_count[lane] : 0);
+  uint64_t key = lane < p.top ? S.best[lane] : 0;
+  if (cluster > 1) {  // to the cluster's first CTA
+    cluster_wait();
+    if (lane < p.top) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cta(&S.part_top[rank][lane], 0)), "l"(key) : "memory");
+    if (lane == 0) {
+      const uint32_t to = in_cta(&S.part_sums[rank], 0);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(all.m) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(all.s) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(all.t) : "memory");
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(in_cta(&S.part_count[rank], 0)), "r"(before) : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
+    all = warp_sum(lane < cluster ? S.part_sums[lane] : Sums{-INFINITY, 0.f, 0.f});
+    before = __reduce_add_sync(0xffffffffu, lane < cluster ? S.part_count[lane] : 0);
+    // of all CTAs' alternatives, each list in order: one after another the largest of the lists' heads
+    int next = 0;
+    for (int k = 0; k < p.top; ++k) {
+      const uint64_t head = lane < cluster && next < p.top ? S.part_top[lane][next] : 0;
+      uint64_t most = head;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, most, o);
+        if (other > most) most = other;
+      }
+      most = __shfl_sync(0xffffffffu, most, 0);
+      if (most != 0 && head == most) ++next;
+      if (lane == k) key = most;
+    }
   }
-  __syncthreads();
   // ---- the row's results
-  Sums all{-INFINITY, 0.f, 0.f};
-  int ahead = 0;
-  for (int c = 0; c < cluster; ++c) all = join(all, S.sums[c]), ahead += S.count[c];
   const bool good = all.s > 0.f && all.s < INFINITY && all.m < INFINITY;
-  const float nan = __uint_as_float(0x7fc00000u), logs = logf(all.s);
-  if (tid == 0) {
-    p.entropy[r] = good ? logs - all.t / all.s : nan;
+  const float nan = __uint_as_float(0x7fc00000u), logs = log2f(all.s);
+  auto share = [&](float x) { return kLn2 * (relative(x, all.m) - logs); };  // the log probability of an element
+  const int64_t place = static_cast<int64_t>(r) * p.top + lane;
+  if (lane == 0) {
+    p.entropy[r] = good ? kLn2 * (logs - all.t / all.s) : nan;
     if (p.tokens) {
-      p.logprobs[r] = good ? given - all.m - logs : nan;
-      p.ranks[r] = good ? ahead : -1;
+      p.logprobs[r] = good ? share(given) : nan;
+      p.ranks[r] = good ? before : -1;
     }
   }
-  const int n = cluster * p.top;
-  for (int c = tid; c < n; c += kThreads) {
-    const uint64_t key = S.best[c / p.top][c % p.top];
-    int place = 0;  // keys differ but for the zeros past a CTA's last element
-    for (int k = 0; k < n; ++k) {
-      const uint64_t other = S.best[k / p.top][k % p.top];
-      place += other > key || (other == key && k < c);
-    }
-    if (place < p.top) {
-      const int64_t at = static_cast<int64_t>(r) * p.top + place;
-      p.top_ids[at] = good && key ? index_of(key) : -1;
-      p.top_logprobs[at] = !good ? nan : key ? logit_of(key) - all.m - logs : -INFINITY;
-    }
+  if (lane < p.top) {
+    p.top_ids[place] = good && key ? index_of(key) : -1;
+    p.top_logprobs[place] = !good ? nan : key ? share(logit_of(key)) : -INFINITY;
   }
+}
+
+// ------------------------------------------------------------------ host side
+std::mutex g_mutex;
+int g_sms[64];
+
+cudaError_t setup(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!g_sms[dev]) {
+    for (auto kernel : {logprobs_kernel<false>, logprobs_kernel<true>})
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)))) != cudaSuccess) return e;
+    int n = 0;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    g_sms[dev] = n;
+  }
+  *sms = g_sms[dev];
+  return cudaSuccess;
 }
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }
@@ -436,12 +601,15 @@ extern "C" int kda_logprobs(const KdaLogprobsArgs* a, void* stream) {
     return kda_internal_fail(KDA_ERR_SHAPE, "a result may not take the place of the tokens");
   const Params p{a->R, a->V, a->num_top, a->logits, a->logits_row_stride, a->tokens, a->logprobs, a->ranks, a->entropy,
                  a->top_ids, a->top_logprobs, a->err_flag};
-  // CTAs per row: as many as are resident at once (four an SM)
+  int sms = 0;
+  cudaError_t e = setup(&sms);
+  if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "setup: %s", cudaGetErrorString(e));
+  // CTAs per row: while all are resident at once
   int cluster = kMaxCluster;
-  while (cluster > 1 && static_cast<int64_t>(a->R) * cluster > 4 * 152) cluster >>= 1;
-  const cudaError_t e = kda_internal_launch_cluster(bf16 ? logprobs_kernel<true> : logprobs_kernel<false>,
-                                                    dim3(static_cast<unsigned>(a->R) * cluster), dim3(kThreads), 0, stream,
-                                                    cluster, p, cluster);
+  while (cluster > 1 && static_cast<int64_t>(a->R) * cluster > kCtasPerSm * sms) cluster >>= 1;
+  e = kda_internal_launch_cluster(bf16 ? logprobs_kernel<true> : logprobs_kernel<false>,
+                                  dim3(static_cast<unsigned>(a->R) * cluster), dim3(kAllThreads), sizeof(Shared), stream,
+                                  cluster, p, cluster);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }

@@ -122,6 +122,16 @@ def test_large_and_small_values(cuda_device):
     check(cuda_device, x, t, 16)
 
 
+@pytest.mark.parametrize("rows_", [6, 800])
+@pytest.mark.parametrize("offset", [9.5e6, 1.2e7, -3e7, 6e8])
+def test_far_offsets(offset, rows_, cuda_device):
+    # logits far from 0, whose steps in fp32 are 1 to 64: differences between them are exact
+    g = torch.Generator().manual_seed(3)
+    step = max(1.0, 2.0 ** (math.floor(math.log2(abs(offset))) - 23))
+    x = (offset + step * torch.randint(-8, 9, (rows_, 700), generator=g)).float()
+    check(cuda_device, x, torch.randint(0, 700, (rows_,), generator=g, dtype=torch.int32), 8)
+
+
 def test_rows_not_asked_for_are_not_read(cuda_device):
     # as verification leaves them: [N, T] tokens with -1 behind those that stand; the rows there hold anything
     x, t = rows(12, 1500, 7)
@@ -168,6 +178,26 @@ def test_graph_stream_and_repeated_calls(cuda_device):
         torch.cuda.synchronize(dev)
         for a, b in zip(first, (call.logprobs, call.ranks, call.entropy, call.top_ids, call.top_logprobs)):
             assert torch.equal(a, b)                     # the same bits every time
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_the_same_bits_under_load(dt, cuda_device):
+    # more rows than CTAs, long enough for every stage of the ring to be used again: a copy that overtakes a reader shows
+    # as a count that is off by a few
+    g = torch.Generator(device=cuda_device).manual_seed(2)
+    x = (torch.randn(1300, 60001, generator=g, device=cuda_device) * 3).to(dt)
+    t = torch.randint(0, 60001, (1300,), generator=g, device=cuda_device, dtype=torch.int32)
+    call = KdaLogprobsCall(x, t, num_top=20)
+    call()
+    results = lambda: (call.ranks, call.top_ids, call.logprobs, call.entropy, call.top_logprobs)  # noqa: E731
+    first = [v.clone() for v in results()]
+    xt = x.gather(1, t.long()[:, None])
+    ranks = (x > xt).sum(1) + ((x == xt) & (torch.arange(60001, device=cuda_device) < t[:, None])).sum(1)
+    assert torch.equal(first[0], ranks.int())
+    for _ in range(20):
+        call()
+        for a, b in zip(first, results()):
+            assert torch.equal(a, b)
 
 
 def test_far_rows(cuda_device):
