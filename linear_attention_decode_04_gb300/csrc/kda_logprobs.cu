@@ -2,9 +2,10 @@
 // alternatives (definition in include/kda_logprobs.h).
 //
 // One pass over the logits, which a warp of its own copies to shared memory in a
-// ring: every thread keeps the largest logit m of its elements, s = sum 2^y and t =
-// sum y 2^y with y = x log2 e - c and c = m log2 e as rounded, from which lse and
-// entropy follow (lse = ln 2 (c + log2 s), entropy = ln 2 (log2 s - t / s)).  y is one
+// ring: every thread keeps s = sum 2^y and t = sum y 2^y with y = x log2 e - c and c =
+// m log2 e as rounded for an m near its largest logit (it follows in steps of 16, for
+// most batches have a new largest in some lane), from which lse and entropy follow (lse
+// = ln 2 (c + log2 s), entropy = ln 2 (log2 s - t / s)).  y is one
 // fused operation, so neither c's rounding nor a large logit costs digits.  The top
 // alternatives cost little beside that pass: the num_top-th largest of the threads'
 // largest logits bounds the num_top-th largest logit from below, and of a thread's
@@ -38,6 +39,7 @@ constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
 constexpr int kList = 1024;                 // elements that a CTA lists as candidates
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kLeast = -200.f;           // of y: 2^y is 0 in fp32 from -150 on, and y 2^y is too where x is -infinity
+constexpr float kStep = 16.f;              // a reference follows a logit that is further above it
 constexpr float kFar = 1e7f;               // from here on m log2 e is rounded by whole numbers: elements are taken relative to m itself
 
 struct Params {
@@ -53,7 +55,8 @@ struct Params {
   int32_t* err;
 };
 
-// Sums of elements relative to their largest, m (see above); s and t are 0 where m is -infinity.
+// Sums of elements relative to one of them, m, which no other is more than kStep above; s and t are 0 where m is
+// -infinity.
 struct Sums {
   float m, s, t;
 };
@@ -124,14 +127,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Sums whose largest is m are relative to c = m log2 e as rounded where |m| < kFar, to m log2 e itself further out, to 0
+// Sums of reference m are relative to c = m log2 e as rounded where |m| < kFar, to m log2 e itself further out, to 0
 // where there is nothing.  (c is rounded wherever it is used: fused into a difference it would be another one.)
 __device__ __forceinline__ bool is_near(float m) { return fabsf(m) < kFar || m == -INFINITY; }
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e); }
 // log2 of an element relative to that, and of m itself.
 __device__ __forceinline__ float relative(float x, float m) { return is_near(m) ? fmaf(x, kLog2e, -reference(m)) : (x - m) * kLog2e; }
 __device__ __forceinline__ float residue(float m) { return fabsf(m) < kFar ? fmaf(m, kLog2e, -reference(m)) : 0.f; }
-// The exponent that takes sums from largest m to largest `to` >= m.
+// The exponent that takes sums from reference m to reference `to` >= m.
 __device__ __forceinline__ float shift(float m, float to) {
   if (m == to) return 0.f;
   return m > -INFINITY ? fmaxf(fmaf(m - to, kLog2e, residue(to) - residue(m)), kLeast) : kLeast;
@@ -270,8 +273,9 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
   } else {
     // ==================================================================== sums
     float c = 0.f;  // the reference
+    bool near = true;
     const float above = float_above(given);
-    // 16 elements: the largest of their halves, then their sums relative to the thread's largest
+    // 16 elements: the largest of their halves, then their sums
     auto see = [&](const uint64_t (&x)[8], int batch, auto index) {
       float top[kHalves];
 #pragma unroll
@@ -282,9 +286,10 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
         if (top[h] > largest[h]) largest[h] = top[h], at[h] = batch;
       }
       const float most = fmaxf(top[0], top[1]);
-      if (most > mine.m) {
+      if (most > mine.m + kStep) {
         mine = scaled(mine, most);
         c = reference(most);
+        near = is_near(most);
       }
       // logits ahead of the given one: x >= given of tokens of a lower index, x >= the float above it of others.
       // (A token drawn from the row has hundreds ahead of it: many warps have one among a few hundred elements.)
@@ -318,9 +323,9 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
         t[k & 1] = fma2(y, e, t[k & 1]);
       }
       float2 s2 = both(add2(s[0], s[1])), t2 = both(add2(t[0], t[1]));
-      // y 2^y is NaN where y is -infinity (ruled out, or that far below), and y is not y where the largest is far out:
+      // y 2^y is NaN where y is -infinity (ruled out, or that far below), and y is not y where the reference is far out:
       // once more, with care
-      if (!(t2.x + t2.y == t2.x + t2.y) || !is_near(mine.m)) {
+      if (!(t2.x + t2.y == t2.x + t2.y) || !near) {
         s2 = t2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
       if (lane == 0) bar_arrive(&S.empty[st]);
     }
     if (edge >= 0) {
-      if (edge_x > mine.m) mine = scaled(mine, edge_x);
+      if (edge_x > mine.m + kStep) mine = scaled(mine, edge_x);
       const float y = at_least(relative(edge_x, mine.m)), e = ex2(y);
       mine.s += e;
       mine.t += y * e;
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
     // elements reach the least of the warps' bounds
     const Sums w = warp_sum(mine);
     const int n = __reduce_add_sync(0xffffffffu, ahead);
-    uint32_t left = order_of(mine.m), bound = 0;
+    uint32_t left = order_of(fmaxf(fmaxf(largest[0], largest[1]), edge >= 0 ? edge_x : -INFINITY)), bound = 0;
     for (int k = 0; k < (p.top + kWarps - 1) / kWarps; ++k) {
       bound = __reduce_max_sync(0xffffffffu, left);
       if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
