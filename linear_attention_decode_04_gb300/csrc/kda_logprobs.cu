@@ -29,14 +29,11 @@
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kAllThreads = kThreads + 32;  // that sum, and a warp that copies
 constexpr int kVecs = 4;                   // 16-byte pieces of a stage, per thread
-constexpr int kStageBytes = kThreads * kVecs * 16, kStages = 3;
-constexpr int kCtasPerSm = 4;
+constexpr int kStages = 3;
 constexpr int kHalves = 2;                 // of a thread's elements, by their place in a batch
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = KDA_LOGPROBS_MAX_TOP;
-constexpr int kList = 1024;                 // elements that a CTA lists as candidates
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kLeast = -200.f;           // of y: 2^y is 0 in fp32 from -150 on, and y 2^y is too where x is -infinity
 constexpr float kStep = 16.f;              // a reference follows a logit that is further above it
@@ -60,9 +57,19 @@ struct Params {
 struct Sums {
   float m, s, t;
 };
+// THREADS that sum, and a warp that copies.
+template <int THREADS>
+struct Cfg {
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kAllThreads = THREADS + 32;
+  static constexpr int kStageBytes = kThreads * kVecs * 16;
+  static constexpr int kCtasPerSm = THREADS > 128 ? 4 : 12;
+  static constexpr int kList = 4 * THREADS;  // elements that a CTA lists as candidates
+};
+template <class C>
 struct Shared {
+  static constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kList = C::kList;
   union {
-    alignas(128) uint8_t stage[kStages][kStageBytes];
+    alignas(128) uint8_t stage[kStages][C::kStageBytes];
     struct {                               // when the row has been seen
       uint64_t list[kList];
       int spot[kThreads * kHalves];        // pieces that are read again: the first vector of each
@@ -203,15 +210,17 @@ struct Row {
   }
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const Params p, int cluster) {
+template <bool BF16, int THREADS>
+__global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtasPerSm) logprobs_kernel(const Params p, int cluster) {
+  using C = Cfg<THREADS>;
+  constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kAllThreads = C::kAllThreads, kList = C::kList;
   using Row = Row<BF16>;
   constexpr int W = Row::W;
   constexpr int kStageVecs = kThreads * kVecs;
   constexpr int kBatch = 16 / W, kHalf = kBatch / kHalves;  // vectors of 16 elements, of half of them
   constexpr int kBatches = kVecs / kBatch;                   // of a stage, per thread
   extern __shared__ __align__(128) uint8_t raw[];
-  Shared& S = *reinterpret_cast<Shared*>(raw);
+  Shared<C>& S = *reinterpret_cast<Shared<C>*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int r = blockIdx.x / cluster, rank = blockIdx.x - r * cluster;
   if (tid == kThreads) {
@@ -377,14 +386,19 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
       mine.t += y * e;
       ahead += edge_x > given || (edge_x == given && edge < token);
     }
-    // ---- the warp's sums, and its share of the bound: each of eight warps has an eighth of num_top threads whose largest
-    // elements reach the least of the warps' bounds
+    // ---- the warp's sums, and its share of the bound: each warp has so many threads whose largest elements reach its own
+    // bound that there are num_top of all warps, as many of it as it has of the threads with elements (the first, and
+    // all of them but in short rows); so num_top elements reach the least of the warps' bounds
     const Sums w = warp_sum(mine);
     const int n = __reduce_add_sync(0xffffffffu, ahead);
     uint32_t left = order_of(fmaxf(fmaxf(largest[0], largest[1]), edge >= 0 ? edge_x : -INFINITY)), bound = 0;
-    for (int k = 0; k < (p.top + kWarps - 1) / kWarps; ++k) {
-      bound = __reduce_max_sync(0xffffffffu, left);
-      if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
+    const int all = min(end - begin, kThreads), own = min(max(all - 32 * warp, 0), 32);
+    if (p.top <= all) {  // (else everything passes)
+      bound = 0xffffffffu;  // (of no concern where the warp has none)
+      for (int k = 0; k < (p.top * own + all - 1) / all; ++k) {
+        bound = __reduce_max_sync(0xffffffffu, left);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, left == bound)) - 1) left = 0;
+      }
     }
     if (lane == 0) S.warp_sums[warp] = w, S.warp_count[warp] = n, S.warp_bound[warp] = bound;
   }
@@ -395,7 +409,7 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) bound = min(bound, S.warp_bound[w]);
     // (-infinity, which threads without elements have too, is left to the end: it would let all ruled-out tokens pass)
-    const float least = fmaxf(logit_of(static_cast<uint64_t>(bound) << 32), -3.4028235e38f);
+    const float least = bound <= order_of(-3.4028235e38f) ? -3.4028235e38f : logit_of(static_cast<uint64_t>(bound) << 32);
     if (warp < kWarps) {
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
@@ -558,6 +572,8 @@ __global__ void __launch_bounds__(kAllThreads, kCtasPerSm) logprobs_kernel(const
 }
 
 // ------------------------------------------------------------------ host side
+// CTAs of 64 threads, of which three times as many are resident, or of 256.
+constexpr int kFew = 64, kMany = 256, kShort = 32768;
 std::mutex g_mutex;
 int g_sms[64];
 
@@ -568,8 +584,8 @@ cudaError_t setup(int* sms) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_mutex);
   if (!g_sms[dev]) {
-    for (auto kernel : {logprobs_kernel<false>, logprobs_kernel<true>})
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)))) != cudaSuccess) return e;
+    for (auto kernel : {logprobs_kernel<false, kFew>, logprobs_kernel<true, kFew>, logprobs_kernel<false, kMany>, logprobs_kernel<true, kMany>})
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared<Cfg<kMany>>)))) != cudaSuccess) return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     g_sms[dev] = n;
@@ -609,12 +625,21 @@ extern "C" int kda_logprobs(const KdaLogprobsArgs* a, void* stream) {
   int sms = 0;
   cudaError_t e = setup(&sms);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "setup: %s", cudaGetErrorString(e));
-  // CTAs per row: while all are resident at once
-  int cluster = kMaxCluster;
-  while (cluster > 1 && static_cast<int64_t>(a->R) * cluster > kCtasPerSm * sms) cluster >>= 1;
-  e = kda_internal_launch_cluster(bf16 ? logprobs_kernel<true> : logprobs_kernel<false>,
-                                  dim3(static_cast<unsigned>(a->R) * cluster), dim3(kAllThreads), sizeof(Shared), stream,
-                                  cluster, p, cluster);
+  // Short rows, where a CTA's start and end count more than its sums, get small CTAs: those of one stage (549 of 424 fp32
+  // logits 4.9 us, with 256 threads 6.7), and where all CTAs are not resident at once those up to kShort bytes (1,000 of
+  // 4,096 fp32 logits 11.8 and 14.3, of 16,000 25.5 and 23.1) or, in many waves, twice that (4,000 of 5,000 30 and 53, of
+  // 16,000 60 and 67, of 32,000 103 and 97).  Others get a cluster of CTAs each while those are resident at once and
+  // each has a stage at least.
+  const int64_t bytes = static_cast<int64_t>(a->V) * (bf16 ? 2 : 4);
+  const int at_once = Cfg<kMany>::kCtasPerSm * sms;
+  const bool few = bytes <= Cfg<kFew>::kStageBytes || (a->R > at_once && bytes <= (a->R > Cfg<kFew>::kCtasPerSm * sms ? 2 : 1) * kShort);
+  int cluster = few ? 1 : kMaxCluster;
+  while (cluster > 1 && (static_cast<int64_t>(a->R) * cluster > at_once || (cluster - 1) * int64_t{Cfg<kMany>::kStageBytes} >= bytes)) cluster >>= 1;
+  auto kernel = few ? (bf16 ? logprobs_kernel<true, kFew> : logprobs_kernel<false, kFew>)
+                    : (bf16 ? logprobs_kernel<true, kMany> : logprobs_kernel<false, kMany>);
+  e = kda_internal_launch_cluster(kernel, dim3(static_cast<unsigned>(a->R) * cluster),
+                                  dim3(few ? Cfg<kFew>::kAllThreads : Cfg<kMany>::kAllThreads),
+                                  few ? sizeof(Shared<Cfg<kFew>>) : sizeof(Shared<Cfg<kMany>>), stream, cluster, p, cluster);
   if (e != cudaSuccess) return kda_internal_fail(KDA_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
   return KDA_OK;
 }

@@ -78,6 +78,24 @@ def test_orders_and_ties(kind, V, cuda_device):
         check(cuda_device, x, torch.tensor([tok, tok], dtype=torch.int32), 32)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R_, V, k", [(20, 1416, 27), (49, 415, 27), (549, 424, 7), (700, 255, 32), (700, 4097, 32), (620, 8192, 20),
+                                      (620, 8200, 20), (1900, 1030, 32), (1900, 5001, 9)])
+def test_short_rows(R_, V, k, dt, cuda_device):
+    # fewer vectors than threads, fewer threads with any than alternatives; small CTAs and large ones
+    x, t = rows(R_, V, R_ * V, dt)
+    check(cuda_device, x, t, k)
+
+
+@pytest.mark.parametrize("V", [9, 130, 600, 5000])
+@pytest.mark.parametrize("kind", ["rising", "equal", "steps", "ruled out"])
+def test_orders_and_ties_in_many_rows(kind, V, cuda_device):
+    i = torch.arange(V, dtype=torch.float32)
+    x = {"rising": i / V, "equal": torch.full((V,), 3.0), "steps": torch.floor(i / 40) % 5,
+         "ruled out": torch.where(i % 97 == 8, i / 64, -math.inf)}[kind].repeat(640, 1)
+    check(cuda_device, x, torch.arange(640, dtype=torch.int32) % V, 32)
+
+
 @pytest.mark.parametrize("rows_", [1, 3, 700])
 def test_large_logits_in_one_threads_elements(rows_, cuda_device):
     # the largest elements all in places that one thread, or few, go through
