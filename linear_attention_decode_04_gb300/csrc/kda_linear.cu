@@ -34,11 +34,22 @@ constexpr int kTileN = 128;                // channels of a CTA's tile
 constexpr int kBlock = 128;                // bytes of k per stage
 constexpr int kMaxSplit = 4;
 constexpr int kMaxStages = 12;
-constexpr int kPitch = 80;                 // bytes between rows of results in shared memory
+
+// Quotients of 0 .. 2^31 - 1 by a divisor of a launch (Granlund and Montgomery 1994, section 4).
+struct Divisor {
+  uint32_t by, factor, shift;
+  Divisor() = default;
+  explicit Divisor(uint32_t n) : by(n), shift(31) {
+    while ((1ull << (shift - 31)) < n) ++shift;
+    factor = static_cast<uint32_t>((1ull << shift) / n + 1);
+  }
+  __device__ __forceinline__ int of(int n) const { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * factor >> shift); }
+};
 
 struct Params {
   int M, N, K, width;          // width: channels of out
   int m_tiles, n_tiles, blocks;  // row tiles, channel tiles (of a CTA or pair), blocks of k
+  Divisor group, rows, last;   // tiles of a group of row tiles; row tiles of one, and of the last one
   int split, stages;           // CTAs (or pairs) per tile, ring depth
   int act;
   bool out_f32, early, vec_out, vec_res;  // vec: rows in 16-byte pieces
@@ -59,6 +70,7 @@ struct Cfg {
   static constexpr int kAcc = GATE == kTwoSums ? 2 : 1;
   static constexpr int kChannels = GATE == kInterleaved ? kTileN / 2 : kTileN;  // of out, of a CTA
   static constexpr int kUnroll = PAIR || ROWS > 64 ? 4 : 2;  // blocks of eight rows that a warp writes at a time
+  static constexpr int kRowBytes = 8 * kUnroll * kChannels / 4 * 2;  // of these rows
   static constexpr int kWeightBytes = kAcc * kTileN * kBlock, kXRows = PAIR ? ROWS / 2 : ROWS;
   static constexpr int kStageBytes = kWeightBytes + kXRows * kBlock;
   static constexpr int kCols = kAcc * ROWS;      // accumulator columns of a tile, of which there are two sets
@@ -66,7 +78,7 @@ struct Cfg {
   // One CTA takes an SM's shared memory; where a short range of k leaves room, the next call's CTAs start beside it.
   static constexpr int kCtasPerSm = PAIR || ROWS > 64 ? 1 : 2;
   // warpgroups that write results; then a warp that copies weights, one that copies rows, and the issuer
-  static constexpr int kGroups = kCtasPerSm == 1 ? 2 : 1, kThreads = 128 * kGroups + 96;
+  static constexpr int kGroups = kCtasPerSm == 2 ? 1 : GATE == kTwoSums ? 2 : 4, kThreads = 128 * kGroups + 96;
   // sums of a tile that several CTAs share: in the stages, when its products have ended, lie a CTA's own and those sent to it
   static constexpr int kPartBytes = kCols / 2 * (kTileN * 8 + 64 * kMaxSplit);
   static_assert(kTmemCols * kCtasPerSm <= 512, "tensor memory");
@@ -75,33 +87,41 @@ struct Cfg {
 // Shared memory: the stages, then this.
 template <class C>
 struct Head {
-  alignas(16) uint8_t rows[4 * C::kGroups][8 * C::kUnroll * kPitch];  // of the warps that write results
+  alignas(16) uint8_t rows[4 * C::kGroups][C::kRowBytes];  // of the warps that write results
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], joined, done;
   uint32_t tmem;
   int failed;
 };
 
-__device__ __forceinline__ float sigmoid_times(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+__device__ __forceinline__ uint64_t twice(float x) { return pair_of(x, x); }
+__device__ __forceinline__ uint64_t sigmoid_times(uint64_t y) {
+  const float2 t = both(mul2(y, twice(-1.44269504088896340736f)));
+  const float2 d = both(add2(pair_of(ex2(t.x), ex2(t.y)), twice(1.f)));
+  return mul2(y, pair_of(reciprocal(d.x), reciprocal(d.y)));
+}
 // y (1 + erf(y / sqrt 2)) / 2 with erfc(x) = t e^(-x^2 + P(t)), t = 1 / (1 + x / 2),
 // P of degree 9: Numerical Recipes' erfcc (Press et al., section 6.2), off by 1.2e-7
-// of itself at any x >= 0, so that the lower tail keeps its digits; -x^2 rounded
-// adds x^2 2^-23.
-__device__ __forceinline__ float gelu(float y) {
-  const float x = fabsf(y) * 0.70710678118654752f, t = __fdividef(1.f, fmaf(0.5f, x, 1.f));
-  float q = 0.17087277f;
-  q = fmaf(q, t, -0.82215223f);
-  q = fmaf(q, t, 1.48851587f);
-  q = fmaf(q, t, -1.13520398f);
-  q = fmaf(q, t, 0.27886807f);
-  q = fmaf(q, t, -0.18628806f);
-  q = fmaf(q, t, 0.09678418f);
-  q = fmaf(q, t, 0.37409196f);
-  q = fmaf(q, t, 1.00002368f);
-  q = fmaf(q, t, -1.26551223f);
-  const float half = 0.5f * t * __expf(fmaf(-x, x, q));  // the normal distribution's lower tail
-  return y * (y > 0.f ? 1.f - half : half);
+// of itself at any x >= 0, so that the lower tail keeps its digits; -x^2 = -y^2 / 2
+// rounded adds x^2 2^-23.  max(y, 0) - |y| erfc(|y| / sqrt 2) / 2 is that of either
+// sign; past 40, where the second part is 0, it stays so for infinity too.
+__device__ __forceinline__ uint64_t gelu(uint64_t y2) {
+  const float2 y = both(y2);
+  const uint64_t a = pair_of(fminf(fabsf(y.x), 40.f), fminf(fabsf(y.y), 40.f)), h = mul2(a, twice(-.5f));
+  const float2 d = both(fma2(a, twice(0.35355339059327376f), twice(1.f)));  // 1 to 16
+  const uint64_t t = mul2(twice(reciprocal(d.x * d.y)), pair_of(d.y, d.x));    // (one operation of the slow unit instead of two)
+  uint64_t q = twice(0.17087277f);
+  q = fma2(q, t, twice(-0.82215223f));
+  q = fma2(q, t, twice(1.48851587f));
+  q = fma2(q, t, twice(-1.13520398f));
+  q = fma2(q, t, twice(0.27886807f));
+  q = fma2(q, t, twice(-0.18628806f));
+  q = fma2(q, t, twice(0.09678418f));
+  q = fma2(q, t, twice(0.37409196f));
+  q = fma2(q, t, twice(1.00002368f));
+  q = fma2(q, t, twice(-1.26551223f));
+  const float2 e = both(mul2(fma2(h, a, q), twice(1.44269504088896340736f)));
+  return fma2(h, mul2(t, pair_of(ex2(e.x), ex2(e.y))), pair_of(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)));
 }
-__device__ __forceinline__ float of_bf16(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -111,101 +131,140 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // interleaved, both halves of 16, BLOCKS times eight rows at a time, as fragments:
 // a thread has lanes r8 + 8 j and two neighbouring rows of each block.  bf16
 // results go through shared memory as four 8 x 8 matrices (eight rows of 32
-// channels, or 16 of 16), rows 80 bytes apart so that they lie in different banks,
-// and from there to memory 16 bytes a thread; residuals come the same way, a trip
-// ahead.  (A loop of few instructions: in a short launch all of them are fetched
-// for the first time, which with 32 rows unrolled took longer than the products of
-// a small matrix.)
+// channels, or 16 of 16), their 16-byte pieces permuted so that a matrix's lie in
+// different banks, and from there to memory a piece per thread: at once, or as the
+// words between its ends where rows start on other boundaries.  Residuals come the
+// same way, a trip ahead.
 template <int GATE, int BLOCKS>
 struct Epilogue {
   static constexpr int kAcc = GATE == kTwoSums ? 2 : 1;
   static constexpr int kWidth = GATE == kInterleaved ? 16 : 32;      // channels of out
   static constexpr int kRows = 256 / kWidth, kSets = 8 * BLOCKS / kRows;  // rows of four matrices; sets of them
-  static constexpr int kParts = kWidth / 8;                          // 16-byte pieces of a row
+  static constexpr int kParts = kWidth / 8;                          // pieces of a row
+  static constexpr int kBytes = 16 * kParts * 8 * BLOCKS;            // of shared memory, a warp's beside the next one's of its group
+  // Where a tile's rows do not end and begin on 16 bytes, the four warps of a group write them together (or a warp by itself).
+  static constexpr bool kAlone = BLOCKS == 1;
+  // Eight channels of a row as loaded: 16 bytes, or from an address between words the words inside, then the last two
+  // bytes, and the first two.
+  struct Piece {
+    uint4 v;
+    uint32_t head;
+  };
+  // What the next trip and the next tile take: loads only, so that nothing waits for them before they are used.
+  struct Ahead {
+    Piece res[kSets];
+    float x_scale;                  // of row `lane` of the trip
+    float scale[kAcc], bias[kAcc];  // of channel `lane` of the warp's, or of lane % 16 in half lane / 16
+  };
   const Params& p;
   uint8_t* stage;                                                    // 8 BLOCKS rows of the warp's own
-  int lane, n0;
+  int warp, lane, n0;
   float scale[kAcc][4], bias[kAcc][4];
 
-  __device__ __forceinline__ Epilogue(const Params& q, uint8_t* st, int channel0, int ln) : p(q), stage(st), lane(ln), n0(channel0) {
+  __device__ __forceinline__ Epilogue(const Params& q, uint8_t* st, int w, int ln) : p(q), stage(st), warp(w), lane(ln) {}
+  __device__ __forceinline__ void group_sync() const { asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + (warp >> 2)) : "memory"); }
+  __device__ __forceinline__ void tile_ahead(int first, Ahead& a) const {
+    const int c = first + lane % kWidth;
+#pragma unroll
+    for (int h = 0; h < kAcc; ++h) {
+      const int n = c + (GATE == kInterleaved ? lane / kWidth : h) * p.width;
+      a.scale[h] = p.w_scale && c < p.width ? p.w_scale[n] : 1.f;
+      a.bias[h] = p.bias && c < p.width ? p.bias[n] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void tile(int first, const Ahead& a) {
+    n0 = first;
 #pragma unroll
     for (int h = 0; h < kAcc; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = n0 + (lane >> 2) + 8 * (GATE == kInterleaved ? j & 1 : j), n = c + (GATE == kInterleaved ? j >> 1 : h) * p.width;
-        const bool live = c < p.width;
-        scale[h][j] = live && p.w_scale ? p.w_scale[n] : 1.f;
-        bias[h][j] = live && p.bias ? p.bias[n] : 0.f;
+        scale[h][j] = __shfl_sync(0xffffffffu, a.scale[h], (lane >> 2) + 8 * j);
+        bias[h][j] = __shfl_sync(0xffffffffu, a.bias[h], (lane >> 2) + 8 * j);
       }
   }
-  __device__ __forceinline__ bool whole() const { return n0 + kWidth <= p.width; }
   // block and fragment of matrix k of set s
   __device__ __forceinline__ static constexpr int block_of(int s, int k) { return GATE == kInterleaved ? 2 * s + (k >> 1) : s; }
   __device__ __forceinline__ static constexpr int lane_of(int k) { return GATE == kInterleaved ? k & 1 : k; }
-  // this thread's row of set s
+  // piece k of row r in shared memory: eight rows' pieces k lie in different banks, and so do the pieces of two rows (four)
+  __device__ __forceinline__ uint8_t* slot(int r, int k) const { return stage + (r * kParts + (k ^ (r / (8 / kParts) & (kParts - 1)))) * 16; }
+  // this thread's row of matrix lane / 8 of set s
   __device__ __forceinline__ uint32_t matrix(int s) const {
-    const int k = lane >> 3, row = GATE == kInterleaved ? 8 * (k >> 1) + (lane & 7) : lane & 7;
-    return s32(stage) + (s * kRows + row) * kPitch + (GATE == kInterleaved ? k & 1 : k) * 16;
+    const int k = lane >> 3;
+    return s32(slot(s * kRows + (GATE == kInterleaved ? 8 * (k >> 1) : 0) + (lane & 7), GATE == kInterleaved ? k & 1 : k));
   }
-  // The residuals of the sets from row m on: 16 bytes of a row, or eight rows of a channel.
-  __device__ __forceinline__ void fetch(int m, uint4 (&res)[kSets]) const {
-    if (!p.residual || n0 >= p.width) return;
+  // this thread's piece of set s: its row, its first channel, and how many of its channels there are
+  __device__ __forceinline__ int row(int s) const { return s * kRows + lane / kParts; }
+  __device__ __forceinline__ static int channel(int first, int ln) { return first + ln % kParts * 8; }
+  __device__ __forceinline__ int there(int m, int c) const { return m < p.M ? p.width - c : 0; }
+  __device__ __forceinline__ static uint32_t word(uint32_t lo, uint32_t hi) { return __funnelshift_l(lo, hi, 16); }  // across a boundary
+  __device__ __forceinline__ static bool odd(const uint16_t* at) { return (reinterpret_cast<uintptr_t>(at) & 2) != 0; }
+  // The rows from m on at the channels from `first` on.
+  __device__ __forceinline__ void fetch(int first, int m, Ahead& a) const {
+    a.x_scale = p.x_scale && lane < 8 * BLOCKS && m + lane < p.M ? p.x_scale[m + lane] : 1.f;
+    if (!p.residual) return;
+    Piece(&res)[kSets] = a.res;
+    const int c = channel(first, lane);
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
-      if (p.vec_res && whole()) {
-        const int at = m + s * kRows + lane / kParts;
-        res[s] = at < p.M ? *reinterpret_cast<const uint4*>(p.residual + at * p.res_stride + n0 + lane % kParts * 8) : make_uint4(0, 0, 0, 0);
+      const int n = there(m + row(s), c);
+      const uint16_t* at = p.residual + (m + row(s)) * p.res_stride + c;
+      if (n >= 8 && p.vec_res) {
+        res[s].v = *reinterpret_cast<const uint4*>(at);
+      } else if (n >= 8) {
+        const bool o = odd(at);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(at + o);
+        if (o) res[s].head = *at;
+        res[s].v.x = w[0], res[s].v.y = w[1], res[s].v.z = w[2];
+        if (o) res[s].v.w = at[7];
+        else res[s].v.w = w[3];
       } else {
         uint32_t v[8];
-        const int row = m + s * kRows + lane / kWidth, c = n0 + lane % kWidth;
-        const uint16_t* at = p.residual + row * p.res_stride + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i, at += p.res_stride * (32 / kWidth)) v[i] = row + i * (32 / kWidth) < p.M && c < p.width ? *at : 0;
-        res[s] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? at[i] : 0;
+        res[s].v = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
       }
     }
   }
-  // Rows m .. m + 8 BLOCKS - 1 from their sums (kTwoSums: those of the second half in `u`).
-  __device__ __forceinline__ void rows(int m, float (&z)[BLOCKS][4][2], float (&u)[BLOCKS][4][2], const uint4 (&res)[kSets]) const {
-    if (n0 >= p.width) return;
+  // Residuals go to shared memory, in which the results follow them.
+  __device__ __forceinline__ void put(int m, const Ahead& a) const {
+    if (!p.residual) return;
+    const Piece(&res)[kSets] = a.res;
+    const int c = channel(n0, lane);
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      uint4 v = res[s].v;
+      if (!p.vec_res && there(m + row(s), c) >= 8 && odd(p.residual + (m + row(s)) * p.res_stride + c))
+        v = make_uint4(res[s].head | v.x << 16, word(v.x, v.y), word(v.y, v.z), v.z >> 16 | v.w << 16);
+      *reinterpret_cast<uint4*>(slot(row(s), lane % kParts)) = v;
+    }
+  }
+  // Rows m .. m + 8 BLOCKS - 1 from their sums (kTwoSums: those of the second half in `u`) and scales.
+  __device__ __forceinline__ void rows(int m, float x_scale, const float (&z)[BLOCKS][4][2], const float (&u)[BLOCKS][4][2]) const {
+    if (n0 >= p.width && (kAlone || p.out_f32)) return;
+    constexpr int kOut = GATE == kInterleaved ? 2 : 4;
+    uint64_t v[BLOCKS][kOut];
 #pragma unroll
     for (int b = 0; b < BLOCKS; ++b) {
-      const int m0 = m + 8 * b + 2 * (lane & 3);
-      const float s[2] = {p.x_scale && m0 < p.M ? p.x_scale[m0] : 1.f, p.x_scale && m0 + 1 < p.M ? p.x_scale[m0 + 1] : 1.f};
+      const int first = 8 * b + 2 * (lane & 3);
+      const uint64_t s = pair_of(__shfl_sync(0xffffffffu, x_scale, first), __shfl_sync(0xffffffffu, x_scale, first + 1));
+      auto sum = [&](const float (&x)[2], int h, int j) { return fma2(mul2(pair_of(x[0], x[1]), s), twice(scale[h][j]), twice(bias[h][j])); };
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          z[b][j][e] = fmaf(z[b][j][e] * s[e], scale[0][j], bias[0][j]);
-          if constexpr (GATE == kTwoSums) z[b][j][e] = sigmoid_times(z[b][j][e]) * fmaf(u[b][j][e] * s[e], scale[1][j], bias[1][j]);
-        }
-        if constexpr (GATE == kInterleaved)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) z[b][j][e] = sigmoid_times(z[b][j][e]) * z[b][j + 2][e];
+      for (int j = 0; j < kOut; ++j) {
+        v[b][j] = sum(z[b][j], 0, j);
+        if constexpr (GATE == kTwoSums) v[b][j] = mul2(sigmoid_times(v[b][j]), sum(u[b][j], 1, j));
+        if constexpr (GATE == kInterleaved) v[b][j] = mul2(sigmoid_times(v[b][j]), sum(z[b][j + 2], 0, j + 2));
       }
     }
     if constexpr (GATE == kNoGate) {
       if (p.act == KDA_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8 * BLOCKS; ++i) z[i >> 3][(i >> 1) & 3][i & 1] = sigmoid_times(z[i >> 3][(i >> 1) & 3][i & 1]);
+        for (int i = 0; i < 4 * BLOCKS; ++i) v[i >> 2][i & 3] = sigmoid_times(v[i >> 2][i & 3]);
       } else if (p.act == KDA_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8 * BLOCKS; ++i) z[i >> 3][(i >> 1) & 3][i & 1] = gelu(z[i >> 3][(i >> 1) & 3][i & 1]);
+        for (int i = 0; i < 4 * BLOCKS; ++i) v[i >> 2][i & 3] = gelu(v[i >> 2][i & 3]);
       }
     }
     if (p.residual) {
-#pragma unroll
-      for (int s = 0; s < kSets; ++s) {
-        if (p.vec_res && whole()) {
-          *reinterpret_cast<uint4*>(stage + (s * kRows + lane / kParts) * kPitch + lane % kParts * 16) = res[s];
-        } else {
-          const uint32_t w[4] = {res[s].x, res[s].y, res[s].z, res[s].w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint16_t*>(stage + (s * kRows + lane / kWidth + i * (32 / kWidth)) * kPitch + lane % kWidth * 2) =
-                static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-        }
-      }
       __syncwarp();
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
@@ -213,8 +272,8 @@ struct Epilogue {
         load_transposed(matrix(s), r);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float(&v)[2] = z[block_of(s, k)][lane_of(k)];
-          v[0] += of_bf16(r[k] & 0xffffu), v[1] += of_bf16(r[k] >> 16);
+          uint64_t& x = v[block_of(s, k)][lane_of(k)];
+          x = add2(x, pair_of(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xffff0000u)));
         }
       }
       __syncwarp();
@@ -228,7 +287,7 @@ struct Epilogue {
         for (int e = 0; e < 2; ++e, out += p.out_stride)
 #pragma unroll
           for (int j = 0; j < kParts; ++j)
-            if (m0 + e < p.M && n0 + (lane >> 2) + 8 * j < p.width) out[8 * j] = z[b][j][e];
+            if (m0 + e < p.M && n0 + (lane >> 2) + 8 * j < p.width) out[8 * j] = e ? both(v[b][j]).y : both(v[b][j]).x;
       }
       return;
     }
@@ -236,25 +295,52 @@ struct Epilogue {
     for (int s = 0; s < kSets; ++s) {
       uint32_t r[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = pack_bf16(z[block_of(s, k)][lane_of(k)][0], z[block_of(s, k)][lane_of(k)][1]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = both(v[block_of(s, k)][lane_of(k)]);
+        r[k] = pack_bf16(x.x, x.y);
+      }
       store_transposed(matrix(s), r);
     }
     __syncwarp();
+    const int tile0 = kAlone ? n0 : n0 - (warp & 3) * kWidth;  // the first channel written together
+    if (p.vec_out && tile0 + (kAlone ? 1 : 4) * kWidth <= p.width) {
+      const int c = channel(n0, lane);
 #pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-      if (p.vec_out && whole()) {
-        const int at = m + s * kRows + lane / kParts;
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + (s * kRows + lane / kParts) * kPitch + lane % kParts * 16);
-        if (at < p.M) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_stride + n0 + lane % kParts * 8) = v;
-      } else {
-        const int row = s * kRows + lane / kWidth, c = n0 + lane % kWidth;
-        uint16_t* out = static_cast<uint16_t*>(p.out) + (m + row) * p.out_stride + c;
+      for (int s = 0; s < kSets; ++s)
+        if (m + row(s) < p.M)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (m + row(s)) * p.out_stride + c) =
+              *reinterpret_cast<const uint4*>(slot(row(s), lane % kParts));
+    } else {
+      // Of a row its 16-byte vectors, a thread each, from two pieces each, and what is left at its ends.
+      constexpr int kLanes = (kAlone ? 1 : 4) * kParts, kAtOnce = 32 / kLanes, kMine = 8 * BLOCKS / (kAlone ? 1 : 4);
+      const int l = lane % kLanes, width = min(p.width - tile0, (kAlone ? 1 : 4) * kWidth);
+      if constexpr (!kAlone) group_sync();
+#pragma unroll 2
+      for (int k = lane / kLanes; k < kMine; k += kAtOnce) {
+        const int r = (kAlone ? 0 : (warp & 3) * kMine) + k;
+        if (m + r >= p.M) continue;
+        uint16_t* const out = static_cast<uint16_t*>(p.out) + (m + r) * p.out_stride + tile0;
+        // piece q of the row, in all warps' memory
+        auto piece = [&](int q) { return slot(r, q % kParts) + (q / kParts - (kAlone ? 0 : warp & 3)) * kBytes; };
+        const int head = min(-static_cast<int>(reinterpret_cast<uintptr_t>(out) >> 1) & 7, width), vectors = (width - head) / 8;
+        if (l < vectors) {
+          const uint4 a = *reinterpret_cast<const uint4*>(piece(l)), b = *reinterpret_cast<const uint4*>(piece(min(l + 1, kLanes - 1)));
+          uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i, out += p.out_stride * (32 / kWidth)) {
-          const uint16_t v = *reinterpret_cast<const uint16_t*>(stage + (row + i * (32 / kWidth)) * kPitch + lane % kWidth * 2);
-          if (m + row + i * (32 / kWidth) < p.M && c < p.width) *out = v;
+          for (int i = 0; i < 6; ++i) x[i] = head & 4 ? x[i + 2] : x[i];
+#pragma unroll
+          for (int i = 0; i < 5; ++i) x[i] = head & 2 ? x[i + 1] : x[i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = head & 1 ? word(x[i], x[i + 1]) : x[i];
+          *reinterpret_cast<uint4*>(out + head + 8 * l) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        for (int e = l; e < 8; e += kLanes) {
+          const int c = head + 8 * vectors + e;
+          if (e < head) out[e] = *reinterpret_cast<const uint16_t*>(piece(0) + 2 * e);
+          if (c < width) out[c] = *reinterpret_cast<const uint16_t*>(piece(c / 8) + c % 8 * 2);
         }
       }
+      if constexpr (!kAlone) group_sync();
     }
     __syncwarp();
   }
@@ -266,11 +352,10 @@ constexpr int kGroup = 10;
 struct TileAt {
   int nt, mt;
   __device__ __forceinline__ TileAt(const Params& p, int tile) {
-    const int groups = (p.m_tiles + kGroup - 1) / kGroup, size = (p.m_tiles + groups - 1) / groups;
-    const int g = tile / (size * p.n_tiles), first = g * size;
-    const int here = min(size, p.m_tiles - first), r = tile - first * p.n_tiles;
-    nt = r / here;
-    mt = first + r - nt * here;
+    const int g = p.group.of(tile), first = g * static_cast<int>(p.rows.by), r = tile - first * p.n_tiles;
+    const bool ends = first + static_cast<int>(p.rows.by) >= p.m_tiles;
+    nt = ends ? p.last.of(r) : p.rows.of(r);
+    mt = first + r - nt * static_cast<int>(ends ? p.last.by : p.rows.by);
   }
 };
 
@@ -452,32 +537,47 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const Parts<C> part(p.split);
     uint8_t* const sent = raw + p.split * part.bytes;  // what the others send
+    using E = Epilogue<GATE, C::kUnroll>;
+    constexpr int kStep = 8 * C::kUnroll;
+    auto channel_of = [&](const TileAt& at) { return (kPair * at.nt + half) * C::kChannels; };
+    TileAt at(p, first);
+    E e(p, S.rows[warp], warp, lane);
+    static_assert(E::kBytes == C::kRowBytes, "a warp's results");
+    typename E::Ahead ahead = {};
+    if (mine > 0 && p.split == 1) {
+      e.tile_ahead(channel_of(at) + wq * E::kWidth, ahead);
+      e.fetch(channel_of(at) + wq * E::kWidth, at.mt * ROWS + kStep * group, ahead);
+    }
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
-      const TileAt at(p, first + i * step);
-      const int m0 = at.mt * ROWS;
-      using E = Epilogue<GATE, C::kUnroll>;
-      const int channel0 = (kPair * at.nt + half) * C::kChannels;
-      E e(p, S.rows[warp], channel0 + wq * E::kWidth, lane);
-      constexpr int kStep = 8 * C::kUnroll;
-      uint4 ahead[E::kSets] = {};
-      if (p.split == 1) e.fetch(m0 + kStep * group, ahead);
-      if (p.x_scale && lane < ROWS / 32 + 1 && m0 + 32 * lane < p.M) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.x_scale + m0 + 32 * lane));
+      const int m0 = at.mt * ROWS, channel0 = channel_of(at);
+      e.tile(channel0 + wq * E::kWidth, ahead);
+      if (i + 1 < mine) {
+        at = TileAt(p, first + (i + 1) * step);
+        e.tile_ahead(channel_of(at) + wq * E::kWidth, ahead);
+      }
       if (lane == 0) bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);  // (one lane: polls are not free for the issuer)
       __syncwarp();
       tc_after();
       if (p.split == 1) {
-#pragma unroll 1
-        for (int col = kStep * group; col < ROWS && m0 + col < p.M; col += kStep * C::kGroups) {
-          float z[C::kUnroll][4][2], u[C::kUnroll][4][2];
-          tm_fragments(lanes + buf * C::kCols + col, z);
-          if constexpr (GATE == kTwoSums) tm_fragments(lanes + buf * C::kCols + ROWS + col, u);
-          uint4 res[E::kSets];
-#pragma unroll
-          for (int i = 0; i < E::kSets; ++i) res[i] = ahead[i];
-          if (col + kStep * C::kGroups < ROWS) e.fetch(m0 + col + kStep * C::kGroups, ahead);
-          e.rows(m0 + col, z, u, res);
-        }
+const int rows = min(ROWS, p.M - m0);
+        bool last;
+        int col = kStep * group;
+        do {  // (a group without rows only fetches for the next tile)
+          const bool here = col < rows;
+          if (here) e.put(m0 + col, ahead);
+          const float x_scale = ahead.x_scale;
+          last = col + kStep * C::kGroups >= rows;
+          if (!last || i + 1 < mine)
+            e.fetch(last ? channel_of(at) + wq * E::kWidth : e.n0, last ? at.mt * ROWS + kStep * group : m0 + col + kStep * C::kGroups, ahead);
+          if (here) {
+            float z[C::kUnroll][4][2], u[C::kUnroll][4][2];
+            tm_fragments(lanes + buf * C::kCols + col, z);
+            if constexpr (GATE == kTwoSums) tm_fragments(lanes + buf * C::kCols + ROWS + col, u);
+            e.rows(m0 + col, x_scale, z, u);
+          }
+          col += kStep * C::kGroups;
+        } while (!last);
       } else {  // this CTA's sums, where the stages were
         uint8_t* const to = raw + (32 * wq / part.channels) * part.bytes;
 #pragma unroll 1
@@ -494,8 +594,8 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
       tc_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (PAIR) bar_arrive_at(in_cta(&S.acc_empty[buf], even));
-        else bar_arrive(&S.acc_empty[buf]);
+        if constexpr (PAIR) bar_signal_at(in_cta(&S.acc_empty[buf], even));
+        else bar_signal(&S.acc_empty[buf]);
       }
       if constexpr (GATE == kInterleaved) continue;  // (never split)
       else if (p.split > 1) {  // (this cluster's only tile)
@@ -510,15 +610,17 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
         // blocks of 32 channels and a few rows, a warp each
         const int wide = part.channels / 32, cb = warp % wide * 32;
         using Own = Epilogue<GATE, 1>;
-        const Own own(p, S.rows[warp], channel0 + share * part.channels + cb, lane);
+        Own own(p, S.rows[warp], warp, lane);
+        typename Own::Ahead own_ahead = {};
+        own.tile_ahead(channel0 + share * part.channels + cb, own_ahead);
+        own.tile(channel0 + share * part.channels + cb, own_ahead);
         if (lane == 0) bar_wait(&S.joined, 0, &S.failed);
         __syncwarp();
 #pragma unroll 1
         for (int block = warp; block < wide * (ROWS / 8); block += 4 * C::kGroups) {
           const int col = block / wide * 8;
           if (m0 + col >= p.M) break;
-          uint4 res[1] = {};
-          own.fetch(m0 + col, res);
+          own.fetch(own.n0, m0 + col, own_ahead);
           float s[2][1][4][2] = {};
 #pragma unroll 1
           for (int r = 0; r < p.split; ++r)
@@ -530,7 +632,8 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
                     part.at((r == share ? raw : sent) + r * part.bytes, h, col / 2 + (lane & 3), cb + (lane >> 2) + 8 * j));
                 s[h][0][j][0] += v.x, s[h][0][j][1] += v.y;
               }
-          own.rows(m0 + col, s[0], s[1], res);
+          own.put(m0 + col, own_ahead);
+          own.rows(m0 + col, own_ahead.x_scale, s[0], s[1]);
         }
       }
     }
@@ -728,6 +831,9 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const int64_t m_tiles = tiles_of(a->M, v.rows), n_tiles = tiles_of(width, v.channels);
   if (m_tiles * n_tiles > 0x7fffffff / 16) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
   p.m_tiles = static_cast<int>(m_tiles), p.n_tiles = static_cast<int>(n_tiles), p.blocks = blocks;
+  const int groups = static_cast<int>((m_tiles + kGroup - 1) / kGroup), of_group = static_cast<int>((m_tiles + groups - 1) / groups);
+  p.group = Divisor(static_cast<uint32_t>(of_group * n_tiles)), p.rows = Divisor(static_cast<uint32_t>(of_group));
+  p.last = Divisor(static_cast<uint32_t>(m_tiles - (m_tiles - 1) / of_group * of_group));
   p.split = plan.split, p.stages = plan.stages;
   p.act = a->activation, p.out_f32 = f32, p.early = a->flags & KDA_LINEAR_EARLY_WEIGHT;
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
