@@ -49,6 +49,7 @@ struct Divisor {
 struct Params {
   int M, N, K, width;          // width: channels of out
   int m_tiles, n_tiles, blocks;  // row tiles, channel tiles (of a CTA or pair), blocks of k
+  int tile_rows;               // rows of a row tile, at most the variant's
   Divisor group, rows, last;   // tiles of a group of row tiles; row tiles of one, and of the last one
   int split, stages;           // CTAs (or pairs) per tile, ring depth
   int act;
@@ -71,14 +72,13 @@ struct Cfg {
   static constexpr int kChannels = GATE == kInterleaved ? kTileN / 2 : kTileN;  // of out, of a CTA
   static constexpr int kUnroll = PAIR || ROWS > 64 ? 4 : 2;  // blocks of eight rows that a warp writes at a time
   static constexpr int kRowBytes = 8 * kUnroll * kChannels / 4 * 2;  // of these rows
-  static constexpr int kWeightBytes = kAcc * kTileN * kBlock, kXRows = PAIR ? ROWS / 2 : ROWS;
-  static constexpr int kStageBytes = kWeightBytes + kXRows * kBlock;
+  static constexpr int kWeightBytes = kAcc * kTileN * kBlock, kStageBytes = kWeightBytes + ROWS / (PAIR ? 2 : 1) * kBlock;
   static constexpr int kCols = kAcc * ROWS;      // accumulator columns of a tile, of which there are two sets
   static constexpr int kTmemCols = 2 * kCols;    // a power of two from 32 on
   // One CTA takes an SM's shared memory; where a short range of k leaves room, the next call's CTAs start beside it.
-  static constexpr int kCtasPerSm = PAIR || ROWS > 64 ? 1 : 2;
+  static constexpr int kCtasPerSm = PAIR || ROWS > 32 ? 1 : 2;
   // warpgroups that write results; then a warp that copies weights, one that copies rows, and the issuer
-  static constexpr int kGroups = kCtasPerSm == 2 ? 1 : GATE == kTwoSums ? 2 : 4, kThreads = 128 * kGroups + 96;
+  static constexpr int kGroups = GATE == kTwoSums ? (ROWS > 32 ? 2 : 1) : ROWS < 64 ? ROWS / 16 : 4, kThreads = 128 * kGroups + 96;
   // sums of a tile that several CTAs share: in the stages, when its products have ended, lie a CTA's own and those sent to it
   static constexpr int kPartBytes = kCols / 2 * (kTileN * 8 + 64 * kMaxSplit);
   static_assert(kTmemCols * kCtasPerSm <= 512, "tensor memory");
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
   const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (share + 1) / p.split);
   const int tiles = p.m_tiles * p.n_tiles, mine = first < tiles ? (tiles - first + step - 1) / step : 0;  // tiles of this cluster
   // columns of the products of a row tile: fewer in one that ends early
-  auto columns = [&](int mt) { return min(ROWS, (p.M - mt * ROWS + 16 * kPair - 1) / (16 * kPair) * (16 * kPair)); };
+  auto columns = [&](int mt) { return min(p.tile_rows, (p.M - mt * p.tile_rows + 16 * kPair - 1) / (16 * kPair) * (16 * kPair)); };
   if (warp == kCopies || warp == kCopies + 1) {
     // ================================================== copies: weights, rows of x
     // (Two warps: one issuing both took longer for them than a short tile's products.)
@@ -482,9 +482,9 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
         }
       });
     } else {
-      produce(C::kXRows * kBlock, false, [&](int st, const TileAt& at, int k) {
+      produce(p.tile_rows / kPair * kBlock, false, [&](int st, const TileAt& at, int k) {
         const uint32_t dst = s32(raw) + st * C::kStageBytes + C::kWeightBytes;
-        const int x = k * kBlock, y = at.mt * ROWS + (PAIR ? half * columns(at.mt) / 2 : 0);
+        const int x = k * kBlock, y = at.mt * p.tile_rows + (PAIR ? half * columns(at.mt) / 2 : 0);
         if constexpr (PAIR) tma_2d_pair(dst, &x_map, x, y, in_cta(&S.full[st], even));
         else tma_2d(dst, &x_map, x, y, &S.full[st]);
       });
@@ -546,11 +546,11 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
     typename E::Ahead ahead = {};
     if (mine > 0 && p.split == 1) {
       e.tile_ahead(channel_of(at) + wq * E::kWidth, ahead);
-      e.fetch(channel_of(at) + wq * E::kWidth, at.mt * ROWS + kStep * group, ahead);
+      e.fetch(channel_of(at) + wq * E::kWidth, at.mt * p.tile_rows + kStep * group, ahead);
     }
     for (int i = 0; i < mine; ++i) {
       const uint32_t buf = i & 1;
-      const int m0 = at.mt * ROWS, channel0 = channel_of(at);
+      const int m0 = at.mt * p.tile_rows, rows = min(p.tile_rows, p.M - m0), channel0 = channel_of(at);
       e.tile(channel0 + wq * E::kWidth, ahead);
       if (i + 1 < mine) {
         at = TileAt(p, first + (i + 1) * step);
@@ -560,7 +560,6 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
       __syncwarp();
       tc_after();
       if (p.split == 1) {
-const int rows = min(ROWS, p.M - m0);
         bool last;
         int col = kStep * group;
         do {  // (a group without rows only fetches for the next tile)
@@ -569,7 +568,7 @@ const int rows = min(ROWS, p.M - m0);
           const float x_scale = ahead.x_scale;
           last = col + kStep * C::kGroups >= rows;
           if (!last || i + 1 < mine)
-            e.fetch(last ? channel_of(at) + wq * E::kWidth : e.n0, last ? at.mt * ROWS + kStep * group : m0 + col + kStep * C::kGroups, ahead);
+            e.fetch(last ? channel_of(at) + wq * E::kWidth : e.n0, last ? at.mt * p.tile_rows + kStep * group : m0 + col + kStep * C::kGroups, ahead);
           if (here) {
             float z[C::kUnroll][4][2], u[C::kUnroll][4][2];
             tm_fragments(lanes + buf * C::kCols + col, z);
@@ -581,7 +580,7 @@ const int rows = min(ROWS, p.M - m0);
       } else {  // this CTA's sums, where the stages were
         uint8_t* const to = raw + (32 * wq / part.channels) * part.bytes;
 #pragma unroll 1
-        for (int col = 8 * group; col < ROWS && m0 + col < p.M; col += 8 * C::kGroups)
+        for (int col = 8 * group; col < rows; col += 8 * C::kGroups)
 #pragma unroll
           for (int h = 0; h < C::kAcc; ++h) {
             float z[1][4][2];
@@ -619,7 +618,7 @@ const int rows = min(ROWS, p.M - m0);
 #pragma unroll 1
         for (int block = warp; block < wide * (ROWS / 8); block += 4 * C::kGroups) {
           const int col = block / wide * 8;
-          if (m0 + col >= p.M) break;
+          if (col >= rows) break;
           own.fetch(own.n0, m0 + col, own_ahead);
           float s[2][1][4][2] = {};
 #pragma unroll 1
@@ -674,27 +673,27 @@ EncodeFn g_encode;
 using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap);
 // What a kernel takes, with and without the gate, for bf16 and e4m3.
 struct Variant {
-  int rows, x_rows, channels;  // rows of a tile; of x per copy; channels of out per tile
+  int rows, unit, channels;    // rows of a tile, at most, and what they are a multiple of; channels of out per tile
   bool pair, interleaved;
   Kernel kernel[2];  // bf16, e4m3
   int threads;
   int stage_bytes, part_bytes, head_bytes;
-  float start, block, join;  // us, see plan_of
+  float start, block, join, results;  // us, see plan_of
 };
 template <int ROWS, int GATE, bool PAIR>
-Variant variant(float start, float block, float join) {
+Variant variant(float start, float block, float join, float results) {
   using C = Cfg<ROWS, GATE, PAIR>;
-  return {ROWS, C::kXRows, C::kChannels * (PAIR ? 2 : 1), PAIR, GATE == kInterleaved, {linear_kernel<ROWS, false, GATE, PAIR>, linear_kernel<ROWS, true, GATE, PAIR>},
-          C::kThreads, C::kStageBytes, C::kPartBytes, static_cast<int>(sizeof(Head<C>)), start, block, join};
+  return {ROWS, 8 * C::kUnroll, C::kChannels * (PAIR ? 2 : 1), PAIR, GATE == kInterleaved, {linear_kernel<ROWS, false, GATE, PAIR>, linear_kernel<ROWS, true, GATE, PAIR>},
+          C::kThreads, C::kStageBytes, C::kPartBytes, static_cast<int>(sizeof(Head<C>)), start, block, join, results};
 }
 constexpr int kPlain = 6, kGatedVariants = 5;
 const Variant kVariants[kPlain + kGatedVariants] = {
-    variant<16, kNoGate, false>(4.5f, .146f, .6f), variant<32, kNoGate, false>(4.7f, .17f, 1.f),
-    variant<64, kNoGate, false>(5.3f, .22f, 1.6f), variant<128, kNoGate, false>(6.f, .246f, 4.f),
-    variant<128, kNoGate, true>(6.3f, .195f, 3.f), variant<256, kNoGate, true>(7.2f, .26f, 0.f),
-    variant<16, kTwoSums, false>(4.8f, .26f, 1.f), variant<32, kTwoSums, false>(5.f, .28f, 1.5f),
-    variant<64, kTwoSums, false>(5.8f, .33f, 2.5f), variant<128, kTwoSums, false>(7.f, .4f, 0.f),
-    variant<256, kInterleaved, true>(8.f, .3f, 0.f)};
+    variant<16, kNoGate, false>(4.5f, .146f, .6f, .8f), variant<32, kNoGate, false>(4.7f, .17f, 1.f, 1.2f),
+    variant<64, kNoGate, false>(5.3f, .22f, 1.6f, 2.4f), variant<128, kNoGate, false>(6.f, .246f, 4.f, 2.1f),
+    variant<128, kNoGate, true>(6.3f, .195f, 3.f, 1.7f), variant<256, kNoGate, true>(7.2f, .26f, 0.f, 3.2f),
+    variant<16, kTwoSums, false>(4.8f, .26f, 1.f, 1.f), variant<32, kTwoSums, false>(5.f, .28f, 1.5f, 1.6f),
+    variant<64, kTwoSums, false>(5.8f, .33f, 2.5f, 3.f), variant<128, kTwoSums, false>(7.f, .4f, 0.f, 4.f),
+    variant<256, kInterleaved, true>(8.f, .3f, 0.f, 3.2f)};
 constexpr int kSmemLimit = 227 * 1024;  // of a CTA
 
 cudaError_t setup(int* sms) {
@@ -724,9 +723,9 @@ cudaError_t setup(int* sms) {
 // What a call runs with: the variant, CTAs (or pairs) that share a tile, ring depth.
 struct Plan {
   const Variant* variant;
-  int split, stages;
+  int split, stages, tile_rows;
 };
-int64_t tiles_of(int n, int size) { return (static_cast<int64_t>(n) + size - 1) / size; }
+int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
 // The variant and split with the least expected time, in us: what a launch takes
 // from its start to its first product and from its last to its results, waves of
 // tiles at a time per block of k each, the weights from HBM meanwhile, and what joining takes each time a tile is shared by twice as many.  Measured on
@@ -736,22 +735,27 @@ int64_t tiles_of(int n, int size) { return (static_cast<int64_t>(n) + size - 1) 
 // tiles of 128 rows (11.5 with 256, 9.0 with 64 rows and one CTA); bf16, 512 x 4,096 x
 // 4,096, 18.9 with pairs and 128 rows (23.6 with 256, 21.8 with 128 and one CTA).
 Plan plan_of(int M, int width, int blocks, bool gated, double bytes, int sms) {
-  Plan best{nullptr, 1, 0};
+  Plan best{nullptr, 1, 0, 0};
   double least = 0;
   for (int i = gated ? kPlain : 0; i < (gated ? kPlain + kGatedVariants : kPlain); ++i) {
     const Variant& v = kVariants[i];
     const int most = std::min((kSmemLimit - v.head_bytes) / v.stage_bytes, kMaxStages);
-    const int64_t tiles = tiles_of(width, v.channels) * tiles_of(M, v.rows), at_once = v.pair ? sms / 2 : sms;
+    // row tiles of much the same height (300 rows as 160 and 140 instead of 256 and 44)
+    const int64_t m_tiles = tiles_of(M, v.rows);
+    const int tile_rows = static_cast<int>(std::min<int64_t>(v.rows, tiles_of(tiles_of(M, m_tiles), v.unit) * v.unit));
+    const double height = m_tiles > 1 ? static_cast<double>(tile_rows) / v.rows : 1;
+    const int64_t tiles = tiles_of(width, v.channels) * m_tiles, at_once = v.pair ? sms / 2 : sms;
     for (int split = 1, log2 = 0; split <= kMaxSplit; split *= 2, ++log2) {
       if (split > 1 && (v.interleaved || tiles * split > at_once || split > blocks || 2 * v.part_bytes > most * v.stage_bytes)) break;
       const int64_t waves = (tiles * split + at_once - 1) / at_once;
       // (of the waves' time and the weights' the shorter hides behind the longer but for some three tenths)
-      const double compute = static_cast<double>(waves) * tiles_of(blocks, split) * v.block, memory = bytes / 6.5e6;
+      const double products = tiles_of(blocks, split) * v.block * (.5 + .5 * height), results = v.results * height;
+      const double compute = products + (waves - 1) * std::max(products, results), memory = bytes / 6.5e6;
       const double us = v.start + std::max(compute, memory) + .3 * std::min(compute, memory) + log2 * v.join;
       if (best.variant && us >= least) continue;
       // no more stages than there is to copy, but room for the sums of a tile in parts
       const int64_t copies = waves * tiles_of(blocks, split), sums = split > 1 ? tiles_of(2 * v.part_bytes, v.stage_bytes) : 1;
-      best = {&v, split, static_cast<int>(std::min<int64_t>(most, std::max(copies, sums)))};
+      best = {&v, split, static_cast<int>(std::min<int64_t>(most, std::max(copies, sums))), tile_rows};
       least = us;
     }
   }
@@ -820,7 +824,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   if (r == CUDA_SUCCESS) {
     const cuuint64_t dims[2] = {k_bytes, static_cast<cuuint64_t>(a->M)};
     const cuuint64_t strides[1] = {x_pitch};
-    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(v.x_rows)};
+    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(plan.tile_rows / (v.pair ? 2 : 1))};
     r = g_encode(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a->x), dims, strides, box, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -828,13 +832,13 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
   Params p{};
   p.M = a->M, p.N = a->N, p.K = a->K, p.width = width;
-  const int64_t m_tiles = tiles_of(a->M, v.rows), n_tiles = tiles_of(width, v.channels);
+  const int64_t m_tiles = tiles_of(a->M, plan.tile_rows), n_tiles = tiles_of(width, v.channels);
   if (m_tiles * n_tiles > 0x7fffffff / 16) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
   p.m_tiles = static_cast<int>(m_tiles), p.n_tiles = static_cast<int>(n_tiles), p.blocks = blocks;
   const int groups = static_cast<int>((m_tiles + kGroup - 1) / kGroup), of_group = static_cast<int>((m_tiles + groups - 1) / groups);
   p.group = Divisor(static_cast<uint32_t>(of_group * n_tiles)), p.rows = Divisor(static_cast<uint32_t>(of_group));
   p.last = Divisor(static_cast<uint32_t>(m_tiles - (m_tiles - 1) / of_group * of_group));
-  p.split = plan.split, p.stages = plan.stages;
+  p.split = plan.split, p.stages = plan.stages, p.tile_rows = plan.tile_rows;
   p.act = a->activation, p.out_f32 = f32, p.early = a->flags & KDA_LINEAR_EARLY_WEIGHT;
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
   p.residual = a->residual, p.res_stride = a->residual_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
