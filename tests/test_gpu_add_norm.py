@@ -55,6 +55,15 @@ def test_matches_64_bits(T, D, residual, cuda_device):
     check(got, x, w, r)
 
 
+@pytest.mark.parametrize("T, D", [(1, 1536), (2, 1544), (3, 504), (5, 1024), (4097, 512), (2049, 1288), (6, 520)])
+def test_short_rows(T, D, cuda_device):
+    # rows of a warp each, several to a CTA, and the first that are not
+    x, r, w = inputs(T, D, T * D)
+    got = outputs(T, D, cuda_device, pad=8)
+    kda_add_norm(x.to(cuda_device), weight=w.to(cuda_device), residual=r.to(cuda_device), **got)
+    check(got, x, w, r)
+
+
 @pytest.mark.parametrize("T, D", [(1, 8), (3, 264), (5, 6144), (41, 4608), (2, 32768)])
 def test_without_norm_or_weight(T, D, cuda_device):
     x, r, _ = inputs(T, D, T * D)

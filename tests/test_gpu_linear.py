@@ -45,6 +45,55 @@ def test_whole_numbers_are_exact(M, N, K, e4m3, cuda_device):
     assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("e4m3, M, N, K", [
+    (False, 17, 16, 16), (False, 2, 17, 592), (False, 22, 16, 592), (False, 2, 19, 1168), (False, 20, 29, 1168),   # 16 rows
+    (False, 27, 9742, 16), (True, 617, 386, 16), (False, 27, 4897, 1456), (False, 311, 401, 1264), (False, 19, 2472, 4096),
+    (False, 762, 16, 3536),                                                                                        # 32 rows
+    (False, 52, 9788, 32), (True, 816, 667, 16), (False, 50, 5323, 2624), (False, 2484, 18, 2576), (False, 51, 2532, 6032),
+    (False, 1364, 20, 6048),                                                                                       # 64 rows
+    (False, 102, 9779, 16), (False, 986, 1158, 16), (False, 4911, 21, 3472),                                       # 128 rows
+    (False, 108, 9959, 416), (False, 1225, 973, 368), (False, 117, 4895, 2496), (False, 2842, 130, 2128),
+    (False, 99, 2463, 5680), (False, 1217, 154, 5824),                                                             # pairs, 128 rows
+    (False, 203, 9760, 16), (False, 1310, 1676, 16), (True, 300, 20000, 256), (True, 2900, 1537, 384)])            # 256 rows
+def test_every_tile_and_share_of_k(e4m3, M, N, K, cuda_device):
+    # one row tile and several, a tile's products in one, two and four parts; results in fp32, and in bf16 onto a residual
+    # in rows on no boundary: sums are whole numbers below 2^24, so there is one right answer
+    g = torch.Generator().manual_seed(M + N + K)
+    x, w = whole_numbers((M, K), g, e4m3), whole_numbers((N, K), g, e4m3)
+    one = dict(x_scale=torch.ones(M, device=cuda_device), weight_scale=torch.ones(N, device=cuda_device)) if e4m3 else {}
+    want = x.float() @ w.float().t()
+    xd, wd = x.to(cuda_device), w.to(cuda_device)
+    for early in (False, True):
+        out = torch.full((M, N), float("nan"), device=cuda_device)
+        kda_linear(xd, wd, out, early_weight=early, **one)
+        assert torch.equal(out.cpu(), want)
+    res = torch.randint(-100, 101, (M, N), generator=g).bfloat16()
+    want = (want + res.float()).bfloat16()
+    for at in (0, 1, 2, 3):
+        for pitch in (N + 5, (N + 15) // 8 * 8):
+            buf = torch.full((M, pitch), 3.0, dtype=torch.bfloat16, device=cuda_device)
+            view = buf[:, at:at + N]
+            view.copy_(res.to(cuda_device))
+            kda_linear(xd, wd, view, residual=view, **one)
+            assert torch.equal(view.cpu(), want), (at, pitch)
+            assert (buf[:, :at] == 3.0).all() and (buf[:, at + N:] == 3.0).all(), (at, pitch)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("e4m3, M, N, K", [(True, 18, 16, 16), (False, 17, 26, 464), (False, 36, 30, 912), (False, 614, 800, 16),
+                                           (False, 1282, 22, 976), (False, 632, 26, 2480), (True, 1246, 824, 16),
+                                           (False, 2682, 26, 1904), (False, 1451, 22, 4768), (False, 1686, 1290, 16),
+                                           (True, 1327, 3590, 16), (True, 300, 6002, 272)])
+def test_every_gated_tile(e4m3, M, N, K, f32, cuda_device):
+    p = problem(M, N, K, e4m3, "silu_gated", True, not f32, M)
+    d = {k: v.to(cuda_device) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    for pad in (0, 3):
+        out = torch.full((M, N // 2 + pad), 9.0, dtype=torch.float32 if f32 else torch.bfloat16, device=cuda_device)
+        kda_linear(out=out[:, :N // 2], **d)
+        close(out[:, :N // 2], p, not f32)
+        assert (out[:, N // 2:] == 9.0).all()
+
+
 def problem(M, N, K, e4m3, act, bias, residual, seed):
     g = torch.Generator().manual_seed(seed)
     p = dict(x=torch.randn(M, K, generator=g), weight=torch.randn(N, K, generator=g) / math.sqrt(K))
