@@ -10,7 +10,9 @@
  *   out[m][n] = silu(y[m][n]) * y[m][H + n] + residual[m][n], n < H
  * x and weight are both bf16 (no scales), or both e4m3 with one scale per row
  * of each, as kda_add_norm.h makes them.  Products are exact and summed in
- * fp32; the epilogue is fp32 and rounded once, to out's type.  A row of x that
+ * fp32 (by tensor cores, which cut sums towards zero: fp32 results from short
+ * sums, so that they are off by no more than about 2^-20 of sums without much
+ * cancellation); the epilogue is fp32 and rounded once, to out's type.  A row of x that
  * is not finite, or whose scale is NaN, reaches no other row.
  */
 #ifndef KDA_LINEAR_H

@@ -34,6 +34,13 @@ constexpr int kTileN = 128;                // channels of a CTA's tile
 constexpr int kBlock = 128;                // bytes of k per stage
 constexpr int kMaxSplit = 4;
 constexpr int kMaxStages = 12;
+// Blocks of k that the tensor cores add up in one sum.  They cut every addition towards zero, which shortens the sum by
+// about 2^-26 of itself per 16 products of bf16 (an eighth of that per 32 of e4m3), always in the same direction: by 2e-5
+// at 16,384 of k.  So fp32 results are made from sums of 896 of k (e4m3 10,752), which are then added up in fp32 with
+// rounding, in the second accumulator: they are off by 1e-6 of themselves, as sums with rounding are, at any k.  bf16
+// results, whose rounding is 2^-9, are made from sums of 65,536 (786,432).  A part's end costs 0.8 us, as the products
+// wait for the accumulator: 4,096 x 8,192 x 4,096 take 153 us in bf16, 163 in fp32 from sums of 2,048 (off by 2e-6) and 189 from 896.
+constexpr int kSegmentF32 = 14, kSegmentBf16 = 1024, kLongerE4m3 = 6;
 
 // Quotients of 0 .. 2^31 - 1 by a divisor of a launch (Granlund and Montgomery 1994, section 4).
 struct Divisor {
@@ -52,6 +59,7 @@ struct Params {
   int tile_rows;               // rows of a row tile, at most the variant's
   Divisor group, rows, last;   // tiles of a group of row tiles; row tiles of one, and of the last one
   int split, stages;           // CTAs (or pairs) per tile, ring depth
+  int segment;                 // blocks of k that the tensor cores sum up at a time
   int act;
   bool out_f32, early, vec_out, vec_res;  // vec: rows in 16-byte pieces
   const float *x_scale, *w_scale, *bias;
@@ -500,11 +508,21 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
         if constexpr (PAIR) commit_both(b, even);
         else commit(b);
       };
+      const bool parts = k1 - k0 > p.segment;
+      uint32_t turn = 0;  // sums so far: in both accumulators in turn, or of parts of k in the first
       for (int i = 0; i < mine && ok; ++i) {
-        const uint32_t buf = i & 1, id = idesc_k(E4M3, kPair * kTileN, columns(TileAt(p, first + i * step).mt));
-        if (i >= 2) ok = warp_wait(&S.acc_empty[buf], ((i >> 1) - 1) & 1, &S.failed);
-        tc_after();
-        for (int k = k0; k < k1 && ok; ++k) {
+        const uint32_t id = idesc_k(E4M3, kPair * kTileN, columns(TileAt(p, first + i * step).mt));
+        uint32_t buf = 0;
+        for (int k = k0, from = k0; k < k1 && ok; ++k) {
+          if (k == k0 || k == from + p.segment) {
+            from = k;
+            buf = parts ? 0 : turn & 1;
+            const uint32_t before = parts ? turn : turn >> 1;  // uses of this accumulator
+            if (before > 0) ok = warp_wait(&S.acc_empty[buf], (before - 1) & 1, &S.failed);
+            if (!ok) break;
+            ++turn;
+            tc_after();
+          }
           ok = warp_wait(&S.full[st], round & 1, &S.failed);
           if (!ok) break;
           tc_after();
@@ -517,11 +535,11 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
               for (int h = 0; h < C::kAcc; ++h) {
                 const uint64_t a = w + h * kTileN * kBlock / 16 + 2 * j, b = x + 2 * j;
                 const uint32_t d = tmem + buf * C::kCols + h * ROWS;
-                if constexpr (PAIR) mma_2cta<E4M3>(d, a, b, id, k > k0 || j > 0);
-                else mma_1cta<E4M3>(d, a, b, id, k > k0 || j > 0);
+                if constexpr (PAIR) mma_2cta<E4M3>(d, a, b, id, k > from || j > 0);
+                else mma_1cta<E4M3>(d, a, b, id, k > from || j > 0);
               }
             signal(&S.empty[st]);
-            if (k == k1 - 1) signal(&S.acc_full[buf]);
+            if (k == k1 - 1 || k == from + p.segment - 1) signal(&S.acc_full[buf]);
           }
           __syncwarp();
           if (++st == p.stages) st = 0, ++round;
@@ -544,21 +562,46 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
     E e(p, S.rows[warp], warp, lane);
     static_assert(E::kBytes == C::kRowBytes, "a warp's results");
     typename E::Ahead ahead = {};
+    const bool parts = k1 - k0 > p.segment;
+    uint32_t turn = 0;  // parts of k so far
     if (mine > 0 && p.split == 1) {
       e.tile_ahead(channel_of(at) + wq * E::kWidth, ahead);
       e.fetch(channel_of(at) + wq * E::kWidth, at.mt * p.tile_rows + kStep * group, ahead);
     }
     for (int i = 0; i < mine; ++i) {
-      const uint32_t buf = i & 1;
+      const uint32_t buf = parts ? 1 : i & 1;
       const int m0 = at.mt * p.tile_rows, rows = min(p.tile_rows, p.M - m0), channel0 = channel_of(at);
       e.tile(channel0 + wq * E::kWidth, ahead);
       if (i + 1 < mine) {
         at = TileAt(p, first + (i + 1) * step);
         e.tile_ahead(channel_of(at) + wq * E::kWidth, ahead);
       }
-      if (lane == 0) bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);  // (one lane: polls are not free for the issuer)
-      __syncwarp();
-      tc_after();
+      if (!parts) {
+        if (lane == 0) bar_wait(&S.acc_full[buf], (i >> 1) & 1, &S.failed);  // (one lane: polls are not free for the issuer)
+        __syncwarp();
+        tc_after();
+      } else {
+        // the first accumulator's sums of parts of k, added up in the second
+        for (int k = k0; k < k1; k += p.segment, ++turn) {
+          if (lane == 0) bar_wait(&S.acc_full[0], turn & 1, &S.failed);
+          __syncwarp();
+          tc_after();
+#pragma unroll 1
+          for (int col = kStep * group; col < rows; col += kStep * C::kGroups)
+#pragma unroll 1
+            for (int c = col; c < col + kStep * C::kAcc; c += 16) {  // (two sums: those of the second half behind the first's)
+              const uint32_t from = lanes + (C::kAcc == 2 && c >= col + kStep ? c - kStep + ROWS : c);
+              tm_add(from, from + C::kCols, k == k0);
+            }
+          tm_put_wait();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) bar_signal_at(in_cta(&S.acc_empty[0], even));
+            else bar_signal(&S.acc_empty[0]);
+          }
+        }
+      }
       if (p.split == 1) {
         bool last;
         int col = kStep * group;
@@ -580,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
       } else {  // this CTA's sums, where the stages were
         uint8_t* const to = raw + (32 * wq / part.channels) * part.bytes;
 #pragma unroll 1
-        for (int col = 8 * group; col < rows; col += 8 * C::kGroups)
+        for (int col = kStep * group; col < rows; col += (col + 8) % kStep ? 8 : kStep * (C::kGroups - 1) + 8)
 #pragma unroll
           for (int h = 0; h < C::kAcc; ++h) {
             float z[1][4][2];
@@ -592,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GAT
       }
       tc_before();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && !parts) {
         if constexpr (PAIR) bar_signal_at(in_cta(&S.acc_empty[buf], even));
         else bar_signal(&S.acc_empty[buf]);
       }
@@ -838,6 +881,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const int groups = static_cast<int>((m_tiles + kGroup - 1) / kGroup), of_group = static_cast<int>((m_tiles + groups - 1) / groups);
   p.group = Divisor(static_cast<uint32_t>(of_group * n_tiles)), p.rows = Divisor(static_cast<uint32_t>(of_group));
   p.last = Divisor(static_cast<uint32_t>(m_tiles - (m_tiles - 1) / of_group * of_group));
+  p.segment = (f32 ? kSegmentF32 : kSegmentBf16) * (e4m3 ? kLongerE4m3 : 1);
   p.split = plan.split, p.stages = plan.stages, p.tile_rows = plan.tile_rows;
   p.act = a->activation, p.out_f32 = f32, p.early = a->flags & KDA_LINEAR_EARLY_WEIGHT;
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;

@@ -94,6 +94,47 @@ def test_every_gated_tile(e4m3, M, N, K, f32, cuda_device):
         assert (out[:, N // 2:] == 9.0).all()
 
 
+@pytest.mark.parametrize("f32, e4m3, M, N, K", [
+    (True, False, 4, 700, 9008), (True, False, 3, 130, 40008), (True, False, 30, 9800, 2112), (True, False, 200, 2570, 4400),
+    (True, False, 1400, 300, 2500 // 8 * 8), (True, False, 700, 9000, 2056), (True, False, 1300, 5130, 4104),
+    (True, True, 9, 1000, 20000), (True, True, 600, 520, 33008), (False, False, 2, 20, 280000), (False, False, 500, 150, 66000)])
+def test_long_sums_in_parts(f32, e4m3, M, N, K, cuda_device):
+    # more of k than is summed up at a time; tiles in turn, tiles shared by CTAs
+    g = torch.Generator().manual_seed(K)
+    x, w = whole_numbers((M, K), g, e4m3), whole_numbers((N, K), g, e4m3)
+    one = dict(x_scale=torch.ones(M, device=cuda_device), weight_scale=torch.ones(N, device=cuda_device)) if e4m3 else {}
+    want = x.float() @ w.float().t()
+    assert want.abs().max() < 2 ** 24
+    out = torch.full((M, N), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device=cuda_device)
+    kda_linear(x.to(cuda_device), w.to(cuda_device), out, **one)
+    assert torch.equal(out.cpu(), want.to(out.dtype))
+
+
+@pytest.mark.parametrize("M, N, K", [(5, 200, 4112), (40, 130, 9000), (130, 4000, 2200), (300, 600, 4104), (600, 9000, 2112)])
+def test_long_gated_sums_in_parts(M, N, K, cuda_device):
+    p = problem(M, N, K, False, "silu_gated", True, False, K)
+    out = torch.full((M, N // 2), float("nan"), device=cuda_device)
+    kda_linear(out=out, **{k: v.to(cuda_device) if isinstance(v, torch.Tensor) else v for k, v in p.items()})
+    close(out, p, False)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("M, N", [(16, 256), (150, 512), (256, 2048)])
+def test_long_sums_are_not_shortened(M, N, e4m3, cuda_device):
+    # The tensor cores cut sums towards zero: half a step each of 2^-23 of the sum so far, whose magnitude grows with the
+    # root of the number of products.  Over 56 additions (896 of k) that takes 2/3 * 56 * 2^-24 * 0.72 = 1.6e-6 of a sum,
+    # which is what any k may be off by in parts of 896; 16,384 in one go would be 18 times that.
+    K = 16384
+    p = problem(M, N, K, e4m3, None, False, False, 11)
+    d = {k: v.to(cuda_device) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    out = torch.zeros(M, N, device=cuda_device)
+    kda_linear(out=out, **d)
+    y = d["x"].double() @ d["weight"].double().t()
+    if e4m3:
+        y = y * d["x_scale"].double()[:, None] * d["weight_scale"].double()
+    assert ((out.double() - y).norm() / y.norm()).item() < 2.0 ** -19
+
+
 def problem(M, N, K, e4m3, act, bias, residual, seed):
     g = torch.Generator().manual_seed(seed)
     p = dict(x=torch.randn(M, K, generator=g), weight=torch.randn(N, K, generator=g) / math.sqrt(K))
