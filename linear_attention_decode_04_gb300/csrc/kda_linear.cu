@@ -107,16 +107,22 @@ __device__ __forceinline__ uint64_t sigmoid_times(uint64_t y) {
   const float2 d = both(add2(pair_of(ex2(t.x), ex2(t.y)), twice(1.f)));
   return mul2(y, pair_of(reciprocal(d.x), reciprocal(d.y)));
 }
+__device__ __forceinline__ float positive(float x) {  // or 0; NaN stays NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+  return r;
+}
 // y (1 + erf(y / sqrt 2)) / 2 with erfc(x) = t e^(-x^2 + P(t)), t = 1 / (1 + x / 2),
 // P of degree 9: Numerical Recipes' erfcc (Press et al., section 6.2), off by 1.2e-7
 // of itself at any x >= 0, so that the lower tail keeps its digits; -x^2 = -y^2 / 2
 // rounded adds x^2 2^-23.  max(y, 0) - |y| erfc(|y| / sqrt 2) / 2 is that of either
-// sign; past 40, where the second part is 0, it stays so for infinity too.
+// sign; past 40, where the second part is 0, it stays so for infinity too.  (The two values belong to different rows: of
+// NaN the second part is that of 40, and NaN comes from the first, so that no row reaches the other one.)
 __device__ __forceinline__ uint64_t gelu(uint64_t y2) {
   const float2 y = both(y2);
   const uint64_t a = pair_of(fminf(fabsf(y.x), 40.f), fminf(fabsf(y.y), 40.f)), h = mul2(a, twice(-.5f));
   const float2 d = both(fma2(a, twice(0.35355339059327376f), twice(1.f)));  // 1 to 16
-  const uint64_t t = mul2(twice(reciprocal(d.x * d.y)), pair_of(d.y, d.x));    // (one operation of the slow unit instead of two)
+  const uint64_t t = mul2(twice(reciprocal(d.x * d.y)), pair_of(d.y, d.x));  // (one operation of the slow unit for both)
   uint64_t q = twice(0.17087277f);
   q = fma2(q, t, twice(-0.82215223f));
   q = fma2(q, t, twice(1.48851587f));
@@ -128,7 +134,7 @@ __device__ __forceinline__ uint64_t gelu(uint64_t y2) {
   q = fma2(q, t, twice(1.00002368f));
   q = fma2(q, t, twice(-1.26551223f));
   const float2 e = both(mul2(fma2(h, a, q), twice(1.44269504088896340736f)));
-  return fma2(h, mul2(t, pair_of(ex2(e.x), ex2(e.y))), pair_of(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)));
+  return fma2(h, mul2(t, pair_of(ex2(e.x), ex2(e.y))), pair_of(positive(y.x), positive(y.y)));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);

@@ -94,6 +94,20 @@ def test_every_gated_tile(e4m3, M, N, K, f32, cuda_device):
         assert (out[:, N // 2:] == 9.0).all()
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("K", [1, 7, 31, 33, 65, 127, 130, 1001])
+@pytest.mark.parametrize("M, N", [(3, 5), (40, 200), (300, 260)])
+def test_any_k(M, N, K, e4m3, cuda_device):
+    # rows that end inside 16 bytes, with something else behind them
+    g = torch.Generator().manual_seed(K)
+    x, w = whole_numbers((M, K), g, e4m3), whole_numbers((N, K), g, e4m3)
+    one = dict(x_scale=torch.ones(M, device=cuda_device), weight_scale=torch.ones(N, device=cuda_device)) if e4m3 else {}
+    pad = -K % 16 + 16
+    out = torch.full((M, N), float("nan"), device=cuda_device)
+    kda_linear(padded(x, pad, cuda_device, 2.0), padded(w, pad, cuda_device, math.nan), out, **one)
+    assert torch.equal(out.cpu(), x.float() @ w.float().t())
+
+
 @pytest.mark.parametrize("f32, e4m3, M, N, K", [
     (True, False, 4, 700, 9008), (True, False, 3, 130, 40008), (True, False, 30, 9800, 2112), (True, False, 200, 2570, 4400),
     (True, False, 1400, 300, 2500 // 8 * 8), (True, False, 700, 9000, 2056), (True, False, 1300, 5130, 4104),
@@ -208,6 +222,26 @@ def test_rows_that_are_not_finite_stay_alone(M, cuda_device):
     rest = [i for i in range(M) if i not in (1, 2)]
     q = {**p, "x": p["x"].view(torch.uint8)[rest].view(F8), "x_scale": p["x_scale"][rest]}
     close(out[rest], q, False)
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M, N", [(5, 64), (40, 300), (300, 520)])
+def test_values_that_are_not_finite(M, N, act, f32, cuda_device):
+    # NaN stays NaN through every activation; infinity is its own gelu and silu, and gelu's lower tail ends at 0
+    x, w = torch.zeros(M, 64, dtype=torch.bfloat16), torch.ones(N, 64, dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    x[0, 3], x[1, 3], x[2, 3], x[3, 3] = math.nan, math.inf, -math.inf, -300.0
+    width = N // 2 if act == "silu_gated" else N
+    out = torch.full((M, width), 5.0, dtype=torch.float32 if f32 else torch.bfloat16, device=cuda_device)
+    kda_linear(x.to(cuda_device), w.to(cuda_device), out, activation=act)
+    got = out.cpu().double()
+    assert got[0].isnan().all()
+    assert (got[1] == math.inf).all()
+    assert act not in (None, "gelu") or (got[2] == (-math.inf if act is None else 0)).all()
+    assert act is None or (got[3].abs() < 1e-37).all()
+    one = {None: 1.0, "silu": 1 / (1 + math.exp(-1)), "gelu": 0.5 * (1 + math.erf(math.sqrt(0.5))), "silu_gated": 1 / (1 + math.exp(-1))}[act]
+    assert ((got[4:] - one).abs() <= (2.0 ** -18 if f32 else 2.0 ** -8)).all()
 
 
 def test_rows_do_not_depend_on_one_another_in_a_tile_size(cuda_device):
