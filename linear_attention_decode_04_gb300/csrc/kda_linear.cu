@@ -73,8 +73,8 @@ struct Params {
 // A gate's two halves: in two accumulators, or 16 and 16 channels in turn in one.
 constexpr int kNoGate = 0, kTwoSums = 1, kInterleaved = 2;
 
-// ROWS of x per tile.
-template <int ROWS, int GATE, bool PAIR>
+// ROWS of x per tile; FEW warpgroups that write results, see kFew.
+template <int ROWS, int GATE, bool PAIR, bool FEW = false>
 struct Cfg {
   static constexpr int kAcc = GATE == kTwoSums ? 2 : 1;
   static constexpr int kChannels = GATE == kInterleaved ? kTileN / 2 : kTileN;  // of out, of a CTA
@@ -86,7 +86,7 @@ struct Cfg {
   // One CTA takes an SM's shared memory; where a short range of k leaves room, the next call's CTAs start beside it.
   static constexpr int kCtasPerSm = PAIR || ROWS > 32 ? 1 : 2;
   // warpgroups that write results; then a warp that copies weights, one that copies rows, and the issuer
-  static constexpr int kGroups = GATE == kTwoSums ? (ROWS > 32 ? 2 : 1) : ROWS < 64 ? ROWS / 16 : 4, kThreads = 128 * kGroups + 96;
+  static constexpr int kGroups = FEW ? 2 : GATE == kTwoSums ? (ROWS > 32 ? 2 : 1) : ROWS < 64 ? ROWS / 16 : 4, kThreads = 128 * kGroups + 96;
   // sums of a tile that several CTAs share: in the stages, when its products have ended, lie a CTA's own and those sent to it
   static constexpr int kPartBytes = kCols / 2 * (kTileN * 8 + 64 * kMaxSplit);
   static_assert(kTmemCols * kCtasPerSm <= 512, "tensor memory");
@@ -388,10 +388,10 @@ struct Parts {
 // Clusters of split CTAs, or split pairs.  A pair's even CTA issues the products
 // of both and counts the copies of both; its odd one copies its half and writes its
 // own channels' results.
-template <int ROWS, bool E4M3, int GATE, bool PAIR>
-__global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR>::kThreads, Cfg<ROWS, GATE, PAIR>::kCtasPerSm)
+template <int ROWS, bool E4M3, int GATE, bool PAIR, bool FEW>
+__global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS, GATE, PAIR, FEW>::kCtasPerSm)
     linear_kernel(const Params p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
-  using C = Cfg<ROWS, GATE, PAIR>;
+  using C = Cfg<ROWS, GATE, PAIR, FEW>;
   constexpr int kPair = PAIR ? 2 : 1, kCopies = 4 * C::kGroups, kIssuer = kCopies + 2;
   extern __shared__ __align__(1024) uint8_t raw[];
   Head<C>& S = *reinterpret_cast<Head<C>*>(raw + p.stages * C::kStageBytes);
@@ -729,10 +729,10 @@ struct Variant {
   int stage_bytes, part_bytes, head_bytes;
   float start, block, join, results;  // us, see plan_of
 };
-template <int ROWS, int GATE, bool PAIR>
+template <int ROWS, int GATE, bool PAIR, bool FEW = false>
 Variant variant(float start, float block, float join, float results) {
-  using C = Cfg<ROWS, GATE, PAIR>;
-  return {ROWS, 8 * C::kUnroll, C::kChannels * (PAIR ? 2 : 1), PAIR, GATE == kInterleaved, {linear_kernel<ROWS, false, GATE, PAIR>, linear_kernel<ROWS, true, GATE, PAIR>},
+  using C = Cfg<ROWS, GATE, PAIR, FEW>;
+  return {ROWS, 8 * C::kUnroll, C::kChannels * (PAIR ? 2 : 1), PAIR, GATE == kInterleaved, {linear_kernel<ROWS, false, GATE, PAIR, FEW>, linear_kernel<ROWS, true, GATE, PAIR, FEW>},
           C::kThreads, C::kStageBytes, C::kPartBytes, static_cast<int>(sizeof(Head<C>)), start, block, join, results};
 }
 constexpr int kPlain = 6, kGatedVariants = 5;
@@ -743,6 +743,13 @@ const Variant kVariants[kPlain + kGatedVariants] = {
     variant<16, kTwoSums, false>(4.8f, .26f, 1.f, 1.f), variant<32, kTwoSums, false>(5.f, .28f, 1.5f, 1.6f),
     variant<64, kTwoSums, false>(5.8f, .33f, 2.5f, 3.f), variant<128, kTwoSums, false>(7.f, .4f, 0.f, 4.f),
     variant<256, kInterleaved, true>(8.f, .3f, 0.f, 3.2f)};
+// The variants of 256 rows (plain, gated) with two warpgroups that write results instead of four: fewer waiting warps (16,384 x
+// 18,432 x 6,144 1,098 us, with four 1,119, both at the power limit), more registers (8,192 x 8,192 x 512 with residual 86 and
+// 91) and fewer rows written at a time (fp32 59 and 64, on no boundary 75 and 101).  Four are for bf16 rows off 16-byte
+// boundaries, which a group writes together (8,192 x 8,191 x 512 83, with two 100), and gates of short k (4,096 x 16,384 x
+// 512 45 and 52, x 2,048 81 and 79).
+const Variant kFew[2] = {variant<256, kNoGate, true, true>(7.2f, .26f, 0.f, 3.2f), variant<256, kInterleaved, true, true>(8.f, .3f, 0.f, 3.2f)};
+constexpr int kFewGatedBlocks = 12;
 constexpr int kSmemLimit = 227 * 1024;  // of a CTA
 
 cudaError_t setup(int* sms) {
@@ -758,9 +765,13 @@ cudaError_t setup(int* sms) {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeFn>(fn);
-    for (const Variant& v : kVariants)
+    auto allow = [&](const Variant& v) {
       for (const Kernel k : v.kernel)
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit)) != cudaSuccess) return e;
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    };
+    for (const Variant& v : kVariants) allow(v);
+    for (const Variant& v : kFew) allow(v);
+    if (e != cudaSuccess) return e;
     int n = 0;
     if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     g_sms[dev] = n;
@@ -852,7 +863,9 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const cuuint32_t ones[3] = {1, 1, 1};
   const int blocks = static_cast<int>((k_bytes + kBlock - 1) / kBlock);
   const Plan plan = plan_of(a->M, width, blocks, gated, static_cast<double>(k_bytes) * a->N, sms);
-  const Variant& v = *plan.variant;
+  const bool vec_out = !f32 && !misaligned(a->out, 15) && a->out_row_stride % 8 == 0;
+  const bool few = plan.variant->rows == 256 && (f32 || vec_out) && (!gated || blocks >= kFewGatedBlocks);
+  const Variant& v = few ? kFew[gated] : *plan.variant;
   CUtensorMap w_map, x_map;
   CUresult r;
   if (v.interleaved) {  // a copy takes 16 channels of each half
@@ -893,7 +906,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   p.x_scale = a->x_scale, p.w_scale = a->weight_scale, p.bias = a->bias;
   p.residual = a->residual, p.res_stride = a->residual_row_stride, p.out = a->out, p.out_stride = a->out_row_stride;
   p.err = a->err_flag;
-  p.vec_out = !f32 && !misaligned(a->out, 15) && a->out_row_stride % 8 == 0;
+  p.vec_out = vec_out;
   p.vec_res = !misaligned(a->residual, 15) && a->residual_row_stride % 8 == 0;
   const int cluster = plan.split * (v.pair ? 2 : 1);
   const int64_t clusters = plan.split > 1 ? m_tiles * n_tiles : std::min<int64_t>(m_tiles * n_tiles, sms / cluster);
