@@ -39,7 +39,7 @@ constexpr int kMaxStages = 12;
 // at 16,384 of k.  So fp32 results are made from sums of 896 of k (e4m3 10,752), which are then added up in fp32 with
 // rounding, in the second accumulator: they are off by 1e-6 of themselves, as sums with rounding are, at any k.  bf16
 // results, whose rounding is 2^-9, are made from sums of 65,536 (786,432).  A part's end costs 0.8 us, as the products
-// wait for the accumulator: 4,096 x 8,192 x 4,096 take 153 us in bf16, 163 in fp32 from sums of 2,048 (off by 2e-6) and 189 from 896.
+// wait for the accumulator: 4,096 x 8,192 x 4,096 take 153 us in bf16, 163 in fp32 from sums of 2,048 (off by 2e-6) and 190 from 896.
 constexpr int kSegmentF32 = 14, kSegmentBf16 = 1024, kLongerE4m3 = 6;
 
 // Quotients of 0 .. 2^31 - 1 by a divisor of a launch (Granlund and Montgomery 1994, section 4).
@@ -385,6 +385,21 @@ struct Parts {
   __device__ __forceinline__ uint8_t* at(uint8_t* part, int h, int q, int c) const { return part + (h * (C::kCols / C::kAcc / 2) + q) * pitch + c * 8; }
 };
 
+// The sums of a part of k in the first accumulator, of a warp's rows, added to those in the second.  (Few columns
+// at a time: 16 cost registers in the calls without parts too.)
+template <class C, int ROWS>
+__device__ __forceinline__ void add_part(uint32_t lanes, int group, int rows, bool first) {
+  constexpr int kStep = 8 * C::kUnroll;
+#pragma unroll 1
+  for (int col = kStep * group; col < rows; col += kStep * C::kGroups)
+#pragma unroll 1
+    for (int c = col; c < col + kStep * C::kAcc; c += 8) {  // (two sums: those of the second half behind the first's)
+      const uint32_t from = lanes + (C::kAcc == 2 && c >= col + kStep ? c - kStep + ROWS : c);
+      tm_add(from, from + C::kCols, first);
+    }
+  tm_put_wait();
+}
+
 // Clusters of split CTAs, or split pairs.  A pair's even CTA issues the products
 // of both and counts the copies of both; its odd one copies its half and writes its
 // own channels' results.
@@ -518,37 +533,34 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
       uint32_t turn = 0;  // sums so far: in both accumulators in turn, or of parts of k in the first
       for (int i = 0; i < mine && ok; ++i) {
         const uint32_t id = idesc_k(E4M3, kPair * kTileN, columns(TileAt(p, first + i * step).mt));
-        uint32_t buf = 0;
-        for (int k = k0, from = k0; k < k1 && ok; ++k) {
-          if (k == k0 || k == from + p.segment) {
-            from = k;
-            buf = parts ? 0 : turn & 1;
-            const uint32_t before = parts ? turn : turn >> 1;  // uses of this accumulator
-            if (before > 0) ok = warp_wait(&S.acc_empty[buf], (before - 1) & 1, &S.failed);
-            if (!ok) break;
-            ++turn;
-            tc_after();
-          }
-          ok = warp_wait(&S.full[st], round & 1, &S.failed);
-          if (!ok) break;
+        for (int from = k0; from < k1 && ok; ++turn) {
+          const int to = parts ? min(from + p.segment, k1) : k1;
+          const uint32_t buf = parts ? 0 : turn & 1, before = parts ? turn : turn >> 1;  // uses of this accumulator
+          if (before > 0) ok = warp_wait(&S.acc_empty[buf], (before - 1) & 1, &S.failed);
           tc_after();
-          if (elect()) {
-            // (descriptors count in 16 bytes, and no address carries out of their field)
-            const uint64_t w = desc + static_cast<uint32_t>(st * (C::kStageBytes / 16)), x = w + C::kWeightBytes / 16;
+          for (int k = from; k < to && ok; ++k) {
+            ok = warp_wait(&S.full[st], round & 1, &S.failed);
+            if (!ok) break;
+            tc_after();
+            if (elect()) {
+              // (descriptors count in 16 bytes, and no address carries out of their field)
+              const uint64_t w = desc + static_cast<uint32_t>(st * (C::kStageBytes / 16)), x = w + C::kWeightBytes / 16;
 #pragma unroll
-            for (int j = 0; j < kBlock / 32; ++j)
+              for (int j = 0; j < kBlock / 32; ++j)
 #pragma unroll
-              for (int h = 0; h < C::kAcc; ++h) {
-                const uint64_t a = w + h * kTileN * kBlock / 16 + 2 * j, b = x + 2 * j;
-                const uint32_t d = tmem + buf * C::kCols + h * ROWS;
-                if constexpr (PAIR) mma_2cta<E4M3>(d, a, b, id, k > from || j > 0);
-                else mma_1cta<E4M3>(d, a, b, id, k > from || j > 0);
-              }
-            signal(&S.empty[st]);
-            if (k == k1 - 1 || k == from + p.segment - 1) signal(&S.acc_full[buf]);
+                for (int h = 0; h < C::kAcc; ++h) {
+                  const uint64_t a = w + h * kTileN * kBlock / 16 + 2 * j, b = x + 2 * j;
+                  const uint32_t d = tmem + buf * C::kCols + h * ROWS;
+                  if constexpr (PAIR) mma_2cta<E4M3>(d, a, b, id, k > from || j > 0);
+                  else mma_1cta<E4M3>(d, a, b, id, k > from || j > 0);
+                }
+              signal(&S.empty[st]);
+              if (k == to - 1) signal(&S.acc_full[buf]);
+            }
+            __syncwarp();
+            if (++st == p.stages) st = 0, ++round;
           }
-          __syncwarp();
-          if (++st == p.stages) st = 0, ++round;
+          from = to;
         }
       }
       if (elect()) signal(&S.done);
@@ -592,14 +604,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
           if (lane == 0) bar_wait(&S.acc_full[0], turn & 1, &S.failed);
           __syncwarp();
           tc_after();
-#pragma unroll 1
-          for (int col = kStep * group; col < rows; col += kStep * C::kGroups)
-#pragma unroll 1
-            for (int c = col; c < col + kStep * C::kAcc; c += 16) {  // (two sums: those of the second half behind the first's)
-              const uint32_t from = lanes + (C::kAcc == 2 && c >= col + kStep ? c - kStep + ROWS : c);
-              tm_add(from, from + C::kCols, k == k0);
-            }
-          tm_put_wait();
+          add_part<C, ROWS>(lanes, group, rows, k == k0);
           tc_before();
           __syncwarp();
           if (lane == 0) {
