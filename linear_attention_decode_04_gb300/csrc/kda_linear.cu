@@ -62,7 +62,7 @@ struct Divisor {
 };
 
 struct Params {
-  int M, N, K, width;          // width: channels of out
+  int M, width;                // rows; channels of out
   int m_tiles, n_tiles, blocks;  // row tiles, channel tiles (of a CTA or pair), blocks of k
   int tile_rows;               // rows of a row tile, at most the variant's
   Divisor group, rows, last;   // tiles of a group of row tiles; row tiles of one, and of the last one
@@ -908,7 +908,7 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   }
   if (r != CUDA_SUCCESS) return kda_internal_fail(KDA_ERR_LAUNCH, "tensor map: error %d", static_cast<int>(r));
   Params p{};
-  p.M = a->M, p.N = a->N, p.K = a->K, p.width = width;
+  p.M = a->M, p.width = width;
   const int64_t m_tiles = tiles_of(a->M, plan.tile_rows), n_tiles = tiles_of(width, v.channels);
   if (m_tiles * n_tiles > 0x7fffffff / 16) return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d: too many tiles", a->M, a->N);
   p.m_tiles = static_cast<int>(m_tiles), p.n_tiles = static_cast<int>(n_tiles), p.blocks = blocks;
