@@ -35,8 +35,10 @@ extern "C" {
 /* flags */
 #define KDA_LINEAR_E4M3 1u         /* x and weight are e4m3 (else bf16) */
 #define KDA_LINEAR_OUT_F32 2u      /* out is fp32 (else bf16) */
-/* The kernel ahead of this one in the stream does not write weight,
- * weight_scale or bias: they may be read while it still runs. */
+/* The kernel directly ahead of this one in the stream does not write weight,
+ * weight_scale or bias: they may be read while it still runs.  (Kernels ahead
+ * of that one may: they have ended by then, as this library's kernels launch
+ * dependents only when all that is ahead of them has.) */
 #define KDA_LINEAR_EARLY_WEIGHT 4u
 
 /*

@@ -16,7 +16,10 @@ KDA_INTERNAL void kda_internal_clear_error();
 
 // Launch `kernel` as a programmatic dependent launch: it may become resident
 // while the stream's previous kernel drains, so it must execute
-// griddepcontrol.wait before it touches memory.  `cluster` > 1 launches
+// griddepcontrol.wait before it touches memory (but for what its caller has
+// allowed it to read early), and launch its own dependents only behind that
+// wait: whoever is launched early then runs beside the kernel directly ahead
+// alone, which is what callers are asked about.  `cluster` > 1 launches
 // clusters of that many CTAs along x.
 template <typename... P, typename... A>
 static inline cudaError_t kda_internal_launch_cluster(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,

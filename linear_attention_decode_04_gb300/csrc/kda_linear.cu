@@ -453,7 +453,6 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
   if (warp == kCopies) asm volatile("barrier.cta.arrive 1, %0;" ::"n"(C::kThreads) : "memory");
   else asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kThreads) : "memory");
   tc_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = warp == kCopies ? 0 : S.tmem;
   const int k0 = static_cast<int>(static_cast<int64_t>(p.blocks) * share / p.split);
   const int k1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (share + 1) / p.split);
@@ -477,6 +476,9 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
       __syncwarp();
       if (early && fills) copy(lane, start, start_k);  // before the kernel ahead has ended
       asm volatile("griddepcontrol.wait;" ::: "memory");
+      // Dependents start only now, when all that is ahead of this call has ended: what they read early need not be
+      // written by this call alone.  (By the warp that copies rows, which knows that tensor memory has been asked for.)
+      if (warp != kCopies) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       if (!early && fills) copy(lane, start, start_k);
       __syncwarp();
       int64_t it = total < p.stages ? total : p.stages;

@@ -163,9 +163,10 @@ class KdaLinearCall(_Call):
       residual     bf16, of out's shape, or None; may be ``out`` itself
       activation   None, "silu", "gelu", or "silu_gated" (silu of the first
                    half of the N channels times the second)
-      early_weight weight, its scale and bias are not written by what runs
-                   ahead of the call in its stream: the kernel may read them
-                   while that still runs"""
+      early_weight weight, its scale and bias are not written by the kernel
+                   directly ahead of the call in its stream: the call may
+                   read them while that still runs (not before whatever is
+                   ahead of that kernel has ended)"""
 
     def __init__(self, x, weight, out, *, x_scale=None, weight_scale=None, bias=None, residual=None,
                  activation: str | None = None, early_weight: bool = False, err_flag=None):
