@@ -204,9 +204,9 @@ __device__ __forceinline__ int consumer_any(int pred) {
   return r;
 }
 
-// Programmatic dependent launch: let the next kernel in the stream be
-// scheduled now, and wait for the previous one to complete (with its memory
-// visible) before touching anything it may have written.
+// Programmatic dependent launch: wait for the previous kernel to complete (with
+// its memory visible) before touching anything it may have written, and only
+// then let the next one in the stream be scheduled.
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -282,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_decode_persistent_kernel(cons
     fence_proxy_async_smem();
   }
   __syncthreads();
-  griddep_launch_dependents();
 
   if (warp == kConsumerWarps) {
     // ------------------------------------------------------------ producer
@@ -384,6 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_decode_persistent_kernel(cons
       }
     }
     griddep_wait();
+    // The next call starts only now, when all that is ahead of this one has
+    // ended: what it reads early need not be written by this call alone.
+    griddep_launch_dependents();
     for (int j = 0; j < it; ++j) {
       const int n = S.info[j][1], h = S.info[j][2];
       const bool early_j = p.early_prefetch && j < kEarlyStages;

@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_decode_multi_kernel(const Par
     fence_proxy_async_smem();
   }
   __syncthreads();
-  griddep_launch_dependents();
 
   auto valid = [&](int slot) { return slot > 0 && slot < p.num_slots; };
   // output buffer of present token m of a unit in stage st
@@ -223,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_decode_multi_kernel(const Par
       early = true;
     }
     griddep_wait();
+    griddep_launch_dependents();  // (behind the wait, as in the single-token kernel)
     for (int st = 0; st < kMStages; ++st) {
       if (units[st] >= 0)
         publish(st, units[st], st == 0 && early, st == 0 && early);

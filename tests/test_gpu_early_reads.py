@@ -8,7 +8,7 @@ import subprocess
 import pytest
 import torch
 
-from linear_attention_decode_04_gb300 import KdaLinearCall, kda_linear
+from linear_attention_decode_04_gb300 import KdaDecodeCall, KdaLinearCall
 from linear_attention_decode_04_gb300 import build as B
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,45 @@ def test_weights_written_two_kernels_ahead(ahead, M, N, K, cuda_device, late_cop
     call()
     torch.cuda.synchronize(dev)
     assert torch.equal(out, x.float() @ new.float().t()) and err.item() == 0
+
+
+def decode(N, H, T, seed, dev, early):
+    """(call, its state pool, its conv windows, its results) of a decode of its own pools"""
+    g = torch.Generator().manual_seed(seed)
+    f = lambda *s: torch.randn(*s, generator=g).to(dev)  # noqa: E731
+    HD, rows, slots = 128 * H, N * T, 1 + N * (T + 1)
+    state, conv, out = f(slots, H, 128, 128) * 0.02, f(slots, 3 * HD, 3).bfloat16(), torch.zeros(rows, HD, device=dev).bfloat16()
+    i32 = dict(dtype=torch.int32, device=dev)
+    spec = dict(tokens_per_seq=T, src_slot=torch.arange(1, N + 1, **i32)) if T > 1 else {}
+    dst = (N + 1 + torch.arange(rows, **i32)).view(N, T) if T > 1 else torch.arange(1, N + 1, **i32)
+    call = KdaDecodeCall(f(rows, 3 * HD).bfloat16(), f(3, 4, HD) * 0.5, conv, state, -torch.rand(rows, H, 128, generator=g).to(dev),
+                         torch.rand(rows, H, generator=g).to(dev).bfloat16(), dst, out, gate=f(rows, HD).bfloat16(),
+                         norm_weight=torch.ones(128, device=dev), early_prefetch=early, **spec)
+    return call, state, conv, out
+
+
+@pytest.mark.parametrize("between", ["product", "decode", "multi"])
+@pytest.mark.parametrize("N, H, T", [(1, 4, 1), (4, 12, 1), (3, 8, 4), (2, 4, 8)])
+def test_states_written_two_kernels_ahead(N, H, T, between, cuda_device, late_copy):
+    dev = cuda_device
+    if between == "product":
+        g = torch.Generator().manual_seed(0)
+        other = KdaLinearCall(whole(g, dev, 4, 64), whole(g, dev, 128, 64), torch.zeros(4, 128, device=dev))
+    else:
+        other = decode(2, 6, 1 if between == "decode" else 4, 5, dev, True)[0]
+    results = []
+    for early in (False, True):
+        call, state, conv, out = decode(N, H, T, 7, dev, early)
+        new = torch.randn(state.shape, generator=torch.Generator().manual_seed(9)).to(dev)
+        other()
+        torch.cuda.synchronize(dev)
+        late_copy(state, new)
+        if not early:                              # one after another
+            torch.cuda.synchronize(dev)
+            assert torch.equal(state, new)
+        other()
+        call()
+        torch.cuda.synchronize(dev)
+        results.append((state, conv, out))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

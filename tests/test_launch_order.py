@@ -24,7 +24,7 @@ def functions(text):
         yield m.group(0), text[m.end():i]
 
 
-@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(B.CSRC, "*.cu"))), ids=os.path.basename)
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(B.CSRC, "*.cu*"))), ids=os.path.basename)
 def test_dependents_start_behind_the_wait(path):
     found = list(functions(open(path).read()))
     # device functions that launch dependents count where kernels call them
