@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
     } else {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&S.tmem)), "n"(C::kTmemCols));
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+      asm volatile("barrier.cta.arrive 6, 64;" ::: "memory");
     }
     tc_before();
   }
@@ -481,6 +482,10 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
       if (warp != kCopies) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       if (!early && fills) copy(lane, start, start_k);
       __syncwarp();
+      // Waits have limits, and a limit counts from when only this call's own work is waited for: behind the kernel ahead,
+      // and, for the warp that began without it, when tensor memory that other calls hold has been given (in a pair it
+      // has been by now).
+      if (!PAIR && warp == kCopies) asm volatile("barrier.cta.sync 6, 64;" ::: "memory");
       int64_t it = total < p.stages ? total : p.stages;
       int i = static_cast<int>(it) / span, k = k0 + static_cast<int>(it) % span, st = 0;
       uint32_t parity = 0;
@@ -530,6 +535,7 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
     }
   } else if (warp == kIssuer) {
     // ========================================================== product issuer
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the limits of its waits count from here)
     if (half == 0) {
       bool ok = true;
       int st = 0;
@@ -706,6 +712,9 @@ __global__ void __launch_bounds__(Cfg<ROWS, GATE, PAIR, FEW>::kThreads, Cfg<ROWS
     cluster_arrive();
     cluster_wait();
   }
+  // (A pair's odd CTA has no products to issue, which may take the pair longer than a wait may: it waits for the last of
+  // them when its results are written.)
+  if (PAIR && half != 0) __syncthreads();
   // every product has ended before the accumulators are given back, and in a pair before either CTA leaves, given up or not
   if (warp == kIssuer && lane == 0 && !bar_wait(&S.done, 0, &S.failed)) bar_drain(&S.done, 0);
   __syncwarp();

@@ -1,6 +1,7 @@
 """What a call may read early (weights, a decode's states) is promised not to be
 written by the kernel directly ahead of it alone: it sees what an earlier one
-wrote, however late that one wrote it."""
+wrote, however late that one wrote it.  And a call's own waits, which have
+limits, begin when what is ahead of it has ended."""
 import ctypes
 import os
 import subprocess
@@ -55,6 +56,21 @@ def test_weights_written_two_kernels_ahead(ahead, M, N, K, cuda_device, late_cop
     call()
     torch.cuda.synchronize(dev)
     assert torch.equal(out, x.float() @ new.float().t()) and err.item() == 0
+
+
+# (the limit of a wait inside a product is 2 s) one CTA a tile, several, pairs, several pairs, many tiles
+@pytest.mark.parametrize("M, N, K", [(4, 128, 64), (20, 300, 2048), (100, 2463, 5680), (300, 512, 256), (2000, 4000, 128)])
+def test_kernel_ahead_takes_longer_than_a_wait_may(M, N, K, cuda_device, late_copy):
+    g, dev = torch.Generator().manual_seed(M + N), cuda_device
+    new, weight = whole(g, dev, M, K), whole(g, dev, N, K)
+    x, out, err = torch.zeros_like(new), torch.zeros(M, N, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    call = KdaLinearCall(x, weight, out, early_weight=M < 200, err_flag=err)
+    call()
+    torch.cuda.synchronize(dev)
+    late_copy(x, new, 2_500_000_000)
+    call()
+    torch.cuda.synchronize(dev)
+    assert err.item() == 0 and torch.equal(out, new.float() @ weight.float().t())
 
 
 def decode(N, H, T, seed, dev, early):
