@@ -10,7 +10,7 @@
  *   y  = h                                 with KDA_ADD_NORM_NO_NORM
  *   residual_out = h,  out = y             rounded to bf16
  *   out_scale[t] = max(max|y|, 2^-100) / 448
- *   out_q        = y / out_scale[t]        rounded to e4m3
+ *   out_q        = y / out_scale[t]        rounded to fp32, then to e4m3
  * The sum is not rounded before the norm, and y not before its code is made;
  * everything in between is fp32.  A row whose y holds a NaN or an infinity
  * gets the scale NaN, and so does all that is made of it.

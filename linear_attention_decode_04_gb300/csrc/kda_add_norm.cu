@@ -13,6 +13,7 @@
 
 #include "kda_add_norm.h"
 #include "kda_internal.h"
+#include "kda_tc.cuh"
 
 namespace {
 
@@ -51,11 +52,19 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint2 codes(const float (&f)[8], float inv) {
+// The quotients by the scale as it is stored, rounded to fp32 and then to codes.  (Products with the rounded reciprocal
+// 448 / amax alone give 1 of 5,000 codes the other neighbour of a value near their middle, mostly the farther one.)  q = f r
+// with r = 1 / scale rounded, and once more with its exact remainder: q + (f - q scale) r is the rounded quotient
+// (Markstein 1990).  A division per element instead: 16,384 rows of 6,144 channels
+// 120 us instead of 105, without residual and norm 71 instead of 56 (with the product alone 104 and 53).
+__device__ __forceinline__ uint2 codes(const float (&f)[8], float scale, float inv) {
+  const uint64_t r = pair_of(inv, inv), minus = pair_of(-scale, -scale);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = pair_of(f[2 * i], f[2 * i + 1]), q = mul2(x, r);
+    w[i] = __nv_cvt_float2_to_fp8x2(both(fma2(fma2(q, minus, x), r, q)), __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
@@ -146,13 +155,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(cons
     top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0);
   }
   const float amax = top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) : __uint_as_float(0x7fc00000u);
-  const float inv = kMaxCode / amax;
+  const float scale = amax / kMaxCode, inv = 1.f / scale;
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
     const int c = tid + i * apart;
-    if (c < n) reinterpret_cast<uint2*>(p.out_q + t * p.out_q_stride)[c] = codes(h[i], inv);
+    if (c < n) reinterpret_cast<uint2*>(p.out_q + t * p.out_q_stride)[c] = codes(h[i], scale, inv);
   }
-  if (tid == 0) p.out_scale[t] = amax / kMaxCode;
+  if (tid == 0) p.out_scale[t] = scale;
 }
 
 bool misaligned(const void* ptr, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(ptr) & mask) != 0; }

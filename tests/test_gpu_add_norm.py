@@ -136,6 +136,22 @@ def test_rows_that_are_not_finite_or_empty(cuda_device):
         assert sc[5].isnan() or norm                    # (an infinite sum of squares makes the row zeros)
 
 
+@pytest.mark.parametrize("T, D, scale", [(4096, 512, 1.0), (2000, 6144, 1e-30), (700, 32768, 1e34), (3000, 520, 3e-5)])
+def test_codes_are_quotients_by_the_stored_scale(T, D, scale, cuda_device):
+    # without the norm y is a sum that fp32 holds, and the codes have one value each: the fp32 quotient, rounded to e4m3
+    x, r, _ = inputs(T, D, T + D, scale=scale)
+    got = outputs(T, D, cuda_device)
+    del got["out"]
+    kda_add_norm(x.to(cuda_device), residual=r.to(cuda_device), norm=False, **got)
+    y = x.float() + r.float()
+    want = y.abs().amax(-1) / 448
+    assert torch.equal(got["out_scale"].cpu(), want)
+    codes = (y / want[:, None]).to(torch.float8_e4m3fn)
+    assert torch.equal(got["out_q"].cpu().view(torch.uint8), codes.view(torch.uint8))
+    # what a product with the rounded reciprocal would get wrong is among them
+    assert (codes.view(torch.uint8) != (y * (448 / y.abs().amax(-1))[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)).any()
+
+
 def test_graph_stream_and_repeated_rows(cuda_device):
     # a row's results do not depend on the rows beside it, the stream or a replay
     dev = cuda_device
