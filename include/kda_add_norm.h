@@ -12,8 +12,10 @@
  *   out_scale[t] = max(max|y|, 2^-100) / 448
  *   out_q        = y / out_scale[t]        rounded to fp32, then to e4m3
  * The sum is not rounded before the norm, and y not before its code is made;
- * everything in between is fp32.  A row whose y holds a NaN or an infinity
- * gets the scale NaN, and so does all that is made of it.
+ * everything in between is fp32, and squares that fp32 does not hold are made
+ * of the row relative to its largest channel, so that any row of finite sums
+ * has its norm.  (A sum past fp32's range is infinite.)  A row whose y holds a
+ * NaN or an infinity gets the scale NaN, and so does all that is made of it.
  */
 #ifndef KDA_ADD_NORM_H
 #define KDA_ADD_NORM_H

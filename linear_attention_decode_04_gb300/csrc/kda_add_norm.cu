@@ -19,6 +19,8 @@ namespace {
 
 constexpr float kMaxCode = 448.f;       // largest e4m3 value
 constexpr float kScaleFloor = 0x1p-100f;
+constexpr float kLeastSquare = 0x1p-120f;  // of a mean: one of squares that fp32 holds with all their digits
+constexpr uint32_t kInfinity = 0x7f800000u;
 constexpr int kShort = 512;               // channels of rows that a warp takes
 constexpr int kRows = 4;                  // of these, in a CTA
 
@@ -68,6 +70,12 @@ __device__ __forceinline__ uint2 codes(const float (&f)[8], float scale, float i
   return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
+__device__ __forceinline__ float warp_total(float x) {  // in all lanes the same
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // A CTA per row, or a warp per row (WARP): a thread holds VECS pieces of 8 channels, as many apart as threads have the row.
 template <int VECS, bool NORM, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(const Params p) {
@@ -104,12 +112,26 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(cons
       }
     }
     if (NORM) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = warp_total(sum);
       if (WARP) total = sum;
       else if (lane == 0) sums[warp] = sum;
     }
   }
+  // the row's largest magnitude, as a bit pattern: NaN above infinity above everything else
+  auto row_top = [&]() {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(h[i][k]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (!WARP) {
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0);
+    }
+    return top;
+  };
   if (!WARP) __syncthreads();
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
@@ -118,11 +140,35 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(cons
   }
   if (NORM) {
     if (!WARP) {
-      total = lane < warps ? sums[lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      total = warp_total(lane < warps ? sums[lane] : 0.f);
     }
-    const float f = 1.f / sqrtf(total / static_cast<float>(p.D) + p.eps);
+    const float square = total / static_cast<float>(p.D) + p.eps;
+    float f = 1.f / sqrtf(square);
+    // Squares that pass fp32's range, or lose digits at its other end: once more, with the row and eps relative to a power
+    // of two near the largest of them.  (All threads of the row have the same sum.)
+    if (!(total < INFINITY) || square < kLeastSquare) {
+      const uint32_t top = row_top();
+      const float most = fmaxf(__uint_as_float(top), sqrtf(p.eps));
+      if (top < kInfinity && most > 0.f && most < INFINITY) {
+        const float by = __uint_as_float(static_cast<uint32_t>(min(max(254 - (__float_as_int(most) >> 23), 1), 254)) << 23);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            h[i][k] *= by;
+            sum = fmaf(h[i][k], h[i][k], sum);
+          }
+        sum = warp_total(sum);
+        if (!WARP) {
+          if (lane == 0) sums[warp] = sum;
+          __syncthreads();
+          sum = warp_total(lane < warps ? sums[lane] : 0.f);
+        }
+        const float e = sqrtf(p.eps) * by;
+        f = 1.f / sqrtf(sum / static_cast<float>(p.D) + e * e);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
       const int c = tid + i * apart;
@@ -143,18 +189,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(cons
     }
   }
   if (!p.out_q) return;
-  uint32_t top = 0;  // as bit patterns: NaN above infinity above everything else
-#pragma unroll
-  for (int i = 0; i < VECS; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(h[i][k]) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (!WARP) {
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0);
-  }
-  const float amax = top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) : __uint_as_float(0x7fc00000u);
+  const uint32_t top = row_top();
+  const float amax = top < kInfinity ? fmaxf(__uint_as_float(top), kScaleFloor) : __uint_as_float(0x7fc00000u);
   const float scale = amax / kMaxCode, inv = 1.f / scale;
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {

@@ -152,6 +152,39 @@ def test_codes_are_quotients_by_the_stored_scale(T, D, scale, cuda_device):
     assert (codes.view(torch.uint8) != (y * (448 / y.abs().amax(-1))[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)).any()
 
 
+@pytest.mark.parametrize("eps", [1e-6, 0.0, 1e-40])
+@pytest.mark.parametrize("T, D", [(9, 264), (9, 512), (9, 520), (9, 6152), (9, 32768)])
+def test_squares_past_the_range_of_fp32(T, D, eps, cuda_device):
+    x, r, w = inputs(T, D, D)
+    # rows as a whole, and one channel of the next ones: squares past 2^128, and far below 2^-126
+    for i, size in enumerate((1e20, 1e37, 1e-22, 1e-36)):
+        x[2 * i], r[2 * i] = (x[2 * i].float() * size).bfloat16(), (r[2 * i].float() * size).bfloat16()
+        x[2 * i + 1, 5] = size
+    got = outputs(T, D, cuda_device)
+    kda_add_norm(x.to(cuda_device), weight=w.to(cuda_device), residual=r.to(cuda_device), eps=eps, **got)
+    finite = torch.isfinite(x.float() + r.float()).all(-1)     # (some channels of the rows of 1e37 are not, in bf16 already)
+    assert got["out_scale"].cpu()[~finite].isnan().all() and finite.sum() >= 7
+    check({k: v.float()[finite.to(v.device)] for k, v in got.items()}, x[finite], w, r[finite], torch.tensor(eps).item())
+    assert (got["out_scale"].cpu()[finite] > 0).all()
+
+
+def test_rows_of_zeros_and_infinities(cuda_device):
+    # 0 / 0 without eps; an infinite sum leaves finite channels 0 and is NaN itself
+    x = torch.zeros(3, 520).bfloat16()
+    x[1, 3], x[2] = 3e38, 1e-20
+    r = torch.zeros_like(x)
+    r[1, 3] = 3e38
+    for eps in (0.0, 1e-6):
+        got = outputs(3, 520, cuda_device)
+        kda_add_norm(x.to(cuda_device), residual=r.to(cuda_device), eps=eps, **got)
+        out = got["out"].cpu().float()
+        assert out[0].isnan().all() if eps == 0 else (out[0] == 0).all()
+        assert out[1, 3].isnan() and (out[1, :3] == 0).all() and (out[1, 4:] == 0).all()
+        assert got["out_scale"][1].isnan()
+        want = 1.0 if eps == 0 else 1e-17
+        assert ((out[2].double() - want).abs() <= want * 2.0 ** -7).all()
+
+
 def test_graph_stream_and_repeated_rows(cuda_device):
     # a row's results do not depend on the rows beside it, the stream or a replay
     dev = cuda_device
