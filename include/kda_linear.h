@@ -51,7 +51,7 @@ extern "C" {
  */
 typedef struct KdaLinearArgs {
   uint32_t struct_size;        /* = sizeof(KdaLinearArgs) */
-  int32_t M;                   /* rows of x; 0 is a no-op */
+  int32_t M;                   /* rows of x, up to 2^31 - 512; 0 is a no-op */
   int32_t N;                   /* rows of weight, 1 .. 2^24; even with KDA_ACT_SILU_GATED */
   int32_t K;                   /* 1 .. 2^24 */
   int32_t activation;          /* KDA_ACT_* */

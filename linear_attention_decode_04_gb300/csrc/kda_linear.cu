@@ -862,7 +862,8 @@ extern "C" int kda_linear(const KdaLinearArgs* a, void* stream) {
   const bool e4m3 = a->flags & KDA_LINEAR_E4M3, f32 = a->flags & KDA_LINEAR_OUT_F32;
   const bool gated = a->activation == KDA_ACT_SILU_GATED;
   constexpr int kMost = 1 << 24;
-  if (a->M < 0 || a->N < 1 || a->N > kMost || a->K < 1 || a->K > kMost || a->activation < 0 ||
+  constexpr int kMostRows = 0x7fffffff - 511;  // rows are counted in 32 bits, to the end of the last tile and what is read ahead
+  if (a->M < 0 || a->M > kMostRows || a->N < 1 || a->N > kMost || a->K < 1 || a->K > kMost || a->activation < 0 ||
       a->activation > KDA_ACT_SILU_GATED || (gated && a->N % 2))
     return kda_internal_fail(KDA_ERR_SHAPE, "M=%d N=%d K=%d activation=%d", a->M, a->N, a->K, a->activation);
   if (a->M == 0) return KDA_OK;

@@ -69,6 +69,14 @@ def test_linear_codes(lib):
         assert call(**kw) == ALIGN, kw
 
 
+@pytest.mark.parametrize("M, code", [(2 ** 31 - 1, SHAPE), (2 ** 31 - 511, SHAPE), (2 ** 31 - 512, ALIGN)])
+def test_linear_rows_are_counted_in_32_bits(lib, M, code):
+    # (one row fewer goes on to the next check, of a pointer that is not aligned)
+    call = caller(lib, "kda_linear", L.KdaLinearArgs, dict(M=M, N=64, K=32, x=0x1000008, weight=0x2000000, out=0x3000000, x_row_stride=32,
+                                                           weight_row_stride=32, out_row_stride=64))
+    assert call() == code
+
+
 def test_logprobs_codes(lib):
     names = ("logits", "tokens", "logprobs", "ranks", "entropy", "top_ids", "top_logprobs", "err_flag")
     at = {n: 0x100000 * (i + 1) for i, n in enumerate(names)}
