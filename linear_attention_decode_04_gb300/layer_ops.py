@@ -17,7 +17,7 @@ import ctypes
 import torch
 
 from .binding import _check, _dense, _rows
-from .step_ops import _Call, _err, _p, _shaped
+from .step_ops import _Args, _Call, _err, _p, _shaped
 
 KDA_ADD_NORM_NO_NORM = 1
 ADD_NORM_MAX_D = 32768
@@ -29,7 +29,7 @@ LOGPROBS_MAX_TOP = 32
 _i32, _i64, _u32, _f32, _ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p
 
 
-class KdaAddNormArgs(ctypes.Structure):
+class KdaAddNormArgs(_Args):
     """Mirror of ``KdaAddNormArgs`` (field order and types must match)."""
     _fields_ = [("struct_size", _u32), ("T", _i32), ("D", _i32), ("flags", _u32), ("eps", _f32), ("x", _ptr),
                 ("x_row_stride", _i64), ("residual", _ptr), ("residual_row_stride", _i64), ("weight", _ptr),
@@ -37,7 +37,7 @@ class KdaAddNormArgs(ctypes.Structure):
                 ("out_q", _ptr), ("out_q_row_stride", _i64), ("out_scale", _ptr)]
 
 
-class KdaLinearArgs(ctypes.Structure):
+class KdaLinearArgs(_Args):
     """Mirror of ``KdaLinearArgs``."""
     _fields_ = [("struct_size", _u32), ("M", _i32), ("N", _i32), ("K", _i32), ("activation", _i32), ("flags", _u32),
                 ("x", _ptr), ("x_row_stride", _i64), ("weight", _ptr), ("weight_row_stride", _i64), ("x_scale", _ptr),
@@ -45,7 +45,7 @@ class KdaLinearArgs(ctypes.Structure):
                 ("out", _ptr), ("out_row_stride", _i64), ("err_flag", _ptr)]
 
 
-class KdaLogprobsArgs(ctypes.Structure):
+class KdaLogprobsArgs(_Args):
     """Mirror of ``KdaLogprobsArgs``."""
     _fields_ = [("struct_size", _u32), ("R", _i32), ("V", _i32), ("num_top", _i32), ("flags", _u32), ("logits", _ptr),
                 ("logits_row_stride", _i64), ("tokens", _ptr), ("logprobs", _ptr), ("ranks", _ptr), ("entropy", _ptr),

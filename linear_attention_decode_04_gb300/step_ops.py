@@ -31,7 +31,18 @@ BLOCK_SIZES = (16, 32, 64, 128, 256)
 _i32, _i64, _u32, _f32, _ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p
 
 
-class KdaBlockTablesArgs(ctypes.Structure):
+class _Args(ctypes.Structure):
+    """Base of the mirrors: whole numbers that do not fit their fields are
+    refused (ctypes would keep their low bits)."""
+
+    def __init__(self, **fields):
+        for name, kind in self._fields_:
+            if kind is _i32 and not -2 ** 31 <= fields.get(name, 0) < 2 ** 31:
+                raise ValueError(f"{name}={fields[name]} does not fit 32 bits")
+        super().__init__(**fields)
+
+
+class KdaBlockTablesArgs(_Args):
     """Mirror of ``KdaBlockTablesArgs`` (field order and types must match)."""
     _fields_ = [("struct_size", _u32), ("B", _i32), ("max_blocks", _i32), ("block_size", _i32), ("num_blocks", _i32),
                 ("T", _i32), ("num_free", _i32), ("cached_lens", _ptr), ("new_lens", _ptr), ("held_blocks", _ptr),
@@ -40,7 +51,7 @@ class KdaBlockTablesArgs(ctypes.Structure):
                 ("cu_seqlens", _ptr), ("seq_lens", _ptr), ("positions", _ptr), ("slot_map", _ptr), ("err_flag", _ptr)]
 
 
-class KdaQkRopeArgs(ctypes.Structure):
+class KdaQkRopeArgs(_Args):
     """Mirror of ``KdaQkRopeArgs``."""
     _fields_ = [("struct_size", _u32), ("T", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
                 ("head_dim", _i32), ("rot_dim", _i32), ("block_size", _i32), ("num_blocks", _i32), ("flags", _u32),
@@ -51,7 +62,7 @@ class KdaQkRopeArgs(ctypes.Structure):
                 ("slot_map", _ptr), ("err_flag", _ptr)]
 
 
-class KdaCacheAttentionArgs(ctypes.Structure):
+class KdaCacheAttentionArgs(_Args):
     """Mirror of ``KdaCacheAttentionArgs``."""
     _fields_ = [("struct_size", _u32), ("B", _i32), ("T", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
                 ("head_dim", _i32), ("block_size", _i32), ("num_blocks", _i32), ("max_blocks", _i32),
@@ -62,7 +73,7 @@ class KdaCacheAttentionArgs(ctypes.Structure):
                 ("workspace", _ptr), ("workspace_bytes", _i64), ("err_flag", _ptr)]
 
 
-class KdaVerifyArgs(ctypes.Structure):
+class KdaVerifyArgs(_Args):
     """Mirror of ``KdaVerifyArgs``."""
     _fields_ = [("struct_size", _u32), ("N", _i32), ("T", _i32), ("V", _i32), ("draft_tokens", _ptr),
                 ("target_probs", _ptr), ("target_row_stride", _i64), ("draft_probs", _ptr), ("draft_row_stride", _i64),

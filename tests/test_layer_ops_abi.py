@@ -104,6 +104,16 @@ def test_host_tensors_are_refused(lib):
         kda_logprobs(z(2, 9))
 
 
+@pytest.mark.parametrize("struct, field", [(L.KdaAddNormArgs, "T"), (L.KdaLinearArgs, "M"), (L.KdaLinearArgs, "N"), (L.KdaLinearArgs, "K"),
+                                           (L.KdaLogprobsArgs, "R"), (L.KdaLogprobsArgs, "V")])
+def test_sizes_past_32_bits_are_refused(struct, field):
+    # (a tensor of 2^32 + 4 rows is none of 4)
+    for n in (2 ** 31, 2 ** 32 + 4):
+        with pytest.raises(ValueError, match=field):
+            struct(**{field: n})
+    assert getattr(struct(**{field: 2 ** 31 - 1}), field) == 2 ** 31 - 1
+
+
 def test_overlaps():
     whole = torch.zeros(6, 40)
     a = whole[:, :16]
