@@ -597,7 +597,7 @@ extern "C" int kda_logprobs(const KdaLogprobsArgs* a, void* stream) {
       misaligned(a->top_logprobs, 3) || misaligned(a->err_flag, 3))
     return kda_internal_fail(KDA_ERR_ALIGN, "a pointer is not aligned as required");
   if (a->tokens && (a->tokens == a->ranks || a->tokens == a->top_ids || static_cast<const void*>(a->tokens) == a->logprobs ||
-                    static_cast<const void*>(a->tokens) == a->entropy))
+                    static_cast<const void*>(a->tokens) == a->entropy || static_cast<const void*>(a->tokens) == a->top_logprobs))
     return kda_internal_fail(KDA_ERR_SHAPE, "a result may not take the place of the tokens");
   const Params p{a->R, a->V, a->num_top, a->logits, a->logits_row_stride, a->tokens, a->logprobs, a->ranks, a->entropy,
                  a->top_ids, a->top_logprobs, a->err_flag};

@@ -94,6 +94,14 @@ def test_logprobs_codes(lib):
     assert call(logits=at["logits"] + 1, flags=1) == ALIGN
 
 
+@pytest.mark.parametrize("result", ["logprobs", "ranks", "entropy", "top_ids", "top_logprobs"])
+def test_logprobs_keep_their_tokens(lib, result):
+    names = ("logits", "tokens", "logprobs", "ranks", "entropy", "top_ids", "top_logprobs")
+    at = {n: 0x100000 * (i + 1) for i, n in enumerate(names)}
+    call = caller(lib, "kda_logprobs", L.KdaLogprobsArgs, dict(R=4, V=100, num_top=5, logits_row_stride=100, **at))
+    assert call(**{result: at["tokens"]}) == SHAPE
+
+
 def test_host_tensors_are_refused(lib):
     z = torch.zeros
     with pytest.raises(ValueError, match="CUDA"):
