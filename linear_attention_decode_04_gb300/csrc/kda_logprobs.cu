@@ -87,7 +87,8 @@ struct Shared {
   Sums warp_sums[kWarps];
   int warp_count[kWarps];
   uint32_t warp_bound[kWarps];
-  int spots, halves, listed, failed;
+  int found[2][kWarps + 1];
+  int spots, halves, listed, none, failed;
   // in a cluster's first CTA: what every CTA has of the row
   uint64_t part_top[kMaxCluster][kMaxTop];
   Sums part_sums[kMaxCluster];
@@ -189,6 +190,39 @@ struct Row {
   }
 };
 
+// Fewer alternatives than asked for: the first elements equal to the bound, and where fewer are above -infinity the first of
+// those that are not, which most are.  For all threads of the CTA.
+template <bool BF16, class C>
+__device__ __forceinline__ void first_equal(Shared<C>& S, int tid, int warp, int lane, const Row<BF16>& row, int begin, int end,
+                                            bool ends, int have, int top, float next) {
+  constexpr int W = Row<BF16>::W;
+  const int head = ends ? row.head : 0, last = head + (end - begin) * W, count = ends ? last + row.tail : last;
+  int turn = 0;
+  for (;; next = -INFINITY) {
+    for (int q0 = 0; q0 < count && have < top; q0 += C::kAllThreads, turn ^= 1) {  // head, slice, tail
+      const int q = q0 + tid, i = q < head ? q : q < last ? row.first(begin) + q - head : q < count ? row.V - row.tail + q - last : -1;
+      const bool here = i >= 0 && row.at(i) == next;
+      const uint32_t found = __ballot_sync(0xffffffffu, here);
+      if (lane == 0) S.found[turn][warp] = __popc(found);
+      __syncthreads();
+      int place = have + __popc(found & ((1u << lane) - 1));
+      for (int w = 0; w <= C::kWarps; ++w) {
+        if (w < warp) place += S.found[turn][w];
+        have += S.found[turn][w];
+      }
+      if (here && place < top) S.best[place] = key_of(next, i);
+    }
+    if (next == -INFINITY) return;
+  }
+}
+
+// For fp32 rows a call, as it is seldom needed (64 x 4 rows of 131,072 35.7 us, inlined 36.2); in bf16 rows the call costs the
+// sums registers (4,099 rows of 100,003 242 us, inlined 238).
+template <class C>
+__device__ __noinline__ void first_equal_f32(Shared<C>& S, Row<false> row, int begin, int end, bool ends, int have, int top, float next) {
+  first_equal<false>(S, threadIdx.x, threadIdx.x >> 5, threadIdx.x & 31, row, begin, end, ends, have, top, next);
+}
+
 template <bool BF16, int THREADS>
 __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtasPerSm) logprobs_kernel(const Params p, int cluster) {
   using C = Cfg<THREADS>;
@@ -206,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
     for (int i = 0; i < kStages; ++i) bar_init(&S.full[i], 1), bar_init(&S.empty[i], kWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 0) S.spots = S.halves = S.listed = S.failed = 0;
+  if (tid == 0) S.spots = S.halves = S.listed = S.none = S.failed = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int token = p.tokens ? p.tokens[r] : 0;
@@ -380,10 +414,13 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
       }
     }
     if (lane == 0) S.warp_sums[warp] = w, S.warp_count[warp] = n, S.warp_bound[warp] = bound;
+    if (lane == 0 && (!(w.s < INFINITY) || w.m == INFINITY)) S.none = 1;
   }
   __syncthreads();
   if (tid == 0 && S.failed && p.err) atomicOr(p.err, KDA_DEVERR_TIMEOUT);
-  if (p.top > 0) {
+  if (S.none) {  // a row with NaN or +infinity is no distribution, and has no alternatives (all of it may reach the bound)
+    if (tid < kMaxTop) S.best[tid] = 0;
+  } else if (p.top > 0) {
     uint32_t bound = S.warp_bound[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) bound = min(bound, S.warp_bound[w]);
@@ -400,11 +437,14 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
       const int n = atomicAdd(&S.listed, 1);
       if (n < kList) S.list[n] = key;
     };
-    if (edge >= 0 && edge_x >= least) list(key_of(edge_x, edge));
     __syncthreads();
-    // ---- the elements at or above it
+    // ---- the elements at or above it.  Where many threads have two, most are equal to it (a row of one value, say): then
+    // those above it, and the first of the others.
+    const bool ties = S.halves > kThreads / 2;
+    const float from = ties ? float_above(least) : least;
+    if (edge >= 0 && edge_x >= from) list(key_of(edge_x, edge));
     const int spots = S.spots * kHalf, vecs = fills * kBatches * kHalf, all = spots + S.halves * vecs;  // vectors; of a half
-    auto scan = [&](float from, auto f) {  // f(key) for those from a value on
+    auto scan = [&](float low, auto f) {  // f(key) for those from a value on
       constexpr int kAhead = 4;
       for (int q0 = tid; q0 < all; q0 += kAhead * kAllThreads) {
         uint4 u[kAhead];
@@ -428,15 +468,15 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
           Row::values(u[a], x);
 #pragma unroll
           for (int e = 0; e < W; ++e) top = fmaxf(top, x[e]);
-          if (top >= from) {
+          if (top >= low) {
 #pragma unroll
             for (int e = 0; e < W; ++e)
-              if (x[e] >= from) f(key_of(x[e], row.first(where[a]) + e));
+              if (x[e] >= low) f(key_of(x[e], row.first(where[a]) + e));
           }
         }
       }
     };
-    scan(least, list);
+    scan(from, list);
     __syncthreads();
     const int n = S.listed;
     if (n <= kList) {
@@ -448,24 +488,10 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
         for (int k = 0; k < n; ++k) before += S.list[k] > key;
         if (before < p.top) S.best[before] = key;
       }
-      // fewer than asked for are above -infinity: then the first of those that are not, which most are
-      if (warp == 0 && n < p.top) {
-        __syncwarp();
-        const int64_t inner = static_cast<int64_t>(end - begin) * W, edges = rank == 0 ? row.head + row.tail : 0;
-        int have = n;
-        for (int64_t q0 = 0; q0 < inner + edges && have < p.top; q0 += 32) {  // head, slice, tail
-          const int64_t q = q0 + lane, h = rank == 0 ? row.head : 0;
-          const int i = q < h ? static_cast<int>(q) : q < h + inner ? static_cast<int>(row.first(begin) + (q - h))
-                      : q < inner + edges ? static_cast<int>(row.V - row.tail + (q - h - inner)) : -1;
-          const bool out = i >= 0 && row.at(i) == -INFINITY;
-          const uint32_t ruled = __ballot_sync(0xffffffffu, out);
-          const int rank_of = have + __popc(ruled & ((1u << lane) - 1));
-          if (out && rank_of < p.top) S.best[rank_of] = key_of(-INFINITY, i);
-          have += __popc(ruled);
-        }
-      }
+      if constexpr (BF16) first_equal<true>(S, tid, warp, lane, row, begin, end, rank == 0, n, p.top, ties ? least : -INFINITY);
+      else if (n < p.top) first_equal_f32(S, row, begin, end, rank == 0, n, p.top, ties ? least : -INFINITY);
     } else {
-      // many elements of few threads reach the bound (rows in order, say), or many are equal: one alternative after another
+      // many elements of few threads reach the bound (rows in order, say): one alternative after another
       uint64_t last = ~0ull;
       for (int k = 0; k < p.top; ++k) {
         uint64_t top = 0;

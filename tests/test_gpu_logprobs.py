@@ -106,6 +106,45 @@ def test_large_logits_in_one_threads_elements(rows_, cuda_device):
     check(cuda_device, x, t, 32)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows_, V", [(2, 700), (2, 5003), (3, 40001), (1, 300007), (700, 1030), (640, 9001)])
+def test_many_equal_elements_at_the_bound(rows_, V, dt, cuda_device):
+    # more of them than a CTA lists, behind few that are larger: the first of them, wherever they begin
+    i = torch.arange(V)
+    few = torch.zeros(V)
+    few[[V - 1, V // 2, 3]] = torch.tensor([2.0, 1.0, 2.0])
+    low = torch.full((V,), -8.0)
+    kinds = [few, torch.where(i >= V - V // 3, 0.0, low), torch.where(i < V // 3, 0.0, low) + 4 * few, torch.where(i % 5 == 2, 0.0, low),
+             torch.where(i >= V - 40, 0.0, low), torch.where(i % 2 == 0, -math.inf, 0.0) + few]
+    for k, x in enumerate(kinds):
+        x = x.repeat(rows_, 1).to(dt)
+        wide = torch.full((rows_, V + 13), 50.0, dtype=dt, device=cuda_device)[:, k:k + V]
+        wide.copy_(x)
+        check(cuda_device, x, torch.full((rows_,), V - 1, dtype=torch.int32), 32, gpu_logits=wide)
+
+
+@pytest.mark.parametrize("R_, V, dt", [(256, 131072, torch.float32), (1000, 100003, torch.bfloat16)])
+def test_rows_of_one_value_take_no_longer_than_a_few_others(R_, V, dt, cuda_device):
+    g = torch.Generator(device=cuda_device).manual_seed(0)
+    t = torch.zeros(R_, dtype=torch.int32, device=cuda_device)
+
+    def time(x):
+        call = KdaLogprobsCall(x.to(dt), t, num_top=20)
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    usual = time(torch.randn(R_, V, generator=g, device=cuda_device) * 3)
+    for v in (0.0, math.nan, math.inf, -math.inf):
+        assert time(torch.full((R_, V), v, device=cuda_device)) < 6 * usual, v
+
+
 def test_ruled_out_tokens(cuda_device):
     x, t = rows(6, 2000, 3)
     x[0, 100:1900] = -math.inf
