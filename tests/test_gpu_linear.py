@@ -94,6 +94,17 @@ def test_every_gated_tile(e4m3, M, N, K, f32, cuda_device):
         assert (out[:, N // 2:] == 9.0).all()
 
 
+@pytest.mark.parametrize("e4m3, M, N, K", [(False, 2455, 19, 11456), (True, 2455, 2, 22912)])
+def test_tiles_of_128_rows_in_four_parts(e4m3, M, N, K, cuda_device):
+    test_every_tile_and_share_of_k(e4m3, M, N, K, cuda_device)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("e4m3, M, N, K", [(True, 1300, 3600, 1600), (False, 1300, 3600, 800), (False, 700, 9008, 776)])
+def test_gated_tiles_of_two_warpgroups(e4m3, M, N, K, f32, cuda_device):
+    test_every_gated_tile(e4m3, M, N, K, f32, cuda_device)
+
+
 @pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("K", [1, 7, 31, 33, 65, 127, 130, 1001])
 @pytest.mark.parametrize("M, N", [(3, 5), (40, 200), (300, 260)])
