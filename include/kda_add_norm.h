@@ -9,7 +9,7 @@
  *   y  = h / sqrt(mean(h^2) + eps) * weight   (a NULL weight counts as ones)
  *   y  = h                                 with KDA_ADD_NORM_NO_NORM
  *   residual_out = h,  out = y             rounded to bf16
- *   out_scale[t] = max(max|y|, 2^-100) / 448
+ *   out_scale[t] = max(max|y|, 2^-100) * (1 / 448), the factor rounded to fp32
  *   out_q        = y / out_scale[t]        rounded to fp32, then to e4m3
  * The sum is not rounded before the norm, and y not before its code is made;
  * everything in between is fp32, and squares that fp32 does not hold are made

@@ -17,7 +17,7 @@
 
 namespace {
 
-constexpr float kMaxCode = 448.f;       // largest e4m3 value
+constexpr float kPerCode = 1.f / 448.f;   // 448 is the largest e4m3 value
 constexpr float kScaleFloor = 0x1p-100f;
 constexpr float kLeastSquare = 0x1p-120f;  // of a mean: one of squares that fp32 holds with all their digits
 constexpr uint32_t kInfinity = 0x7f800000u;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) add_norm_kernel(cons
   if (!p.out_q) return;
   const uint32_t top = row_top();
   const float amax = top < kInfinity ? fmaxf(__uint_as_float(top), kScaleFloor) : __uint_as_float(0x7fc00000u);
-  const float scale = amax / kMaxCode, inv = 1.f / scale;
+  const float scale = amax * kPerCode, inv = 1.f / scale;
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
     const int c = tid + i * apart;

@@ -144,7 +144,7 @@ def test_codes_are_quotients_by_the_stored_scale(T, D, scale, cuda_device):
     del got["out"]
     kda_add_norm(x.to(cuda_device), residual=r.to(cuda_device), norm=False, **got)
     y = x.float() + r.float()
-    want = y.abs().amax(-1) / 448
+    want = y.abs().amax(-1) * (torch.tensor(1.0) / 448)
     assert torch.equal(got["out_scale"].cpu(), want)
     codes = (y / want[:, None]).to(torch.float8_e4m3fn)
     assert torch.equal(got["out_q"].cpu().view(torch.uint8), codes.view(torch.uint8))
