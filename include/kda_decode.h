@@ -53,7 +53,9 @@ extern "C" {
  * previous layer's decode, with its own pools).  The call may then start
  * streaming state and conv state while that kernel is still running; all
  * per-token inputs (qkv, g, beta, gate) are still read only after it has
- * completed.  Without this flag nothing is read before it completes. */
+ * completed.  Without this flag nothing is read before it completes.  (Kernels
+ * ahead of that one have ended by then: this library's kernels launch
+ * dependents only when all that is ahead of them has.) */
 #define KDA_EARLY_PREFETCH    4u /* (with src_slot: it too is not written by that kernel) */
 /* g and beta hold raw logits and the kernel activates them (the page's
  * "safe gate" variant; formula below, in KdaDecodeArgs.lower_bound). */

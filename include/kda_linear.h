@@ -12,7 +12,8 @@
  * of each, as kda_add_norm.h makes them.  Products are exact and summed in
  * fp32 (by tensor cores, which cut sums towards zero: fp32 results from short
  * sums, so that they are off by no more than about 2^-20 of sums without much
- * cancellation); the epilogue is fp32 and rounded once, to out's type.  A row of x that
+ * cancellation); the epilogue is fp32 and rounded once, to out's type (silu's
+ * values below 2^-119 come out as 0).  A row of x that
  * is not finite, or whose scale is NaN, reaches no other row.
  */
 #ifndef KDA_LINEAR_H
@@ -38,7 +39,9 @@ extern "C" {
 /* The kernel directly ahead of this one in the stream does not write weight,
  * weight_scale or bias: they may be read while it still runs.  (Kernels ahead
  * of that one may: they have ended by then, as this library's kernels launch
- * dependents only when all that is ahead of them has.) */
+ * dependents only when all that is ahead of them has.  Behind a kernel of
+ * another library that launches dependents sooner than that, the promise is
+ * about whatever may still be running ahead of it too.) */
 #define KDA_LINEAR_EARLY_WEIGHT 4u
 
 /*

@@ -3,8 +3,8 @@
 //
 // A CTA (or a warp) per row: the row stays in registers from its load to its
 // codes, so that every byte crosses HBM once, which bounds large calls: 16,384
-// rows of 6,144 channels with residual and 8-bit output, 705 MB, 102.7 us,
-// 6.9 TB/s (some of it from L2; a copy has 6.8).  256 rows take 4.1 us (2.1 at
+// rows of 6,144 channels with residual and 8-bit output, 705 MB, 103.2 us,
+// 6.8 TB/s (some of it from L2; a copy has 6.8).  256 rows take 4.1 us (2.1 at
 // that rate), 4 rows of 2,048 2.9: the launch, a load and its two reductions.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -54,11 +54,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// The quotients by the scale as it is stored, rounded to fp32 and then to codes.  (Products with the rounded reciprocal
-// 448 / amax alone give 1 of 5,000 codes the other neighbour of a value near their middle, mostly the farther one.)  q = f r
-// with r = 1 / scale rounded, and once more with its exact remainder: q + (f - q scale) r is the rounded quotient
-// (Markstein 1990).  A division per element instead: 16,384 rows of 6,144 channels
-// 120 us instead of 105, without residual and norm 71 instead of 56 (with the product alone 104 and 53).
+// The quotients by the scale as it is stored, rounded to fp32 and then to codes.  (Products with 448 / amax as rounded give
+// 229 of 9.5 million codes of bf16 rows the other neighbour of a quotient near their middle.)  q = f r with r = 1 / scale
+// rounded, and once more with its exact remainder: q + (f - q scale) r is the rounded quotient (Markstein 1990).  A
+// division per element instead: 16,384 rows of 6,144 channels 120 us instead of 104, without residual and norm 71 instead
+// of 55 (with the product alone 104 and 53).
 __device__ __forceinline__ uint2 codes(const float (&f)[8], float scale, float inv) {
   const uint64_t r = pair_of(inv, inv), minus = pair_of(-scale, -scale);
   uint32_t w[4];

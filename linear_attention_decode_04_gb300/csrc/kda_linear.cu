@@ -19,7 +19,7 @@
 // What bounds it: with few rows the weights' bytes (64 x 18,432 x 6,144 in e4m3
 // 21.7 us, 5.3 TB/s; 64 x 16,384 x 6,144 gated in bf16 37.3 us, 5.4 TB/s), behind
 // a start of some 4.5 us and the results of the last tile (4 x 4,608 x 2,048
-// 6.2 us); with many the tensor cores, at the card's power limit (16,384 x 18,432 x
+// 5.9 to 6.2 us); with many the tensor cores, at the card's power limit (16,384 x 18,432 x
 // 6,144 in e4m3 1.1 ms, 3.3 PFLOP/s, 0.98 ms from a cool start; 8,192 x 8,192 x
 // 8,192 in bf16 0.63 ms, 1.7 PFLOP/s); with short k the results' arithmetic and
 // stores (8,192 x 8,192 x 128 43 us, 3.1 TB/s written).

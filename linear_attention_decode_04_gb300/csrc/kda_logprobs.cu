@@ -15,9 +15,10 @@
 // reach the bound.
 //
 // What bounds it: many fp32 rows HBM (1,000 rows of 131,072 94 us, 5.5 TB/s), bf16
-// rows the issue of some 10 instructions per element (4,099 rows of 100,003 197
-// us, 4.2 TB/s), few rows the launch, a CTA's share of the row and the join
-// (one row of 131,072 7.5 us).
+// rows the issue of 19 instructions per element, 80% of all slots (4,099 rows of
+// 100,003 198 us, 4.1 TB/s), few rows the launch, a CTA's share of the row and the
+// join (one row of 131,072 7.4 to 7.9 us).  Rows of one value, whose elements all
+// reach the bound, take two to three times as long.
 //
 // Orders are those of 64-bit keys, the logit's bits in an order-preserving form
 // above the complement of the index: keys differ, so ties go to the lower index and
