@@ -439,11 +439,9 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
       if (n < kList) S.list[n] = key;
     };
     __syncthreads();
-    // ---- the elements at or above it.  Where many threads have two, most are equal to it (a row of one value, say): then
-    // those above it, and the first of the others.
-    const bool ties = S.halves > kThreads / 2;
-    const float from = ties ? float_above(least) : least;
-    if (edge >= 0 && edge_x >= from) list(key_of(edge_x, edge));
+    // ---- the elements at or above it.  Where many threads have two, or they are more than the list takes, most are equal to
+    // it (a row of one value, say): then those above it, and the first of the others.
+    bool ties = S.halves > kThreads / 2;
     const int spots = S.spots * kHalf, vecs = fills * kBatches * kHalf, all = spots + S.halves * vecs;  // vectors; of a half
     auto scan = [&](float low, auto f) {  // f(key) for those from a value on
       constexpr int kAhead = 4;
@@ -477,9 +475,18 @@ __global__ void __launch_bounds__(Cfg<THREADS>::kAllThreads, Cfg<THREADS>::kCtas
         }
       }
     };
-    scan(from, list);
-    __syncthreads();
-    const int n = S.listed;
+    int n;
+    for (;; ties = true) {
+      const float from = ties ? float_above(least) : least;
+      if (edge >= 0 && edge_x >= from) list(key_of(edge_x, edge));
+      scan(from, list);
+      __syncthreads();
+      n = S.listed;
+      if (n <= kList || ties) break;
+      __syncthreads();
+      if (tid == 0) S.listed = 0;
+      __syncthreads();
+    }
     if (n <= kList) {
       if (tid < p.top && tid >= n) S.best[tid] = 0;
       for (int c = tid; c < n; c += kAllThreads) {
