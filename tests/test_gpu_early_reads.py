@@ -113,3 +113,39 @@ def test_states_written_two_kernels_ahead(N, H, T, between, cuda_device, late_co
         results.append((state, conv, out))
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_two_kernels_ahead_in_a_captured_step(cuda_device, late_copy):
+    # the same order as edges of a graph: weights and states written first, a small call, then those that read them early
+    g, dev = torch.Generator().manual_seed(1), cuda_device
+    between = KdaLinearCall(whole(g, dev, 4, 64), whole(g, dev, 128, 64), torch.zeros(4, 128, device=dev))
+    x, new = whole(g, dev, 20, 512), whole(g, dev, 300, 512)
+    weight, out = torch.zeros_like(new), torch.zeros(20, 300, device=dev)
+    product = KdaLinearCall(x, weight, out, early_weight=True)
+    call, state, conv, y = decode(2, 4, 1, 3, dev, True)
+    fresh, windows = state * 3, conv.clone()
+    state.copy_(fresh)
+    weight.copy_(new)
+    torch.cuda.synchronize(dev)
+    between()
+    call()
+    product()
+    torch.cuda.synchronize(dev)
+    want = [t.clone() for t in (state, conv, y, out)]
+    assert torch.equal(out, x.float() @ new.float().t())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        late_copy(state, fresh)
+        between()
+        call()
+        late_copy(weight, new)
+        between()
+        product()
+    for _ in range(3):
+        for t in (state, weight, y, out):
+            t.zero_()
+        conv.copy_(windows)
+        graph.replay()
+        torch.cuda.synchronize(dev)
+        for a, b in zip(want, (state, conv, y, out)):
+            assert torch.equal(a, b)
